@@ -36,10 +36,10 @@
  * sdt_launch or an entry point's arguments change, or entry points are added
  * (4: the off-ladder rungs 5-7, the [K][N] workspace entry points and
  * sdt_stream_read_runs; 5: sdt_mfma_ceiling, and loader waves: the `loaders`
- * field of sdt_tile and sdt_launch).
+ * field of sdt_tile and sdt_launch; 6: the MX4 and expert entry points).
  * sdt_abi_version() reports the version the library was built with: a caller
  * compiled against another header must not pass these structures to it. */
-#define SDT_ABI_VERSION 5
+#define SDT_ABI_VERSION 6
 
 #ifdef __cplusplus
 extern "C" {
@@ -280,6 +280,226 @@ int gemv_bf16_m1_kn(int64_t N, int64_t K, const void* x,
                     const void* B, int64_t ldb, void* y, void* stream);
 int gemv_bf16_m1_kn_ws(int64_t N, int64_t K, const void* x, const void* B, int64_t ldb,
                        void* y, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---- MX4: microscaled 4-bit matrices ------------------------------------------
+ * An MX4 matrix holds rows of K values in blocks of 32 consecutive k that share
+ * a scale 2^(e - 127), e a byte (e = 255: every value of the block is NaN).
+ * Values are e2m1 codes (sign, 2 exponent bits, 1 fraction bit: 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6 and their negatives), two to a byte, the even k in the low nibble.
+ *   Q: row r is the sdt_mx4_row_bytes(K) = 16 ceil(K / 32) bytes from
+ *      Q + r * ldq (ldq in bytes); codes past K are zero.
+ *   S: the scale bytes, in tiles of 64 rows x 256 k (8 blocks): 512 bytes each,
+ *      the byte of row r, block b of a tile at
+ *      ((b / 2) * 16 + r % 16) * 8 + (r / 16) * 2 + b % 2, so that the 64 lanes
+ *      of a wave read the scales of one scaled MFMA's operand rows side by side.
+ *      Tile (i, j) (rows 64 i.., k 256 j..) is at S + (i * ceil(K / 256) + j) *
+ *      512; the bytes of rows and blocks past the matrix are zero (the products
+ *      rely on it).  sdt_mx4_scale_bytes(rows, K) bytes in all;
+ *      mx4_pack_scales makes it from row-major scale bytes.
+ * Requirements everywhere: Q and S 16-byte aligned, ldq a multiple of 16 and
+ * at least the row bytes (the row bytes alone for a single row), K at most
+ * 2^23, ldq below 2^22 + 16. */
+
+/* Bytes of one row of codes, 16 ceil(K / 32), and of the tiled scales of a rows
+ * x K matrix; -1 for negative sizes.  Host-only. */
+int64_t sdt_mx4_row_bytes(int64_t K);
+int64_t sdt_mx4_scale_bytes(int64_t rows, int64_t K);
+
+/* Q, S = X (rows x K, row stride ldx >= K elements, any alignment of the
+ * element type; 16-byte aligned rows load fastest).  Per block: e = floor(log2(max |x|)) - 2 + 127
+ * clamped to [0, 254], each element x / 2^(e - 127) rounded to the nearest
+ * code, ties to the even one, saturated at 6 (sign kept, also of zeros); a
+ * block of zeros has e = 0; a block that holds an infinity or a NaN has e = 255
+ * and zero codes.  rows == 0 or K == 0 is a no-op.  Limits: as above, rows at
+ * most 2^31 - 1. */
+int mx4_quantize_f16(int64_t rows, int64_t K, const void* X, int64_t ldx,
+                     void* Q, int64_t ldq, void* S, void* stream);
+int mx4_quantize_bf16(int64_t rows, int64_t K, const void* X, int64_t ldx,
+                      void* Q, int64_t ldq, void* S, void* stream);
+
+/* The same for rows named by a list on the device: row p of Q, S (p < rows) is
+ * row index[p] / divisor of X (divisor 0: row p of X), which has xrows rows;
+ * where index[p] < 0, or the row is outside X, the row's codes are left as they
+ * are and its scales are zero.  moe_plan's `rows` with divisor topk copies each
+ * token's row to its experts' segments. */
+int mx4_quantize_rows_f16(int64_t rows, int64_t K, const void* X, int64_t xrows, int64_t ldx,
+                          const int32_t* index, int divisor,
+                          void* Q, int64_t ldq, void* S, void* stream);
+int mx4_quantize_rows_bf16(int64_t rows, int64_t K, const void* X, int64_t xrows, int64_t ldx,
+                           const int32_t* index, int divisor,
+                           void* Q, int64_t ldq, void* S, void* stream);
+
+/* Y (rows x K, row stride ldy >= K elements) = the values Q, S stand for, in
+ * the type of the name (rounded to nearest even where it cannot hold them). */
+int mx4_dequantize_f16(int64_t rows, int64_t K, const void* Q, int64_t ldq, const void* S,
+                       void* Y, int64_t ldy, void* stream);
+int mx4_dequantize_bf16(int64_t rows, int64_t K, const void* Q, int64_t ldq, const void* S,
+                        void* Y, int64_t ldy, void* stream);
+int mx4_dequantize_f32(int64_t rows, int64_t K, const void* Q, int64_t ldq, const void* S,
+                       void* Y, int64_t ldy, void* stream);
+
+/* S (tiled) = row-major scale bytes R, block b of row r at R[r * ldr + b],
+ * ldr >= ceil(K / 32). */
+int mx4_pack_scales(int64_t rows, int64_t K, const void* R, int64_t ldr, void* S, void* stream);
+
+/* C = A . B^T for MX4 matrices A (M x K) and B (N x K): the exact products of
+ * the values, accumulated in fp32 on the scaled MFMAs, rounded once to the
+ * type of the name.  C as gemm_f16's: 16-byte aligned, ldc >= N a multiple of 8.  M == 0 or
+ * N == 0 is a no-op; K == 0 writes zeros.  Deterministic.  Few rows (M <= 64
+ * where the tiles would leave the device idle) stream B once through a kernel
+ * without LDS staging; others run 64 x 64, 128 x 128 or 256 x 256 tiles by the
+ * output-block count, as the 16-bit products do. */
+int gemm_mx4_f16(int64_t M, int64_t N, int64_t K,
+                 const void* A, int64_t lda, const void* SA,
+                 const void* B, int64_t ldb, const void* SB,
+                 void* C, int64_t ldc, void* stream);
+int gemm_mx4_bf16(int64_t M, int64_t N, int64_t K,
+                  const void* A, int64_t lda, const void* SA,
+                  const void* B, int64_t ldb, const void* SB,
+                  void* C, int64_t ldc, void* stream);
+
+/* y(n) = sum_k x(k) * B(n, k): the M = 1 product of K 16-bit activations (type
+ * of the name, any alignment of it) with an MX4 weight matrix; fp32
+ * accumulation, y in the type of the name.  N == 0 is a no-op, K == 0 writes
+ * zeros.  Deterministic. */
+int gemv_mx4_m1_f16(int64_t N, int64_t K, const void* x,
+                    const void* B, int64_t ldb, const void* SB, void* y, void* stream);
+int gemv_mx4_m1_bf16(int64_t N, int64_t K, const void* x,
+                     const void* B, int64_t ldb, const void* SB, void* y, void* stream);
+
+/* ---- experts: routing, plan, grouped products ----------------------------------- */
+
+/* How tokens choose experts. */
+typedef struct sdt_route {
+    int topk;          /* experts a token takes, 1 .. 64 */
+    int score;         /* 0: softmax over the experts; 1: sigmoid of each logit */
+    int groups;        /* the experts in this many equal groups (1: no groups) */
+    int groups_kept;   /* groups a token may choose from */
+    int group_top;     /* a group's worth: the sum of its 1 or 2 best */
+    int renormalize;   /* 1: the weights are divided by their sum */
+    float scale;       /* and multiplied by this */
+} sdt_route;
+
+/* idx, weights (T x topk, tight, int32 and fp32) = the experts of T tokens from
+ * their logits (T x E, row stride ld >= E elements, in the type of the name).
+ * Choice: without a bias by the logits themselves; with one (E fp32 values) by
+ * score + bias in 64 bits.  With groups > 1 only the groups_kept groups of
+ * largest worth are chosen from (worth: of the same values; group_top == 2
+ * without a bias: the sum of the two largest scores in 64 bits).  Largest
+ * first; ties go to the lower index, groups likewise.  Weights: the scores
+ * (never the bias) of the chosen, over their sum where renormalize is set,
+ * times scale.  A NaN logit counts as -infinity, whose score is 0; a row with
+ * nothing but these has zero weights (its choice follows the ties); +infinity
+ * takes the whole softmax, shared evenly.  A NaN of score + bias counts as
+ * -infinity.  SDT_ERR_INVALID_ARG: E < 1, topk outside [1, min(64, groups_kept *
+ * E / groups)], groups not a divisor of E, groups_kept outside [1, groups],
+ * group_top not 1 or 2 or larger than a group, a score or flag outside its
+ * values, a scale that is not finite, ld < E, a null pointer (bias may be
+ * NULL).  SDT_ERR_UNSUPPORTED: E > 1024, groups > 64, T past 2^31 - 1.
+ * T == 0 is a no-op. */
+int moe_route_f32(int64_t T, int64_t E, const void* logits, int64_t ld, const float* bias,
+                  const sdt_route* cfg, int32_t* idx, float* weights, void* stream);
+int moe_route_f16(int64_t T, int64_t E, const void* logits, int64_t ld, const float* bias,
+                  const sdt_route* cfg, int32_t* idx, float* weights, void* stream);
+int moe_route_bf16(int64_t T, int64_t E, const void* logits, int64_t ld, const float* bias,
+                   const sdt_route* cfg, int32_t* idx, float* weights, void* stream);
+
+/* dlogits (T x E, row stride ldd, the logits' type) from dweights (T x topk,
+ * fp32): the gradient of the weights with the choice idx held fixed (the bias
+ * only chooses, its gradient is zero).  An idx outside [0, E) takes no part;
+ * rows whose weights are all zero by definition have zero gradients.  Checks as
+ * moe_route. */
+int moe_route_backward_f32(int64_t T, int64_t E, const void* logits, int64_t ld,
+                           const sdt_route* cfg, const int32_t* idx, const float* dweights,
+                           void* dlogits, int64_t ldd, void* stream);
+int moe_route_backward_f16(int64_t T, int64_t E, const void* logits, int64_t ld,
+                           const sdt_route* cfg, const int32_t* idx, const float* dweights,
+                           void* dlogits, int64_t ldd, void* stream);
+int moe_route_backward_bf16(int64_t T, int64_t E, const void* logits, int64_t ld,
+                            const sdt_route* cfg, const int32_t* idx, const float* dweights,
+                            void* dlogits, int64_t ldd, void* stream);
+
+/* Where the tokens of each expert lie: device arrays owned by the caller.  A
+ * slot is token * topk + j.  The slots of expert e, in rising order, take the
+ * rows offsets[e] .. offsets[e] + counts[e] - 1; every expert's rows start at a
+ * multiple of 64.  sdt_moe_plan_rows(tokens, topk, experts) rows are enough for
+ * any choice. */
+typedef struct sdt_moe_plan {
+    int64_t tokens;
+    int topk;
+    int experts;
+    int32_t* counts;   /* experts */
+    int32_t* offsets;  /* experts + 1 */
+    int32_t* rows;     /* plan rows: the slot of each row, -1 where there is none */
+    int32_t* pos;      /* tokens * topk: the row of each slot, -1 where its expert
+                          is outside [0, experts) */
+    int32_t* tiles;    /* plan rows / 64: the expert of 64 rows, -1 where there is none */
+} sdt_moe_plan;
+
+/* Rows of a plan: 64 floor((R + 63 min(experts, R)) / 64), R = tokens * topk;
+ * -1 for sizes that are negative, have topk < 1 or experts < 1, or give more
+ * than 2^31 - 1 rows.  Host-only. */
+int64_t sdt_moe_plan_rows(int64_t tokens, int topk, int experts);
+
+/* Fills the plan's arrays from idx (tokens x topk, tight).  Deterministic, no
+ * workspace.  tokens == 0: counts and offsets are zeroed.  SDT_ERR_UNSUPPORTED:
+ * experts > 1024. */
+int moe_plan(const int32_t* idx, const sdt_moe_plan* plan, void* stream);
+
+/* One MX4 weight matrix per expert: expert e's codes at q + e * q_expert (rows
+ * ldq apart) and tiled scales at s + e * s_expert (all in bytes, multiples of 16). */
+typedef struct sdt_mx4_experts {
+    const void* q;
+    int64_t ldq;
+    int64_t q_expert;
+    const void* s;
+    int64_t s_expert;
+} sdt_mx4_experts;
+
+/* C(p, :) = A(p, :) . B_e^T for every row p of the plan that holds a slot, e its
+ * expert: A (plan rows x K, MX4), B_e (N x K), C (plan rows x N, type of the
+ * name, 16-byte aligned, ldc a multiple of 8).  With `up`: C = silu(A . B_e^T) *
+ * (A . up_e^T), silu(g) = g / (1 + exp(-g)), computed in fp32 and rounded once.
+ * Rows without a slot are not written.  Few rows an expert stream the weights,
+ * many run tiles, as gemm_mx4. */
+int moe_gemm_mx4_f16(const sdt_moe_plan* plan, int64_t N, int64_t K,
+                     const void* A, int64_t lda, const void* SA,
+                     const sdt_mx4_experts* B, const sdt_mx4_experts* up,
+                     void* C, int64_t ldc, void* stream);
+int moe_gemm_mx4_bf16(const sdt_moe_plan* plan, int64_t N, int64_t K,
+                      const void* A, int64_t lda, const void* SA,
+                      const sdt_mx4_experts* B, const sdt_mx4_experts* up,
+                      void* C, int64_t ldc, void* stream);
+
+/* Y(t, :) = sum_j weights(t, j) * D(pos(t, j), :), in fp32, j rising, slots
+ * with pos < 0 left out, rounded once: D (plan rows x N) and Y (tokens x N) in
+ * the type of the name, 16-byte aligned rows (ldd, ldy multiples of 8). */
+int moe_combine_f16(const sdt_moe_plan* plan, int64_t N, const void* D, int64_t ldd,
+                    const float* weights, void* Y, int64_t ldy, void* stream);
+int moe_combine_bf16(const sdt_moe_plan* plan, int64_t N, const void* D, int64_t ldd,
+                     const float* weights, void* Y, int64_t ldy, void* stream);
+
+/* A layer of gated experts in one call: Y = sum over a token's experts of
+ * weight * (silu(x G_e^T) * (x U_e^T)) D_e^T, x and the gated product quantised
+ * to MX4 before each product (the gated product and the experts' outputs are
+ * rounded to the type of the name first).  The calls above in order: moe_plan,
+ * mx4_quantize_rows, moe_gemm_mx4 with `up`, mx4_quantize_rows, moe_gemm_mx4,
+ * moe_combine; the results are theirs, bit for bit.  X (tokens x K, stride ldx
+ * elements), gate and up (N x K), down (K x N), Y (tokens x K, ldy a multiple
+ * of 8, 16-byte aligned).  workspace: device memory, 16-byte aligned, at least
+ * sdt_moe_experts_workspace_size bytes (fewer: SDT_ERR_INVALID_ARG); no
+ * initialisation; calls that share it must be ordered on one stream. */
+typedef struct sdt_moe_layer {
+    int64_t N, K;
+    sdt_mx4_experts gate, up, down;
+} sdt_moe_layer;
+int64_t sdt_moe_experts_workspace_size(int64_t tokens, int topk, int experts, int64_t N, int64_t K);
+int moe_experts_mx4_f16(const sdt_moe_layer* layer, const int32_t* idx, const float* weights,
+                        const sdt_moe_plan* plan, const void* X, int64_t ldx, void* Y, int64_t ldy,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+int moe_experts_mx4_bf16(const sdt_moe_layer* layer, const int32_t* idx, const float* weights,
+                         const sdt_moe_plan* plan, const void* X, int64_t ldx, void* Y, int64_t ldy,
+                         void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ---- test / benchmark extras ---------------------------------------------- */
 

@@ -33,10 +33,19 @@ EXPORTS = (
     "sdt_workspace_init", "sdt_pick_tile_ws", "sdt_abi_version", "sdt_stream_read_grid",
     "gemm_f16_noalloc", "gemv_f16_m1_kn_ws", "gemv_bf16_m1_kn_ws", "sdt_gemv_kn_workspace_size",
     "sdt_stream_read_runs", "sdt_mfma_ceiling",
+    "sdt_mx4_row_bytes", "sdt_mx4_scale_bytes", "mx4_pack_scales",
+    "mx4_quantize_f16", "mx4_quantize_bf16", "mx4_quantize_rows_f16", "mx4_quantize_rows_bf16",
+    "mx4_dequantize_f16", "mx4_dequantize_bf16", "mx4_dequantize_f32",
+    "gemm_mx4_f16", "gemm_mx4_bf16", "gemv_mx4_m1_f16", "gemv_mx4_m1_bf16",
+    "moe_route_f32", "moe_route_f16", "moe_route_bf16",
+    "moe_route_backward_f32", "moe_route_backward_f16", "moe_route_backward_bf16",
+    "sdt_moe_plan_rows", "moe_plan", "moe_gemm_mx4_f16", "moe_gemm_mx4_bf16",
+    "moe_combine_f16", "moe_combine_bf16",
+    "sdt_moe_experts_workspace_size", "moe_experts_mx4_f16", "moe_experts_mx4_bf16",
 )
 
 # The include/sdt.h version these structures and signatures follow.
-ABI_VERSION = 5
+ABI_VERSION = 6
 
 
 class SdtTile(ctypes.Structure):
@@ -59,6 +68,29 @@ class SdtLaunch(ctypes.Structure):
                 ("kgroups", ctypes.c_int), ("stagger", ctypes.c_int),
                 ("splits", ctypes.c_int), ("split_algo", ctypes.c_int),
                 ("persistent", ctypes.c_int), ("loaders", ctypes.c_int)]
+
+
+class SdtRoute(ctypes.Structure):
+    """sdt_route: how tokens choose experts (route_cfg makes one)."""
+    _fields_ = [("topk", ctypes.c_int), ("score", ctypes.c_int), ("groups", ctypes.c_int),
+                ("groups_kept", ctypes.c_int), ("group_top", ctypes.c_int),
+                ("renormalize", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class SdtMoePlan(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("topk", ctypes.c_int), ("experts", ctypes.c_int),
+                ("counts", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+                ("rows", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("tiles", ctypes.c_void_p)]
+
+
+class SdtMx4Experts(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("q_expert", ctypes.c_int64),
+                ("s", ctypes.c_void_p), ("s_expert", ctypes.c_int64)]
+
+
+class SdtMoeLayer(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("K", ctypes.c_int64), ("gate", SdtMx4Experts),
+                ("up", SdtMx4Experts), ("down", SdtMx4Experts)]
 
 
 class SdtError(RuntimeError):
@@ -147,11 +179,45 @@ def lib():
                  "gemv_f16_m1_kn_ws", "gemv_bf16_m1_kn_ws", "sdt_stream_read_runs",
                  "sdt_mfma_ceiling"):
         getattr(L, name).restype = _int
+    _declare_mx4(L)
     if L.sdt_abi_version() != ABI_VERSION:
         raise RuntimeError(f"{LIB_PATH} has ABI version {L.sdt_abi_version()}, this binding "
                            f"expects {ABI_VERSION}: rebuild the library")
     _lib = L
     return L
+
+
+def _declare_mx4(L):
+    plan, experts = ctypes.POINTER(SdtMoePlan), ctypes.POINTER(SdtMx4Experts)
+    route, layer = ctypes.POINTER(SdtRoute), ctypes.POINTER(SdtMoeLayer)
+    L.sdt_mx4_row_bytes.argtypes = [_i64]
+    L.sdt_mx4_scale_bytes.argtypes = [_i64, _i64]
+    L.mx4_pack_scales.argtypes = [_i64, _i64, _vp, _i64, _vp, _vp]
+    L.sdt_moe_plan_rows.argtypes = [_i64, _int, _int]
+    L.moe_plan.argtypes = [_vp, plan, _vp]
+    L.sdt_moe_experts_workspace_size.argtypes = [_i64, _int, _int, _i64, _i64]
+    for t in ("f16", "bf16"):
+        getattr(L, f"mx4_quantize_{t}").argtypes = [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp]
+        getattr(L, f"mx4_quantize_rows_{t}").argtypes = [_i64, _i64, _vp, _i64, _i64, _vp, _int,
+                                                         _vp, _i64, _vp, _vp]
+        getattr(L, f"gemm_mx4_{t}").argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp,
+                                                _vp, _i64, _vp]
+        getattr(L, f"gemv_mx4_m1_{t}").argtypes = [_i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp]
+        getattr(L, f"moe_gemm_mx4_{t}").argtypes = [plan, _i64, _i64, _vp, _i64, _vp, experts,
+                                                    experts, _vp, _i64, _vp]
+        getattr(L, f"moe_combine_{t}").argtypes = [plan, _i64, _vp, _i64, _vp, _vp, _i64, _vp]
+        getattr(L, f"moe_experts_mx4_{t}").argtypes = [layer, _vp, _vp, plan, _vp, _i64, _vp, _i64,
+                                                       _vp, _i64, _vp]
+    for t in ("f32", "f16", "bf16"):
+        getattr(L, f"mx4_dequantize_{t}").argtypes = [_i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp]
+        getattr(L, f"moe_route_{t}").argtypes = [_i64, _i64, _vp, _i64, _vp, route, _vp, _vp, _vp]
+        getattr(L, f"moe_route_backward_{t}").argtypes = [_i64, _i64, _vp, _i64, route, _vp, _vp,
+                                                          _vp, _i64, _vp]
+    for name in EXPORTS[EXPORTS.index("sdt_mx4_row_bytes"):]:
+        getattr(L, name).restype = _int
+    for name in ("sdt_mx4_row_bytes", "sdt_mx4_scale_bytes", "sdt_moe_plan_rows",
+                 "sdt_moe_experts_workspace_size"):
+        getattr(L, name).restype = _i64
 
 
 # ---- host-only helpers ------------------------------------------------------
@@ -582,3 +648,389 @@ def gemm_f16_raw(M, N, K, A_ptr, lda, B_ptr, ldb, C_ptr, ldc, stream_ptr=None) -
 
 def gemv_f16_m1_raw(N, K, x_ptr, B_ptr, ldb, y_ptr, stream_ptr=None) -> int:
     return int(lib().gemv_f16_m1(int(N), int(K), x_ptr, B_ptr, int(ldb), y_ptr, stream_ptr))
+
+
+# ---- MX4 matrices ---------------------------------------------------------------
+
+def mx4_row_bytes(K: int) -> int:
+    return -(-int(K) // 32) * 16
+
+
+def mx4_scale_bytes(rows: int, K: int) -> int:
+    return -(-int(rows) // 64) * -(-int(K) // 256) * 512
+
+
+class Mx4:
+    """An MX4 matrix on the device (the format: include/sdt.h): uint8 codes `q`
+    [rows, >= mx4_row_bytes(K)] with unit stride along a row, and the tiled scale
+    bytes `s` [mx4_scale_bytes(rows, K)].  With a leading dimension on both, one
+    matrix per expert."""
+
+    __slots__ = ("q", "s", "rows", "K")
+
+    def __init__(self, q, s, rows: int, K: int):
+        import torch
+        rows, K = int(rows), int(K)
+        if q.dtype is not torch.uint8 or s.dtype is not torch.uint8:
+            raise TypeError("Mx4: codes and scales must be uint8")
+        if not q.is_cuda or s.device != q.device:
+            raise TypeError("Mx4: codes and scales must be on one device")
+        if q.dim() not in (2, 3) or s.dim() != q.dim() - 1 or q.shape[:-2] != s.shape[:-1]:
+            raise ValueError(f"Mx4: codes {tuple(q.shape)} and scales {tuple(s.shape)} do not match")
+        if q.shape[-2] != rows or q.shape[-1] < mx4_row_bytes(K) or \
+                s.shape[-1] < mx4_scale_bytes(rows, K):
+            raise ValueError(f"Mx4: codes {tuple(q.shape)} and scales {tuple(s.shape)} cannot hold "
+                             f"{rows} x {K}")
+        if q.stride(-1) != 1 or s.stride(-1) != 1:
+            raise ValueError("Mx4: unit stride along rows of codes and along the scales")
+        self.q, self.s, self.rows, self.K = q, s, rows, K
+
+    @classmethod
+    def empty(cls, rows: int, K: int, experts: int | None = None, device="cuda") -> "Mx4":
+        import torch
+        lead = () if experts is None else (int(experts),)
+        q = torch.empty(lead + (int(rows), mx4_row_bytes(K)), dtype=torch.uint8, device=device)
+        s = torch.empty(lead + (mx4_scale_bytes(rows, K),), dtype=torch.uint8, device=device)
+        return cls(q, s, rows, K)
+
+    def ldq(self) -> int:
+        """Bytes from row to row (a single row's are its own bytes)."""
+        return self.q.stride(-2) if self.rows > 1 else max(self.q.stride(-2), mx4_row_bytes(self.K))
+
+    def _one(self, name):
+        if self.q.dim() != 2:
+            raise ValueError(f"{name} must be one matrix, not one per expert")
+        return self.q.data_ptr(), self.ldq(), self.s.data_ptr()
+
+    def _experts(self, experts, name) -> SdtMx4Experts:
+        if self.q.dim() != 3 or self.q.shape[0] != experts:
+            raise ValueError(f"{name} must hold one matrix for each of {experts} experts")
+        return SdtMx4Experts(self.q.data_ptr(), self.ldq(), self.q.stride(0), self.s.data_ptr(),
+                             self.s.stride(0))
+
+
+def _check(rc: int, where: str) -> None:
+    if rc != SDT_OK:
+        raise SdtError(rc, where)
+
+
+def _quantize(entry, X, out, dtype, stream):
+    px, ldx = _rows(X, "X", dtype)
+    if tuple(X.shape) != (out.rows, out.K):
+        raise ValueError(f"shape mismatch X{tuple(X.shape)} out ({out.rows}, {out.K})")
+    q, ldq, s = out._one("out")
+    _check(getattr(lib(), entry)(out.rows, out.K, px, ldx, q, ldq, s, _stream_handle(stream)), entry)
+
+
+def mx4_quantize_f16(X, out: Mx4, stream=None) -> None:
+    """out = X [rows, K] quantised to MX4."""
+    import torch
+    _quantize("mx4_quantize_f16", X, out, torch.float16, stream)
+
+
+def mx4_quantize_bf16(X, out: Mx4, stream=None) -> None:
+    import torch
+    _quantize("mx4_quantize_bf16", X, out, torch.bfloat16, stream)
+
+
+def _quantize_rows(entry, X, index, divisor, out, dtype, stream):
+    import torch
+    px, ldx = _rows(X, "X", dtype)
+    if X.shape[1] != out.K or tuple(index.shape) != (out.rows,):
+        raise ValueError(f"shape mismatch X{tuple(X.shape)} index{tuple(index.shape)} out "
+                         f"({out.rows}, {out.K})")
+    _ints(index, "index")
+    q, ldq, s = out._one("out")
+    _check(getattr(lib(), entry)(out.rows, out.K, px, X.shape[0], ldx, index.data_ptr(),
+                                 int(divisor), q, ldq, s, _stream_handle(stream)), entry)
+
+
+def mx4_quantize_rows_f16(X, index, divisor: int, out: Mx4, stream=None) -> None:
+    """Row p of out = row index[p] // divisor of X (divisor 0: row p), quantised;
+    rows with index[p] < 0 keep their codes and get zero scales."""
+    import torch
+    _quantize_rows("mx4_quantize_rows_f16", X, index, divisor, out, torch.float16, stream)
+
+
+def mx4_quantize_rows_bf16(X, index, divisor: int, out: Mx4, stream=None) -> None:
+    import torch
+    _quantize_rows("mx4_quantize_rows_bf16", X, index, divisor, out, torch.bfloat16, stream)
+
+
+def _dequantize(entry, m, Y, dtype, stream):
+    py, ldy = _rows(Y, "Y", dtype)
+    if tuple(Y.shape) != (m.rows, m.K):
+        raise ValueError(f"shape mismatch matrix ({m.rows}, {m.K}) Y{tuple(Y.shape)}")
+    q, ldq, s = m._one("matrix")
+    _check(getattr(lib(), entry)(m.rows, m.K, q, ldq, s, py, ldy, _stream_handle(stream)), entry)
+
+
+def mx4_dequantize_f16(m: Mx4, Y, stream=None) -> None:
+    """Y [rows, K] = the values of an MX4 matrix."""
+    import torch
+    _dequantize("mx4_dequantize_f16", m, Y, torch.float16, stream)
+
+
+def mx4_dequantize_bf16(m: Mx4, Y, stream=None) -> None:
+    import torch
+    _dequantize("mx4_dequantize_bf16", m, Y, torch.bfloat16, stream)
+
+
+def mx4_dequantize_f32(m: Mx4, Y, stream=None) -> None:
+    import torch
+    _dequantize("mx4_dequantize_f32", m, Y, torch.float32, stream)
+
+
+def mx4_pack_scales(scales, out: Mx4, stream=None) -> None:
+    """out.s = row-major scale bytes [rows, ceil(K / 32)], tiled."""
+    import torch
+    p, ld = _rows(scales, "scales", torch.uint8)
+    if tuple(scales.shape) != (out.rows, -(-out.K // 32)):
+        raise ValueError(f"shape mismatch scales{tuple(scales.shape)} out ({out.rows}, {out.K})")
+    _, _, s = out._one("out")
+    _check(lib().mx4_pack_scales(out.rows, out.K, p, ld, s, _stream_handle(stream)),
+           "mx4_pack_scales")
+
+
+def _gemm_mx4(entry, A, B, C, dtype, stream):
+    if A.K != B.K or tuple(C.shape) != (A.rows, B.rows):
+        raise ValueError(f"shape mismatch A({A.rows}, {A.K}) B({B.rows}, {B.K}) C{tuple(C.shape)}")
+    pa, lda, sa = A._one("A")
+    pb, ldb, sb = B._one("B")
+    pc, ldc = _rows(C, "C", dtype)
+    _check(getattr(lib(), entry)(A.rows, B.rows, A.K, pa, lda, sa, pb, ldb, sb, pc, ldc,
+                                 _stream_handle(stream)), entry)
+
+
+def gemm_mx4_f16(A: Mx4, B: Mx4, C, stream=None) -> None:
+    """C[M, N] = A[M, K] . B[N, K]^T for MX4 matrices, fp32 accumulate, fp16 out."""
+    import torch
+    _gemm_mx4("gemm_mx4_f16", A, B, C, torch.float16, stream)
+
+
+def gemm_mx4_bf16(A: Mx4, B: Mx4, C, stream=None) -> None:
+    import torch
+    _gemm_mx4("gemm_mx4_bf16", A, B, C, torch.bfloat16, stream)
+
+
+def _gemv_mx4(entry, x, B, y, dtype, stream):
+    if x.dtype != dtype or y.dtype != dtype:
+        raise TypeError(f"x and y must be {dtype}")
+    if not x.is_cuda or not y.is_cuda:
+        raise TypeError("x and y must be device tensors")
+    if x.dim() != 1 or y.dim() != 1 or x.stride(0) != 1 or y.stride(0) != 1:
+        raise ValueError("x and y must be contiguous vectors")
+    if x.shape[0] != B.K or y.shape[0] != B.rows:
+        raise ValueError(f"shape mismatch x{tuple(x.shape)} B({B.rows}, {B.K}) y{tuple(y.shape)}")
+    pb, ldb, sb = B._one("B")
+    _check(getattr(lib(), entry)(B.rows, B.K, x.data_ptr(), pb, ldb, sb, y.data_ptr(),
+                                 _stream_handle(stream)), entry)
+
+
+def gemv_mx4_m1_f16(x, B: Mx4, y, stream=None) -> None:
+    """y[N] = x[K] . B[N, K]^T with 16-bit activations and MX4 weights."""
+    import torch
+    _gemv_mx4("gemv_mx4_m1_f16", x, B, y, torch.float16, stream)
+
+
+def gemv_mx4_m1_bf16(x, B: Mx4, y, stream=None) -> None:
+    import torch
+    _gemv_mx4("gemv_mx4_m1_bf16", x, B, y, torch.bfloat16, stream)
+
+
+# ---- experts -----------------------------------------------------------------------
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def route_cfg(topk: int, score: str = "softmax", groups: int = 1, groups_kept: int = 1,
+              group_top: int = 1, renormalize: bool = True, scale: float = 1.0) -> SdtRoute:
+    """How tokens choose experts (sdt_route)."""
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    return SdtRoute(int(topk), _SCORES[score], int(groups), int(groups_kept), int(group_top),
+                    1 if renormalize else 0, float(scale))
+
+
+def _ints(t, name):
+    import torch
+    if t.dtype is not torch.int32:
+        raise TypeError(f"{name} must be int32, got {t.dtype}")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _floats(t, name):
+    import torch
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _logit_type(t, name):
+    import torch
+    kinds = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
+    if t.dtype not in kinds:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    return kinds[t.dtype]
+
+
+def moe_route(logits, idx, weights, cfg: SdtRoute, bias=None, stream=None) -> None:
+    """idx [T, topk] int32, weights [T, topk] float32 = the experts of T tokens
+    from their logits [T, E]."""
+    kind = _logit_type(logits, "logits")
+    p, ld = _rows(logits, "logits", logits.dtype)
+    T, E = logits.shape
+    if tuple(idx.shape) != (T, cfg.topk) or tuple(weights.shape) != (T, cfg.topk):
+        raise ValueError(f"shape mismatch logits{tuple(logits.shape)} topk {cfg.topk} "
+                         f"idx{tuple(idx.shape)} weights{tuple(weights.shape)}")
+    if bias is not None and tuple(bias.shape) != (E,):
+        raise ValueError(f"bias must hold {E} values")
+    b = None if bias is None else _floats(bias, "bias")
+    entry = "moe_route_" + kind
+    _check(getattr(lib(), entry)(T, E, p, ld, b, ctypes.byref(cfg), _ints(idx, "idx"),
+                                 _floats(weights, "weights"), _stream_handle(stream)), entry)
+
+
+def moe_route_backward(logits, idx, dweights, dlogits, cfg: SdtRoute, stream=None) -> None:
+    """dlogits [T, E] (the logits' type) from dweights [T, topk] float32."""
+    kind = _logit_type(logits, "logits")
+    p, ld = _rows(logits, "logits", logits.dtype)
+    d, ldd = _rows(dlogits, "dlogits", logits.dtype)
+    T, E = logits.shape
+    if tuple(idx.shape) != (T, cfg.topk) or tuple(dweights.shape) != (T, cfg.topk) or \
+            tuple(dlogits.shape) != (T, E):
+        raise ValueError(f"shape mismatch logits{tuple(logits.shape)} topk {cfg.topk} "
+                         f"idx{tuple(idx.shape)} dweights{tuple(dweights.shape)} "
+                         f"dlogits{tuple(dlogits.shape)}")
+    entry = "moe_route_backward_" + kind
+    _check(getattr(lib(), entry)(T, E, p, ld, ctypes.byref(cfg), _ints(idx, "idx"),
+                                 _floats(dweights, "dweights"), d, ldd, _stream_handle(stream)),
+           entry)
+
+
+def moe_plan_rows(tokens: int, topk: int, experts: int) -> int:
+    """Rows of a plan's segments, enough for any choice of experts."""
+    v = int(lib().sdt_moe_plan_rows(int(tokens), int(topk), int(experts)))
+    if v < 0:
+        raise SdtError(SDT_ERR_INVALID_ARG, "sdt_moe_plan_rows")
+    return v
+
+
+class MoePlan:
+    """The arrays of a plan (sdt_moe_plan) for `tokens` tokens of `topk` experts
+    each out of `experts`: int32 device tensors counts, offsets, rows, pos, tiles."""
+
+    __slots__ = ("tokens", "topk", "experts", "size", "counts", "offsets", "rows", "pos", "tiles",
+                 "_struct")
+
+    @classmethod
+    def empty(cls, tokens: int, topk: int, experts: int, device="cuda") -> "MoePlan":
+        import torch
+        p = cls()
+        p.tokens, p.topk, p.experts = int(tokens), int(topk), int(experts)
+        p.size = moe_plan_rows(tokens, topk, experts)
+        sizes = (p.experts, p.experts + 1, p.size, p.tokens * p.topk, p.size // 64)
+        flat = torch.empty(sum(sizes), dtype=torch.int32, device=device)
+        p.counts, p.offsets, p.rows, p.pos, p.tiles = flat.split(sizes)
+        base, at = flat.data_ptr(), 0
+        ptrs = []
+        for n in sizes:
+            ptrs.append(base + 4 * at)
+            at += n
+        p._struct = SdtMoePlan(p.tokens, p.topk, p.experts, *ptrs)
+        return p
+
+
+def moe_plan(idx, plan: MoePlan, stream=None) -> None:
+    """Fills plan from idx [tokens, topk]: the slots sorted by expert."""
+    if tuple(idx.shape) != (plan.tokens, plan.topk):
+        raise ValueError(f"idx must be ({plan.tokens}, {plan.topk}), got {tuple(idx.shape)}")
+    _check(lib().moe_plan(_ints(idx, "idx"), ctypes.byref(plan._struct), _stream_handle(stream)),
+           "moe_plan")
+
+
+def _moe_gemm_mx4(entry, plan, A, B, C, up, dtype, stream):
+    if A.K != B.K or A.rows != plan.size or tuple(C.shape) != (plan.size, B.rows) or \
+            (up is not None and (up.K, up.rows) != (B.K, B.rows)):
+        raise ValueError(f"shape mismatch plan {plan.size} rows A({A.rows}, {A.K}) "
+                         f"B({B.rows}, {B.K}) C{tuple(C.shape)}")
+    pa, lda, sa = A._one("A")
+    pc, ldc = _rows(C, "C", dtype)
+    b = B._experts(plan.experts, "B")
+    u = None if up is None else ctypes.byref(up._experts(plan.experts, "up"))
+    _check(getattr(lib(), entry)(ctypes.byref(plan._struct), B.rows, B.K, pa, lda, sa,
+                                 ctypes.byref(b), u, pc, ldc, _stream_handle(stream)), entry)
+
+
+def moe_gemm_mx4_f16(plan: MoePlan, A: Mx4, B: Mx4, C, up: Mx4 | None = None, stream=None) -> None:
+    """C[p] = A[p] . B_e^T for the plan's rows, e a row's expert; with `up`,
+    silu(A . B_e^T) * (A . up_e^T)."""
+    import torch
+    _moe_gemm_mx4("moe_gemm_mx4_f16", plan, A, B, C, up, torch.float16, stream)
+
+
+def moe_gemm_mx4_bf16(plan: MoePlan, A: Mx4, B: Mx4, C, up: Mx4 | None = None,
+                      stream=None) -> None:
+    import torch
+    _moe_gemm_mx4("moe_gemm_mx4_bf16", plan, A, B, C, up, torch.bfloat16, stream)
+
+
+def _moe_combine(entry, plan, D, weights, Y, dtype, stream):
+    pd, ldd = _rows(D, "D", dtype)
+    py, ldy = _rows(Y, "Y", dtype)
+    N = D.shape[1]
+    if D.shape[0] != plan.size or tuple(Y.shape) != (plan.tokens, N) or \
+            tuple(weights.shape) != (plan.tokens, plan.topk):
+        raise ValueError(f"shape mismatch plan {plan.size} rows D{tuple(D.shape)} "
+                         f"weights{tuple(weights.shape)} Y{tuple(Y.shape)}")
+    _check(getattr(lib(), entry)(ctypes.byref(plan._struct), N, pd, ldd,
+                                 _floats(weights, "weights"), py, ldy, _stream_handle(stream)), entry)
+
+
+def moe_combine_f16(plan: MoePlan, D, weights, Y, stream=None) -> None:
+    """Y[t] = sum_j weights[t, j] * D[pos(t, j)]."""
+    import torch
+    _moe_combine("moe_combine_f16", plan, D, weights, Y, torch.float16, stream)
+
+
+def moe_combine_bf16(plan: MoePlan, D, weights, Y, stream=None) -> None:
+    import torch
+    _moe_combine("moe_combine_bf16", plan, D, weights, Y, torch.bfloat16, stream)
+
+
+def moe_experts_workspace_size(tokens: int, topk: int, experts: int, N: int, K: int) -> int:
+    """Workspace bytes of moe_experts_mx4."""
+    v = int(lib().sdt_moe_experts_workspace_size(int(tokens), int(topk), int(experts), int(N),
+                                                 int(K)))
+    if v < 0:
+        raise SdtError(SDT_ERR_INVALID_ARG, "sdt_moe_experts_workspace_size")
+    return v
+
+
+def moe_experts_mx4(layer: SdtMoeLayer, X, idx, weights, plan: MoePlan, Y, workspace,
+                    stream=None) -> None:
+    """A layer of gated MX4 experts in one call (moe.Mx4Experts keeps the layer);
+    workspace: a uint8 device tensor of moe_experts_workspace_size bytes."""
+    import torch
+    entry = {torch.float16: "moe_experts_mx4_f16", torch.bfloat16: "moe_experts_mx4_bf16"}.get(X.dtype)
+    if entry is None:
+        raise TypeError(f"X must be float16 or bfloat16, got {X.dtype}")
+    shape = (plan.tokens, layer.K)
+    if tuple(X.shape) != shape or tuple(Y.shape) != shape or \
+            tuple(idx.shape) != (plan.tokens, plan.topk) or tuple(weights.shape) != tuple(idx.shape):
+        raise ValueError(f"shape mismatch X{tuple(X.shape)} Y{tuple(Y.shape)} idx{tuple(idx.shape)} "
+                         f"weights{tuple(weights.shape)}")
+    px, ldx = _rows(X, "X", X.dtype)
+    py, ldy = _rows(Y, "Y", X.dtype)
+    _check(getattr(lib(), entry)(ctypes.byref(layer), _ints(idx, "idx"),
+                                 _floats(weights, "weights"), ctypes.byref(plan._struct), px, ldx,
+                                 py, ldy, workspace.data_ptr(), workspace.numel(),
+                                 _stream_handle(stream)), entry)

@@ -13,6 +13,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,7 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libsdt.so")
 ARCH = "gfx950"
 
-SOURCES = [os.path.join(CSRC, "sdt.hip"), os.path.join(CSRC, "launcher.cpp")]
+SOURCES = [os.path.join(CSRC, "sdt.hip"), os.path.join(CSRC, "mx4.hip"),
+           os.path.join(CSRC, "launcher.cpp")]
 
 # Packed fp32 vector ops are switched off for every device compile.
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
@@ -34,21 +37,29 @@ def hipcc() -> str:
 
 
 def build(resource_usage: bool = False, verbose: bool = False) -> str:
+    """Compile every source (side by side) and link them."""
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
-           "-Wall", "-I", INCLUDE, "-I", CSRC] + DEVICE_FLAGS
+    flags = [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
+             "-Wall", "-I", INCLUDE, "-I", CSRC] + DEVICE_FLAGS
     if resource_usage:
-        cmd += ["-Rpass-analysis=kernel-resource-usage"]
-    cmd += SOURCES + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    noise = "is not a recognized feature for this target"
-    err = "\n".join(l for l in res.stderr.splitlines() if noise not in l)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
-    if (resource_usage or verbose) and err:
-        print(err)
+        flags += ["-Rpass-analysis=kernel-resource-usage"]
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        noise = "is not a recognized feature for this target"
+        err = "\n".join(l for l in res.stderr.splitlines() if noise not in l)
+        if res.returncode != 0:
+            raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
+        if (resource_usage or verbose) and err:
+            print(err)
+
+    with tempfile.TemporaryDirectory() as d:
+        objs = [os.path.join(d, os.path.basename(s) + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(len(SOURCES)) as pool:
+            list(pool.map(lambda so: run(flags + ["-c", so[0], "-o", so[1]]), zip(SOURCES, objs)))
+        run([hipcc(), f"--offload-arch={ARCH}", "-shared"] + objs + ["-o", tmp])
     os.replace(tmp, LIB)
     write_build_info()
     return LIB
@@ -102,15 +113,18 @@ def resource_summary(path: str) -> str:
     write them as a markdown table (one row per kernel instantiation:
     registers, spills, LDS, occupancy) to `path`."""
     import re
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
-           "-I", INCLUDE, "-I", CSRC] + DEVICE_FLAGS + [
-           "-Rpass-analysis=kernel-resource-usage", "--cuda-device-only", "-c",
-           os.path.join(CSRC, "sdt.hip"), "-o", os.devnull]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stderr}")
+    report = ""
+    for source in SOURCES[:2]:
+        cmd = [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+               "-I", INCLUDE, "-I", CSRC] + DEVICE_FLAGS + [
+               "-Rpass-analysis=kernel-resource-usage", "--cuda-device-only", "-c",
+               source, "-o", os.devnull]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stderr}")
+        report += res.stderr
     rows, cur = [], None
-    for line in res.stderr.splitlines():
+    for line in report.splitlines():
         m = re.search(r"remark: Function Name: (\S+)", line)
         if m:
             cur = {"mangled": m.group(1)}
@@ -123,7 +137,7 @@ def resource_summary(path: str) -> str:
                            capture_output=True, text=True).stdout.splitlines()
     out = ["# Kernel resources: every instantiation in libsdt.so (gfx950)", "",
            "The compiler's own report (`-Rpass-analysis=kernel-resource-usage`) for the",
-           "device code of `shape_driven_tile_amd/csrc/sdt.hip`, written by", "",
+           "device code of `shape_driven_tile_amd/csrc/sdt.hip` and `mx4.hip`, written by", "",
            "    python -m shape_driven_tile_amd.build --resource-summary "
            "profiles/kernel_resource_usage.md", "",
            "VGPRs and AGPRs are per lane (the two files are allocated together on",

@@ -1275,15 +1275,4 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(GemmParams p) {
     }
 }
 
-// C = 0 for K == 0 (the empty sum), M x N with stride ldc.
-__global__ void fill_zero_kernel(uint16_t* C, int64_t ldc, int M, int N) {
-    const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int64_t total = (int64_t)M * N;
-    for (int64_t e = idx; e < total; e += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t m = e / N;
-        const int64_t n = e - m * N;
-        C[m * ldc + n] = 0;
-    }
-}
-
 }  // namespace sdt

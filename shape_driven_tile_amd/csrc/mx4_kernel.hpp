@@ -1,0 +1,825 @@
+// MX4 (microscaled 4-bit) kernels for gfx950: quantisation, the values back,
+// and products on the scaled MFMAs.
+//
+// The format (sdt.h): blocks of 32 k share a scale 2^(e - 127); values are
+// e2m1 codes.  v_mfma_scale_f32_16x16x128_f8f6f4 takes, per lane, one operand
+// row's block of 32 codes (16 bytes) and that block's scale byte: lane l holds
+// row l % 16 and the block of quarter l / 16.  It adds over k in a fixed tree
+// whatever block a quarter holds, so a k-tile of 256 (8 blocks, 128 bytes a
+// row) runs as two MFMAs, s = 0 and 1, in which quarter g holds block 2 g + s.
+// A lane's two scale bytes of a row are then neighbours, and with four 16-row
+// parts to a 64-row scale tile its eight bytes are one 8-byte load, picked
+// apart by the instruction's byte selects: no instruction is spent on scales
+// in the loop.  Blocks past K have scale bytes of zero on both sides: their
+// products are below 36 * 2^-254, so the loop needs no partial k-tile: nothing
+// is masked in it.
+#pragma once
+
+#include "gemm_kernel.hpp"
+
+namespace sdt {
+
+typedef int int8v_t __attribute__((ext_vector_type(8)));
+typedef int int2_t __attribute__((ext_vector_type(2)));
+typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
+typedef float floatx2_t __attribute__((ext_vector_type(2)));
+
+constexpr int kMx4Tile = 512;      // bytes of a scale tile: 64 rows x 8 blocks
+
+// The float 2^(e - 127) of a scale byte (255: NaN).
+__device__ __forceinline__ float mx4_scale_value(int e) {
+    const uint32_t bits = e == 0 ? 0x00400000u : e == 255 ? 0x7fc00000u : (uint32_t)e << 23;
+    return __builtin_bit_cast(float, bits);
+}
+
+// Offset in its tile of the scale byte of row r % 64, block b % 8.
+__device__ __forceinline__ int mx4_scale_offset(int r, int b) {
+    return (((b >> 1) & 3) * 16 + (r & 15)) * 8 + ((r >> 4) & 3) * 2 + (b & 1);
+}
+
+// Element types of the conversions.  `quad` is two packed 16-bit elements.
+struct Mx4F16 : F16 {
+    static constexpr uint32_t kInf = 0x7c00;
+    static __device__ __forceinline__ uint32_t to_codes(uint32_t old, uint32_t two, float scale,
+                                                        int sel) {
+        const half2_t v = __builtin_bit_cast(half2_t, two);
+        switch (sel) {   // an immediate of the instruction
+            case 0: return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, v, scale, 0);
+            case 1: return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, v, scale, 1);
+            case 2: return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, v, scale, 2);
+            default: return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, v, scale, 3);
+        }
+    }
+    // The codes of byte `sel` as two packed elements, unscaled (exact).
+    static __device__ __forceinline__ vec2 codes(uint32_t w, int sel) {
+        switch (sel) {
+            case 0: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
+            case 1: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
+            case 2: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2);
+            default: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
+        }
+    }
+    static __device__ __forceinline__ float widen(uint32_t bits16) {
+        return (float)__builtin_bit_cast(_Float16, (uint16_t)bits16);
+    }
+};
+struct Mx4BF16 : BF16 {
+    static constexpr uint32_t kInf = 0x7f80;
+    static __device__ __forceinline__ uint32_t to_codes(uint32_t old, uint32_t two, float scale,
+                                                        int sel) {
+        const bf16x2_t v = __builtin_bit_cast(bf16x2_t, two);
+        switch (sel) {
+            case 0: return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, v, scale, 0);
+            case 1: return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, v, scale, 1);
+            case 2: return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, v, scale, 2);
+            default: return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, v, scale, 3);
+        }
+    }
+    static __device__ __forceinline__ vec2 codes(uint32_t w, int sel) {
+        switch (sel) {
+            case 0: return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0);
+            case 1: return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1);
+            case 2: return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2);
+            default: return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3);
+        }
+    }
+    static __device__ __forceinline__ float widen(uint32_t bits16) {
+        return __builtin_bit_cast(float, bits16 << 16);
+    }
+};
+
+// ---- quantisation ---------------------------------------------------------------
+
+struct Mx4Quant {
+    const uint16_t* X;
+    int64_t ldx;           // elements
+    const int32_t* index;  // rows named by a list (nullptr: row p itself)
+    int divisor;           // with a list: source row index[p] / divisor (0: p)
+    int64_t xrows;
+    uint8_t* Q;
+    int64_t ldq;           // bytes
+    uint8_t* S;
+    int64_t rows;
+    int K, nkt;
+};
+
+// One workgroup per 64 x 256 tile (one scale tile).  32 lanes take a row's 256
+// elements, 8 each (16 bytes); 4 lanes share a block and agree on its maximum
+// by two lane exchanges.  The maximum is taken on the 16-bit patterns without
+// their sign, whose order is that of the magnitudes (an infinity or a NaN lies
+// at or above the infinity's pattern).  All eight rows of a lane are loaded
+// before the first is used.
+template <typename Elt, bool VEC>
+__global__ __launch_bounds__(256) void mx4_quantize_kernel(Mx4Quant p) {
+    __shared__ uint8_t sm[kMx4Tile];
+    const int t = threadIdx.x;
+    const int64_t rt = blockIdx.x / p.nkt;
+    const int kt = blockIdx.x - (int)(rt * p.nkt);
+    const int l32 = t & 31;
+    const int k = kt * 256 + l32 * 8;
+    const int nb = (p.K + 31) / 32;
+    const int valid = p.K - k;             // elements of this lane's eight below K
+
+    uint4_t v[8];
+    bool have[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t row = rt * 64 + (t >> 5) + 8 * i;
+        int64_t src = row;
+        bool ok = row < p.rows;
+        if (p.index != nullptr && ok) {
+            const int idx = p.index[row];
+            ok = idx >= 0;
+            if (p.divisor > 0) src = idx / p.divisor;
+            ok = ok && src < p.xrows;
+        }
+        have[i] = ok;
+        v[i] = uint4_t{0, 0, 0, 0};
+        if (ok) {
+            const uint16_t* x = p.X + src * p.ldx + k;
+            if (VEC && valid >= 8) {
+                v[i] = *reinterpret_cast<const uint4_t*>(x);
+            } else {
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const uint32_t lo = 2 * d < valid ? x[2 * d] : 0u;
+                    const uint32_t hi = 2 * d + 1 < valid ? x[2 * d + 1] : 0u;
+                    v[i][d] = lo | (hi << 16);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = (t >> 5) + 8 * i;
+        ushort2_t m = {0, 0};
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const uint32_t w = v[i][d] & 0x7fff7fffu;
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(ushort2_t, w));
+        }
+        uint32_t top = m[0] > m[1] ? m[0] : m[1];
+        top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+        const bool special = top >= Elt::kInf;
+        const uint32_t bits = __builtin_bit_cast(uint32_t, Elt::widen(top));
+        const int e = special ? 255 : max((int)(bits >> 23) - 2, 0);
+        uint32_t q = 0;
+        if (!special) {
+            const float scale = mx4_scale_value(e);
+            q = Elt::to_codes(q, v[i][0], scale, 0);
+            q = Elt::to_codes(q, v[i][1], scale, 1);
+            q = Elt::to_codes(q, v[i][2], scale, 2);
+            q = Elt::to_codes(q, v[i][3], scale, 3);
+        }
+        const int b = l32 >> 2;
+        const int64_t row = rt * 64 + r;
+        const bool in = kt * 8 + b < nb;
+        if (in && have[i])
+            *reinterpret_cast<uint32_t*>(p.Q + row * p.ldq + kt * 128 + l32 * 4) = q;
+        if ((l32 & 3) == 0) sm[mx4_scale_offset(r, b)] = in && have[i] ? (uint8_t)e : 0;
+    }
+    __syncthreads();
+    if (t < kMx4Tile / 4)
+        reinterpret_cast<uint32_t*>(p.S + (int64_t)blockIdx.x * kMx4Tile)[t] =
+            reinterpret_cast<const uint32_t*>(sm)[t];
+}
+
+struct Mx4Dequant {
+    const uint8_t* Q;
+    int64_t ldq;
+    const uint8_t* S;
+    void* Y;
+    int64_t ldy;     // elements
+    int64_t rows;
+    int K, nkt;
+};
+
+// The values back: the tile split of the quantiser, eight values a lane.
+// OUT: 0 fp16, 1 bf16, 2 fp32.  A code's value and its scale are exact in
+// fp32; 16-bit outputs are rounded from there.
+template <int OUT, bool VEC>
+__global__ __launch_bounds__(256) void mx4_dequantize_kernel(Mx4Dequant p) {
+    __shared__ uint32_t sm[kMx4Tile / 4];
+    const int t = threadIdx.x;
+    const int64_t rt = blockIdx.x / p.nkt;
+    const int kt = blockIdx.x - (int)(rt * p.nkt);
+    if (t < kMx4Tile / 4)
+        sm[t] = reinterpret_cast<const uint32_t*>(p.S + (int64_t)blockIdx.x * kMx4Tile)[t];
+    const int l32 = t & 31;
+    const int k = kt * 256 + l32 * 8;
+    const int valid = p.K - k;
+    uint32_t q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t row = rt * 64 + (t >> 5) + 8 * i;
+        q[i] = row < p.rows && valid > 0
+                   ? *reinterpret_cast<const uint32_t*>(p.Q + row * p.ldq + kt * 128 + l32 * 4)
+                   : 0u;
+    }
+    __syncthreads();
+    const uint8_t* sc = reinterpret_cast<const uint8_t*>(sm);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = (t >> 5) + 8 * i;
+        const int64_t row = rt * 64 + r;
+        if (row >= p.rows || valid <= 0) continue;
+        const float scale = mx4_scale_value(sc[mx4_scale_offset(r, l32 >> 2)]);
+        float f[8];
+        {
+            const floatx2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 0);
+            const floatx2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 1);
+            const floatx2_t c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 2);
+            const floatx2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 3);
+            f[0] = a[0] * scale; f[1] = a[1] * scale;
+            f[2] = b[0] * scale; f[3] = b[1] * scale;
+            f[4] = c[0] * scale; f[5] = c[1] * scale;
+            f[6] = d[0] * scale; f[7] = d[1] * scale;
+        }
+        if constexpr (OUT == 2) {
+            float* y = static_cast<float*>(p.Y) + row * p.ldy + k;
+            if (VEC && valid >= 8) {
+                *reinterpret_cast<floatx4_t*>(y) = floatx4_t{f[0], f[1], f[2], f[3]};
+                *reinterpret_cast<floatx4_t*>(y + 4) = floatx4_t{f[4], f[5], f[6], f[7]};
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < valid) y[j] = f[j];
+            }
+        } else {
+            typedef std::conditional_t<OUT == 0, _Float16, __bf16> scalar;
+            uint16_t h[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const scalar s = (scalar)f[j];
+                h[j] = __builtin_bit_cast(uint16_t, s);
+            }
+            uint16_t* y = static_cast<uint16_t*>(p.Y) + row * p.ldy + k;
+            if (VEC && valid >= 8) {
+                *reinterpret_cast<uint4_t*>(y) = __builtin_bit_cast(uint4_t, h);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < valid) y[j] = h[j];
+            }
+        }
+    }
+}
+
+// Row-major scale bytes into tiles: one workgroup of 256 per 64 x 8 tile.
+__global__ __launch_bounds__(256) void mx4_pack_scales_kernel(const uint8_t* R, int64_t ldr,
+                                                                     int64_t rows, int nb, int nkt,
+                                                                     uint8_t* S) {
+    const int64_t rt = blockIdx.x / nkt;
+    const int kt = blockIdx.x - (int)(rt * nkt);
+    for (int i = threadIdx.x; i < kMx4Tile; i += 256) {
+        const int r = i >> 3, b = i & 7;
+        const int64_t row = rt * 64 + r;
+        const int blk = kt * 8 + b;
+        const uint8_t v = row < rows && blk < nb ? R[row * ldr + blk] : 0;
+        S[(int64_t)blockIdx.x * kMx4Tile + mx4_scale_offset(r, b)] = v;
+    }
+}
+
+// ---- products ----------------------------------------------------------------------
+
+struct Mx4Gemm {
+    const uint8_t *A, *B, *B2;     // codes (B2: the gated product's second matrix)
+    const uint8_t *SA, *SB, *SB2;  // tiled scales
+    uint16_t* C;
+    int64_t lda, ldb, ldb2, ldc;   // bytes; ldc elements
+    int M, N;
+    int rowbytes, nkt;             // codes of one row; k-tiles
+    int gm, gn, nxcd;              // output tiles (grouped: gm 64-row tiles of the plan)
+    // grouped products: the plan, and the experts' strides in bytes
+    const int32_t *tiles, *offsets, *counts;
+    int64_t eqb, esb, eqb2, esb2;
+};
+
+// acc += B_frag . A_frag^T over one 128-deep half; BYTE_A, BYTE_B pick the
+// lane's scale bytes.
+template <int BYTE_B, int BYTE_A>
+__device__ __forceinline__ floatx4_t mx4_mfma(int4_t b, int4_t a, floatx4_t c, int sb, int sa) {
+    const int8v_t b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+    const int8v_t a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b8, a8, c, 4, 4, BYTE_B, sb, BYTE_A, sa);
+}
+
+// One 16-row part of a 64-row scale tile: byte 2 (part % 2) + s of dword
+// part / 2 of the lane's eight.
+template <int S, int PB, int PA>
+__device__ __forceinline__ floatx4_t mx4_mfma_part(int4_t b, int4_t a, floatx4_t c, int sb, int sa) {
+    return mx4_mfma<2 * (PB & 1) + S, 2 * (PA & 1) + S>(b, a, c, sb, sa);
+}
+
+// silu(g) * u of the gated product, in fp32.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    const float s = g / (1.0f + expf(-g));
+    return s * u;
+}
+
+// Rows and expert of 64-row tile `g` of a plan for tiles of BM rows: false
+// where a tile of BM rows does not start there.
+__device__ __forceinline__ bool mx4_group(const Mx4Gemm& p, int g, int bm64, int& e, int64_t& m0,
+                                          int& rows) {
+    e = __builtin_amdgcn_readfirstlane(p.tiles[g]);
+    if (e < 0) return false;
+    const int first = p.offsets[e];
+    if (((g - first / 64) % bm64) != 0) return false;
+    m0 = (int64_t)g * 64;
+    rows = __builtin_amdgcn_readfirstlane(first + p.counts[e] - g * 64);
+    return rows > 0;
+}
+
+// The few-row product: 16 columns of C per workgroup, whose NW waves split the
+// k-tiles (w, w + NW, ...) and read B straight from memory, each code once;
+// up to 64 rows of A (four 16-row parts, skipped where there are no rows).
+// The waves' partial sums are added in wave order through LDS.  Bound by the
+// stream of B: 16 loads of 1 KB are in flight per wave pair, and the many small
+// workgroups keep every CU loading.
+template <typename Elt, bool GROUPED, bool GATED, int NW>
+__global__ __launch_bounds__(NW * 64) void mx4_skinny_kernel(Mx4Gemm p) {
+    typedef typename Elt::scalar scalar;
+    constexpr int U = 2;                     // k-tiles loaded together
+    __shared__ floatx4_t red[(GATED ? 2 : 1) * NW * 4 * 64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l = xcd_remap(blockIdx.x, gridDim.x, p.nxcd);
+    const int g = l / p.gn, nt = l - g * p.gn;
+    int e = 0, rows;
+    int64_t m0;
+    if constexpr (GROUPED) {
+        if (!mx4_group(p, g, 1, e, m0, rows)) return;
+        rows = min(rows, 64);
+    } else {
+        m0 = (int64_t)g * 64;
+        rows = (int)min((int64_t)64, p.M - m0);
+    }
+    const int nmb = (rows + 15) >> 4;
+    const int n0 = nt * 16;
+    const int fr = lane & 15, fq = lane >> 4;
+
+    const int rows_b = min(16, p.N - n0);
+    const uint32_t sbytes_b = (uint32_t)p.nkt * kMx4Tile;
+    const __amdgpu_buffer_rsrc_t ra =
+        make_rsrc(p.A + m0 * p.lda, (uint32_t)((rows - 1) * p.lda + p.rowbytes));
+    const __amdgpu_buffer_rsrc_t rsa = make_rsrc(p.SA + (m0 / 64) * sbytes_b, sbytes_b);
+    const __amdgpu_buffer_rsrc_t rb =
+        make_rsrc(p.B + e * p.eqb + (int64_t)n0 * p.ldb, (uint32_t)((rows_b - 1) * p.ldb + p.rowbytes));
+    const __amdgpu_buffer_rsrc_t rsb =
+        make_rsrc(p.SB + e * p.esb + (int64_t)(n0 / 64) * sbytes_b, sbytes_b);
+    const __amdgpu_buffer_rsrc_t rb2 = make_rsrc(
+        GATED ? p.B2 + e * p.eqb2 + (int64_t)n0 * p.ldb2 : p.B,
+        GATED ? (uint32_t)((rows_b - 1) * p.ldb2 + p.rowbytes) : 0u);
+    const __amdgpu_buffer_rsrc_t rsb2 = make_rsrc(
+        GATED ? p.SB2 + e * p.esb2 + (int64_t)(n0 / 64) * sbytes_b : p.SB, GATED ? sbytes_b : 0u);
+
+    const uint32_t voff_a = (uint32_t)(fr * p.lda) + fq * 32;
+    const uint32_t voff_b = (uint32_t)(fr * p.ldb) + fq * 32;
+    const uint32_t voff_b2 = GATED ? (uint32_t)(fr * p.ldb2) + fq * 32 : 0u;
+    const uint32_t voff_sb = lane * 8 + ((n0 >> 4) & 3) * 2;
+
+    floatx4_t acc[4], acc2[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        acc[j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+        acc2[j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    // The k offset goes into the lane offset, which the descriptor's range check
+    // covers: the last row's bytes past its blocks are not read.
+    auto load16 = [](__amdgpu_buffer_rsrc_t r, uint32_t off) {
+        return __builtin_bit_cast(int4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+    };
+    for (int kt0 = wave; kt0 < p.nkt; kt0 += NW * U) {
+        int4_t fb[U][2], fb2[U][2], fa[U][2];
+        int sb[U], sb2[U];
+        int2_t sa[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kt = kt0 + u * NW;
+            // past the last k-tile: an offset past every descriptor, read as zero
+            const bool in = kt < p.nkt;
+            const uint32_t so = in ? (uint32_t)kt * 128 : 0x40000000u;
+            const uint32_t ss = in ? (uint32_t)kt * kMx4Tile : 0x40000000u;
+            fb[u][0] = load16(rb, voff_b + so);
+            fb[u][1] = load16(rb, voff_b + 16 + so);
+            sb[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsb, voff_sb + ss, 0, 0);
+            if constexpr (GATED) {
+                fb2[u][0] = load16(rb2, voff_b2 + so);
+                fb2[u][1] = load16(rb2, voff_b2 + 16 + so);
+                sb2[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsb2, voff_sb + ss, 0, 0);
+            }
+            fa[u][0] = load16(ra, voff_a + so);
+            fa[u][1] = load16(ra, voff_a + 16 + so);
+            sa[u] = __builtin_bit_cast(
+                int2_t, __builtin_amdgcn_raw_buffer_load_b64(rsa, lane * 8 + ss, 0, 0));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kt = kt0 + u * NW;
+            const uint32_t so = kt < p.nkt ? (uint32_t)kt * 128 : 0x40000000u;
+            acc[0] = mx4_mfma<0, 0>(fb[u][0], fa[u][0], acc[0], sb[u], sa[u][0]);
+            acc[0] = mx4_mfma<1, 1>(fb[u][1], fa[u][1], acc[0], sb[u], sa[u][0]);
+            if constexpr (GATED) {
+                acc2[0] = mx4_mfma<0, 0>(fb2[u][0], fa[u][0], acc2[0], sb2[u], sa[u][0]);
+                acc2[0] = mx4_mfma<1, 1>(fb2[u][1], fa[u][1], acc2[0], sb2[u], sa[u][0]);
+            }
+#pragma unroll
+            for (int j = 1; j < 4; ++j) {
+                if (j < nmb) {
+                    const uint32_t va = voff_a + (uint32_t)(j * 16 * p.lda) + so;
+                    const int4_t a0 = load16(ra, va), a1 = load16(ra, va + 16);
+                    const int s = sa[u][j >> 1];
+                    if (j & 1) {
+                        acc[j] = mx4_mfma<0, 2>(fb[u][0], a0, acc[j], sb[u], s);
+                        acc[j] = mx4_mfma<1, 3>(fb[u][1], a1, acc[j], sb[u], s);
+                        if constexpr (GATED) {
+                            acc2[j] = mx4_mfma<0, 2>(fb2[u][0], a0, acc2[j], sb2[u], s);
+                            acc2[j] = mx4_mfma<1, 3>(fb2[u][1], a1, acc2[j], sb2[u], s);
+                        }
+                    } else {
+                        acc[j] = mx4_mfma<0, 0>(fb[u][0], a0, acc[j], sb[u], s);
+                        acc[j] = mx4_mfma<1, 1>(fb[u][1], a1, acc[j], sb[u], s);
+                        if constexpr (GATED) {
+                            acc2[j] = mx4_mfma<0, 0>(fb2[u][0], a0, acc2[j], sb2[u], s);
+                            acc2[j] = mx4_mfma<1, 1>(fb2[u][1], a1, acc2[j], sb2[u], s);
+                        }
+                    }
+                }
+            }
+        }
+    }
+    // Part j of every wave to LDS, then wave j adds part j in wave order.
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j < nmb) {
+            red[(wave * 4 + j) * 64 + lane] = acc[j];
+            if constexpr (GATED) red[((NW + wave) * 4 + j) * 64 + lane] = acc2[j];
+        }
+    }
+    __syncthreads();
+    for (int j = wave; j < nmb; j += NW) {
+        floatx4_t s = red[j * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) s += red[(w * 4 + j) * 64 + lane];
+        if constexpr (GATED) {
+            floatx4_t s2 = red[(NW * 4 + j) * 64 + lane];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) s2 += red[((NW + w) * 4 + j) * 64 + lane];
+#pragma unroll
+            for (int d = 0; d < 4; ++d) s[d] = silu_mul(s[d], s2[d]);
+        }
+        // lane l: row l % 16 of the part, columns 4 (l / 16) .. + 3
+        const int m = j * 16 + fr;
+        if (m >= rows) continue;
+        const int n = n0 + fq * 4;
+        uint16_t h[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const scalar v = (scalar)s[d];
+            h[d] = __builtin_bit_cast(uint16_t, v);
+        }
+        uint16_t* c = p.C + (m0 + m) * p.ldc + n;
+        if (n + 3 < p.N) {
+            *reinterpret_cast<uint2_t*>(c) = __builtin_bit_cast(uint2_t, h);
+        } else {
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                if (n + d < p.N) c[d] = h[d];
+        }
+    }
+}
+
+// The tiled product: BM x BN outputs per workgroup, WM x WN compute waves of
+// 16x16x128 MFMAs and as many loader waves, which issue every global -> LDS
+// load (the layout of gemm_kernel's HELP form: NS stages, one barrier per
+// k-tile).  A stage holds the codes of BM + BN rows x 128 bytes and their
+// scale tiles.  16-byte chunk 2 g + s of row r (block 2 g + s of the k-tile) is
+// kept at position (4 s + g) ^ swz_pp(r), so a fragment read of half s has the
+// conflict-free pattern of the 16-bit kernels.  GATED: the B rows of a wave are
+// 32 of the first matrix and the same 32 of the second, so a lane holds both
+// factors of its outputs; BN / 2 columns per workgroup.  GROUPED: rows are a
+// plan's, the expert's matrices are found from the row tile.
+template <typename Elt, int BM, int BN, int WM, int WN, int NS, bool GROUPED, bool GATED>
+__global__ __launch_bounds__(WM * WN * 128) void mx4_gemm_kernel(Mx4Gemm p) {
+    constexpr int NW = WM * WN;
+    constexpr int WTM = BM / WM, WTN = BN / WN;
+    constexpr int FM = WTM / 16, FN = WTN / 16;
+    constexpr int A_UNITS = BM * 8, B_UNITS = BN * 8;
+    constexpr int SA_UNITS = BM / 64 * 32, SB_UNITS = BN / 64 * 32;
+    constexpr int S_BASE = A_UNITS + B_UNITS;
+    constexpr int STAGE = S_BASE + SA_UNITS + SB_UNITS;
+    constexpr int A_DMA = A_UNITS / (64 * NW), B_DMA = B_UNITS / (64 * NW);
+    constexpr int ST = (BM + BN) / 64;            // scale tiles of a stage
+    constexpr int S_DMA = (ST + NW - 1) / NW;     // per loader wave (spare waves repeat a tile)
+    constexpr int L = A_DMA + B_DMA + S_DMA;
+    static_assert(A_UNITS % (64 * NW) == 0 && B_UNITS % (64 * NW) == 0, "whole 8-row slabs");
+    static_assert(BM % 64 == 0 && BN % 64 == 0, "whole scale tiles");
+    static_assert(!GATED || (WTN == 64 && BN == 128), "gated: 32 + 32 columns per wave");
+    static_assert(WTM == 32 || WTM % 64 == 0, "a wave's rows: halves of or whole scale tiles");
+    static_assert(WTN == 32 || WTN == 64, "a wave's columns: half of or a whole scale tile");
+    static_assert(NS * STAGE * 16 <= 160 * 1024, "stages fit the LDS");
+    static_assert(NW * 256 <= NS * STAGE, "epilogue stage");
+    __shared__ int4_t smem[NS * STAGE];
+
+    const int t = threadIdx.x;
+    const int lane = t & 63;
+    const int wave_id = __builtin_amdgcn_readfirstlane(t >> 6);
+    const bool loader = wave_id >= NW;
+    const int wave = wave_id % NW;
+    const int wave_m = wave % WM, wave_n = wave / WM;
+
+    const int BNO = GATED ? BN / 2 : BN;          // output columns
+    const int logical = xcd_remap(blockIdx.x, p.gm * p.gn, p.nxcd);
+    int64_t m0, n0;
+    int e = 0, limit;                             // limit: rows of C past m0 that exist
+    if constexpr (GROUPED) {
+        const int g = logical / p.gn;
+        if (!mx4_group(p, g, BM / 64, e, m0, limit)) return;
+        n0 = (int64_t)(logical - g * p.gn) * BNO;
+    } else {
+        GemmParams gp;
+        gp.gm = p.gm;
+        gp.gn = p.gn;
+        grouped_origin(gp, logical, BM, BNO, m0, n0);
+        limit = (int)min((int64_t)p.M - m0, (int64_t)BM);
+    }
+    const int rows_a = min(limit, BM);
+    const int rows_b = (int)min((int64_t)BNO, (int64_t)p.N - n0);
+    const uint32_t srow = (uint32_t)p.nkt * kMx4Tile;   // scale bytes of 64 rows
+
+    if (loader) {
+        const __amdgpu_buffer_rsrc_t ra =
+            make_rsrc(p.A + m0 * p.lda, (uint32_t)((rows_a - 1) * p.lda + p.rowbytes));
+        const __amdgpu_buffer_rsrc_t rb =
+            make_rsrc(p.B + e * p.eqb + n0 * p.ldb, (uint32_t)((rows_b - 1) * p.ldb + p.rowbytes));
+        const __amdgpu_buffer_rsrc_t rb2 =
+            make_rsrc(GATED ? p.B2 + e * p.eqb2 + n0 * p.ldb2 : p.B,
+                      GATED ? (uint32_t)((rows_b - 1) * p.ldb2 + p.rowbytes) : 0u);
+        const __amdgpu_buffer_rsrc_t rsa =
+            make_rsrc(p.SA + (m0 / 64) * srow, (uint32_t)((rows_a + 63) / 64) * srow);
+        const __amdgpu_buffer_rsrc_t rsb = make_rsrc(p.SB + e * p.esb + (n0 / 64) * srow,
+                                                     (uint32_t)((rows_b + 63) / 64) * srow);
+        const __amdgpu_buffer_rsrc_t rsb2 =
+            make_rsrc(GATED ? p.SB2 + e * p.esb2 + (n0 / 64) * srow : p.SB,
+                      GATED ? (uint32_t)((rows_b + 63) / 64) * srow : 0u);
+        uint32_t voff_a[A_DMA], voff_b[B_DMA];
+#pragma unroll
+        for (int j = 0; j < A_DMA; ++j) {
+            const int row = (wave * A_DMA + j) * 8 + (lane >> 3);
+            const int pos = (lane & 7) ^ swz_pp(row);
+            voff_a[j] = (uint32_t)(row * p.lda) + ((pos & 3) * 2 + (pos >> 2)) * 16;
+        }
+#pragma unroll
+        for (int j = 0; j < B_DMA; ++j) {
+            const int row = (wave * B_DMA + j) * 8 + (lane >> 3);
+            const int pos = (lane & 7) ^ swz_pp(row);
+            // gated: LDS rows 64 w + 32 h + i are row 32 w + i of matrix h
+            const int src = GATED ? (row >> 6) * 32 + (row & 31) : row;
+            voff_b[j] = (uint32_t)(src * (GATED && (row & 32) ? p.ldb2 : p.ldb)) +
+                        ((pos & 3) * 2 + (pos >> 2)) * 16;
+        }
+        auto load_tile = [&](int kt, int stage) {
+            int4_t* base = smem + stage * STAGE;
+            // in the lane offset, which the descriptor's range check covers: the
+            // last row's bytes past its blocks are not read
+            const uint32_t koff = (uint32_t)kt * 128;
+#pragma unroll
+            for (int j = 0; j < A_DMA; ++j)
+                dma16(ra, base + (wave * A_DMA + j) * 64, voff_a[j] + koff, 0);
+#pragma unroll
+            for (int j = 0; j < B_DMA; ++j) {
+                const bool second = GATED && (((wave * B_DMA + j) * 8) & 32) != 0;
+                dma16(second ? rb2 : rb, base + A_UNITS + (wave * B_DMA + j) * 64, voff_b[j] + koff, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < S_DMA; ++j) {
+                const int st = (wave * S_DMA + j) % ST;
+                int4_t* dst = base + S_BASE + st * 32;
+                if (lane < 32) {
+                    if (st < BM / 64)
+                        dma16(rsa, dst, st * srow + lane * 16, kt * kMx4Tile);
+                    else if (GATED && st > BM / 64)
+                        dma16(rsb2, dst, lane * 16, kt * kMx4Tile);
+                    else
+                        dma16(rsb, dst, (st - BM / 64) * srow + lane * 16, kt * kMx4Tile);
+                }
+            }
+        };
+        const int npro = min(p.nkt, NS);
+        for (int j = 0; j < npro; ++j) load_tile(j, j);
+        if (p.nkt > NS)
+            wait_global_loads<(NS - 1) * L>();
+        else
+            wait_global_loads<0>();
+        __syncthreads();
+        int s = 0, i = 0;
+        for (; i + NS < p.nkt; ++i) {
+            wait_global_loads<(NS - 2) * L>();
+            __syncthreads();
+            load_tile(i + NS, s);
+            s = (s + 1 == NS) ? 0 : s + 1;
+        }
+        for (; i < p.nkt; ++i) {
+            wait_global_loads<0>();
+            __syncthreads();
+        }
+        return;
+    }
+
+    floatx4_t acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+
+    const int frow = lane & 15, fq = lane >> 4;
+    const int fsw = swz_pp(frow);
+    const int a_row0 = wave_m * WTM + frow;
+    const int b_row0 = A_UNITS / 8 + wave_n * WTN + frow;
+    constexpr int SAW = FM / 2, SBW = FN / 2;     // scale dwords per lane (two parts each)
+    int4_t fa[2][FM], fb[2][FN];
+    auto read_half = [&](int stage, int s) {
+        const int4_t* base = smem + stage * STAGE;
+        const int chunk = (4 * s + fq) ^ fsw;
+#pragma unroll
+        for (int j = 0; j < FM; ++j) fa[s][j] = base[(a_row0 + j * 16) * 8 + chunk];
+#pragma unroll
+        for (int i = 0; i < FN; ++i) fb[s][i] = base[(b_row0 + i * 16) * 8 + chunk];
+    };
+    auto read_scales = [&](int stage, int (&sa)[SAW], int (&sb)[SBW]) {
+        const int* sbase = reinterpret_cast<const int*>(smem + stage * STAGE + S_BASE);
+#pragma unroll
+        for (int d = 0; d < SAW; ++d) {
+            const int part = wave_m * FM + 2 * d;      // 16-row part of the tile's BM rows
+            sa[d] = sbase[(part >> 2) * 128 + lane * 2 + ((part >> 1) & 1)];
+        }
+#pragma unroll
+        for (int d = 0; d < SBW; ++d) {
+            if constexpr (GATED) {
+                // dword d: matrix d's columns 32 wave_n .. + 31 of its one tile
+                sb[d] = sbase[(BM / 64 + d) * 128 + lane * 2 + (wave_n & 1)];
+            } else {
+                const int part = wave_n * FN + 2 * d;
+                sb[d] = sbase[(BM / 64 + (part >> 2)) * 128 + lane * 2 + ((part >> 1) & 1)];
+            }
+        }
+    };
+    auto mfma_half = [&](auto half, const int (&sa)[SAW], const int (&sb)[SBW]) {
+        constexpr int S = decltype(half)::value;
+#pragma unroll
+        for (int i = 0; i < FN; i += 2)
+#pragma unroll
+            for (int j = 0; j < FM; j += 2) {
+                acc[i][j] = mx4_mfma_part<S, 0, 0>(fb[S][i], fa[S][j], acc[i][j], sb[i / 2], sa[j / 2]);
+                acc[i][j + 1] =
+                    mx4_mfma_part<S, 0, 1>(fb[S][i], fa[S][j + 1], acc[i][j + 1], sb[i / 2], sa[j / 2]);
+                acc[i + 1][j] =
+                    mx4_mfma_part<S, 1, 0>(fb[S][i + 1], fa[S][j], acc[i + 1][j], sb[i / 2], sa[j / 2]);
+                acc[i + 1][j + 1] = mx4_mfma_part<S, 1, 1>(fb[S][i + 1], fa[S][j + 1], acc[i + 1][j + 1],
+                                                           sb[i / 2], sa[j / 2]);
+            }
+    };
+    using Half0 = std::integral_constant<int, 0>;
+    using Half1 = std::integral_constant<int, 1>;
+
+    __syncthreads();
+    int sa[SAW], sb[SBW];
+    int s = 0;
+    if (p.nkt > 0) {
+        read_half(0, 0);
+        read_scales(0, sa, sb);
+    }
+    for (int i = 0; i < p.nkt; ++i) {
+        const int sn = (s + 1 == NS) ? 0 : s + 1;
+        read_half(s, 1);
+        mfma_half(Half0{}, sa, sb);
+        // the rest of tile i is in registers: its stage may be refilled
+        __syncthreads();
+        int na[SAW], nb[SBW];
+        if (i + 1 < p.nkt) {
+            read_half(sn, 0);
+            read_scales(sn, na, nb);
+        }
+        mfma_half(Half1{}, sa, sb);
+#pragma unroll
+        for (int d = 0; d < SAW; ++d) sa[d] = na[d];
+#pragma unroll
+        for (int d = 0; d < SBW; ++d) sb[d] = nb[d];
+        s = sn;
+    }
+
+    // The stages are not read any more after the last k-tile's barrier (with no
+    // k-tile nothing was): 4 KB of them per wave stage its output.
+    GemmParams gp;
+    gp.C = p.C;
+    gp.ldc = p.ldc;
+    gp.M = (int)(m0 + rows_a);
+    gp.N = p.N;
+    int4_t* stage = smem + wave * 256;
+    const int64_t mb = m0 + wave_m * WTM;
+    if constexpr (GATED) {
+        floatx4_t out[FN / 2][FM];
+#pragma unroll
+        for (int i = 0; i < FN / 2; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    out[i][j][d] = silu_mul(acc[i][j][d], acc[i + FN / 2][j][d]);
+        gemm_epilogue<Elt, 16>(gp, out, mb, n0 + wave_n * (WTN / 2), lane, stage);
+    } else {
+        gemm_epilogue<Elt, 16>(gp, acc, mb, n0 + wave_n * WTN, lane, stage);
+    }
+}
+
+// ---- 16-bit activations, MX4 weights, one token -------------------------------------
+
+struct Mx4Gemv {
+    const uint16_t* x;
+    const uint8_t* B;
+    int64_t ldb;
+    const uint8_t* SB;
+    uint16_t* y;
+    int N, K, rowbytes, nkt;
+};
+
+// y of 16 rows of B per workgroup, whose NW waves split the k-tiles.  Lane l
+// takes row l % 16, blocks 2 (l / 16) and + 1 of a k-tile: 32 bytes of codes,
+// converted two at a time to the activations' type (exact) and multiplied by
+// pairs into an fp32 sum per block, which the block's scale then multiplies
+// once.  The four quarters' sums are added by lane exchanges, the waves' in
+// wave order through LDS.
+template <typename Elt, int NW>
+__global__ __launch_bounds__(NW * 64) void mx4_gemv_kernel(Mx4Gemv p) {
+    typedef typename Elt::scalar scalar;
+    typedef typename Elt::vec2 vec2;
+    __shared__ float red[NW * 16];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = blockIdx.x * 16;
+    const int fr = lane & 15, fq = lane >> 4;
+    const int rows_b = min(16, p.N - n0);
+    const uint32_t srow = (uint32_t)p.nkt * kMx4Tile;
+    const __amdgpu_buffer_rsrc_t rb =
+        make_rsrc(p.B + (int64_t)n0 * p.ldb, (uint32_t)((rows_b - 1) * p.ldb + p.rowbytes));
+    const __amdgpu_buffer_rsrc_t rsb = make_rsrc(p.SB + (int64_t)(n0 / 64) * srow, srow);
+    const uint32_t voff_b = (uint32_t)(fr * p.ldb) + fq * 32;
+    const uint32_t voff_s = lane * 8 + ((n0 >> 4) & 3) * 2;
+    const bool aligned = (reinterpret_cast<uintptr_t>(p.x) & 15) == 0;
+    float sum = 0.0f;
+    for (int kt = wave; kt < p.nkt; kt += NW) {
+        int4_t w[2];
+        w[0] = __builtin_bit_cast(int4_t,
+                                  __builtin_amdgcn_raw_buffer_load_b128(rb, voff_b + kt * 128, 0, 0));
+        w[1] = __builtin_bit_cast(
+            int4_t, __builtin_amdgcn_raw_buffer_load_b128(rb, voff_b + 16 + kt * 128, 0, 0));
+        const int sc =
+            (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsb, voff_s, kt * kMx4Tile, 0);
+        const int k0 = kt * 256 + fq * 64;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int kb = k0 + s * 32;
+            const int valid = p.K - kb;
+            if (valid <= 0) continue;
+            uint4_t xv[4];
+            if (aligned && valid >= 32) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    xv[c] = *reinterpret_cast<const uint4_t*>(p.x + kb + 8 * c);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        const int k = 8 * c + 2 * d;
+                        const uint32_t lo = k < valid ? p.x[kb + k] : 0u;
+                        const uint32_t hi = k + 1 < valid ? p.x[kb + k + 1] : 0u;
+                        xv[c][d] = lo | (hi << 16);
+                    }
+            }
+            float part = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const uint32_t xw = xv[c][d];
+                    part = Elt::dot2(Elt::codes((uint32_t)w[s][c], d), __builtin_bit_cast(vec2, xw), part);
+                }
+            sum += part * mx4_scale_value((sc >> (8 * s)) & 255);
+        }
+    }
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    if (lane < 16) red[wave * 16 + lane] = sum;
+    __syncthreads();
+    if (threadIdx.x < rows_b) {
+        float s = red[threadIdx.x];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) s += red[w * 16 + threadIdx.x];
+        const scalar v = (scalar)s;
+        p.y[n0 + threadIdx.x] = __builtin_bit_cast(uint16_t, v);
+    }
+}
+
+}  // namespace sdt

@@ -12,6 +12,7 @@
 #include "gemm_kernel.hpp"
 #include "gemv_kernel.hpp"
 #include "launcher.hpp"
+#include "runtime.hpp"
 #include "sdt.h"
 
 namespace sdt {
@@ -30,13 +31,11 @@ thread_local int g_last_hip_error = 0;
 
 constexpr sdt_launch kAuto = {-1, -1, -1, -1, -1, -1, -1, -1};
 
-struct DeviceInfo {
-    int num_cu = 0;
-    int nxcd = 1;
-};
 constexpr int kMaxDevices = 64;
 std::mutex g_dev_mutex;
 DeviceInfo g_dev[kMaxDevices];
+
+}  // namespace
 
 int fail_hip(hipError_t e) {
     g_last_hip_error = (int)e;
@@ -65,6 +64,8 @@ int device_info(DeviceInfo* out) {
     *out = g_dev[dev];
     return SDT_OK;
 }
+
+namespace {
 
 // One launch of gemm_kernel; a k-split launch (splits > 1) runs the
 // instantiation built for it, `splits` workgroups per tile, followed (with
@@ -175,6 +176,17 @@ __global__ void fill_words_kernel(uint32_t* w, int64_t words) {
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < words;
          i += (int64_t)gridDim.x * blockDim.x)
         w[i] = 0u;
+}
+
+// C = 0 for K == 0 (the empty sum), M x N with stride ldc.
+__global__ void fill_zero_kernel(uint16_t* C, int64_t ldc, int M, int N) {
+    const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const int64_t total = (int64_t)M * N;
+    for (int64_t e = idx; e < total; e += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t m = e / N;
+        const int64_t n = e - m * N;
+        C[m * ldc + n] = 0;
+    }
 }
 
 int fill_words(uint32_t* w, int64_t words, hipStream_t stream) {
