@@ -10,6 +10,7 @@
 #include "launcher.hpp"
 #include "moe_kernel.hpp"
 #include "mx4_kernel.hpp"
+#include "mx4_pp_kernel.hpp"
 #include "runtime.hpp"
 #include "sdt.h"
 
@@ -149,6 +150,12 @@ int gemm(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void
     p.nkt = (int)k_tiles(K);
     p.nxcd = dev.nxcd;
     if (M <= 64) return launch_skinny<Elt, false, false>(p, 1, stream);
+    if (ceil_div(M, 256) * ceil_div(N, 256) >= dev.num_cu / 2) {
+        p.gm = (int)ceil_div(M, 256);
+        p.gn = (int)ceil_div(N, 256);
+        return launch(reinterpret_cast<const void*>(&mx4_pp_kernel<Elt>), (int64_t)p.gm * p.gn, 512,
+                      p, stream);
+    }
     if (ceil_div(M, 128) * ceil_div(N, 128) >= dev.num_cu / 2)
         return launch_tile<Elt, 128, 128, 2, 2, 4, false, false>(p, ceil_div(M, 128), stream);
     return launch_tile<Elt, 64, 64, 2, 2, 4, false, false>(p, ceil_div(M, 64), stream);
