@@ -152,7 +152,7 @@ __global__ __launch_bounds__(512) void mx4_pp_kernel(Mx4Gemm p) {
     // ---- prologue: A(0), B(0), B(1), the first scales -------------------------------
     const int nkt = p.nkt;
     if (nkt > 0) {
-        load_scales(0, sc);
+        load_scales(0, next);
         dma(0, 0);
         if (grp == 1 && nkt > 1) dma(1, 1);
     }
@@ -169,8 +169,20 @@ __global__ __launch_bounds__(512) void mx4_pp_kernel(Mx4Gemm p) {
         constexpr int LEFT = decltype(left)::value;       // k-tiles after this one (2: or more)
         const int sa = i & 1;
         const int sb2 = (sb == 0) ? 2 : sb - 1;   // (i + 2) % 3
-        if constexpr (LEFT >= 1) load_scales(i + 1, next);
-        __builtin_amdgcn_sched_barrier(0);        // before the stage loads: see the wait below
+        // The scales of this k-tile, which have arrived, leave the registers that
+        // those of the next are loaded into.
+        auto scales = [&]() {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int d = 0; d < 3; ++d) {
+                sc[d] = next[d];
+                asm volatile("" : "+v"(sc[d]));   // copied here, not before a wait above
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (LEFT >= 1) load_scales(i + 1, next);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        if constexpr (G == 0) scales();
         if constexpr (G == 0 && LEFT >= 1) dma(i + 1, sa ^ 1);
         if constexpr (G == 1 && LEFT >= 2) dma(i + 2, sb2);
         read_tile(sa, sb);
@@ -181,9 +193,13 @@ __global__ __launch_bounds__(512) void mx4_pp_kernel(Mx4Gemm p) {
             __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
         }
-        // B(i+1) must be in LDS before group 0 reads k-tile i + 1 in the next
-        // phase; the scales issued before B(i+2) have arrived with it.
-        if constexpr (G == 1) wait_global_loads<LEFT >= 2 ? DMA : 0>();
+        if constexpr (G == 1) {
+            // B(i+1) must be in LDS before group 0 reads k-tile i + 1 in the next
+            // phase; the scales of k-tile i were issued after it and before B(i+2).
+            __builtin_amdgcn_sched_barrier(0);
+            wait_global_loads<LEFT >= 2 ? DMA : 0>();
+            scales();
+        }
         wait_lds();
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
@@ -193,10 +209,6 @@ __global__ __launch_bounds__(512) void mx4_pp_kernel(Mx4Gemm p) {
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-        if constexpr (LEFT >= 1) {
-#pragma unroll
-            for (int d = 0; d < 3; ++d) sc[d] = next[d];
-        }
         sb = (sb == 2) ? 0 : sb + 1;
         ++i;
     };
