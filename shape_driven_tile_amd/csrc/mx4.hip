@@ -110,7 +110,7 @@ int launch_tile(Mx4Gemm p, int64_t row_tiles, void* stream) {
     p.gm = (int)row_tiles;
     p.gn = (int)ceil_div(p.N, GATED ? BN / 2 : BN);
     return launch(reinterpret_cast<const void*>(&mx4_gemm_kernel<Elt, BM, BN, WM, WN, NS, GROUPED, GATED>),
-                  (int64_t)p.gm * p.gn, WM * WN * 128, p, stream);
+                  (int64_t)p.gm * p.gn, WM * WN * 64, p, stream);
 }
 
 template <typename Elt, bool GROUPED, bool GATED>
@@ -157,7 +157,7 @@ int gemm(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void
                       p, stream);
     }
     if (ceil_div(M, 128) * ceil_div(N, 128) >= dev.num_cu / 2)
-        return launch_tile<Elt, 128, 128, 2, 2, 4, false, false>(p, ceil_div(M, 128), stream);
+        return launch_tile<Elt, 128, 128, 2, 2, 2, false, false>(p, ceil_div(M, 128), stream);
     return launch_tile<Elt, 64, 64, 2, 2, 4, false, false>(p, ceil_div(M, 64), stream);
 }
 
@@ -340,10 +340,10 @@ int moe_gemm(const sdt_moe_plan* plan, int64_t N, int64_t K, const void* A, int6
         return up ? launch_skinny<Elt, true, true>(p, groups, stream)
                   : launch_skinny<Elt, true, false>(p, groups, stream);
     if (per <= 64)
-        return up ? launch_tile<Elt, 64, 128, 2, 2, 4, true, true>(p, groups, stream)
-                  : launch_tile<Elt, 64, 128, 2, 2, 4, true, false>(p, groups, stream);
-    return up ? launch_tile<Elt, 128, 128, 2, 2, 4, true, true>(p, groups, stream)
-              : launch_tile<Elt, 128, 128, 2, 2, 4, true, false>(p, groups, stream);
+        return up ? launch_tile<Elt, 64, 128, 2, 2, 3, true, true>(p, groups, stream)
+                  : launch_tile<Elt, 64, 128, 2, 2, 3, true, false>(p, groups, stream);
+    return up ? launch_tile<Elt, 128, 128, 2, 2, 2, true, true>(p, groups, stream)
+              : launch_tile<Elt, 128, 128, 2, 2, 2, true, false>(p, groups, stream);
 }
 
 template <typename S>

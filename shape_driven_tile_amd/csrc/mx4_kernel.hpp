@@ -490,18 +490,21 @@ __global__ __launch_bounds__(NW * 64) void mx4_skinny_kernel(Mx4Gemm p) {
     }
 }
 
-// The tiled product: BM x BN outputs per workgroup, WM x WN compute waves of
-// 16x16x128 MFMAs and as many loader waves, which issue every global -> LDS
-// load (the layout of gemm_kernel's HELP form: NS stages, one barrier per
-// k-tile).  A stage holds the codes of BM + BN rows x 128 bytes and their
-// scale tiles.  16-byte chunk 2 g + s of row r (block 2 g + s of the k-tile) is
-// kept at position (4 s + g) ^ swz_pp(r), so a fragment read of half s has the
-// conflict-free pattern of the 16-bit kernels.  GATED: the B rows of a wave are
-// 32 of the first matrix and the same 32 of the second, so a lane holds both
-// factors of its outputs; BN / 2 columns per workgroup.  GROUPED: rows are a
-// plan's, the expert's matrices are found from the row tile.
+// The tiled product: BM x BN outputs per workgroup, WM x WN waves of 16x16x128
+// MFMAs.  A stage holds the codes of BM + BN rows x 128 bytes and their scale
+// tiles, loaded straight into LDS; NS stages.  16-byte chunk 2 g + s of row r
+// (block 2 g + s of the k-tile) is kept at position (4 s + g) ^ swz_pp(r), so a
+// fragment read of half s has the conflict-free pattern of the 16-bit kernels.
+// One barrier per k-tile: after it the loads of k-tile i + NS go into the stage
+// that k-tile i has left, the fragments of i + 1 are read into a second set of
+// registers, and the MFMAs of i run.  The LDS of two workgroups fits a CU: one's
+// prologue, waits and epilogue run under the other's MFMAs.
+// GATED: the B rows of a wave are 32 of the first matrix and the same 32 of the
+// second, so a lane holds both factors of its outputs; BN / 2 columns per
+// workgroup.  GROUPED: rows are a plan's, the expert's matrices are found from
+// the row tile.
 template <typename Elt, int BM, int BN, int WM, int WN, int NS, bool GROUPED, bool GATED>
-__global__ __launch_bounds__(WM * WN * 128) void mx4_gemm_kernel(Mx4Gemm p) {
+__global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
     constexpr int NW = WM * WN;
     constexpr int WTM = BM / WM, WTN = BN / WN;
     constexpr int FM = WTM / 16, FN = WTN / 16;
@@ -511,22 +514,20 @@ __global__ __launch_bounds__(WM * WN * 128) void mx4_gemm_kernel(Mx4Gemm p) {
     constexpr int STAGE = S_BASE + SA_UNITS + SB_UNITS;
     constexpr int A_DMA = A_UNITS / (64 * NW), B_DMA = B_UNITS / (64 * NW);
     constexpr int ST = (BM + BN) / 64;            // scale tiles of a stage
-    constexpr int S_DMA = (ST + NW - 1) / NW;     // per loader wave (spare waves repeat a tile)
+    constexpr int S_DMA = (ST + NW - 1) / NW;     // per wave (spare waves repeat a tile)
     constexpr int L = A_DMA + B_DMA + S_DMA;
     static_assert(A_UNITS % (64 * NW) == 0 && B_UNITS % (64 * NW) == 0, "whole 8-row slabs");
     static_assert(BM % 64 == 0 && BN % 64 == 0, "whole scale tiles");
     static_assert(!GATED || (WTN == 64 && BN == 128), "gated: 32 + 32 columns per wave");
     static_assert(WTM == 32 || WTM % 64 == 0, "a wave's rows: halves of or whole scale tiles");
     static_assert(WTN == 32 || WTN == 64, "a wave's columns: half of or a whole scale tile");
-    static_assert(NS * STAGE * 16 <= 160 * 1024, "stages fit the LDS");
+    static_assert(2 * NS * STAGE * 16 <= 160 * 1024, "the stages of two workgroups fit the LDS");
     static_assert(NW * 256 <= NS * STAGE, "epilogue stage");
     __shared__ int4_t smem[NS * STAGE];
 
     const int t = threadIdx.x;
     const int lane = t & 63;
-    const int wave_id = __builtin_amdgcn_readfirstlane(t >> 6);
-    const bool loader = wave_id >= NW;
-    const int wave = wave_id % NW;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wave_m = wave % WM, wave_n = wave / WM;
 
     const int BNO = GATED ? BN / 2 : BN;          // output columns
@@ -548,84 +549,63 @@ __global__ __launch_bounds__(WM * WN * 128) void mx4_gemm_kernel(Mx4Gemm p) {
     const int rows_b = (int)min((int64_t)BNO, (int64_t)p.N - n0);
     const uint32_t srow = (uint32_t)p.nkt * kMx4Tile;   // scale bytes of 64 rows
 
-    if (loader) {
-        const __amdgpu_buffer_rsrc_t ra =
-            make_rsrc(p.A + m0 * p.lda, (uint32_t)((rows_a - 1) * p.lda + p.rowbytes));
-        const __amdgpu_buffer_rsrc_t rb =
-            make_rsrc(p.B + e * p.eqb + n0 * p.ldb, (uint32_t)((rows_b - 1) * p.ldb + p.rowbytes));
-        const __amdgpu_buffer_rsrc_t rb2 =
-            make_rsrc(GATED ? p.B2 + e * p.eqb2 + n0 * p.ldb2 : p.B,
-                      GATED ? (uint32_t)((rows_b - 1) * p.ldb2 + p.rowbytes) : 0u);
-        const __amdgpu_buffer_rsrc_t rsa =
-            make_rsrc(p.SA + (m0 / 64) * srow, (uint32_t)((rows_a + 63) / 64) * srow);
-        const __amdgpu_buffer_rsrc_t rsb = make_rsrc(p.SB + e * p.esb + (n0 / 64) * srow,
-                                                     (uint32_t)((rows_b + 63) / 64) * srow);
-        const __amdgpu_buffer_rsrc_t rsb2 =
-            make_rsrc(GATED ? p.SB2 + e * p.esb2 + (n0 / 64) * srow : p.SB,
-                      GATED ? (uint32_t)((rows_b + 63) / 64) * srow : 0u);
-        uint32_t voff_a[A_DMA], voff_b[B_DMA];
+    const __amdgpu_buffer_rsrc_t ra =
+        make_rsrc(p.A + m0 * p.lda, (uint32_t)((rows_a - 1) * p.lda + p.rowbytes));
+    const __amdgpu_buffer_rsrc_t rb =
+        make_rsrc(p.B + e * p.eqb + n0 * p.ldb, (uint32_t)((rows_b - 1) * p.ldb + p.rowbytes));
+    const __amdgpu_buffer_rsrc_t rb2 =
+        make_rsrc(GATED ? p.B2 + e * p.eqb2 + n0 * p.ldb2 : p.B,
+                  GATED ? (uint32_t)((rows_b - 1) * p.ldb2 + p.rowbytes) : 0u);
+    const __amdgpu_buffer_rsrc_t rsa =
+        make_rsrc(p.SA + (m0 / 64) * srow, (uint32_t)((rows_a + 63) / 64) * srow);
+    const __amdgpu_buffer_rsrc_t rsb = make_rsrc(p.SB + e * p.esb + (n0 / 64) * srow,
+                                                 (uint32_t)((rows_b + 63) / 64) * srow);
+    const __amdgpu_buffer_rsrc_t rsb2 =
+        make_rsrc(GATED ? p.SB2 + e * p.esb2 + (n0 / 64) * srow : p.SB,
+                  GATED ? (uint32_t)((rows_b + 63) / 64) * srow : 0u);
+    uint32_t voff_a[A_DMA], voff_b[B_DMA];
 #pragma unroll
-        for (int j = 0; j < A_DMA; ++j) {
-            const int row = (wave * A_DMA + j) * 8 + (lane >> 3);
-            const int pos = (lane & 7) ^ swz_pp(row);
-            voff_a[j] = (uint32_t)(row * p.lda) + ((pos & 3) * 2 + (pos >> 2)) * 16;
-        }
+    for (int j = 0; j < A_DMA; ++j) {
+        const int row = (wave * A_DMA + j) * 8 + (lane >> 3);
+        const int pos = (lane & 7) ^ swz_pp(row);
+        voff_a[j] = (uint32_t)(row * p.lda) + ((pos & 3) * 2 + (pos >> 2)) * 16;
+    }
+#pragma unroll
+    for (int j = 0; j < B_DMA; ++j) {
+        const int row = (wave * B_DMA + j) * 8 + (lane >> 3);
+        const int pos = (lane & 7) ^ swz_pp(row);
+        // gated: LDS rows 64 w + 32 h + i are row 32 w + i of matrix h
+        const int src = GATED ? (row >> 6) * 32 + (row & 31) : row;
+        voff_b[j] = (uint32_t)(src * (GATED && (row & 32) ? p.ldb2 : p.ldb)) +
+                    ((pos & 3) * 2 + (pos >> 2)) * 16;
+    }
+    auto load_tile = [&](int kt, int stage) {
+        int4_t* base = smem + stage * STAGE;
+        // in the lane offset, which the descriptor's range check covers: the
+        // last row's bytes past its blocks are not read
+        const uint32_t koff = (uint32_t)kt * 128;
+#pragma unroll
+        for (int j = 0; j < A_DMA; ++j)
+            dma16(ra, base + (wave * A_DMA + j) * 64, voff_a[j] + koff, 0);
 #pragma unroll
         for (int j = 0; j < B_DMA; ++j) {
-            const int row = (wave * B_DMA + j) * 8 + (lane >> 3);
-            const int pos = (lane & 7) ^ swz_pp(row);
-            // gated: LDS rows 64 w + 32 h + i are row 32 w + i of matrix h
-            const int src = GATED ? (row >> 6) * 32 + (row & 31) : row;
-            voff_b[j] = (uint32_t)(src * (GATED && (row & 32) ? p.ldb2 : p.ldb)) +
-                        ((pos & 3) * 2 + (pos >> 2)) * 16;
+            const bool second = GATED && (((wave * B_DMA + j) * 8) & 32) != 0;
+            dma16(second ? rb2 : rb, base + A_UNITS + (wave * B_DMA + j) * 64, voff_b[j] + koff, 0);
         }
-        auto load_tile = [&](int kt, int stage) {
-            int4_t* base = smem + stage * STAGE;
-            // in the lane offset, which the descriptor's range check covers: the
-            // last row's bytes past its blocks are not read
-            const uint32_t koff = (uint32_t)kt * 128;
 #pragma unroll
-            for (int j = 0; j < A_DMA; ++j)
-                dma16(ra, base + (wave * A_DMA + j) * 64, voff_a[j] + koff, 0);
-#pragma unroll
-            for (int j = 0; j < B_DMA; ++j) {
-                const bool second = GATED && (((wave * B_DMA + j) * 8) & 32) != 0;
-                dma16(second ? rb2 : rb, base + A_UNITS + (wave * B_DMA + j) * 64, voff_b[j] + koff, 0);
+        for (int j = 0; j < S_DMA; ++j) {
+            const int st = (wave * S_DMA + j) % ST;
+            int4_t* dst = base + S_BASE + st * 32;
+            if (lane < 32) {
+                if (st < BM / 64)
+                    dma16(rsa, dst, st * srow + lane * 16, kt * kMx4Tile);
+                else if (GATED && st > BM / 64)
+                    dma16(rsb2, dst, lane * 16, kt * kMx4Tile);
+                else
+                    dma16(rsb, dst, (st - BM / 64) * srow + lane * 16, kt * kMx4Tile);
             }
-#pragma unroll
-            for (int j = 0; j < S_DMA; ++j) {
-                const int st = (wave * S_DMA + j) % ST;
-                int4_t* dst = base + S_BASE + st * 32;
-                if (lane < 32) {
-                    if (st < BM / 64)
-                        dma16(rsa, dst, st * srow + lane * 16, kt * kMx4Tile);
-                    else if (GATED && st > BM / 64)
-                        dma16(rsb2, dst, lane * 16, kt * kMx4Tile);
-                    else
-                        dma16(rsb, dst, (st - BM / 64) * srow + lane * 16, kt * kMx4Tile);
-                }
-            }
-        };
-        const int npro = min(p.nkt, NS);
-        for (int j = 0; j < npro; ++j) load_tile(j, j);
-        if (p.nkt > NS)
-            wait_global_loads<(NS - 1) * L>();
-        else
-            wait_global_loads<0>();
-        __syncthreads();
-        int s = 0, i = 0;
-        for (; i + NS < p.nkt; ++i) {
-            wait_global_loads<(NS - 2) * L>();
-            __syncthreads();
-            load_tile(i + NS, s);
-            s = (s + 1 == NS) ? 0 : s + 1;
         }
-        for (; i < p.nkt; ++i) {
-            wait_global_loads<0>();
-            __syncthreads();
-        }
-        return;
-    }
+    };
 
     floatx4_t acc[FN][FM];
 #pragma unroll
@@ -638,75 +618,95 @@ __global__ __launch_bounds__(WM * WN * 128) void mx4_gemm_kernel(Mx4Gemm p) {
     const int a_row0 = wave_m * WTM + frow;
     const int b_row0 = A_UNITS / 8 + wave_n * WTN + frow;
     constexpr int SAW = FM / 2, SBW = FN / 2;     // scale dwords per lane (two parts each)
-    int4_t fa[2][FM], fb[2][FN];
-    auto read_half = [&](int stage, int s) {
-        const int4_t* base = smem + stage * STAGE;
-        const int chunk = (4 * s + fq) ^ fsw;
-#pragma unroll
-        for (int j = 0; j < FM; ++j) fa[s][j] = base[(a_row0 + j * 16) * 8 + chunk];
-#pragma unroll
-        for (int i = 0; i < FN; ++i) fb[s][i] = base[(b_row0 + i * 16) * 8 + chunk];
+    struct Frags {
+        int4_t a[2][FM], b[2][FN];
+        int sa[SAW], sb[SBW];
     };
-    auto read_scales = [&](int stage, int (&sa)[SAW], int (&sb)[SBW]) {
-        const int* sbase = reinterpret_cast<const int*>(smem + stage * STAGE + S_BASE);
+    auto read_tile = [&](int stage, Frags& f) {
+        const int4_t* base = smem + stage * STAGE;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int chunk = (4 * s + fq) ^ fsw;
+#pragma unroll
+            for (int j = 0; j < FM; ++j) f.a[s][j] = base[(a_row0 + j * 16) * 8 + chunk];
+#pragma unroll
+            for (int i = 0; i < FN; ++i) f.b[s][i] = base[(b_row0 + i * 16) * 8 + chunk];
+        }
+        const int* sbase = reinterpret_cast<const int*>(base + S_BASE);
 #pragma unroll
         for (int d = 0; d < SAW; ++d) {
             const int part = wave_m * FM + 2 * d;      // 16-row part of the tile's BM rows
-            sa[d] = sbase[(part >> 2) * 128 + lane * 2 + ((part >> 1) & 1)];
+            f.sa[d] = sbase[(part >> 2) * 128 + lane * 2 + ((part >> 1) & 1)];
         }
 #pragma unroll
         for (int d = 0; d < SBW; ++d) {
             if constexpr (GATED) {
                 // dword d: matrix d's columns 32 wave_n .. + 31 of its one tile
-                sb[d] = sbase[(BM / 64 + d) * 128 + lane * 2 + (wave_n & 1)];
+                f.sb[d] = sbase[(BM / 64 + d) * 128 + lane * 2 + (wave_n & 1)];
             } else {
                 const int part = wave_n * FN + 2 * d;
-                sb[d] = sbase[(BM / 64 + (part >> 2)) * 128 + lane * 2 + ((part >> 1) & 1)];
+                f.sb[d] = sbase[(BM / 64 + (part >> 2)) * 128 + lane * 2 + ((part >> 1) & 1)];
             }
         }
     };
-    auto mfma_half = [&](auto half, const int (&sa)[SAW], const int (&sb)[SBW]) {
+    auto mfma_half = [&](auto half, const Frags& f) {
         constexpr int S = decltype(half)::value;
 #pragma unroll
         for (int i = 0; i < FN; i += 2)
 #pragma unroll
             for (int j = 0; j < FM; j += 2) {
-                acc[i][j] = mx4_mfma_part<S, 0, 0>(fb[S][i], fa[S][j], acc[i][j], sb[i / 2], sa[j / 2]);
-                acc[i][j + 1] =
-                    mx4_mfma_part<S, 0, 1>(fb[S][i], fa[S][j + 1], acc[i][j + 1], sb[i / 2], sa[j / 2]);
-                acc[i + 1][j] =
-                    mx4_mfma_part<S, 1, 0>(fb[S][i + 1], fa[S][j], acc[i + 1][j], sb[i / 2], sa[j / 2]);
-                acc[i + 1][j + 1] = mx4_mfma_part<S, 1, 1>(fb[S][i + 1], fa[S][j + 1], acc[i + 1][j + 1],
-                                                           sb[i / 2], sa[j / 2]);
+                const int b = f.sb[i / 2], a = f.sa[j / 2];
+                acc[i][j] = mx4_mfma_part<S, 0, 0>(f.b[S][i], f.a[S][j], acc[i][j], b, a);
+                acc[i][j + 1] = mx4_mfma_part<S, 0, 1>(f.b[S][i], f.a[S][j + 1], acc[i][j + 1], b, a);
+                acc[i + 1][j] = mx4_mfma_part<S, 1, 0>(f.b[S][i + 1], f.a[S][j], acc[i + 1][j], b, a);
+                acc[i + 1][j + 1] =
+                    mx4_mfma_part<S, 1, 1>(f.b[S][i + 1], f.a[S][j + 1], acc[i + 1][j + 1], b, a);
             }
     };
-    using Half0 = std::integral_constant<int, 0>;
-    using Half1 = std::integral_constant<int, 1>;
+    auto barrier = [&]() {
+        // not __syncthreads: its release would wait for every load in flight
+        wait_lds();
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+    };
 
-    __syncthreads();
-    int sa[SAW], sb[SBW];
-    int s = 0;
-    if (p.nkt > 0) {
-        read_half(0, 0);
-        read_scales(0, sa, sb);
-    }
-    for (int i = 0; i < p.nkt; ++i) {
+    const int nkt = p.nkt;
+    Frags f[2];
+    int i = 0, s = 0;                             // k-tile, its stage
+    auto step = [&](auto waits, Frags& cur, Frags& next) {
+        wait_global_loads<decltype(waits)::value>();   // k-tile i + 1 has landed
+        barrier();
         const int sn = (s + 1 == NS) ? 0 : s + 1;
-        read_half(s, 1);
-        mfma_half(Half0{}, sa, sb);
-        // the rest of tile i is in registers: its stage may be refilled
-        __syncthreads();
-        int na[SAW], nb[SBW];
-        if (i + 1 < p.nkt) {
-            read_half(sn, 0);
-            read_scales(sn, na, nb);
-        }
-        mfma_half(Half1{}, sa, sb);
+        if (i + NS < nkt) load_tile(i + NS, s);
+        if (i + 1 < nkt) read_tile(sn, next);
+        mfma_half(std::integral_constant<int, 0>{}, cur);
+        mfma_half(std::integral_constant<int, 1>{}, cur);
+        // keeps the MFMAs, values to the compiler, before the waits that follow
 #pragma unroll
-        for (int d = 0; d < SAW; ++d) sa[d] = na[d];
+        for (int n = 0; n < FN; ++n)
 #pragma unroll
-        for (int d = 0; d < SBW; ++d) sb[d] = nb[d];
+            for (int m = 0; m < FM; ++m) asm volatile("" : "+v"(acc[n][m]));
         s = sn;
+        ++i;
+    };
+    using Steady = std::integral_constant<int, (NS - 2) * L>;
+    using Last = std::integral_constant<int, 0>;
+
+    for (int j = 0; j < min(nkt, NS); ++j) load_tile(j, j);
+    if (nkt >= NS)
+        wait_global_loads<(NS - 1) * L>();
+    else
+        wait_global_loads<0>();
+    barrier();
+    if (nkt > 0) read_tile(0, f[0]);
+    while (i + NS < nkt) {                        // k-tiles i + 1 .. i + NS - 1, and i + NS for the second
+        step(Steady{}, f[0], f[1]);
+        step(Steady{}, f[1], f[0]);
+    }
+    while (i < nkt) {
+        step(Last{}, f[0], f[1]);
+        if (i < nkt) step(Last{}, f[1], f[0]);
     }
 
     // The stages are not read any more after the last k-tile's barrier (with no
