@@ -309,34 +309,78 @@ struct PlanParams {
 
 // One workgroup per expert.  Each counts every expert's slots in LDS (integer
 // adds: any order gives the same counts), so each knows where its segment
-// starts; then it passes over the slots once more and places its own in order,
-// by ballots within waves and a prefix over the waves.  No workgroup needs
-// another's result.
+// starts; then it passes over the slots once more and places its own in order.
+// No workgroup needs another's result.  Bound by the latency of reading idx
+// twice: every wave owns a contiguous sixteenth of the slots and reads four to a
+// lane, kPlanLoads loads in flight, so neither pass has a barrier inside.
+constexpr int kPlanLoads = 8;
+
+struct SlotQuad {
+    int32_t v[4];
+};
+
 __global__ __launch_bounds__(1024) void moe_plan_kernel(PlanParams p) {
     __shared__ int hist[kMaxExperts];
-    __shared__ int wsum[17];
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    __shared__ int wcount[16], wbefore[16];
+    const int t = threadIdx.x, lane = t & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int e = blockIdx.x;
     for (int i = t; i < p.E; i += 1024) hist[i] = 0;
     __syncthreads();
-    for (int i = t; i < p.R; i += 1024) {
-        const int v = p.idx[i];
-        if (v >= 0 && v < p.E)
-            atomicAdd(&hist[v], 1);
-        else if (e == 0)
-            p.pos[i] = -1;
+    // this wave's quads of slots
+    const int quads = (int)(((int64_t)p.R + 3) / 4);
+    const int per = (quads + 15) / 16;
+    const int first = min(wave * per, quads), last = min(first + per, quads);
+    auto load = [&](int q0, SlotQuad (&v)[kPlanLoads]) {
+#pragma unroll
+        for (int u = 0; u < kPlanLoads; ++u) {
+            const int q = q0 + u * 64 + lane;
+            const int64_t i = (int64_t)q * 4;
+            if (q < last && i + 3 < p.R) {
+                __builtin_memcpy(&v[u], p.idx + i, 16);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[u].v[c] = q < last && i + c < p.R ? p.idx[i + c] : -1;
+            }
+        }
+    };
+    int mine = 0;                              // slots of this wave that chose e
+    for (int q0 = first; q0 < last; q0 += 64 * kPlanLoads) {
+        SlotQuad v[kPlanLoads];
+        load(q0, v);
+#pragma unroll
+        for (int u = 0; u < kPlanLoads; ++u) {
+            if (q0 + u * 64 >= last) break;
+            const int q = q0 + u * 64 + lane;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int x = v[u].v[c];
+                const int64_t i = (int64_t)q * 4 + c;
+                mine += __popcll(__ballot(x == e));
+                if (q < last && i < p.R) {
+                    if (x >= 0 && x < p.E)
+                        atomicAdd(&hist[x], 1);
+                    else if (e == 0)
+                        p.pos[i] = -1;
+                }
+            }
+        }
     }
+    if (lane == 0) wcount[wave] = mine;
     __syncthreads();
     // rows before this expert's
     int before = 0;
     for (int i = t; i < e; i += 1024) before += (hist[i] + 63) & ~63;
 #pragma unroll
     for (int m = 32; m > 0; m >>= 1) before += __shfl_xor(before, m);
-    if (lane == 0) wsum[wave] = before;
+    if (lane == 0) wbefore[wave] = before;
     __syncthreads();
-    int start = 0;
-    for (int w = 0; w < 16; ++w) start += wsum[w];
-    const int count = hist[e];
+    int start = 0, row0 = 0, count = 0;
+    for (int w = 0; w < 16; ++w) {
+        start += wbefore[w];
+        if (w < wave) row0 += wcount[w];
+        count += wcount[w];
+    }
     const int end = start + ((count + 63) & ~63);
     if (t == 0) {
         p.counts[e] = count;
@@ -349,25 +393,32 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(PlanParams p) {
         for (int i = end + t; i < p.cap; i += 1024) p.rows[i] = -1;
         for (int i = end / 64 + t; i < p.cap / 64; i += 1024) p.tiles[i] = -1;
     }
-    int placed = 0;
-    for (int i0 = 0; i0 < p.R && placed < count; i0 += 1024) {
-        const int i = i0 + t;
-        const bool hit = i < p.R && p.idx[i] == e;
-        const uint64_t mask = __ballot(hit);
-        __syncthreads();
-        if (lane == 0) wsum[wave] = __popcll(mask);
-        __syncthreads();
-        int off = placed, all = 0;
-        for (int w = 0; w < 16; ++w) {
-            if (w < wave) off += wsum[w];
-            all += wsum[w];
+    if (mine == 0) return;
+    int row = start + row0;                    // of this wave's next slot
+    const uint64_t below = (1ull << lane) - 1;
+    for (int q0 = first; q0 < last; q0 += 64 * kPlanLoads) {
+        SlotQuad v[kPlanLoads];
+        load(q0, v);
+#pragma unroll
+        for (int u = 0; u < kPlanLoads; ++u) {
+            if (q0 + u * 64 >= last) break;
+            const int i = (int)((uint32_t)(q0 + u * 64 + lane) * 4u);   // used where it is a slot
+            int at = row, all = 0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint64_t mask = __ballot(v[u].v[c] == e);
+                at += __popcll(mask & below);
+                all += __popcll(mask);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (v[u].v[c] == e) {
+                    p.rows[at] = i + c;
+                    p.pos[i + c] = at;
+                    ++at;
+                }
+            row += all;
         }
-        if (hit) {
-            const int row = start + off + __popcll(mask & ((1ull << lane) - 1));
-            p.rows[row] = i;
-            p.pos[i] = row;
-        }
-        placed += all;
     }
 }
 

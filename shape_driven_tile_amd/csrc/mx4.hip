@@ -72,10 +72,8 @@ int quantize(int64_t rows, int64_t K, const void* X, int64_t xrows, int64_t ldx,
     p.rows = rows;
     p.K = (int)K;
     p.nkt = (int)k_tiles(K);
-    const bool vec = !misaligned(X, 16) && ldx % 8 == 0;
-    const void* k = vec ? reinterpret_cast<const void*>(&mx4_quantize_kernel<Elt, true>)
-                        : reinterpret_cast<const void*>(&mx4_quantize_kernel<Elt, false>);
-    return launch(k, ceil_div(rows, 64) * p.nkt, 256, p, stream);
+    return launch(reinterpret_cast<const void*>(&mx4_quantize_kernel<Elt>),
+                  ceil_div(rows, 64) * p.nkt, 256, p, stream);
 }
 
 template <int OUT>
@@ -97,19 +95,18 @@ int dequantize(int64_t rows, int64_t K, const void* Q, int64_t ldq, const void* 
     p.rows = rows;
     p.K = (int)K;
     p.nkt = (int)k_tiles(K);
-    const bool vec = !misaligned(Y, 16) && (ldy * z) % 16 == 0;
-    const void* k = vec ? reinterpret_cast<const void*>(&mx4_dequantize_kernel<OUT, true>)
-                        : reinterpret_cast<const void*>(&mx4_dequantize_kernel<OUT, false>);
-    return launch(k, ceil_div(rows, 64) * p.nkt, 256, p, stream);
+    return launch(reinterpret_cast<const void*>(&mx4_dequantize_kernel<OUT>),
+                  ceil_div(rows, 64) * p.nkt, 256, p, stream);
 }
 
 // ---- products -----------------------------------------------------------------------
 
-template <typename Elt, int BM, int BN, int WM, int WN, int NS, bool GROUPED, bool GATED>
+template <typename Elt, int BM, int BN, int WM, int WN, int NS, bool GROUPED, bool GATED,
+          bool QOUT = false>
 int launch_tile(Mx4Gemm p, int64_t row_tiles, void* stream) {
     p.gm = (int)row_tiles;
     p.gn = (int)ceil_div(p.N, GATED ? BN / 2 : BN);
-    return launch(reinterpret_cast<const void*>(&mx4_gemm_kernel<Elt, BM, BN, WM, WN, NS, GROUPED, GATED>),
+    return launch(reinterpret_cast<const void*>(&mx4_gemm_kernel<Elt, BM, BN, WM, WN, NS, GROUPED, GATED, QOUT>),
                   (int64_t)p.gm * p.gn, WM * WN * 64, p, stream);
 }
 
@@ -290,10 +287,41 @@ int check_experts(int64_t N, int64_t K, const sdt_mx4_experts* B) {
     return SDT_OK;
 }
 
+// Rows an expert where the tokens choose evenly: picks the grouped kernel.
+int64_t rows_per_expert(const sdt_moe_plan* plan) {
+    return plan->tokens * plan->topk / plan->experts;
+}
+constexpr int64_t kSkinnyRows = 16;   // up to these the weights are streamed
+
+// What a grouped product takes and gives besides its matrices: A's rows by token
+// (gather; the A given then has one row per token) and a quantised output.
+struct MoeExtra {
+    bool gather = false;
+    uint8_t *qo = nullptr, *so = nullptr;
+    int64_t ldqo = 0;
+};
+
+template <typename Elt>
+int launch_grouped(Mx4Gemm p, const sdt_moe_plan* plan, int64_t rows, bool gated, bool quantized,
+                   void* stream) {
+    const int64_t groups = rows / 64;
+    const int64_t per = rows_per_expert(plan);
+    if (per <= kSkinnyRows)
+        return gated ? launch_skinny<Elt, true, true>(p, groups, stream)
+                     : launch_skinny<Elt, true, false>(p, groups, stream);
+    if (per <= 64)
+        return quantized ? launch_tile<Elt, 64, 128, 2, 2, 3, true, true, true>(p, groups, stream)
+               : gated   ? launch_tile<Elt, 64, 128, 2, 2, 3, true, true>(p, groups, stream)
+                         : launch_tile<Elt, 64, 128, 2, 2, 3, true, false>(p, groups, stream);
+    return quantized ? launch_tile<Elt, 128, 128, 2, 2, 2, true, true, true>(p, groups, stream)
+           : gated   ? launch_tile<Elt, 128, 128, 2, 2, 2, true, true>(p, groups, stream)
+                     : launch_tile<Elt, 128, 128, 2, 2, 2, true, false>(p, groups, stream);
+}
+
 template <typename Elt>
 int moe_gemm(const sdt_moe_plan* plan, int64_t N, int64_t K, const void* A, int64_t lda,
              const void* SA, const sdt_mx4_experts* B, const sdt_mx4_experts* up, void* C,
-             int64_t ldc, void* stream) {
+             int64_t ldc, void* stream, const MoeExtra& x = {}) {
     int64_t rows;
     int rc = check_plan(plan, &rows);
     if (rc != SDT_OK) return rc;
@@ -301,7 +329,7 @@ int moe_gemm(const sdt_moe_plan* plan, int64_t N, int64_t K, const void* A, int6
     rc = check_experts(N, K, B);
     if (rc == SDT_OK && up) rc = check_experts(N, K, up);
     if (rc != SDT_OK || rows == 0 || N == 0) return rc;
-    rc = check_out(rows, N, C, ldc);
+    if (!x.qo) rc = check_out(rows, N, C, ldc);
     if (rc == SDT_OK) rc = check_mx4(rows, K, A, lda, SA);
     if (rc != SDT_OK) return rc;
     if (N > INT_MAX) return SDT_ERR_UNSUPPORTED;
@@ -334,16 +362,34 @@ int moe_gemm(const sdt_moe_plan* plan, int64_t N, int64_t K, const void* A, int6
         p.eqb2 = up->q_expert;
         p.esb2 = up->s_expert;
     }
-    const int64_t groups = rows / 64;
-    const int64_t per = plan->tokens * plan->topk / plan->experts;   // rows an expert, evenly spread
-    if (per <= 16)
-        return up ? launch_skinny<Elt, true, true>(p, groups, stream)
-                  : launch_skinny<Elt, true, false>(p, groups, stream);
-    if (per <= 64)
-        return up ? launch_tile<Elt, 64, 128, 2, 2, 3, true, true>(p, groups, stream)
-                  : launch_tile<Elt, 64, 128, 2, 2, 3, true, false>(p, groups, stream);
-    return up ? launch_tile<Elt, 128, 128, 2, 2, 2, true, true>(p, groups, stream)
-              : launch_tile<Elt, 128, 128, 2, 2, 2, true, false>(p, groups, stream);
+    if (x.gather) {
+        p.slots = plan->rows;
+        p.topk = plan->topk;
+        p.abytes = (uint32_t)(plan->tokens * lda);
+    }
+    p.QO = x.qo;
+    p.SO = x.so;
+    p.ldqo = x.ldqo;
+    p.nkto = (int)k_tiles(N);
+    return launch_grouped<Elt>(p, plan, rows, up != nullptr, x.qo != nullptr, stream);
+}
+
+template <typename Elt>
+int quantize_tokens(const sdt_moe_plan* plan, int64_t K, const void* X, int64_t ldx, void* Q,
+                    int64_t ldq, void* S, void* stream) {
+    Mx4QuantTokens p;
+    p.X = static_cast<const uint16_t*>(X);
+    p.ldx = ldx;
+    p.pos = plan->pos;
+    p.Q = static_cast<uint8_t*>(Q);
+    p.ldq = ldq;
+    p.S = static_cast<uint8_t*>(S);
+    p.tokens = plan->tokens;
+    p.topk = plan->topk;
+    p.K = (int)K;
+    p.nkt = (int)k_tiles(K);
+    return launch(reinterpret_cast<const void*>(&mx4_quantize_tokens_kernel<Elt>),
+                  ceil_div(p.tokens, 64) * p.nkt, 256, p, stream);
 }
 
 template <typename S>
@@ -431,11 +477,24 @@ int moe_layer(const sdt_moe_layer* layer, const int32_t* idx, const float* weigh
     uint8_t* w = static_cast<uint8_t*>(workspace);
     rc = moe_plan(idx, plan, stream);
     if (rc != SDT_OK || K == 0) return rc;
-    rc = quantize<Elt>(rows, K, X, T, ldx, plan->rows, plan->topk, w + l.xq, l.ldx, w + l.xs, stream);
+    // The tokens are quantised once each and the first product gathers their rows,
+    // while 32-bit offsets reach them all; with many rows an expert the gated
+    // product comes out quantised.
+    MoeExtra x;
+    x.gather = T * l.ldx <= (int64_t)kNoRow;
+    rc = x.gather ? quantize_tokens<Elt>(plan, K, X, ldx, w + l.xq, l.ldx, w + l.xs, stream)
+                  : quantize<Elt>(rows, K, X, T, ldx, plan->rows, plan->topk, w + l.xq, l.ldx,
+                                  w + l.xs, stream);
+    const bool fused = N > 0 && rows_per_expert(plan) > kSkinnyRows;
+    if (fused) {
+        x.qo = w + l.hq;
+        x.so = w + l.hs;
+        x.ldqo = l.ldhq;
+    }
     if (rc == SDT_OK)
         rc = moe_gemm<Elt>(plan, N, K, w + l.xq, l.ldx, w + l.xs, &layer->gate, &layer->up, w + l.h,
-                           l.ldh, stream);
-    if (rc == SDT_OK)
+                           l.ldh, stream, x);
+    if (rc == SDT_OK && !fused)
         rc = quantize<Elt>(rows, N, w + l.h, rows, l.ldh, plan->rows, 0, w + l.hq, l.ldhq, w + l.hs,
                            stream);
     if (rc == SDT_OK)

@@ -103,13 +103,58 @@ struct Mx4Quant {
     int K, nkt;
 };
 
+// Sixteen-byte accesses at any alignment of the element: the memory system takes
+// them, and a row that starts off 16 bytes costs no more than the lines it
+// straddles.
+typedef uint4_t __attribute__((aligned(2))) uint4_any_t;
+
+// Eight elements from x, of which `valid` lie below K: none past K is read.
+__device__ __forceinline__ uint4_t mx4_load8(const uint16_t* x, int valid) {
+    if (valid >= 8) return *reinterpret_cast<const uint4_any_t*>(x);
+    uint4_t v = {0, 0, 0, 0};
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const uint32_t lo = 2 * d < valid ? x[2 * d] : 0u;
+        const uint32_t hi = 2 * d + 1 < valid ? x[2 * d + 1] : 0u;
+        v[d] = lo | (hi << 16);
+    }
+    return v;
+}
+
+// The largest magnitude of packed elements, as a 16-bit pattern without its
+// sign: the patterns' order is the magnitudes' (an infinity or a NaN lies at or
+// above the infinity's).
+__device__ __forceinline__ uint32_t mx4_top(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const uint32_t w[4] = {a & 0x7fff7fffu, b & 0x7fff7fffu, c & 0x7fff7fffu, d & 0x7fff7fffu};
+    ushort2_t m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(ushort2_t, w[i]));
+    return m[0] > m[1] ? m[0] : m[1];
+}
+
+// Scale byte of a block whose largest magnitude is `top`, and the codes of eight
+// of its elements (zeros in a block that holds an infinity or a NaN).
+template <typename Elt>
+__device__ __forceinline__ int mx4_encode(uint32_t top, uint32_t a, uint32_t b, uint32_t c,
+                                          uint32_t d, uint32_t& q) {
+    const uint32_t bits = __builtin_bit_cast(uint32_t, Elt::widen(top));
+    const int e = top >= Elt::kInf ? 255 : max((int)(bits >> 23) - 2, 0);
+    q = 0;
+    if (e != 255) {
+        const float scale = mx4_scale_value(e);
+        q = Elt::to_codes(q, a, scale, 0);
+        q = Elt::to_codes(q, b, scale, 1);
+        q = Elt::to_codes(q, c, scale, 2);
+        q = Elt::to_codes(q, d, scale, 3);
+    }
+    return e;
+}
+
 // One workgroup per 64 x 256 tile (one scale tile).  32 lanes take a row's 256
 // elements, 8 each (16 bytes); 4 lanes share a block and agree on its maximum
-// by two lane exchanges.  The maximum is taken on the 16-bit patterns without
-// their sign, whose order is that of the magnitudes (an infinity or a NaN lies
-// at or above the infinity's pattern).  All eight rows of a lane are loaded
-// before the first is used.
-template <typename Elt, bool VEC>
+// by two lane exchanges.  All eight rows of a lane are loaded before the first
+// is used.
+template <typename Elt>
 __global__ __launch_bounds__(256) void mx4_quantize_kernel(Mx4Quant p) {
     __shared__ uint8_t sm[kMx4Tile];
     const int t = threadIdx.x;
@@ -135,43 +180,16 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(Mx4Quant p) {
         }
         have[i] = ok;
         v[i] = uint4_t{0, 0, 0, 0};
-        if (ok) {
-            const uint16_t* x = p.X + src * p.ldx + k;
-            if (VEC && valid >= 8) {
-                v[i] = *reinterpret_cast<const uint4_t*>(x);
-            } else {
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const uint32_t lo = 2 * d < valid ? x[2 * d] : 0u;
-                    const uint32_t hi = 2 * d + 1 < valid ? x[2 * d + 1] : 0u;
-                    v[i][d] = lo | (hi << 16);
-                }
-            }
-        }
+        if (ok) v[i] = mx4_load8(p.X + src * p.ldx + k, valid);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int r = (t >> 5) + 8 * i;
-        ushort2_t m = {0, 0};
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const uint32_t w = v[i][d] & 0x7fff7fffu;
-            m = __builtin_elementwise_max(m, __builtin_bit_cast(ushort2_t, w));
-        }
-        uint32_t top = m[0] > m[1] ? m[0] : m[1];
+        uint32_t top = mx4_top(v[i][0], v[i][1], v[i][2], v[i][3]);
         top = max(top, (uint32_t)__shfl_xor((int)top, 1));
         top = max(top, (uint32_t)__shfl_xor((int)top, 2));
-        const bool special = top >= Elt::kInf;
-        const uint32_t bits = __builtin_bit_cast(uint32_t, Elt::widen(top));
-        const int e = special ? 255 : max((int)(bits >> 23) - 2, 0);
-        uint32_t q = 0;
-        if (!special) {
-            const float scale = mx4_scale_value(e);
-            q = Elt::to_codes(q, v[i][0], scale, 0);
-            q = Elt::to_codes(q, v[i][1], scale, 1);
-            q = Elt::to_codes(q, v[i][2], scale, 2);
-            q = Elt::to_codes(q, v[i][3], scale, 3);
-        }
+        uint32_t q;
+        const int e = mx4_encode<Elt>(top, v[i][0], v[i][1], v[i][2], v[i][3], q);
         const int b = l32 >> 2;
         const int64_t row = rt * 64 + r;
         const bool in = kt * 8 + b < nb;
@@ -183,6 +201,65 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(Mx4Quant p) {
     if (t < kMx4Tile / 4)
         reinterpret_cast<uint32_t*>(p.S + (int64_t)blockIdx.x * kMx4Tile)[t] =
             reinterpret_cast<const uint32_t*>(sm)[t];
+}
+
+struct Mx4QuantTokens {
+    const uint16_t* X;
+    int64_t ldx;           // elements
+    const int32_t* pos;    // plan row of each slot (token * topk + j), -1: none
+    uint8_t* Q;
+    int64_t ldq;           // bytes
+    uint8_t* S;
+    int64_t tokens;
+    int topk, K, nkt;
+};
+
+// The layer's tokens, each quantised once: codes by token (the products gather
+// their rows), scales to the tiles of every plan row of the token, two bytes per
+// pair of blocks.  Rounded once per token instead of topk times: 4096 tokens of
+// 2048, 6 experts each, 22 -> 9 us against quantising the plan's rows.
+template <typename Elt>
+__global__ __launch_bounds__(256) void mx4_quantize_tokens_kernel(Mx4QuantTokens p) {
+    __shared__ uint16_t sm[64 * 4];        // scale bytes of 64 tokens, by pairs of blocks
+    const int t = threadIdx.x;
+    const int64_t rt = blockIdx.x / p.nkt;
+    const int kt = blockIdx.x - (int)(rt * p.nkt);
+    const int l32 = t & 31;
+    const int k = kt * 256 + l32 * 8;
+    const int nb = (p.K + 31) / 32;
+    const int valid = p.K - k;
+    uint4_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t row = rt * 64 + (t >> 5) + 8 * i;
+        v[i] = uint4_t{0, 0, 0, 0};
+        if (row < p.tokens) v[i] = mx4_load8(p.X + row * p.ldx + k, valid);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = (t >> 5) + 8 * i;
+        uint32_t top = mx4_top(v[i][0], v[i][1], v[i][2], v[i][3]);
+        top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+        uint32_t q;
+        const int e = mx4_encode<Elt>(top, v[i][0], v[i][1], v[i][2], v[i][3], q);
+        const int b = l32 >> 2;
+        const int64_t row = rt * 64 + r;
+        const bool in = kt * 8 + b < nb;
+        if (in && row < p.tokens)
+            *reinterpret_cast<uint32_t*>(p.Q + row * p.ldq + kt * 128 + l32 * 4) = q;
+        if ((l32 & 3) == 0) reinterpret_cast<uint8_t*>(sm)[r * 8 + b] = in ? (uint8_t)e : 0;
+    }
+    __syncthreads();
+    const int slots = (int)min((int64_t)64, p.tokens - rt * 64) * p.topk;
+    for (int i = t; i < slots * 4; i += 256) {
+        const int slot = i >> 2, g = i & 3;
+        const int row = p.pos[rt * 64 * p.topk + slot];
+        if (row < 0) continue;
+        uint8_t* tile = p.S + ((int64_t)(row >> 6) * p.nkt + kt) * kMx4Tile;
+        *reinterpret_cast<uint16_t*>(tile + mx4_scale_offset(row & 63, 2 * g)) =
+            sm[slot / p.topk * 4 + g];
+    }
 }
 
 struct Mx4Dequant {
@@ -198,7 +275,7 @@ struct Mx4Dequant {
 // The values back: the tile split of the quantiser, eight values a lane.
 // OUT: 0 fp16, 1 bf16, 2 fp32.  A code's value and its scale are exact in
 // fp32; 16-bit outputs are rounded from there.
-template <int OUT, bool VEC>
+template <int OUT>
 __global__ __launch_bounds__(256) void mx4_dequantize_kernel(Mx4Dequant p) {
     __shared__ uint32_t sm[kMx4Tile / 4];
     const int t = threadIdx.x;
@@ -238,9 +315,10 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(Mx4Dequant p) {
         }
         if constexpr (OUT == 2) {
             float* y = static_cast<float*>(p.Y) + row * p.ldy + k;
-            if (VEC && valid >= 8) {
-                *reinterpret_cast<floatx4_t*>(y) = floatx4_t{f[0], f[1], f[2], f[3]};
-                *reinterpret_cast<floatx4_t*>(y + 4) = floatx4_t{f[4], f[5], f[6], f[7]};
+            typedef floatx4_t __attribute__((aligned(4))) floatx4_any_t;
+            if (valid >= 8) {
+                *reinterpret_cast<floatx4_any_t*>(y) = floatx4_t{f[0], f[1], f[2], f[3]};
+                *reinterpret_cast<floatx4_any_t*>(y + 4) = floatx4_t{f[4], f[5], f[6], f[7]};
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -255,8 +333,8 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(Mx4Dequant p) {
                 h[j] = __builtin_bit_cast(uint16_t, s);
             }
             uint16_t* y = static_cast<uint16_t*>(p.Y) + row * p.ldy + k;
-            if (VEC && valid >= 8) {
-                *reinterpret_cast<uint4_t*>(y) = __builtin_bit_cast(uint4_t, h);
+            if (valid >= 8) {
+                *reinterpret_cast<uint4_any_t*>(y) = __builtin_bit_cast(uint4_t, h);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -294,7 +372,31 @@ struct Mx4Gemm {
     // grouped products: the plan, and the experts' strides in bytes
     const int32_t *tiles, *offsets, *counts;
     int64_t eqb, esb, eqb2, esb2;
+    // rows of A by token: row p of the plan is A's row slots[p] / topk (nullptr: p)
+    const int32_t* slots;
+    int topk;
+    uint32_t abytes;               // of all of A's rows, at most kNoRow
+    // gated product quantised (QOUT): codes, scales and their k-tiles
+    uint8_t *QO, *SO;
+    int64_t ldqo;
+    int nkto;
 };
+
+// A row offset that lies past every descriptor, with any k offset added.
+constexpr uint32_t kNoRow = 0x40000000u;
+
+// Byte offset of row `row` (of `rows`) of a workgroup whose first is m0.
+__device__ __forceinline__ uint32_t mx4_row_offset(const Mx4Gemm& p, int64_t m0, int row, int rows) {
+    if (p.slots == nullptr) return (uint32_t)(row * p.lda);
+    if (row >= rows) return kNoRow;
+    return (uint32_t)(p.slots[m0 + row] / p.topk) * (uint32_t)p.lda;
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t mx4_rows_rsrc(const Mx4Gemm& p, int64_t m0,
+                                                                int rows) {
+    return p.slots == nullptr
+               ? make_rsrc(p.A + m0 * p.lda, (uint32_t)((rows - 1) * p.lda + p.rowbytes))
+               : make_rsrc(p.A, p.abytes);
+}
 
 // acc += B_frag . A_frag^T over one 128-deep half; BYTE_A, BYTE_B pick the
 // lane's scale bytes.
@@ -312,10 +414,14 @@ __device__ __forceinline__ floatx4_t mx4_mfma_part(int4_t b, int4_t a, floatx4_t
     return mx4_mfma<2 * (PB & 1) + S, 2 * (PA & 1) + S>(b, a, c, sb, sa);
 }
 
-// silu(g) * u of the gated product, in fp32.
+// silu(g) * u of the gated product, in fp32.  The empty asm keeps the product an
+// fp32 value: left to itself the compiler rounds s * u straight to fp16 in some
+// kernels and not in others, and the layer's results would depend on which ran.
 __device__ __forceinline__ float silu_mul(float g, float u) {
     const float s = g / (1.0f + expf(-g));
-    return s * u;
+    float r = s * u;
+    asm("" : "+v"(r));
+    return r;
 }
 
 // Rows and expert of 64-row tile `g` of a plan for tiles of BM rows: false
@@ -361,8 +467,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_skinny_kernel(Mx4Gemm p) {
 
     const int rows_b = min(16, p.N - n0);
     const uint32_t sbytes_b = (uint32_t)p.nkt * kMx4Tile;
-    const __amdgpu_buffer_rsrc_t ra =
-        make_rsrc(p.A + m0 * p.lda, (uint32_t)((rows - 1) * p.lda + p.rowbytes));
+    const __amdgpu_buffer_rsrc_t ra = mx4_rows_rsrc(p, m0, rows);
     const __amdgpu_buffer_rsrc_t rsa = make_rsrc(p.SA + (m0 / 64) * sbytes_b, sbytes_b);
     const __amdgpu_buffer_rsrc_t rb =
         make_rsrc(p.B + e * p.eqb + (int64_t)n0 * p.ldb, (uint32_t)((rows_b - 1) * p.ldb + p.rowbytes));
@@ -374,7 +479,9 @@ __global__ __launch_bounds__(NW * 64) void mx4_skinny_kernel(Mx4Gemm p) {
     const __amdgpu_buffer_rsrc_t rsb2 = make_rsrc(
         GATED ? p.SB2 + e * p.esb2 + (int64_t)(n0 / 64) * sbytes_b : p.SB, GATED ? sbytes_b : 0u);
 
-    const uint32_t voff_a = (uint32_t)(fr * p.lda) + fq * 32;
+    uint32_t voff_a[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) voff_a[j] = mx4_row_offset(p, m0, j * 16 + fr, rows) + fq * 32;
     const uint32_t voff_b = (uint32_t)(fr * p.ldb) + fq * 32;
     const uint32_t voff_b2 = GATED ? (uint32_t)(fr * p.ldb2) + fq * 32 : 0u;
     const uint32_t voff_sb = lane * 8 + ((n0 >> 4) & 3) * 2;
@@ -409,8 +516,8 @@ __global__ __launch_bounds__(NW * 64) void mx4_skinny_kernel(Mx4Gemm p) {
                 fb2[u][1] = load16(rb2, voff_b2 + 16 + so);
                 sb2[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsb2, voff_sb + ss, 0, 0);
             }
-            fa[u][0] = load16(ra, voff_a + so);
-            fa[u][1] = load16(ra, voff_a + 16 + so);
+            fa[u][0] = load16(ra, voff_a[0] + so);
+            fa[u][1] = load16(ra, voff_a[0] + 16 + so);
             sa[u] = __builtin_bit_cast(
                 int2_t, __builtin_amdgcn_raw_buffer_load_b64(rsa, lane * 8 + ss, 0, 0));
         }
@@ -427,7 +534,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_skinny_kernel(Mx4Gemm p) {
 #pragma unroll
             for (int j = 1; j < 4; ++j) {
                 if (j < nmb) {
-                    const uint32_t va = voff_a + (uint32_t)(j * 16 * p.lda) + so;
+                    const uint32_t va = voff_a[j] + so;
                     const int4_t a0 = load16(ra, va), a1 = load16(ra, va + 16);
                     const int s = sa[u][j >> 1];
                     if (j & 1) {
@@ -490,6 +597,64 @@ __global__ __launch_bounds__(NW * 64) void mx4_skinny_kernel(Mx4Gemm p) {
     }
 }
 
+// The gated product of a workgroup (64 columns: a wave has 32, one block, of its
+// 16 FM rows) rounded to the type, quantised and stored: what mx4_quantize makes
+// of it, without its way through memory.  Lane l holds columns 16 i + 4 (l / 16)
+// .. + 3 of row l % 16 of part j in out[i][j]; a row's block is in four lanes.
+template <typename Elt, int BM, int FM>
+__device__ __forceinline__ void mx4_store_quantized(const Mx4Gemm& p, const floatx4_t (&out)[2][FM],
+                                                    int64_t m0, int64_t n0, int rows, int wave_m,
+                                                    int wave_n, int lane, int4_t* smem) {
+    typedef typename Elt::scalar scalar;
+    constexpr int WTM = FM * 16;
+    // codes: 16 bytes per row of the wave; scales: two bytes (the waves' blocks) per
+    // row in the order of the scale tile, whose quarter they are
+    uint16_t* codes = reinterpret_cast<uint16_t*>(smem) + (wave_n * BM + wave_m * WTM) * 8;
+    uint8_t* scales = reinterpret_cast<uint8_t*>(smem) + 2 * BM * 16;
+    const int fr = lane & 15, fq = lane >> 4;
+    const int64_t block = n0 / 32 + wave_n;
+    const int nb = (p.N + 31) / 32;
+    const bool in = block < nb;
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const scalar lo = (scalar)out[c >> 1][j][2 * (c & 1)];
+            const scalar hi = (scalar)out[c >> 1][j][2 * (c & 1) + 1];
+            w[c] = __builtin_bit_cast(uint16_t, lo) |
+                   ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
+        }
+        uint32_t top = mx4_top(w[0], w[1], w[2], w[3]);
+        top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+        uint32_t q;
+        const int e = mx4_encode<Elt>(top, w[0], w[1], w[2], w[3], q);
+        codes[(j * 16 + fr) * 8 + fq] = (uint16_t)q;
+        codes[(j * 16 + fr) * 8 + 4 + fq] = (uint16_t)(q >> 16);
+        const int r = wave_m * WTM + j * 16 + fr;
+        if (fq == 0)
+            scales[(r >> 6) * 128 + fr * 8 + ((r >> 4) & 3) * 2 + wave_n] =
+                in && r < rows ? (uint8_t)e : 0;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (lane < WTM && wave_m * WTM + lane < rows && in)
+        *reinterpret_cast<int4_t*>(p.QO + (m0 + wave_m * WTM + lane) * p.ldqo + block * 16) =
+            reinterpret_cast<const int4_t*>(codes)[lane];
+    __syncthreads();
+    // 128 bytes a quarter; the last columns' workgroup also clears the quarters
+    // past them, whose blocks hold nothing
+    const int t = threadIdx.x;
+    const int g0 = (int)(n0 / 64) & 3;
+    const int quarters = n0 + 64 >= p.N ? 4 - g0 : 1;
+    const int st = t >> 7, g = (t >> 5) & 3;      // 64-row tile, quarter past g0
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(scales) + st * 32 + (t & 31);
+    if (st * 64 < min(rows, BM) && g < quarters) {
+        uint8_t* tile = p.SO + ((m0 / 64 + st) * p.nkto + n0 / 256) * kMx4Tile + (g0 + g) * 128;
+        reinterpret_cast<uint32_t*>(tile)[t & 31] = g == 0 ? *from : 0u;
+    }
+}
+
 // The tiled product: BM x BN outputs per workgroup, WM x WN waves of 16x16x128
 // MFMAs.  A stage holds the codes of BM + BN rows x 128 bytes and their scale
 // tiles, loaded straight into LDS; NS stages.  16-byte chunk 2 g + s of row r
@@ -503,7 +668,8 @@ __global__ __launch_bounds__(NW * 64) void mx4_skinny_kernel(Mx4Gemm p) {
 // second, so a lane holds both factors of its outputs; BN / 2 columns per
 // workgroup.  GROUPED: rows are a plan's, the expert's matrices are found from
 // the row tile.
-template <typename Elt, int BM, int BN, int WM, int WN, int NS, bool GROUPED, bool GATED>
+template <typename Elt, int BM, int BN, int WM, int WN, int NS, bool GROUPED, bool GATED,
+          bool QOUT = false>
 __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
     constexpr int NW = WM * WN;
     constexpr int WTM = BM / WM, WTN = BN / WN;
@@ -549,8 +715,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
     const int rows_b = (int)min((int64_t)BNO, (int64_t)p.N - n0);
     const uint32_t srow = (uint32_t)p.nkt * kMx4Tile;   // scale bytes of 64 rows
 
-    const __amdgpu_buffer_rsrc_t ra =
-        make_rsrc(p.A + m0 * p.lda, (uint32_t)((rows_a - 1) * p.lda + p.rowbytes));
+    const __amdgpu_buffer_rsrc_t ra = mx4_rows_rsrc(p, m0, rows_a);
     const __amdgpu_buffer_rsrc_t rb =
         make_rsrc(p.B + e * p.eqb + n0 * p.ldb, (uint32_t)((rows_b - 1) * p.ldb + p.rowbytes));
     const __amdgpu_buffer_rsrc_t rb2 =
@@ -568,7 +733,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
     for (int j = 0; j < A_DMA; ++j) {
         const int row = (wave * A_DMA + j) * 8 + (lane >> 3);
         const int pos = (lane & 7) ^ swz_pp(row);
-        voff_a[j] = (uint32_t)(row * p.lda) + ((pos & 3) * 2 + (pos >> 2)) * 16;
+        voff_a[j] = mx4_row_offset(p, m0, row, rows_a) + ((pos & 3) * 2 + (pos >> 2)) * 16;
     }
 #pragma unroll
     for (int j = 0; j < B_DMA; ++j) {
@@ -727,6 +892,10 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
 #pragma unroll
                 for (int d = 0; d < 4; ++d)
                     out[i][j][d] = silu_mul(acc[i][j][d], acc[i + FN / 2][j][d]);
+        if constexpr (QOUT) {
+            mx4_store_quantized<Elt, BM, FM>(p, out, m0, n0, rows_a, wave_m, wave_n, lane, smem);
+            return;
+        }
         gemm_epilogue<Elt, 16>(gp, out, mb, n0 + wave_n * (WTN / 2), lane, stage);
     } else {
         gemm_epilogue<Elt, 16>(gp, acc, mb, n0 + wave_n * WTN, lane, stage);
