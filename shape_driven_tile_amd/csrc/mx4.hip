@@ -101,22 +101,35 @@ int dequantize(int64_t rows, int64_t K, const void* Q, int64_t ldq, const void* 
 
 // ---- products -----------------------------------------------------------------------
 
+// Two workgroups a CU take the tiles in turn; one per tile on k-loops too short
+// for that (the loads would run more than a tile ahead).  row_tiles: of a plan,
+// as many as any choice of experts can give.
 template <typename Elt, int BM, int BN, int WM, int WN, int NS, bool GROUPED, bool GATED,
           bool QOUT = false>
-int launch_tile(Mx4Gemm p, int64_t row_tiles, void* stream) {
+int launch_tile(Mx4Gemm p, int64_t row_tiles, int num_cu, void* stream) {
     p.gm = (int)row_tiles;
     p.gn = (int)ceil_div(p.N, GATED ? BN / 2 : BN);
-    return launch(reinterpret_cast<const void*>(&mx4_gemm_kernel<Elt, BM, BN, WM, WN, NS, GROUPED, GATED, QOUT>),
-                  (int64_t)p.gm * p.gn, WM * WN * 64, p, stream);
+    const int64_t tiles = row_tiles * p.gn;
+    if (tiles > INT_MAX) return SDT_ERR_UNSUPPORTED;
+    const int64_t grid = p.nkt > NS || p.nkt == 0 ? std::min<int64_t>(tiles, 2 * num_cu) : tiles;
+    return launch(
+        reinterpret_cast<const void*>(&mx4_gemm_kernel<Elt, BM, BN, WM, WN, NS, GROUPED, GATED, QOUT>),
+        grid, WM * WN * 64, p, stream);
 }
 
-template <typename Elt, bool GROUPED, bool GATED>
-int launch_skinny(Mx4Gemm p, int64_t groups, void* stream) {
-    constexpr int NW = 4;
+// Waves that split the k-tiles: two where the workgroups outnumber the CUs (two of
+// them share one: 64 tokens of 32 experts, 50 -> 45 and 35 -> 28 us against four),
+// four where not (64 x 4096 x 4096, 64 workgroups: 7.5 us against 9.0 with two).
+template <typename Elt, bool GROUPED, bool GATED, bool QOUT = false>
+int launch_skinny(Mx4Gemm p, int64_t groups, int num_cu, void* stream) {
     p.gm = (int)groups;
-    p.gn = (int)ceil_div(p.N, 16);
-    return launch(reinterpret_cast<const void*>(&mx4_skinny_kernel<Elt, GROUPED, GATED, NW>),
-                  (int64_t)p.gm * p.gn, NW * 64, p, stream);
+    p.gn = (int)ceil_div(p.N, GATED ? 32 : 64);
+    const int64_t grid = (int64_t)p.gm * p.gn;
+    if (grid > num_cu)
+        return launch(reinterpret_cast<const void*>(&mx4_skinny_kernel<Elt, GROUPED, GATED, QOUT, 2>),
+                      grid, 2 * 64, p, stream);
+    return launch(reinterpret_cast<const void*>(&mx4_skinny_kernel<Elt, GROUPED, GATED, QOUT, 4>), grid,
+                  4 * 64, p, stream);
 }
 
 template <typename Elt>
@@ -146,7 +159,7 @@ int gemm(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void
     p.rowbytes = (int)row_bytes(K);
     p.nkt = (int)k_tiles(K);
     p.nxcd = dev.nxcd;
-    if (M <= 64) return launch_skinny<Elt, false, false>(p, 1, stream);
+    if (M <= 64) return launch_skinny<Elt, false, false>(p, 1, dev.num_cu, stream);
     if (ceil_div(M, 256) * ceil_div(N, 256) >= dev.num_cu / 2) {
         p.gm = (int)ceil_div(M, 256);
         p.gn = (int)ceil_div(N, 256);
@@ -154,8 +167,9 @@ int gemm(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void
                       p, stream);
     }
     if (ceil_div(M, 128) * ceil_div(N, 128) >= dev.num_cu / 2)
-        return launch_tile<Elt, 128, 128, 2, 2, 2, false, false>(p, ceil_div(M, 128), stream);
-    return launch_tile<Elt, 64, 64, 2, 2, 4, false, false>(p, ceil_div(M, 64), stream);
+        return launch_tile<Elt, 128, 128, 2, 2, 2, false, false>(p, ceil_div(M, 128), dev.num_cu,
+                                                                 stream);
+    return launch_tile<Elt, 64, 64, 2, 2, 4, false, false>(p, ceil_div(M, 64), dev.num_cu, stream);
 }
 
 template <typename Elt>
@@ -293,35 +307,28 @@ int64_t rows_per_expert(const sdt_moe_plan* plan) {
 }
 constexpr int64_t kSkinnyRows = 16;   // up to these the weights are streamed
 
-// What a grouped product takes and gives besides its matrices: A's rows by token
-// (gather; the A given then has one row per token) and a quantised output.
-struct MoeExtra {
-    bool gather = false;
-    uint8_t *qo = nullptr, *so = nullptr;
-    int64_t ldqo = 0;
-};
-
-template <typename Elt>
-int launch_grouped(Mx4Gemm p, const sdt_moe_plan* plan, int64_t rows, bool gated, bool quantized,
-                   void* stream) {
-    const int64_t groups = rows / 64;
-    const int64_t per = rows_per_expert(plan);
-    if (per <= kSkinnyRows)
-        return gated ? launch_skinny<Elt, true, true>(p, groups, stream)
-                     : launch_skinny<Elt, true, false>(p, groups, stream);
-    if (per <= 64)
-        return quantized ? launch_tile<Elt, 64, 128, 2, 2, 3, true, true, true>(p, groups, stream)
-               : gated   ? launch_tile<Elt, 64, 128, 2, 2, 3, true, true>(p, groups, stream)
-                         : launch_tile<Elt, 64, 128, 2, 2, 3, true, false>(p, groups, stream);
-    return quantized ? launch_tile<Elt, 128, 128, 2, 2, 2, true, true, true>(p, groups, stream)
-           : gated   ? launch_tile<Elt, 128, 128, 2, 2, 2, true, true>(p, groups, stream)
-                     : launch_tile<Elt, 128, 128, 2, 2, 2, true, false>(p, groups, stream);
+template <typename Elt, int BM, int BN, int NS>
+int launch_grouped_tile(const Mx4Gemm& p, const sdt_moe_plan* plan, bool gated, int num_cu,
+                        void* stream) {
+    // every expert's rows end inside a tile at most once
+    const int64_t R = plan->tokens * plan->topk;
+    const int64_t row_tiles = (R + (BM - 1) * std::min<int64_t>(plan->experts, R)) / BM;
+    if (p.QO) return launch_tile<Elt, BM, BN, 2, 2, NS, true, true, true>(p, row_tiles, num_cu, stream);
+    if (gated) return launch_tile<Elt, BM, BN, 2, 2, NS, true, true>(p, row_tiles, num_cu, stream);
+    return launch_tile<Elt, BM, BN, 2, 2, NS, true, false>(p, row_tiles, num_cu, stream);
 }
+
+// The gated product's quantised form, where its codes and scales are wanted.
+struct Mx4Out {
+    uint8_t* q;
+    uint8_t* s;
+    int64_t ldq;
+};
 
 template <typename Elt>
 int moe_gemm(const sdt_moe_plan* plan, int64_t N, int64_t K, const void* A, int64_t lda,
              const void* SA, const sdt_mx4_experts* B, const sdt_mx4_experts* up, void* C,
-             int64_t ldc, void* stream, const MoeExtra& x = {}) {
+             int64_t ldc, void* stream, const Mx4Out& out = {}) {
     int64_t rows;
     int rc = check_plan(plan, &rows);
     if (rc != SDT_OK) return rc;
@@ -329,7 +336,7 @@ int moe_gemm(const sdt_moe_plan* plan, int64_t N, int64_t K, const void* A, int6
     rc = check_experts(N, K, B);
     if (rc == SDT_OK && up) rc = check_experts(N, K, up);
     if (rc != SDT_OK || rows == 0 || N == 0) return rc;
-    if (!x.qo) rc = check_out(rows, N, C, ldc);
+    if (!out.q) rc = check_out(rows, N, C, ldc);
     if (rc == SDT_OK) rc = check_mx4(rows, K, A, lda, SA);
     if (rc != SDT_OK) return rc;
     if (N > INT_MAX) return SDT_ERR_UNSUPPORTED;
@@ -362,16 +369,18 @@ int moe_gemm(const sdt_moe_plan* plan, int64_t N, int64_t K, const void* A, int6
         p.eqb2 = up->q_expert;
         p.esb2 = up->s_expert;
     }
-    if (x.gather) {
-        p.slots = plan->rows;
-        p.topk = plan->topk;
-        p.abytes = (uint32_t)(plan->tokens * lda);
-    }
-    p.QO = x.qo;
-    p.SO = x.so;
-    p.ldqo = x.ldqo;
+    p.experts = plan->experts;
+    p.QO = out.q;
+    p.SO = out.s;
+    p.ldqo = out.ldq;
     p.nkto = (int)k_tiles(N);
-    return launch_grouped<Elt>(p, plan, rows, up != nullptr, x.qo != nullptr, stream);
+    const int64_t per = rows_per_expert(plan);
+    if (per <= kSkinnyRows)
+        return p.QO ? launch_skinny<Elt, true, true, true>(p, rows / 64, dev.num_cu, stream)
+               : up ? launch_skinny<Elt, true, true>(p, rows / 64, dev.num_cu, stream)
+                    : launch_skinny<Elt, true, false>(p, rows / 64, dev.num_cu, stream);
+    return per <= 64 ? launch_grouped_tile<Elt, 64, 128, 3>(p, plan, up, dev.num_cu, stream)
+                     : launch_grouped_tile<Elt, 128, 128, 2>(p, plan, up, dev.num_cu, stream);
 }
 
 template <typename Elt>
@@ -389,7 +398,7 @@ int quantize_tokens(const sdt_moe_plan* plan, int64_t K, const void* X, int64_t 
     p.K = (int)K;
     p.nkt = (int)k_tiles(K);
     return launch(reinterpret_cast<const void*>(&mx4_quantize_tokens_kernel<Elt>),
-                  ceil_div(p.tokens, 64) * p.nkt, 256, p, stream);
+                  ceil_div(p.tokens, 16) * p.nkt, 256, p, stream);
 }
 
 template <typename S>
@@ -422,8 +431,8 @@ int combine(const sdt_moe_plan* plan, int64_t N, const void* D, int64_t ldd, con
 
 // The layer's buffers, one after another, each from a multiple of 256 bytes.
 struct LayerLayout {
-    int64_t xq, xs, h, hq, hs, d, bytes;
-    int64_t ldx, ldh, ldhq, ldd;   // bytes, elements, bytes, elements
+    int64_t xq, xs, hq, hs, d, bytes;
+    int64_t ldx, ldhq, ldd;   // bytes, bytes, elements
 };
 LayerLayout layer_layout(int64_t rows, int64_t N, int64_t K) {
     LayerLayout l;
@@ -435,11 +444,9 @@ LayerLayout layer_layout(int64_t rows, int64_t N, int64_t K) {
     };
     l.ldx = row_bytes(K);
     l.ldhq = row_bytes(N);
-    l.ldh = ceil_div(N, 8) * 8;
     l.ldd = ceil_div(K, 8) * 8;
     l.xq = take(rows * l.ldx);
     l.xs = take(sdt_mx4_scale_bytes(rows, K));
-    l.h = take(rows * l.ldh * 2);
     l.hq = take(rows * l.ldhq);
     l.hs = take(sdt_mx4_scale_bytes(rows, N));
     l.d = take(rows * l.ldd * 2);
@@ -477,26 +484,15 @@ int moe_layer(const sdt_moe_layer* layer, const int32_t* idx, const float* weigh
     uint8_t* w = static_cast<uint8_t*>(workspace);
     rc = moe_plan(idx, plan, stream);
     if (rc != SDT_OK || K == 0) return rc;
-    // The tokens are quantised once each and the first product gathers their rows,
-    // while 32-bit offsets reach them all; with many rows an expert the gated
-    // product comes out quantised.
-    MoeExtra x;
-    x.gather = T * l.ldx <= (int64_t)kNoRow;
-    rc = x.gather ? quantize_tokens<Elt>(plan, K, X, ldx, w + l.xq, l.ldx, w + l.xs, stream)
-                  : quantize<Elt>(rows, K, X, T, ldx, plan->rows, plan->topk, w + l.xq, l.ldx,
-                                  w + l.xs, stream);
-    const bool fused = N > 0 && rows_per_expert(plan) > kSkinnyRows;
-    if (fused) {
-        x.qo = w + l.hq;
-        x.so = w + l.hs;
-        x.ldqo = l.ldhq;
-    }
+    // Every token is read and quantised once; the gated product comes out quantised.
+    rc = plan->topk <= kMaxTopk
+             ? quantize_tokens<Elt>(plan, K, X, ldx, w + l.xq, l.ldx, w + l.xs, stream)
+             : quantize<Elt>(rows, K, X, T, ldx, plan->rows, plan->topk, w + l.xq, l.ldx, w + l.xs,
+                             stream);
+    const Mx4Out hq = {w + l.hq, w + l.hs, l.ldhq};
     if (rc == SDT_OK)
-        rc = moe_gemm<Elt>(plan, N, K, w + l.xq, l.ldx, w + l.xs, &layer->gate, &layer->up, w + l.h,
-                           l.ldh, stream, x);
-    if (rc == SDT_OK && !fused)
-        rc = quantize<Elt>(rows, N, w + l.h, rows, l.ldh, plan->rows, 0, w + l.hq, l.ldhq, w + l.hs,
-                           stream);
+        rc = moe_gemm<Elt>(plan, N, K, w + l.xq, l.ldx, w + l.xs, &layer->gate, &layer->up, nullptr, 0,
+                           stream, hq);
     if (rc == SDT_OK)
         rc = moe_gemm<Elt>(plan, K, N, w + l.hq, l.ldhq, w + l.hs, &layer->down, nullptr, w + l.d,
                            l.ldd, stream);

@@ -182,8 +182,11 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(Mx4Quant p) {
         v[i] = uint4_t{0, 0, 0, 0};
         if (ok) v[i] = mx4_load8(p.X + src * p.ldx + k, valid);
     }
+    if (t < kMx4Tile / 4) reinterpret_cast<uint32_t*>(sm)[t] = 0;
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+        if (rt * 64 + 8 * i >= p.rows) break;
         const int r = (t >> 5) + 8 * i;
         uint32_t top = mx4_top(v[i][0], v[i][1], v[i][2], v[i][3]);
         top = max(top, (uint32_t)__shfl_xor((int)top, 1));
@@ -214,29 +217,33 @@ struct Mx4QuantTokens {
     int topk, K, nkt;
 };
 
-// The layer's tokens, each quantised once: codes by token (the products gather
-// their rows), scales to the tiles of every plan row of the token, two bytes per
-// pair of blocks.  Rounded once per token instead of topk times: 4096 tokens of
-// 2048, 6 experts each, 22 -> 9 us against quantising the plan's rows.
+// The layer's tokens, each read and quantised once; codes and scales go to every
+// plan row of the token.  Bound by the writes of the rows' codes; 16 tokens x 256 a
+// workgroup, so that a decode batch also fills the CUs.
 template <typename Elt>
 __global__ __launch_bounds__(256) void mx4_quantize_tokens_kernel(Mx4QuantTokens p) {
-    __shared__ uint16_t sm[64 * 4];        // scale bytes of 64 tokens, by pairs of blocks
+    __shared__ uint16_t sm[16 * 4];        // scale bytes of 16 tokens, by pairs of blocks
+    __shared__ int32_t to[16 * 64];        // plan rows of their slots (topk <= 64)
     const int t = threadIdx.x;
-    const int64_t rt = blockIdx.x / p.nkt;
-    const int kt = blockIdx.x - (int)(rt * p.nkt);
+    const int64_t t0 = blockIdx.x / p.nkt;
+    const int kt = blockIdx.x - (int)(t0 * p.nkt);
+    const int64_t first = t0 * 16;
     const int l32 = t & 31;
     const int k = kt * 256 + l32 * 8;
     const int nb = (p.K + 31) / 32;
     const int valid = p.K - k;
-    uint4_t v[8];
+    uint4_t v[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t row = rt * 64 + (t >> 5) + 8 * i;
+    for (int i = 0; i < 2; ++i) {
+        const int64_t row = first + (t >> 5) + 8 * i;
         v[i] = uint4_t{0, 0, 0, 0};
         if (row < p.tokens) v[i] = mx4_load8(p.X + row * p.ldx + k, valid);
     }
+    const int slots = (int)min((int64_t)16, p.tokens - first) * p.topk;
+    for (int i = t; i < slots; i += 256) to[i] = p.pos[first * p.topk + i];
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 2; ++i) {
         const int r = (t >> 5) + 8 * i;
         uint32_t top = mx4_top(v[i][0], v[i][1], v[i][2], v[i][3]);
         top = max(top, (uint32_t)__shfl_xor((int)top, 1));
@@ -244,17 +251,20 @@ __global__ __launch_bounds__(256) void mx4_quantize_tokens_kernel(Mx4QuantTokens
         uint32_t q;
         const int e = mx4_encode<Elt>(top, v[i][0], v[i][1], v[i][2], v[i][3], q);
         const int b = l32 >> 2;
-        const int64_t row = rt * 64 + r;
         const bool in = kt * 8 + b < nb;
-        if (in && row < p.tokens)
-            *reinterpret_cast<uint32_t*>(p.Q + row * p.ldq + kt * 128 + l32 * 4) = q;
         if ((l32 & 3) == 0) reinterpret_cast<uint8_t*>(sm)[r * 8 + b] = in ? (uint8_t)e : 0;
+        if (in && first + r < p.tokens) {
+            uint8_t* q0 = p.Q + kt * 128 + l32 * 4;
+            for (int j = 0; j < p.topk; ++j) {
+                const int64_t at = to[r * p.topk + j];
+                if (at >= 0) *reinterpret_cast<uint32_t*>(q0 + at * p.ldq) = q;
+            }
+        }
     }
     __syncthreads();
-    const int slots = (int)min((int64_t)64, p.tokens - rt * 64) * p.topk;
     for (int i = t; i < slots * 4; i += 256) {
         const int slot = i >> 2, g = i & 3;
-        const int row = p.pos[rt * 64 * p.topk + slot];
+        const int row = to[slot];
         if (row < 0) continue;
         uint8_t* tile = p.S + ((int64_t)(row >> 6) * p.nkt + kt) * kMx4Tile;
         *reinterpret_cast<uint16_t*>(tile + mx4_scale_offset(row & 63, 2 * g)) =
@@ -371,31 +381,18 @@ struct Mx4Gemm {
     int gm, gn, nxcd;              // output tiles (grouped: gm 64-row tiles of the plan)
     // grouped products: the plan, and the experts' strides in bytes
     const int32_t *tiles, *offsets, *counts;
+    int experts;
     int64_t eqb, esb, eqb2, esb2;
-    // rows of A by token: row p of the plan is A's row slots[p] / topk (nullptr: p)
-    const int32_t* slots;
-    int topk;
-    uint32_t abytes;               // of all of A's rows, at most kNoRow
     // gated product quantised (QOUT): codes, scales and their k-tiles
     uint8_t *QO, *SO;
     int64_t ldqo;
     int nkto;
 };
 
-// A row offset that lies past every descriptor, with any k offset added.
-constexpr uint32_t kNoRow = 0x40000000u;
-
-// Byte offset of row `row` (of `rows`) of a workgroup whose first is m0.
-__device__ __forceinline__ uint32_t mx4_row_offset(const Mx4Gemm& p, int64_t m0, int row, int rows) {
-    if (p.slots == nullptr) return (uint32_t)(row * p.lda);
-    if (row >= rows) return kNoRow;
-    return (uint32_t)(p.slots[m0 + row] / p.topk) * (uint32_t)p.lda;
-}
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t mx4_rows_rsrc(const Mx4Gemm& p, int64_t m0,
-                                                                int rows) {
-    return p.slots == nullptr
-               ? make_rsrc(p.A + m0 * p.lda, (uint32_t)((rows - 1) * p.lda + p.rowbytes))
-               : make_rsrc(p.A, p.abytes);
+// A value that no work of this kernel writes, from a uniform address, by a scalar load.
+__device__ __forceinline__ int uniform_load(const int32_t* p) {
+    return *reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(
+        reinterpret_cast<uint64_t>(p));
 }
 
 // acc += B_frag . A_frag^T over one 128-deep half; BYTE_A, BYTE_B pick the
@@ -414,260 +411,415 @@ __device__ __forceinline__ floatx4_t mx4_mfma_part(int4_t b, int4_t a, floatx4_t
     return mx4_mfma<2 * (PB & 1) + S, 2 * (PA & 1) + S>(b, a, c, sb, sa);
 }
 
-// silu(g) * u of the gated product, in fp32.  The empty asm keeps the product an
-// fp32 value: left to itself the compiler rounds s * u straight to fp16 in some
-// kernels and not in others, and the layer's results would depend on which ran.
+// silu(g) * u = g / (1 + exp(-g)) * u of the gated product, in fp32: 2^t by the
+// hardware instruction (one step off), t = -g log2(e) in two parts so that the
+// rounding of t does not grow with g, and the hardware reciprocal (one step off).
+// Limited to +-88, where 2^t is still finite and 1 / (1 + 2^t) already below the
+// normal numbers.  The library's expf and division took 3 us of a
+// 128 x 64 tile's 11.  The empty asm keeps the product an fp32 value: left to
+// itself the compiler rounds s * u straight to fp16 in some kernels and not in
+// others, and the layer's results would depend on which ran.
 __device__ __forceinline__ float silu_mul(float g, float u) {
-    const float s = g / (1.0f + expf(-g));
+    constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147182f;
+    const float x = -__builtin_amdgcn_fmed3f(g, -88.0f, 88.0f);
+    const float t = x * kLog2e;
+    const float low = __builtin_fmaf(x, kLog2e, -t) + x * kLog2eLow;
+    const float z = __builtin_amdgcn_exp2f(t);
+    const float ez = __builtin_fmaf(z * kLn2, low, z);
+    const float s = g * __builtin_amdgcn_rcpf(1.0f + ez);
     float r = s * u;
     asm("" : "+v"(r));
     return r;
 }
 
-// Rows and expert of 64-row tile `g` of a plan for tiles of BM rows: false
-// where a tile of BM rows does not start there.
-__device__ __forceinline__ bool mx4_group(const Mx4Gemm& p, int g, int bm64, int& e, int64_t& m0,
-                                          int& rows) {
-    e = __builtin_amdgcn_readfirstlane(p.tiles[g]);
+// Expert, first row and rows of 64-row tile `g` of a plan; false where it has none.
+__device__ __forceinline__ bool mx4_group(const Mx4Gemm& p, int g, int& e, int64_t& m0, int& rows) {
+    e = uniform_load(p.tiles + g);
     if (e < 0) return false;
-    const int first = p.offsets[e];
-    if (((g - first / 64) % bm64) != 0) return false;
     m0 = (int64_t)g * 64;
-    rows = __builtin_amdgcn_readfirstlane(first + p.counts[e] - g * 64);
+    rows = min(uniform_load(p.offsets + e) + uniform_load(p.counts + e) - g * 64, 64);
     return rows > 0;
 }
 
-// The few-row product: 16 columns of C per workgroup, whose NW waves split the
-// k-tiles (w, w + NW, ...) and read B straight from memory, each code once;
-// up to 64 rows of A (four 16-row parts, skipped where there are no rows).
-// The waves' partial sums are added in wave order through LDS.  Bound by the
-// stream of B: 16 loads of 1 KB are in flight per wave pair, and the many small
-// workgroups keep every CU loading.
-template <typename Elt, bool GROUPED, bool GATED, int NW>
-__global__ __launch_bounds__(NW * 64) void mx4_skinny_kernel(Mx4Gemm p) {
+// Two values rounded to the type, packed.
+template <typename Elt>
+__device__ __forceinline__ uint32_t mx4_pack2(float a, float b) {
     typedef typename Elt::scalar scalar;
-    constexpr int U = 2;                     // k-tiles loaded together
-    __shared__ floatx4_t red[(GATED ? 2 : 1) * NW * 4 * 64];
+    const scalar lo = (scalar)a, hi = (scalar)b;
+    return __builtin_bit_cast(uint16_t, lo) | ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
+}
+
+// The few-row product: BN columns of C (gated: of each matrix) and up to 64 rows
+// per workgroup, whose NW waves split the k-tiles (w, w + NW, ...) and stream B
+// once.  Bound by that stream.  Every wave has LDS of its own, so the loop has no
+// barrier: rows come straight into it, eight lanes to a row's 128 bytes, several
+// k-tiles in flight, and are read from there as fragments.  (Loaded as fragments,
+// a lane to a row, each instruction touches 64 lines: 5.8 bytes a clock and CU,
+// a third of what memory gives.)  Few rows (NMB = 1: 16) leave the LDS to more
+// stages.  The waves' partial sums are added in wave order.
+constexpr int kSkinnyWaveLds = 35 * 1024;
+
+template <typename Elt, bool GROUPED, bool GATED, bool QOUT, int NW, int NMB>
+__device__ __forceinline__ void mx4_skinny_body(const Mx4Gemm& p, char* smem, int e, int64_t m0,
+                                                int n0, int rows) {
+    typedef typename Elt::scalar scalar;
+    constexpr int MATS = GATED ? 2 : 1;
+    constexpr int BN = 64 / MATS;
+    constexpr int PB = BN / 16;                   // 16-column parts of a matrix
+    constexpr int B_BYTES = BN * 128, A_BYTES = NMB * 16 * 128;
+    constexpr int STAGE = MATS * (B_BYTES + kMx4Tile) + A_BYTES + kMx4Tile;
+    constexpr int NS = kSkinnyWaveLds / STAGE >= 3 ? 3 : 2;
+    constexpr int L = MATS * (B_BYTES / 1024 + 1) + A_BYTES / 1024 + 1;
+    static_assert(NS * STAGE <= kSkinnyWaveLds, "a wave's stages");
+    static_assert(MATS * PB * NMB * 1024 <= kSkinnyWaveLds, "a wave's sums");
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l = xcd_remap(blockIdx.x, gridDim.x, p.nxcd);
-    const int g = l / p.gn, nt = l - g * p.gn;
-    int e = 0, rows;
-    int64_t m0;
-    if constexpr (GROUPED) {
-        if (!mx4_group(p, g, 1, e, m0, rows)) return;
-        rows = min(rows, 64);
-    } else {
-        m0 = (int64_t)g * 64;
-        rows = (int)min((int64_t)64, p.M - m0);
-    }
-    const int nmb = (rows + 15) >> 4;
-    const int n0 = nt * 16;
     const int fr = lane & 15, fq = lane >> 4;
+    const int rows_b = min(BN, p.N - n0);
+    const uint32_t srow = (uint32_t)p.nkt * kMx4Tile;
 
-    const int rows_b = min(16, p.N - n0);
-    const uint32_t sbytes_b = (uint32_t)p.nkt * kMx4Tile;
-    const __amdgpu_buffer_rsrc_t ra = mx4_rows_rsrc(p, m0, rows);
-    const __amdgpu_buffer_rsrc_t rsa = make_rsrc(p.SA + (m0 / 64) * sbytes_b, sbytes_b);
-    const __amdgpu_buffer_rsrc_t rb =
-        make_rsrc(p.B + e * p.eqb + (int64_t)n0 * p.ldb, (uint32_t)((rows_b - 1) * p.ldb + p.rowbytes));
-    const __amdgpu_buffer_rsrc_t rsb =
-        make_rsrc(p.SB + e * p.esb + (int64_t)(n0 / 64) * sbytes_b, sbytes_b);
-    const __amdgpu_buffer_rsrc_t rb2 = make_rsrc(
-        GATED ? p.B2 + e * p.eqb2 + (int64_t)n0 * p.ldb2 : p.B,
-        GATED ? (uint32_t)((rows_b - 1) * p.ldb2 + p.rowbytes) : 0u);
-    const __amdgpu_buffer_rsrc_t rsb2 = make_rsrc(
-        GATED ? p.SB2 + e * p.esb2 + (int64_t)(n0 / 64) * sbytes_b : p.SB, GATED ? sbytes_b : 0u);
-
-    uint32_t voff_a[4];
+    __amdgpu_buffer_rsrc_t rb[MATS], rsb[MATS];
+    uint32_t voff_b[MATS][B_BYTES / 1024], voff_a[A_BYTES / 1024];
+    const int pos = (lane & 7) ^ swz_pp(lane >> 3);   // chunk of the k-tile at this place
+    const uint32_t chunk = ((pos & 3) * 2 + (pos >> 2)) * 16;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) voff_a[j] = mx4_row_offset(p, m0, j * 16 + fr, rows) + fq * 32;
-    const uint32_t voff_b = (uint32_t)(fr * p.ldb) + fq * 32;
-    const uint32_t voff_b2 = GATED ? (uint32_t)(fr * p.ldb2) + fq * 32 : 0u;
-    const uint32_t voff_sb = lane * 8 + ((n0 >> 4) & 3) * 2;
-
-    floatx4_t acc[4], acc2[4];
+    for (int m = 0; m < MATS; ++m) {
+        const uint8_t* q = m == 0 ? p.B + e * p.eqb : p.B2 + e * p.eqb2;
+        const uint8_t* sc = m == 0 ? p.SB + e * p.esb : p.SB2 + e * p.esb2;
+        const int64_t ld = m == 0 ? p.ldb : p.ldb2;
+        rb[m] = make_rsrc(q + (int64_t)n0 * ld, (uint32_t)((rows_b - 1) * ld + p.rowbytes));
+        rsb[m] = make_rsrc(sc + (int64_t)(n0 / 64) * srow, srow);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        acc[j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-        acc2[j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < B_BYTES / 1024; ++j)
+            voff_b[m][j] = (uint32_t)((j * 8 + (lane >> 3)) * ld) + chunk;
     }
-    // The k offset goes into the lane offset, which the descriptor's range check
-    // covers: the last row's bytes past its blocks are not read.
-    auto load16 = [](__amdgpu_buffer_rsrc_t r, uint32_t off) {
-        return __builtin_bit_cast(int4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-    };
-    for (int kt0 = wave; kt0 < p.nkt; kt0 += NW * U) {
-        int4_t fb[U][2], fb2[U][2], fa[U][2];
-        int sb[U], sb2[U];
-        int2_t sa[U];
+    const __amdgpu_buffer_rsrc_t ra =
+        make_rsrc(p.A + m0 * p.lda, (uint32_t)((rows - 1) * p.lda + p.rowbytes));
+    const __amdgpu_buffer_rsrc_t rsa = make_rsrc(p.SA + (m0 / 64) * srow, srow);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int kt = kt0 + u * NW;
-            // past the last k-tile: an offset past every descriptor, read as zero
-            const bool in = kt < p.nkt;
-            const uint32_t so = in ? (uint32_t)kt * 128 : 0x40000000u;
-            const uint32_t ss = in ? (uint32_t)kt * kMx4Tile : 0x40000000u;
-            fb[u][0] = load16(rb, voff_b + so);
-            fb[u][1] = load16(rb, voff_b + 16 + so);
-            sb[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsb, voff_sb + ss, 0, 0);
-            if constexpr (GATED) {
-                fb2[u][0] = load16(rb2, voff_b2 + so);
-                fb2[u][1] = load16(rb2, voff_b2 + 16 + so);
-                sb2[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsb2, voff_sb + ss, 0, 0);
-            }
-            fa[u][0] = load16(ra, voff_a[0] + so);
-            fa[u][1] = load16(ra, voff_a[0] + 16 + so);
-            sa[u] = __builtin_bit_cast(
-                int2_t, __builtin_amdgcn_raw_buffer_load_b64(rsa, lane * 8 + ss, 0, 0));
+    for (int j = 0; j < A_BYTES / 1024; ++j)
+        voff_a[j] = (uint32_t)((j * 8 + (lane >> 3)) * p.lda) + chunk;
+
+    char* const mine = smem + wave * kSkinnyWaveLds;
+    auto load = [&](int kt, int stage) {
+        int4_t* at = reinterpret_cast<int4_t*>(mine + stage * STAGE);
+        // in the lane offset, which the descriptor's range check covers
+        const uint32_t koff = (uint32_t)kt * 128;
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) {
+#pragma unroll
+            for (int j = 0; j < B_BYTES / 1024; ++j) dma16(rb[m], at + j * 64, voff_b[m][j] + koff, 0);
+            at += B_BYTES / 16;
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int kt = kt0 + u * NW;
-            const uint32_t so = kt < p.nkt ? (uint32_t)kt * 128 : 0x40000000u;
-            acc[0] = mx4_mfma<0, 0>(fb[u][0], fa[u][0], acc[0], sb[u], sa[u][0]);
-            acc[0] = mx4_mfma<1, 1>(fb[u][1], fa[u][1], acc[0], sb[u], sa[u][0]);
-            if constexpr (GATED) {
-                acc2[0] = mx4_mfma<0, 0>(fb2[u][0], fa[u][0], acc2[0], sb2[u], sa[u][0]);
-                acc2[0] = mx4_mfma<1, 1>(fb2[u][1], fa[u][1], acc2[0], sb2[u], sa[u][0]);
-            }
+        for (int j = 0; j < A_BYTES / 1024; ++j) dma16(ra, at + j * 64, voff_a[j] + koff, 0);
+        at += A_BYTES / 16;
+        if (lane < 32) {
 #pragma unroll
-            for (int j = 1; j < 4; ++j) {
-                if (j < nmb) {
-                    const uint32_t va = voff_a[j] + so;
-                    const int4_t a0 = load16(ra, va), a1 = load16(ra, va + 16);
-                    const int s = sa[u][j >> 1];
-                    if (j & 1) {
-                        acc[j] = mx4_mfma<0, 2>(fb[u][0], a0, acc[j], sb[u], s);
-                        acc[j] = mx4_mfma<1, 3>(fb[u][1], a1, acc[j], sb[u], s);
-                        if constexpr (GATED) {
-                            acc2[j] = mx4_mfma<0, 2>(fb2[u][0], a0, acc2[j], sb2[u], s);
-                            acc2[j] = mx4_mfma<1, 3>(fb2[u][1], a1, acc2[j], sb2[u], s);
-                        }
-                    } else {
-                        acc[j] = mx4_mfma<0, 0>(fb[u][0], a0, acc[j], sb[u], s);
-                        acc[j] = mx4_mfma<1, 1>(fb[u][1], a1, acc[j], sb[u], s);
-                        if constexpr (GATED) {
-                            acc2[j] = mx4_mfma<0, 0>(fb2[u][0], a0, acc2[j], sb2[u], s);
-                            acc2[j] = mx4_mfma<1, 1>(fb2[u][1], a1, acc2[j], sb2[u], s);
-                        }
+            for (int m = 0; m < MATS; ++m) dma16(rsb[m], at + m * 32, lane * 16, kt * kMx4Tile);
+            dma16(rsa, at + MATS * 32, lane * 16, kt * kMx4Tile);
+        }
+    };
+
+    floatx4_t acc[MATS][PB][NMB];
+#pragma unroll
+    for (int m = 0; m < MATS; ++m)
+#pragma unroll
+        for (int i = 0; i < PB; ++i)
+#pragma unroll
+            for (int j = 0; j < NMB; ++j) acc[m][i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+
+    const int n = (p.nkt - wave + NW - 1) / NW;   // this wave's k-tiles (0 or less: none)
+    const int fsw = swz_pp(fr);
+    for (int j = 0; j < min(n, NS); ++j) load(wave + j * NW, j);
+    int stage = 0;
+    for (int j = 0; j < n; ++j) {
+        const int younger = min(n - 1 - j, NS - 1);   // k-tiles that may stay in flight
+        if (NS > 2 && younger == 2)
+            wait_global_loads<NS == 3 ? 2 * L : 0>();
+        else if (younger == 1)
+            wait_global_loads<L>();
+        else
+            wait_global_loads<0>();
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+        const int4_t* at = reinterpret_cast<const int4_t*>(mine + stage * STAGE);
+        int4_t fb[MATS][2][PB], fa[2][NMB];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int c = (4 * s + fq) ^ fsw;
+#pragma unroll
+            for (int m = 0; m < MATS; ++m)
+#pragma unroll
+                for (int i = 0; i < PB; ++i)
+                    fb[m][s][i] = at[m * (B_BYTES / 16) + (i * 16 + fr) * 8 + c];
+#pragma unroll
+            for (int i = 0; i < NMB; ++i)
+                fa[s][i] = at[MATS * (B_BYTES / 16) + (i * 16 + fr) * 8 + c];
+        }
+        const int2_t* sc = reinterpret_cast<const int2_t*>(at + (MATS * B_BYTES + A_BYTES) / 16);
+        int2_t sb[MATS];
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) sb[m] = sc[m * 64 + lane];
+        const int2_t sa = sc[MATS * 64 + lane];
+        // BN = 32: the columns are one half of the scale tile, a dword of the lane's two
+        if constexpr (BN == 32) {
+#pragma unroll
+            for (int m = 0; m < MATS; ++m) sb[m][0] = (n0 & 32) ? sb[m][1] : sb[m][0];
+        }
+        wait_lds();
+        __builtin_amdgcn_sched_barrier(0);
+        if (j + NS < n) load(wave + (j + NS) * NW, stage);
+        auto half = [&](auto which) {
+            constexpr int S = decltype(which)::value;
+#pragma unroll
+            for (int m = 0; m < MATS; ++m)
+#pragma unroll
+                for (int i = 0; i < PB; i += 2) {
+                    const int b = sb[m][i >> 1];
+                    acc[m][i][0] = mx4_mfma_part<S, 0, 0>(fb[m][S][i], fa[S][0], acc[m][i][0], b, sa[0]);
+                    acc[m][i + 1][0] =
+                        mx4_mfma_part<S, 1, 0>(fb[m][S][i + 1], fa[S][0], acc[m][i + 1][0], b, sa[0]);
+                    if constexpr (NMB == 4) {
+                        acc[m][i][1] =
+                            mx4_mfma_part<S, 0, 1>(fb[m][S][i], fa[S][1], acc[m][i][1], b, sa[0]);
+                        acc[m][i + 1][1] = mx4_mfma_part<S, 1, 1>(fb[m][S][i + 1], fa[S][1],
+                                                                  acc[m][i + 1][1], b, sa[0]);
+                        acc[m][i][2] =
+                            mx4_mfma_part<S, 0, 0>(fb[m][S][i], fa[S][2], acc[m][i][2], b, sa[1]);
+                        acc[m][i + 1][2] = mx4_mfma_part<S, 1, 0>(fb[m][S][i + 1], fa[S][2],
+                                                                  acc[m][i + 1][2], b, sa[1]);
+                        acc[m][i][3] =
+                            mx4_mfma_part<S, 0, 1>(fb[m][S][i], fa[S][3], acc[m][i][3], b, sa[1]);
+                        acc[m][i + 1][3] = mx4_mfma_part<S, 1, 1>(fb[m][S][i + 1], fa[S][3],
+                                                                  acc[m][i + 1][3], b, sa[1]);
                     }
+                }
+        };
+        half(std::integral_constant<int, 0>{});
+        half(std::integral_constant<int, 1>{});
+        stage = stage + 1 == NS ? 0 : stage + 1;
+    }
+
+    // Every wave's sums to its own LDS, then wave j adds row part j (and its columns'
+    // parts) in wave order.
+    floatx4_t* red = reinterpret_cast<floatx4_t*>(mine);
+#pragma unroll
+    for (int m = 0; m < MATS; ++m)
+#pragma unroll
+        for (int i = 0; i < PB; ++i)
+#pragma unroll
+            for (int j = 0; j < NMB; ++j) red[((m * PB + i) * NMB + j) * 64 + lane] = acc[m][i][j];
+    __syncthreads();
+    auto total = [&](int m, int i, int j) {
+        const char* at = smem + (((m * PB + i) * NMB + j) * 64 + lane) * 16;
+        floatx4_t s = *reinterpret_cast<const floatx4_t*>(at);
+#pragma unroll
+        for (int w = 1; w < NW; ++w)
+            s += *reinterpret_cast<const floatx4_t*>(at + w * kSkinnyWaveLds);
+        return s;
+    };
+    auto output = [&](int i, int j) {             // part (i, j): row fr, columns 4 fq .. + 3
+        floatx4_t s = total(0, i, j);
+        if constexpr (GATED) {
+            const floatx4_t u = total(1, i, j);
+#pragma unroll
+            for (int d = 0; d < 4; ++d) s[d] = silu_mul(s[d], u[d]);
+        }
+        return s;
+    };
+    if constexpr (QOUT) {
+        for (int j = wave; j < NMB; j += NW) {
+            const int r = j * 16 + fr;
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const floatx4_t s = output(i, j);
+                w[2 * i] = mx4_pack2<Elt>(s[0], s[1]);
+                w[2 * i + 1] = mx4_pack2<Elt>(s[2], s[3]);
+            }
+            uint32_t top = mx4_top(w[0], w[1], w[2], w[3]);
+            top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+            top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+            uint32_t q;
+            const int ex = mx4_encode<Elt>(top, w[0], w[1], w[2], w[3], q);
+            if (r >= rows) continue;
+            const int block = n0 / 32, nb = (p.N + 31) / 32;
+            uint16_t* to = reinterpret_cast<uint16_t*>(p.QO + (m0 + r) * p.ldqo + block * 16);
+            to[fq] = (uint16_t)q;
+            to[4 + fq] = (uint16_t)(q >> 16);
+            uint8_t* tile = p.SO + (m0 / 64 * p.nkto + block / 8) * kMx4Tile;
+            if (fq == 0) tile[mx4_scale_offset(r, block & 7)] = (uint8_t)ex;
+            // the last block's workgroup clears those past it, which hold nothing
+            if (fq == 1 && block == nb - 1)
+                for (int x = block + 1; x & 7; ++x) tile[mx4_scale_offset(r, x & 7)] = 0;
+        }
+    } else {
+        for (int u = wave; u < PB * NMB; u += NW) {
+            const int i = u / NMB, j = u - i * NMB;
+            const floatx4_t s = output(i, j);
+            const int m = j * 16 + fr;
+            if (m >= rows) continue;
+            const int c0 = n0 + i * 16 + fq * 4;
+            uint16_t* c = p.C + (m0 + m) * p.ldc + c0;
+            if (c0 + 3 < p.N) {
+                *reinterpret_cast<uint2_t*>(c) =
+                    uint2_t{mx4_pack2<Elt>(s[0], s[1]), mx4_pack2<Elt>(s[2], s[3])};
+            } else {
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const scalar v = (scalar)s[d];
+                    if (c0 + d < p.N) c[d] = __builtin_bit_cast(uint16_t, v);
                 }
             }
         }
     }
-    // Part j of every wave to LDS, then wave j adds part j in wave order.
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (j < nmb) {
-            red[(wave * 4 + j) * 64 + lane] = acc[j];
-            if constexpr (GATED) red[((NW + wave) * 4 + j) * 64 + lane] = acc2[j];
-        }
+}
+
+template <typename Elt, bool GROUPED, bool GATED, bool QOUT, int NW>
+__global__ __launch_bounds__(NW * 64) void mx4_skinny_kernel(Mx4Gemm p) {
+    __shared__ int4_t smem[NW * kSkinnyWaveLds / 16];
+    const int l = xcd_remap(blockIdx.x, gridDim.x, p.nxcd);
+    const int g = l / p.gn, nt = l - g * p.gn;
+    const int n0 = nt * (GATED ? 32 : 64);
+    int e = 0, rows;
+    int64_t m0;
+    if constexpr (GROUPED) {
+        if (!mx4_group(p, g, e, m0, rows)) return;
+    } else {
+        m0 = (int64_t)g * 64;
+        rows = (int)min((int64_t)64, p.M - m0);
     }
-    __syncthreads();
-    for (int j = wave; j < nmb; j += NW) {
-        floatx4_t s = red[j * 64 + lane];
+    char* const lds = reinterpret_cast<char*>(smem);
+    if (rows <= 16)
+        mx4_skinny_body<Elt, GROUPED, GATED, QOUT, NW, 1>(p, lds, e, m0, n0, rows);
+    else
+        mx4_skinny_body<Elt, GROUPED, GATED, QOUT, NW, 4>(p, lds, e, m0, n0, rows);
+}
+
+// ---- epilogues in registers ------------------------------------------------------------
+// Lane l holds, of the 16 x 16 part (i, j) of a wave's outputs, row l % 16 and
+// columns 4 (l / 16) .. + 3.  Lanes of different quarters swap registers
+// (v_permlane16_swap: rows 1, 3 of the first operand against rows 0, 2 of the
+// second; v_permlane32_swap: its upper half against the lower) until each holds
+// 16 bytes of one row, so that no LDS is needed beside the stages in flight.
+
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+
+// A wave's FN x FM parts, rows mb .. (of M), columns nb .. (of N): 16-byte stores,
+// 64 bytes of 16 rows at a time.  Whole in columns they go through a descriptor
+// that drops the rows past M.
+template <typename Elt, int FN, int FM>
+__device__ __forceinline__ void mx4_store(uint16_t* C, int64_t ldc, const floatx4_t (&acc)[FN][FM],
+                                          int64_t mb, int64_t M, int64_t nb, int N, int lane) {
+    const int fr = lane & 15, fq = lane >> 4;
+    const int64_t left = M - mb;
+    if (left <= 0) return;
+    const int rows = (int)min(left, (int64_t)(FM * 16));
+    const bool whole = nb + FN * 16 <= N && ldc < (1 << 24);
+    C += mb * ldc + nb;
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(C, (uint32_t)((rows - 1) * ldc + FN * 16) * 2);
+    const int n = (fq & 1) * 16 + (fq >> 1) * 8;
+    const uint32_t off = (uint32_t)(fr * (int)ldc + n) * 2;
 #pragma unroll
-        for (int w = 1; w < NW; ++w) s += red[(w * 4 + j) * 64 + lane];
-        if constexpr (GATED) {
-            floatx4_t s2 = red[(NW * 4 + j) * 64 + lane];
+    for (int j = 0; j < FM; ++j) {
 #pragma unroll
-            for (int w = 1; w < NW; ++w) s2 += red[((NW + w) * 4 + j) * 64 + lane];
+        for (int i = 0; i < FN; i += 2) {
+            uint32_t a0 = mx4_pack2<Elt>(acc[i][j][0], acc[i][j][1]);
+            uint32_t a1 = mx4_pack2<Elt>(acc[i][j][2], acc[i][j][3]);
+            uint32_t b0 = mx4_pack2<Elt>(acc[i + 1][j][0], acc[i + 1][j][1]);
+            uint32_t b1 = mx4_pack2<Elt>(acc[i + 1][j][2], acc[i + 1][j][3]);
+            swap16(a0, b0);                           // quarters 0, 2: part i; 1, 3: part i + 1
+            swap16(a1, b1);
+            const uint4_t v = {a0, a1, b0, b1};
+            if (whole) {
+                __builtin_amdgcn_raw_buffer_store_b128(v, r, off + (uint32_t)(j * 32 * (int)ldc) + i * 32,
+                                                       0, 0);
+            } else if (j * 16 + fr < rows) {
+                uint16_t* c = C + (j * 16 + fr) * ldc + n + i * 16;
 #pragma unroll
-            for (int d = 0; d < 4; ++d) s[d] = silu_mul(s[d], s2[d]);
-        }
-        // lane l: row l % 16 of the part, columns 4 (l / 16) .. + 3
-        const int m = j * 16 + fr;
-        if (m >= rows) continue;
-        const int n = n0 + fq * 4;
-        uint16_t h[4];
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const scalar v = (scalar)s[d];
-            h[d] = __builtin_bit_cast(uint16_t, v);
-        }
-        uint16_t* c = p.C + (m0 + m) * p.ldc + n;
-        if (n + 3 < p.N) {
-            *reinterpret_cast<uint2_t*>(c) = __builtin_bit_cast(uint2_t, h);
-        } else {
-#pragma unroll
-            for (int d = 0; d < 4; ++d)
-                if (n + d < p.N) c[d] = h[d];
+                for (int d = 0; d < 8; ++d) {
+                    const uint32_t w = v[d >> 1];
+                    if (nb + i * 16 + n + d < N) c[d] = (uint16_t)(w >> (16 * (d & 1)));
+                }
+            }
         }
     }
 }
 
-// The gated product of a workgroup (64 columns: a wave has 32, one block, of its
-// 16 FM rows) rounded to the type, quantised and stored: what mx4_quantize makes
-// of it, without its way through memory.  Lane l holds columns 16 i + 4 (l / 16)
-// .. + 3 of row l % 16 of part j in out[i][j]; a row's block is in four lanes.
-template <typename Elt, int BM, int FM>
+// A wave's 32 columns of the gated product (block n0 / 32 + wave_n) rounded to the
+// type, quantised and stored: what mx4_quantize makes of it, without its way
+// through memory.  `rows`: rows of the tile that exist.
+template <typename Elt, int FM>
 __device__ __forceinline__ void mx4_store_quantized(const Mx4Gemm& p, const floatx4_t (&out)[2][FM],
                                                     int64_t m0, int64_t n0, int rows, int wave_m,
-                                                    int wave_n, int lane, int4_t* smem) {
-    typedef typename Elt::scalar scalar;
-    constexpr int WTM = FM * 16;
-    // codes: 16 bytes per row of the wave; scales: two bytes (the waves' blocks) per
-    // row in the order of the scale tile, whose quarter they are
-    uint16_t* codes = reinterpret_cast<uint16_t*>(smem) + (wave_n * BM + wave_m * WTM) * 8;
-    uint8_t* scales = reinterpret_cast<uint8_t*>(smem) + 2 * BM * 16;
+                                                    int wave_n, int lane) {
+    static_assert(FM == 2 || FM == 4, "a wave's rows: half of or a whole scale tile");
     const int fr = lane & 15, fq = lane >> 4;
     const int64_t block = n0 / 32 + wave_n;
-    const int nb = (p.N + 31) / 32;
-    const bool in = block < nb;
+    const bool in = block < (p.N + 31) / 32;
+    uint32_t q[4] = {0, 0, 0, 0};
+    int e = 0;                                        // of row 16 fq + fr of the wave's
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
         uint32_t w[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const scalar lo = (scalar)out[c >> 1][j][2 * (c & 1)];
-            const scalar hi = (scalar)out[c >> 1][j][2 * (c & 1) + 1];
-            w[c] = __builtin_bit_cast(uint16_t, lo) |
-                   ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
-        }
+        for (int c = 0; c < 4; ++c)
+            w[c] = mx4_pack2<Elt>(out[c >> 1][j][2 * (c & 1)], out[c >> 1][j][2 * (c & 1) + 1]);
         uint32_t top = mx4_top(w[0], w[1], w[2], w[3]);
         top = max(top, (uint32_t)__shfl_xor((int)top, 16));
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-        uint32_t q;
-        const int e = mx4_encode<Elt>(top, w[0], w[1], w[2], w[3], q);
-        codes[(j * 16 + fr) * 8 + fq] = (uint16_t)q;
-        codes[(j * 16 + fr) * 8 + 4 + fq] = (uint16_t)(q >> 16);
-        const int r = wave_m * WTM + j * 16 + fr;
-        if (fq == 0)
-            scales[(r >> 6) * 128 + fr * 8 + ((r >> 4) & 3) * 2 + wave_n] =
-                in && r < rows ? (uint8_t)e : 0;
+        const int ej = mx4_encode<Elt>(top, w[0], w[1], w[2], w[3], q[j]);
+        e = fq == j ? ej : e;
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    if (lane < WTM && wave_m * WTM + lane < rows && in)
-        *reinterpret_cast<int4_t*>(p.QO + (m0 + wave_m * WTM + lane) * p.ldqo + block * 16) =
-            reinterpret_cast<const int4_t*>(codes)[lane];
-    __syncthreads();
-    // 128 bytes a quarter; the last columns' workgroup also clears the quarters
+    // transposed: lane (fr, fq) has the codes of row 16 fq + fr, quarter c's in q[c]:
+    // low half of columns 4 c .., high half of columns 16 + 4 c ..
+    swap16(q[0], q[1]);
+    swap16(q[2], q[3]);
+    swap32(q[0], q[2]);
+    swap32(q[1], q[3]);
+    const int r = wave_m * FM * 16 + fq * 16 + fr;
+    if (fq >= FM || (r & ~63) >= rows) return;
+    if (in && r < rows) {
+        const uint4_t v = {(q[0] & 0xffffu) | (q[1] << 16), (q[2] & 0xffffu) | (q[3] << 16),
+                           (q[0] >> 16) | (q[1] & 0xffff0000u), (q[2] >> 16) | (q[3] & 0xffff0000u)};
+        *reinterpret_cast<uint4_t*>(p.QO + (m0 + r) * p.ldqo + block * 16) = v;
+    }
+    // a byte per row and block; the last columns' workgroup also clears the quarters
     // past them, whose blocks hold nothing
-    const int t = threadIdx.x;
     const int g0 = (int)(n0 / 64) & 3;
-    const int quarters = n0 + 64 >= p.N ? 4 - g0 : 1;
-    const int st = t >> 7, g = (t >> 5) & 3;      // 64-row tile, quarter past g0
-    const uint32_t* from = reinterpret_cast<const uint32_t*>(scales) + st * 32 + (t & 31);
-    if (st * 64 < min(rows, BM) && g < quarters) {
-        uint8_t* tile = p.SO + ((m0 / 64 + st) * p.nkto + n0 / 256) * kMx4Tile + (g0 + g) * 128;
-        reinterpret_cast<uint32_t*>(tile)[t & 31] = g == 0 ? *from : 0u;
-    }
+    uint8_t* tile = p.SO + ((m0 + r) / 64 * p.nkto + n0 / 256) * kMx4Tile;
+    tile[mx4_scale_offset(r & 63, 2 * g0 + wave_n)] = in && r < rows ? (uint8_t)e : 0;
+    if (n0 + 64 >= p.N)
+        for (int g = g0 + 1; g < 4; ++g) tile[mx4_scale_offset(r & 63, 2 * g + wave_n)] = 0;
 }
 
-// The tiled product: BM x BN outputs per workgroup, WM x WN waves of 16x16x128
-// MFMAs.  A stage holds the codes of BM + BN rows x 128 bytes and their scale
-// tiles, loaded straight into LDS; NS stages.  16-byte chunk 2 g + s of row r
-// (block 2 g + s of the k-tile) is kept at position (4 s + g) ^ swz_pp(r), so a
-// fragment read of half s has the conflict-free pattern of the 16-bit kernels.
-// One barrier per k-tile: after it the loads of k-tile i + NS go into the stage
-// that k-tile i has left, the fragments of i + 1 are read into a second set of
-// registers, and the MFMAs of i run.  The LDS of two workgroups fits a CU: one's
-// prologue, waits and epilogue run under the other's MFMAs.
+// The tiled product: output tiles of BM x BN, WM x WN waves of 16x16x128 MFMAs.
+// A stage holds the codes of BM + BN rows x 128 bytes and their scale tiles,
+// loaded straight into LDS; NS stages.  16-byte chunk 2 g + s of row r (block
+// 2 g + s of the k-tile) is kept at position (4 s + g) ^ swz_pp(r), so a fragment
+// read of half s has the conflict-free pattern of the 16-bit kernels.
+//
+// A workgroup takes tiles in turn, its k-tiles one stream: once the fragments of a
+// k-tile are in registers the loads of the one NS further on go into its stage,
+// under the second half of its MFMAs.  Past a tile's last k-tile the loads are
+// the next tile's, so neither its first loads nor the epilogue (in registers)
+// leaves the memory idle.  Two workgroups share a CU: one's LDS reads and waits
+// run under the other's MFMAs.
+//
 // GATED: the B rows of a wave are 32 of the first matrix and the same 32 of the
-// second, so a lane holds both factors of its outputs; BN / 2 columns per
-// workgroup.  GROUPED: rows are a plan's, the expert's matrices are found from
-// the row tile.
+// second, so a lane holds both factors of its outputs; BN / 2 columns per tile.
+// GROUPED: a tile's rows are one expert's of a plan; the tiles are counted from
+// the plan's counts, so the grid holds no empty ones.
 template <typename Elt, int BM, int BN, int WM, int WN, int NS, bool GROUPED, bool GATED,
           bool QOUT = false>
 __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
@@ -682,58 +834,113 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
     constexpr int ST = (BM + BN) / 64;            // scale tiles of a stage
     constexpr int S_DMA = (ST + NW - 1) / NW;     // per wave (spare waves repeat a tile)
     constexpr int L = A_DMA + B_DMA + S_DMA;
+    constexpr int BNO = GATED ? BN / 2 : BN;      // output columns
+    constexpr int PRE = GROUPED ? 512 : 1;        // pairs of experts (kMaxExperts / 2)
     static_assert(A_UNITS % (64 * NW) == 0 && B_UNITS % (64 * NW) == 0, "whole 8-row slabs");
     static_assert(BM % 64 == 0 && BN % 64 == 0, "whole scale tiles");
     static_assert(!GATED || (WTN == 64 && BN == 128), "gated: 32 + 32 columns per wave");
     static_assert(WTM == 32 || WTM % 64 == 0, "a wave's rows: halves of or whole scale tiles");
     static_assert(WTN == 32 || WTN == 64, "a wave's columns: half of or a whole scale tile");
-    static_assert(2 * NS * STAGE * 16 <= 160 * 1024, "the stages of two workgroups fit the LDS");
-    static_assert(NW * 256 <= NS * STAGE, "epilogue stage");
+    static_assert(2 * (NS * STAGE * 16 + PRE * 4 + 64) <= 160 * 1024, "two workgroups fit the LDS");
     __shared__ int4_t smem[NS * STAGE];
+    __shared__ int upto[PRE];                     // row tiles of the pairs of experts up to each
+    __shared__ int wsum[NW];
 
     const int t = threadIdx.x;
     const int lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wave_m = wave % WM, wave_n = wave / WM;
+    const int nkt = p.nkt;
 
-    const int BNO = GATED ? BN / 2 : BN;          // output columns
-    const int logical = xcd_remap(blockIdx.x, p.gm * p.gn, p.nxcd);
-    int64_t m0, n0;
-    int e = 0, limit;                             // limit: rows of C past m0 that exist
+    int row_tiles = p.gm;
     if constexpr (GROUPED) {
-        const int g = logical / p.gn;
-        if (!mx4_group(p, g, BM / 64, e, m0, limit)) return;
-        n0 = (int64_t)(logical - g * p.gn) * BNO;
-    } else {
-        GemmParams gp;
-        gp.gm = p.gm;
-        gp.gn = p.gn;
-        grouped_origin(gp, logical, BM, BNO, m0, n0);
-        limit = (int)min((int64_t)p.M - m0, (int64_t)BM);
+        constexpr int EPT = PRE / (NW * 64);
+        int c[EPT], sum = 0;
+#pragma unroll
+        for (int u = 0; u < EPT; ++u) {
+            const int x = (t * EPT + u) * 2;
+            sum += x < p.experts ? (int)((uint32_t)(p.counts[x] + BM - 1) / BM) : 0;
+            sum += x + 1 < p.experts ? (int)((uint32_t)(p.counts[x + 1] + BM - 1) / BM) : 0;
+            c[u] = sum;
+        }
+        int scan = sum;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(scan, d);
+            if (lane >= d) scan += o;
+        }
+        if (lane == 63) wsum[wave] = scan;
+        __syncthreads();
+        int before = scan - sum;
+        row_tiles = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            before += w < wave ? wsum[w] : 0;
+            row_tiles += wsum[w];
+        }
+#pragma unroll
+        for (int u = 0; u < EPT; ++u) upto[t * EPT + u] = before + c[u];
+        __syncthreads();
+        row_tiles = __builtin_amdgcn_readfirstlane(row_tiles);
     }
-    const int rows_a = min(limit, BM);
-    const int rows_b = (int)min((int64_t)BNO, (int64_t)p.N - n0);
-    const uint32_t srow = (uint32_t)p.nkt * kMx4Tile;   // scale bytes of 64 rows
+    // This workgroup's tiles: every XCD has a contiguous range, its workgroups
+    // take it in turn.
+    const int total = row_tiles * p.gn;
+    const int xcd = blockIdx.x % p.nxcd;
+    const int turn = ((int)gridDim.x - xcd + p.nxcd - 1) / p.nxcd;
+    const int last = (xcd + 1) * (total / p.nxcd) + min(xcd + 1, total % p.nxcd);
+    int tile = xcd * (total / p.nxcd) + min(xcd, total % p.nxcd) + blockIdx.x / p.nxcd;
+    if (tile >= last) return;
 
-    const __amdgpu_buffer_rsrc_t ra = mx4_rows_rsrc(p, m0, rows_a);
-    const __amdgpu_buffer_rsrc_t rb =
-        make_rsrc(p.B + e * p.eqb + n0 * p.ldb, (uint32_t)((rows_b - 1) * p.ldb + p.rowbytes));
-    const __amdgpu_buffer_rsrc_t rb2 =
-        make_rsrc(GATED ? p.B2 + e * p.eqb2 + n0 * p.ldb2 : p.B,
-                  GATED ? (uint32_t)((rows_b - 1) * p.ldb2 + p.rowbytes) : 0u);
-    const __amdgpu_buffer_rsrc_t rsa =
-        make_rsrc(p.SA + (m0 / 64) * srow, (uint32_t)((rows_a + 63) / 64) * srow);
-    const __amdgpu_buffer_rsrc_t rsb = make_rsrc(p.SB + e * p.esb + (n0 / 64) * srow,
-                                                 (uint32_t)((rows_b + 63) / 64) * srow);
-    const __amdgpu_buffer_rsrc_t rsb2 =
-        make_rsrc(GATED ? p.SB2 + e * p.esb2 + (n0 / 64) * srow : p.SB,
-                  GATED ? (uint32_t)((rows_b + 63) / 64) * srow : 0u);
+    struct Place {
+        int64_t m0, n0;
+        int rows;                                 // of the tile that exist
+        int e;
+    };
+    auto locate = [&](int l) {
+        Place x;
+        x.e = 0;
+        if constexpr (GROUPED) {
+            const int tm = l / p.gn;
+            x.n0 = (int64_t)(l - tm * p.gn) * BNO;
+            int before = 0;                       // the pairs whose tiles all lie before tm
+            for (int c = 0; 2 * c < p.experts; c += 64) {
+                const bool in = 2 * (c + lane) < p.experts && upto[c + lane] <= tm;
+                before += __popcll(__ballot(in));
+            }
+            before = __builtin_amdgcn_readfirstlane(before);
+            int t0 = before == 0 ? 0 : __builtin_amdgcn_readfirstlane(upto[before - 1]);
+            x.e = 2 * before;
+            // scalar loads: a vector load's wait would be for every load in flight
+            const int odd = x.e + 1 < p.experts ? 1 : 0;
+            const int c0 = uniform_load(p.counts + x.e), c1 = uniform_load(p.counts + x.e + odd);
+            const int o0 = uniform_load(p.offsets + x.e), o1 = uniform_load(p.offsets + x.e + odd);
+            const int first = (int)((uint32_t)(c0 + BM - 1) / BM);
+            const bool second = tm - t0 >= first;
+            t0 += second ? first : 0;
+            x.e += second ? 1 : 0;
+            const int count = second ? c1 : c0;
+            const int64_t row0 = second ? o1 : o0;
+            x.m0 = row0 + (int64_t)(tm - t0) * BM;
+            x.rows = min(count - (tm - t0) * BM, BM);
+        } else {
+            GemmParams gp;
+            gp.gm = p.gm;
+            gp.gn = p.gn;
+            grouped_origin(gp, l, BM, BNO, x.m0, x.n0);
+            x.rows = (int)min((int64_t)p.M - x.m0, (int64_t)BM);
+        }
+        return x;
+    };
+
+    // ---- the stream of k-tiles: the loads' position ------------------------------------
+    const uint32_t srow = (uint32_t)nkt * kMx4Tile;   // scale bytes of 64 rows
     uint32_t voff_a[A_DMA], voff_b[B_DMA];
 #pragma unroll
     for (int j = 0; j < A_DMA; ++j) {
         const int row = (wave * A_DMA + j) * 8 + (lane >> 3);
         const int pos = (lane & 7) ^ swz_pp(row);
-        voff_a[j] = mx4_row_offset(p, m0, row, rows_a) + ((pos & 3) * 2 + (pos >> 2)) * 16;
+        voff_a[j] = (uint32_t)(row * p.lda) + ((pos & 3) * 2 + (pos >> 2)) * 16;
     }
 #pragma unroll
     for (int j = 0; j < B_DMA; ++j) {
@@ -744,11 +951,30 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
         voff_b[j] = (uint32_t)(src * (GATED && (row & 32) ? p.ldb2 : p.ldb)) +
                     ((pos & 3) * 2 + (pos >> 2)) * 16;
     }
-    auto load_tile = [&](int kt, int stage) {
+    Place at = locate(tile), next_at = at;        // the tile that is multiplied, that is loaded
+    int load_kt = 0;
+    bool loads = nkt > 0;                         // loads are left
+    __amdgpu_buffer_rsrc_t ra, rb, rb2, rsa, rsb, rsb2;
+    auto describe = [&](const Place& x) {
+        const int rows_b = (int)min((int64_t)BNO, (int64_t)p.N - x.n0);
+        const uint32_t sa = (uint32_t)((x.rows + 63) / 64) * srow;
+        const uint32_t sb = (uint32_t)((rows_b + 63) / 64) * srow;
+        ra = make_rsrc(p.A + x.m0 * p.lda, (uint32_t)((x.rows - 1) * p.lda + p.rowbytes));
+        rb = make_rsrc(p.B + x.e * p.eqb + x.n0 * p.ldb,
+                       (uint32_t)((rows_b - 1) * p.ldb + p.rowbytes));
+        rsa = make_rsrc(p.SA + (x.m0 / 64) * srow, sa);
+        rsb = make_rsrc(p.SB + x.e * p.esb + (x.n0 / 64) * srow, sb);
+        if constexpr (GATED) {
+            rb2 = make_rsrc(p.B2 + x.e * p.eqb2 + x.n0 * p.ldb2,
+                            (uint32_t)((rows_b - 1) * p.ldb2 + p.rowbytes));
+            rsb2 = make_rsrc(p.SB2 + x.e * p.esb2 + (x.n0 / 64) * srow, sb);
+        }
+    };
+    auto load_codes = [&](int stage) {
         int4_t* base = smem + stage * STAGE;
         // in the lane offset, which the descriptor's range check covers: the
         // last row's bytes past its blocks are not read
-        const uint32_t koff = (uint32_t)kt * 128;
+        const uint32_t koff = (uint32_t)load_kt * 128;
 #pragma unroll
         for (int j = 0; j < A_DMA; ++j)
             dma16(ra, base + (wave * A_DMA + j) * 64, voff_a[j] + koff, 0);
@@ -757,26 +983,41 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
             const bool second = GATED && (((wave * B_DMA + j) * 8) & 32) != 0;
             dma16(second ? rb2 : rb, base + A_UNITS + (wave * B_DMA + j) * 64, voff_b[j] + koff, 0);
         }
+    };
+    auto load_scales = [&](int stage) {
 #pragma unroll
         for (int j = 0; j < S_DMA; ++j) {
             const int st = (wave * S_DMA + j) % ST;
-            int4_t* dst = base + S_BASE + st * 32;
+            int4_t* dst = smem + stage * STAGE + S_BASE + st * 32;
             if (lane < 32) {
                 if (st < BM / 64)
-                    dma16(rsa, dst, st * srow + lane * 16, kt * kMx4Tile);
+                    dma16(rsa, dst, st * srow + lane * 16, load_kt * kMx4Tile);
                 else if (GATED && st > BM / 64)
-                    dma16(rsb2, dst, lane * 16, kt * kMx4Tile);
+                    dma16(rsb2, dst, lane * 16, load_kt * kMx4Tile);
                 else
-                    dma16(rsb, dst, (st - BM / 64) * srow + lane * 16, kt * kMx4Tile);
+                    dma16(rsb, dst, (st - BM / 64) * srow + lane * 16, load_kt * kMx4Tile);
+            }
+        }
+    };
+    auto advance = [&]() {
+        if (++load_kt == nkt) {
+            load_kt = 0;
+            tile += turn;
+            loads = tile < last;
+            if (loads) {
+                next_at = locate(tile);
+                describe(next_at);
             }
         }
     };
 
     floatx4_t acc[FN][FM];
+    auto clear = [&]() {
 #pragma unroll
-    for (int i = 0; i < FN; ++i)
+        for (int i = 0; i < FN; ++i)
 #pragma unroll
-        for (int j = 0; j < FM; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < FM; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    };
 
     const int frow = lane & 15, fq = lane >> 4;
     const int fsw = swz_pp(frow);
@@ -787,16 +1028,16 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
         int4_t a[2][FM], b[2][FN];
         int sa[SAW], sb[SBW];
     };
-    auto read_tile = [&](int stage, Frags& f) {
+    auto read_half = [&](int stage, int s, Frags& f) {
         const int4_t* base = smem + stage * STAGE;
+        const int chunk = (4 * s + fq) ^ fsw;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int chunk = (4 * s + fq) ^ fsw;
+        for (int j = 0; j < FM; ++j) f.a[s][j] = base[(a_row0 + j * 16) * 8 + chunk];
 #pragma unroll
-            for (int j = 0; j < FM; ++j) f.a[s][j] = base[(a_row0 + j * 16) * 8 + chunk];
-#pragma unroll
-            for (int i = 0; i < FN; ++i) f.b[s][i] = base[(b_row0 + i * 16) * 8 + chunk];
-        }
+        for (int i = 0; i < FN; ++i) f.b[s][i] = base[(b_row0 + i * 16) * 8 + chunk];
+    };
+    auto read_scales = [&](int stage, Frags& f) {
+        const int4_t* base = smem + stage * STAGE;
         const int* sbase = reinterpret_cast<const int*>(base + S_BASE);
 #pragma unroll
         for (int d = 0; d < SAW; ++d) {
@@ -828,6 +1069,14 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
                     mx4_mfma_part<S, 1, 1>(f.b[S][i + 1], f.a[S][j + 1], acc[i + 1][j + 1], b, a);
             }
     };
+    // The MFMAs are values to the compiler: an empty asm that reads them keeps it
+    // from moving them past the waits and barriers that follow.
+    auto pin = [&]() {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j) asm volatile("" : "+v"(acc[i][j]));
+    };
     auto barrier = [&]() {
         // not __syncthreads: its release would wait for every load in flight
         wait_lds();
@@ -835,70 +1084,90 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
     };
-
-    const int nkt = p.nkt;
-    Frags f[2];
-    int i = 0, s = 0;                             // k-tile, its stage
-    auto step = [&](auto waits, Frags& cur, Frags& next) {
-        wait_global_loads<decltype(waits)::value>();   // k-tile i + 1 has landed
-        barrier();
-        const int sn = (s + 1 == NS) ? 0 : s + 1;
-        if (i + NS < nkt) load_tile(i + NS, s);
-        if (i + 1 < nkt) read_tile(sn, next);
-        mfma_half(std::integral_constant<int, 0>{}, cur);
-        mfma_half(std::integral_constant<int, 1>{}, cur);
-        // keeps the MFMAs, values to the compiler, before the waits that follow
+    auto store = [&]() {
+        const int64_t mb = at.m0 + wave_m * WTM, M = at.m0 + at.rows;
+        if constexpr (GATED) {
+            floatx4_t out[FN / 2][FM];
 #pragma unroll
-        for (int n = 0; n < FN; ++n)
+            for (int i = 0; i < FN / 2; ++i)
 #pragma unroll
-            for (int m = 0; m < FM; ++m) asm volatile("" : "+v"(acc[n][m]));
-        s = sn;
-        ++i;
+                for (int j = 0; j < FM; ++j)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+                        out[i][j][d] = silu_mul(acc[i][j][d], acc[i + FN / 2][j][d]);
+            if constexpr (QOUT)
+                mx4_store_quantized<Elt, FM>(p, out, at.m0, at.n0, at.rows, wave_m, wave_n, lane);
+            else
+                mx4_store<Elt, FN / 2, FM>(p.C, p.ldc, out, mb, M, at.n0 + wave_n * (WTN / 2), p.N,
+                                           lane);
+        } else {
+            mx4_store<Elt, FN, FM>(p.C, p.ldc, acc, mb, M, at.n0 + wave_n * WTN, p.N, lane);
+        }
     };
-    using Steady = std::integral_constant<int, (NS - 2) * L>;
-    using Last = std::integral_constant<int, 0>;
 
-    for (int j = 0; j < min(nkt, NS); ++j) load_tile(j, j);
-    if (nkt >= NS)
+    clear();
+    if (nkt == 0) {                               // every sum is empty
+        for (; tile < last; tile += turn) {
+            at = locate(tile);
+            store();
+        }
+        return;
+    }
+    describe(at);
+    for (int j = 0; j < NS && loads; ++j) {
+        load_codes(j);
+        load_scales(j);
+        advance();
+    }
+    // k-tile 0 has landed (the others may still be on their way)
+    if (loads)
         wait_global_loads<(NS - 1) * L>();
     else
         wait_global_loads<0>();
     barrier();
-    if (nkt > 0) read_tile(0, f[0]);
-    while (i + NS < nkt) {                        // k-tiles i + 1 .. i + NS - 1, and i + NS for the second
-        step(Steady{}, f[0], f[1]);
-        step(Steady{}, f[1], f[0]);
-    }
-    while (i < nkt) {
-        step(Last{}, f[0], f[1]);
-        if (i < nkt) step(Last{}, f[1], f[0]);
-    }
-
-    // The stages are not read any more after the last k-tile's barrier (with no
-    // k-tile nothing was): 4 KB of them per wave stage its output.
-    GemmParams gp;
-    gp.C = p.C;
-    gp.ldc = p.ldc;
-    gp.M = (int)(m0 + rows_a);
-    gp.N = p.N;
-    int4_t* stage = smem + wave * 256;
-    const int64_t mb = m0 + wave_m * WTM;
-    if constexpr (GATED) {
-        floatx4_t out[FN / 2][FM];
+    // One k-tile a turn: `kt` of tile `at`, landed in stage s.
+    int kt = 0, s = 0;
+    for (;;) {
+        // The loads stand in this tile or the next (the host sees to nkt > NS where
+        // a workgroup has more than one): is there a next?
+        const bool more = loads || next_at.m0 != at.m0 || next_at.n0 != at.n0;
+        Frags f;
+        read_half(s, 0, f);
+        read_scales(s, f);
+        read_half(s, 1, f);
+        mfma_half(std::integral_constant<int, 0>{}, f);
+        pin();
+        barrier();                                // every wave has read stage s
+        const bool full = loads;                  // NS - 1 younger k-tiles than the next will fly
+        if (loads) {
+            load_codes(s);
+            mfma_half(std::integral_constant<int, 1>{}, f);
+            // a load between every two MFMAs (masks: 0x020 global read, 0x008 MFMA)
 #pragma unroll
-        for (int i = 0; i < FN / 2; ++i)
-#pragma unroll
-            for (int j = 0; j < FM; ++j)
-#pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    out[i][j][d] = silu_mul(acc[i][j][d], acc[i + FN / 2][j][d]);
-        if constexpr (QOUT) {
-            mx4_store_quantized<Elt, BM, FM>(p, out, m0, n0, rows_a, wave_m, wave_n, lane, smem);
-            return;
+            for (int m = 0; m < A_DMA + B_DMA; ++m) {
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, FM * FN / (A_DMA + B_DMA), 0);
+            }
+            pin();
+            load_scales(s);
+            advance();
+        } else {
+            mfma_half(std::integral_constant<int, 1>{}, f);
+            pin();
         }
-        gemm_epilogue<Elt, 16>(gp, out, mb, n0 + wave_n * (WTN / 2), lane, stage);
-    } else {
-        gemm_epilogue<Elt, 16>(gp, acc, mb, n0 + wave_n * WTN, lane, stage);
+        s = (s + 1 == NS) ? 0 : s + 1;
+        if (++kt == nkt) {
+            store();
+            if (!more) return;
+            kt = 0;
+            at = next_at;
+            clear();
+        }
+        if (full)
+            wait_global_loads<(NS - 1) * L>();    // stores, if any, only make it longer
+        else
+            wait_global_loads<0>();
+        barrier();                                // the next k-tile has landed
     }
 }
 

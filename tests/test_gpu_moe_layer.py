@@ -106,3 +106,20 @@ def test_plan_of_ragged_slots(E, R):
                                ref.plan(flat[:, None], E),
                                ("counts", "offsets", "rows", "pos", "tiles")):
         assert np.array_equal(got.cpu().numpy(), want), what
+
+
+def test_layer_of_many_slots_a_token():
+    """More slots a token than the router chooses: the layer takes any plan."""
+    import torch
+    T, topk, E, N, K = 20, 70, 8, 64, 96
+    layer, parts = make_layer(E, N, K, "bf16", 3)
+    rng = np.random.default_rng(8)
+    x = torch.from_numpy(rng.standard_normal((T, K))).bfloat16().to(DEV)
+    idx = dev(rng.integers(-1, E, (T, topk)).astype(np.int32))
+    w = dev(rng.random((T, topk)).astype(np.float32))
+    say("layer of 70 slots a token")
+    y = layer(x, idx, w)
+    torch.cuda.synchronize()
+    want = by_parts(parts, x, idx, w, "bf16")
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
