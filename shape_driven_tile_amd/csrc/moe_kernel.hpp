@@ -36,20 +36,69 @@ __device__ __forceinline__ float route_load(const void* p, int64_t i) {
     if constexpr (std::is_same_v<T, __bf16>) return (float)static_cast<const __bf16*>(p)[i];
 }
 
-template <typename V>
-__device__ __forceinline__ V wave_sum(V v) {
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
-    return v;
+// One step of a reduction towards lane 63: lanes without a source, or of rows
+// outside ROWS, get `none`.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t none, uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xf, false);
+}
+template <typename V, typename F>
+__device__ __forceinline__ V wave_reduce(V v, F f) {
+    v = f(v, std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xf>{});   // row_shr:1
+    v = f(v, std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xf>{});
+    v = f(v, std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xf>{});
+    v = f(v, std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xf>{});
+    v = f(v, std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});   // row_bcast:15
+    return f(v, std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});  // :31
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __builtin_bit_cast(float, lane_value(__builtin_bit_cast(uint32_t, v), lane));
+}
+// Over the wave, known to every lane.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = wave_reduce(v, [](uint32_t x, auto c, auto r) {
+        const uint32_t o = dpp<decltype(c)::value, decltype(r)::value>(0, x);
+        return x > o ? x : o;
+    });
+    return lane_value(v, 63);
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
-    return v;
+    v = wave_reduce(v, [](float x, auto c, auto r) {
+        const uint32_t o = dpp<decltype(c)::value, decltype(r)::value>(0xff800000u,
+                                                                       __builtin_bit_cast(uint32_t, x));
+        return fmaxf(x, __builtin_bit_cast(float, o));
+    });
+    return lane_value(v, 63);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    v = wave_reduce(v, [](float x, auto c, auto r) {
+        const uint32_t o = dpp<decltype(c)::value, decltype(r)::value>(0, __builtin_bit_cast(uint32_t, x));
+        return x + __builtin_bit_cast(float, o);
+    });
+    return lane_value(v, 63);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+    v = wave_reduce(v, [](double x, auto c, auto r) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, x);
+        const uint64_t lo = dpp<decltype(c)::value, decltype(r)::value>(0, (uint32_t)u);
+        const uint64_t hi = dpp<decltype(c)::value, decltype(r)::value>(0, (uint32_t)(u >> 32));
+        return x + __builtin_bit_cast(double, (hi << 32) | lo);
+    });
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint64_t lo = lane_value((uint32_t)u, 63), hi = lane_value((uint32_t)(u >> 32), 63);
+    return __builtin_bit_cast(double, (hi << 32) | lo);
 }
 
-// Keys whose unsigned order is the order of the doubles (-0 as +0, a NaN as
+// Keys whose unsigned order is the order of the values (-0 as +0, a NaN as
 // -infinity).  0 is below every key: an expert that may not be chosen.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    if (v != v) v = -__builtin_inff();
+    const uint32_t u = __builtin_bit_cast(uint32_t, v + 0.0f);
+    return (u >> 31) ? ~u : (u | 0x80000000u);
+}
 __device__ __forceinline__ uint64_t order_key(double v) {
     if (v != v) v = -__builtin_inf();
     const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);
@@ -59,148 +108,172 @@ __device__ __forceinline__ double key_value(uint64_t k) {
     return __builtin_bit_cast(double, (k >> 63) ? (k & 0x7fffffffffffffffull) : ~k);
 }
 
-// (key, index) of the largest key over the wave, the lowest index among equals.
-__device__ __forceinline__ void wave_best(uint64_t& k, int& i) {
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) {
-        const uint64_t ok = __shfl_xor((unsigned long long)k, m);
-        const int oi = __shfl_xor(i, m);
-        if (ok > k || (ok == k && oi < i)) {
-            k = ok;
-            i = oi;
-        }
-    }
+// The lowest lane that holds the wave's largest key.
+__device__ __forceinline__ int best_lane(uint32_t k) {
+    const uint32_t top = wave_max(k);
+    return __builtin_ctzll(__ballot(k == top));
+}
+__device__ __forceinline__ int best_lane(uint64_t k) {
+    const uint32_t hi = (uint32_t)(k >> 32);
+    const uint32_t tophi = wave_max(hi);
+    const uint32_t lo = hi == tophi ? (uint32_t)k : 0u;
+    const uint32_t toplo = wave_max(lo);
+    return __builtin_ctzll(__ballot(hi == tophi && (uint32_t)k == toplo));
 }
 
-// One wave per token; lane l holds experts l, l + 64, ... (EPL of them).
-// Every score is formed from the logits in registers; the choice is topk
-// rounds of a wave-wide maximum on 64-bit keys.  Keys come from the logits in
-// fp32 or, with a bias or worths summed over two, from scores in 64 bits, so
-// that two experts tie only where their definitions do.
-template <typename T, int EPL>
+// One wave per token; lane l holds experts l EPL .. + EPL - 1, so the lowest
+// lane among equals has the lowest expert.  Every score is formed from the
+// logits in registers; the choice is topk rounds of a wave-wide maximum, six
+// steps of lane-crossing operands (DPP) on 32-bit keys.  Keys come from the
+// logits in fp32 or (WIDE), with a bias or worths summed over two, from scores in
+// 64 bits, so that two experts tie only where their definitions do.  Bound by
+// the rounds' instructions: 16384 tokens, 8 of 128 experts (bf16): 35 us with
+// lane exchanges through LDS on 64-bit keys, 10 us so.
+template <typename T, int EPL, bool WIDE>
 __global__ __launch_bounds__(256) void moe_route_kernel(RouteParams p) {
+    typedef std::conditional_t<WIDE, uint64_t, uint32_t> Key;
+    __shared__ Key shared_keys[4][EPL * 64];      // groups: a wave's keys by expert
     const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int wave = threadIdx.x >> 6;
+    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
     if (t >= p.T) return;
     const float ninf = -__builtin_inff();
+    const int e0 = lane * EPL;
     float x[EPL];
     float top = ninf;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-        const int e = j * 64 + lane;
-        x[j] = e < p.E ? route_load<T>(p.logits, t * p.ld + e) : ninf;
+        x[j] = e0 + j < p.E ? route_load<T>(p.logits, t * p.ld + e0 + j) : ninf;
         if (x[j] != x[j]) x[j] = ninf;
         top = fmaxf(top, x[j]);
     }
-    top = wave_max(top);
     // scores: softmax's numerators (the largest logit's is 1, also an infinite
     // one's) or sigmoids
-    const bool wide = p.bias != nullptr || p.group_top == 2;
     float s[EPL];
-    double sd[EPL];
-    float total = 0.0f;
-    double totald = 0.0;
+    double sd[WIDE ? EPL : 1];
+    if (p.score == 0) {
+        top = wave_max(top);
+        float total = 0.0f;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        sd[j] = 0.0;
-        if (p.score == 0) {
+        for (int j = 0; j < EPL; ++j) {
             s[j] = x[j] == ninf ? 0.0f : x[j] == top ? 1.0f : expf(x[j] - top);
             total += s[j];
-            if (wide) {
-                sd[j] = x[j] == ninf ? 0.0 : x[j] == top ? 1.0 : exp((double)x[j] - (double)top);
-                totald += sd[j];
-            }
-        } else {
-            s[j] = x[j] == ninf ? 0.0f : 1.0f / (1.0f + expf(-x[j]));
-            if (wide) sd[j] = x[j] == ninf ? 0.0 : 1.0 / (1.0 + exp(-(double)x[j]));
         }
-    }
-    if (p.score == 0) {
         total = wave_sum(total);
         const float inv = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) s[j] *= inv;
-        if (wide) {
+        if constexpr (WIDE) {
+            double totald = 0.0;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) {
+                sd[j] = x[j] == ninf ? 0.0 : x[j] == top ? 1.0 : exp((double)x[j] - (double)top);
+                totald += sd[j];
+            }
             totald = wave_sum(totald);
 #pragma unroll
             for (int j = 0; j < EPL; ++j) sd[j] = totald > 0.0 ? sd[j] / totald : 0.0;
         }
-    }
-    uint64_t key[EPL];
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        const int e = j * 64 + lane;
-        const double c = p.bias != nullptr ? sd[j] + (e < p.E ? (double)p.bias[e] : 0.0) : (double)x[j];
-        key[j] = e < p.E ? order_key(c) : 0;
-    }
-    if (p.groups > 1) {
-        // a group's worth: its best value, or the sum of its two best
-        const int per = p.E / p.groups;
-        uint64_t worth = 0;               // lane g: group g's
-        for (int g = 0; g < p.groups; ++g) {
-            uint64_t b1 = 0, b2 = 0;
-#pragma unroll
-            for (int j = 0; j < EPL; ++j) {
-                const int e = j * 64 + lane;
-                if (e / per == g && e < p.E) {
-                    const uint64_t v = p.bias != nullptr || p.group_top == 1 ? key[j] : order_key(sd[j]);
-                    if (v > b1) {
-                        b2 = b1;
-                        b1 = v;
-                    } else if (v > b2) {
-                        b2 = v;
-                    }
-                }
-            }
-#pragma unroll
-            for (int m = 32; m > 0; m >>= 1) {
-                const uint64_t o1 = __shfl_xor((unsigned long long)b1, m);
-                const uint64_t o2 = __shfl_xor((unsigned long long)b2, m);
-                const uint64_t lo = o1 < b1 ? o1 : b1;
-                b1 = o1 < b1 ? b1 : o1;
-                b2 = b2 > o2 ? b2 : o2;
-                b2 = b2 > lo ? b2 : lo;
-            }
-            const uint64_t w = p.group_top == 1 ? b1 : order_key(key_value(b1) + key_value(b2));
-            if (lane == g) worth = w;
-        }
-        uint64_t keptmask = 0;
-        for (int r = 0; r < p.kept; ++r) {
-            uint64_t k = worth;
-            int i = lane;
-            wave_best(k, i);
-            keptmask |= 1ull << i;
-            if (lane == i) worth = 0;
-        }
+    } else {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            const int e = j * 64 + lane;
-            if (e < p.E && !((keptmask >> (e / per)) & 1)) key[j] = 0;
+            s[j] = x[j] == ninf ? 0.0f : 1.0f / (1.0f + expf(-x[j]));
+            if constexpr (WIDE) sd[j] = x[j] == ninf ? 0.0 : 1.0 / (1.0 + exp(-(double)x[j]));
         }
     }
-    // topk rounds; lane r keeps the r-th choice
+    Key key[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        const int e = e0 + j;
+        if constexpr (WIDE) {
+            const double c =
+                p.bias != nullptr ? sd[j] + (e < p.E ? (double)p.bias[e] : 0.0) : (double)x[j];
+            key[j] = e < p.E ? order_key(c) : 0;
+        } else {
+            key[j] = e < p.E ? order_key(x[j]) : 0;
+        }
+    }
+    if (p.groups > 1) {
+        // A group's worth: its best value, or the sum of its two best.  `parts` lanes
+        // scan a group, then merge.
+        const int per = p.E / p.groups;
+        Key* mine = shared_keys[wave];
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            Key v = key[j];
+            if constexpr (WIDE)
+                if (p.bias == nullptr && p.group_top == 2) v = order_key(sd[j]);
+            mine[e0 + j] = v;
+        }
+        // other lanes' keys: LDS runs a wave's accesses in order, the fence keeps
+        // the compiler from reordering them
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        const int shift = 31 - __builtin_clz(64 / p.groups);     // parts = 1 << shift
+        const int g = lane >> shift, part = lane & ((1 << shift) - 1);
+        Key b1 = 0, b2 = 0;
+        if (g < p.groups)
+            for (int i = part; i < per; i += 1 << shift) {
+                const Key v = mine[g * per + i];
+                const Key lo = v < b1 ? v : b1;
+                b1 = v > b1 ? v : b1;
+                b2 = lo > b2 ? lo : b2;
+            }
+        for (int m = 1; m < 1 << shift; m <<= 1) {
+            Key o1, o2;
+            if constexpr (WIDE) {
+                o1 = __shfl_xor((unsigned long long)b1, m);
+                o2 = __shfl_xor((unsigned long long)b2, m);
+            } else {
+                o1 = (uint32_t)__shfl_xor((int)b1, m);
+                o2 = (uint32_t)__shfl_xor((int)b2, m);
+            }
+            const Key lo = o1 < b1 ? o1 : b1;
+            b1 = o1 < b1 ? b1 : o1;
+            b2 = b2 > o2 ? b2 : o2;
+            b2 = b2 > lo ? b2 : lo;
+        }
+        Key worth = b1;
+        if constexpr (WIDE)
+            if (p.group_top == 2) worth = order_key(key_value(b1) + key_value(b2));
+        if (part != 0 || g >= p.groups) worth = 0;
+        uint64_t keptmask = 0;
+        for (int r = 0; r < p.kept; ++r) {
+            const int l = best_lane(worth);
+            keptmask |= 1ull << (l >> shift);
+            if (lane == l) worth = 0;
+        }
+        int eg = e0 / per, rem = e0 - eg * per;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            if (e0 + j >= p.E || !((keptmask >> eg) & 1)) key[j] = 0;
+            if (++rem == per) {
+                rem = 0;
+                ++eg;
+            }
+        }
+    }
+    // topk rounds over the lanes' best; lane r keeps the r-th choice
     int mine = 0;
     float w = 0.0f;
     for (int r = 0; r < p.topk; ++r) {
-        uint64_t k = key[0];
-        int i = lane;
+        Key best = key[0];
+        int at = 0;
+        float sv = s[0];
 #pragma unroll
         for (int j = 1; j < EPL; ++j)
-            if (key[j] > k) {
-                k = key[j];
-                i = j * 64 + lane;
-            }
-        wave_best(k, i);
-        float sv = 0.0f;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if (i == j * 64 + lane) {
-                key[j] = 0;
+            if (key[j] > best) {
+                best = key[j];
+                at = j;
                 sv = s[j];
             }
-        sv = __shfl(sv, i & 63);
+        const int l = best_lane(best);
+        const int e = l * EPL + (int)lane_value((uint32_t)at, l);
+        sv = lane_value(sv, l);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            if (e0 + j == e) key[j] = 0;
         if (lane == r) {
-            mine = i;
+            mine = e;
             w = sv;
         }
     }
@@ -214,31 +287,37 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteParams p) {
     }
 }
 
-// The gradient of the logits, one wave per token.  With p_j the chosen scores
-// over their sum S (renormalised) or the scores: ds_j = scale / S * (dw_j -
-// sum_i dw_i p_i), or scale * dw_j; a sigmoid's dl = s (1 - s) ds.  Softmax:
-// dl = s (ds - sum ds s); renormalised, that sum is zero by construction and
-// s_j / S = p_j, so dl_j = scale p_j (dw_j - sum dw p) on the chosen and
-// exactly zero elsewhere.
+// The gradient of the logits, one wave per token (lanes hold experts as above).
+// With p_j the chosen scores over their sum S (renormalised) or the scores: ds_j
+// = scale / S * (dw_j - sum_i dw_i p_i), or scale * dw_j; a sigmoid's dl = s (1 -
+// s) ds.  Softmax: dl = s (ds - sum ds s); renormalised, that sum is zero by
+// construction and s_j / S = p_j, so dl_j = scale p_j (dw_j - sum dw p) on the
+// chosen and exactly zero elsewhere.
 template <typename T, int EPL>
 __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteParams p) {
     const int lane = threadIdx.x & 63;
     const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (t >= p.T) return;
     const float ninf = -__builtin_inff();
+    const int e0 = lane * EPL;
+    int e_r = -1;
+    float dw_r = 0.0f;
+    if (lane < p.topk) {
+        e_r = p.idx[t * p.topk + lane];
+        dw_r = p.dweights[t * p.topk + lane];
+    }
     float x[EPL], s[EPL], ds[EPL];
     float top = ninf;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-        const int e = j * 64 + lane;
-        x[j] = e < p.E ? route_load<T>(p.logits, t * p.ld + e) : ninf;
+        x[j] = e0 + j < p.E ? route_load<T>(p.logits, t * p.ld + e0 + j) : ninf;
         if (x[j] != x[j]) x[j] = ninf;
         top = fmaxf(top, x[j]);
         ds[j] = 0.0f;
     }
-    float total = 0.0f;
     if (p.score == 0) {
         top = wave_max(top);
+        float total = 0.0f;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             s[j] = x[j] == ninf ? 0.0f : x[j] == top ? 1.0f : expf(x[j] - top);
@@ -254,23 +333,17 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteParams p) 
     }
     // the weights' gradients to their experts' lanes (an expert named twice
     // gets the sum, in slot order), and the chosen scores' sums
-    int e_r = -1;
-    float dw_r = 0.0f;
-    if (lane < p.topk) {
-        e_r = p.idx[t * p.topk + lane];
-        dw_r = p.dweights[t * p.topk + lane];
-    }
     float S = 0.0f, inner = 0.0f;
     float n[EPL];                          // times an expert was chosen
 #pragma unroll
     for (int j = 0; j < EPL; ++j) n[j] = 0.0f;
     for (int r = 0; r < p.topk; ++r) {
-        const int e = __shfl(e_r, r);
-        const float dw = __shfl(dw_r, r);
+        const int e = (int)lane_value((uint32_t)e_r, r);
+        const float dw = lane_value(dw_r, r);
         if (e < 0 || e >= p.E) continue;
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-            if (e == j * 64 + lane) {
+            if (e == e0 + j) {
                 ds[j] += dw;
                 n[j] += 1.0f;
                 S += s[j];
@@ -278,9 +351,9 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteParams p) 
             }
     }
     float out[EPL];
+    inner = wave_sum(inner);
     if (p.renormalize) {
         S = wave_sum(S);
-        inner = wave_sum(inner);
         const float inv = S > 0.0f ? 1.0f / S : 0.0f;
         const float mean = inner * inv;
 #pragma unroll
@@ -289,16 +362,13 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteParams p) 
             out[j] = p.score == 0 ? d : d * (1.0f - s[j]);
         }
     } else {
-        inner = wave_sum(inner);
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
             out[j] = p.scale * (p.score == 0 ? s[j] * (ds[j] - inner) : s[j] * (1.0f - s[j]) * ds[j]);
     }
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        const int e = j * 64 + lane;
-        if (e < p.E) static_cast<T*>(p.dlogits)[t * p.ldd + e] = (T)out[j];
-    }
+    for (int j = 0; j < EPL; ++j)
+        if (e0 + j < p.E) static_cast<T*>(p.dlogits)[t * p.ldd + e0 + j] = (T)out[j];
 }
 
 struct PlanParams {

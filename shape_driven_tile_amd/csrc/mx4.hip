@@ -233,18 +233,20 @@ RouteParams route_params(int64_t T, int64_t E, const void* logits, int64_t ld, c
 }
 
 template <typename T, int EPL>
-const void* route_kernel(bool backward) {
-    return backward ? reinterpret_cast<const void*>(&moe_route_backward_kernel<T, EPL>)
-                    : reinterpret_cast<const void*>(&moe_route_kernel<T, EPL>);
+const void* route_kernel(const RouteParams& p, bool backward) {
+    if (backward) return reinterpret_cast<const void*>(&moe_route_backward_kernel<T, EPL>);
+    return p.bias != nullptr || p.group_top == 2
+               ? reinterpret_cast<const void*>(&moe_route_kernel<T, EPL, true>)
+               : reinterpret_cast<const void*>(&moe_route_kernel<T, EPL, false>);
 }
 
 template <typename T>
 int launch_route(RouteParams& p, bool backward, void* stream) {
-    const void* k = p.E <= 64    ? route_kernel<T, 1>(backward)
-                    : p.E <= 128 ? route_kernel<T, 2>(backward)
-                    : p.E <= 256 ? route_kernel<T, 4>(backward)
-                    : p.E <= 512 ? route_kernel<T, 8>(backward)
-                                 : route_kernel<T, 16>(backward);
+    const void* k = p.E <= 64    ? route_kernel<T, 1>(p, backward)
+                    : p.E <= 128 ? route_kernel<T, 2>(p, backward)
+                    : p.E <= 256 ? route_kernel<T, 4>(p, backward)
+                    : p.E <= 512 ? route_kernel<T, 8>(p, backward)
+                                 : route_kernel<T, 16>(p, backward);
     return launch(k, ceil_div(p.T, 4), 256, p, stream);
 }
 
