@@ -350,10 +350,12 @@ def check_gemv_kn_args(N, K, x_ptr, B_ptr, ldb, y_ptr) -> int:
 # ---- compute entry points (torch tensors on a ROCm device) -------------------
 
 def _stream_handle(stream):
+    """The HIP stream of `stream`, or the current one of the current device (asked
+    for its handle: a torch.cuda.Stream object would cost 2.8 us a call)."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _rows(t, name, dtype=None):
@@ -688,10 +690,14 @@ class Mx4:
     @classmethod
     def empty(cls, rows: int, K: int, experts: int | None = None, device="cuda") -> "Mx4":
         import torch
+        rows, K = int(rows), int(K)
         lead = () if experts is None else (int(experts),)
-        q = torch.empty(lead + (int(rows), mx4_row_bytes(K)), dtype=torch.uint8, device=device)
-        s = torch.empty(lead + (mx4_scale_bytes(rows, K),), dtype=torch.uint8, device=device)
-        return cls(q, s, rows, K)
+        m = cls.__new__(cls)                 # tensors that fit by construction: no checks
+        m.q = torch.empty(lead + (rows, -(-K // 32) * 16), dtype=torch.uint8, device=device)
+        m.s = torch.empty(lead + (-(-rows // 64) * -(-K // 256) * 512,), dtype=torch.uint8,
+                          device=device)
+        m.rows, m.K = rows, K
+        return m
 
     def ldq(self) -> int:
         """Bytes from row to row (a single row's are its own bytes)."""
@@ -935,17 +941,17 @@ class MoePlan:
     def empty(cls, tokens: int, topk: int, experts: int, device="cuda") -> "MoePlan":
         import torch
         p = cls()
-        p.tokens, p.topk, p.experts = int(tokens), int(topk), int(experts)
-        p.size = moe_plan_rows(tokens, topk, experts)
-        sizes = (p.experts, p.experts + 1, p.size, p.tokens * p.topk, p.size // 64)
+        p.tokens, p.topk, p.experts = tokens, topk, experts = int(tokens), int(topk), int(experts)
+        p.size = size = moe_plan_rows(tokens, topk, experts)
+        sizes = (experts, experts + 1, size, tokens * topk, size // 64)
         flat = torch.empty(sum(sizes), dtype=torch.int32, device=device)
         p.counts, p.offsets, p.rows, p.pos, p.tiles = flat.split(sizes)
-        base, at = flat.data_ptr(), 0
-        ptrs = []
-        for n in sizes:
-            ptrs.append(base + 4 * at)
-            at += n
-        p._struct = SdtMoePlan(p.tokens, p.topk, p.experts, *ptrs)
+        at = flat.data_ptr()
+        offsets = at + 4 * experts
+        rows = offsets + 4 * experts + 4
+        pos = rows + 4 * size
+        p._struct = SdtMoePlan(tokens, topk, experts, at, offsets, rows, pos,
+                               pos + 4 * tokens * topk)
         return p
 
 

@@ -29,13 +29,17 @@ class Mx4Experts:
                                      up._experts(self.experts, "up"),
                                      down._experts(self.experts, "down"))
         self._workspace = None
+        self._holds = None                       # the sizes that the buffer was last checked for
 
     def workspace(self, tokens: int, topk: int):
         import torch
+        if self._holds == (tokens, topk):
+            return self._workspace
         need = sdt.moe_experts_workspace_size(tokens, topk, self.experts, self.N, self.K)
         if self._workspace is None or self._workspace.numel() < need:
             self._workspace = torch.empty(max(need, 16), dtype=torch.uint8,
                                           device=self.weights[0].q.device)
+        self._holds = (tokens, topk)
         return self._workspace
 
     def __call__(self, x, idx, weights, plan: sdt.MoePlan | None = None, out=None, stream=None):
@@ -51,7 +55,9 @@ class Mx4Experts:
             raise ValueError(f"plan is of {plan.tokens} tokens, {plan.topk} of {plan.experts} experts")
         if out is None:
             ld = -(-self.K // 8) * 8
-            out = torch.empty(T, ld, dtype=x.dtype, device=x.device)[:, :self.K]
+            out = torch.empty(T, ld, dtype=x.dtype, device=x.device)
+            if ld != self.K:
+                out = out[:, :self.K]
         sdt.moe_experts_mx4(self.layer, x, idx, weights, plan, out, self.workspace(T, topk), stream)
         return out
 
