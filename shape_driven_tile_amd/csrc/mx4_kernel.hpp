@@ -1182,81 +1182,113 @@ struct Mx4Gemv {
     int N, K, rowbytes, nkt;
 };
 
-// y of 16 rows of B per workgroup, whose NW waves split the k-tiles.  Lane l
-// takes row l % 16, blocks 2 (l / 16) and + 1 of a k-tile: 32 bytes of codes,
-// converted two at a time to the activations' type (exact) and multiplied by
-// pairs into an fp32 sum per block, which the block's scale then multiplies
-// once.  The four quarters' sums are added by lane exchanges, the waves' in
-// wave order through LDS.
+// y of 16 rows of B per workgroup, whose NW waves split the k-tiles.  Bound by the
+// stream of B, which comes as in mx4_skinny_body: straight into LDS of each wave,
+// eight lanes to a row's 128 bytes, NS k-tiles in flight.  The activations are in
+// LDS, kGemvK of them at a time, zeros past K.  Lane l takes row l % 16, blocks
+// 2 (l / 16) and + 1 of a k-tile: the codes are converted two at a time to
+// the activations' type (exact) and multiplied by pairs into an fp32 sum per
+// block, which the block's scale then multiplies once.  The four quarters' sums
+// are added by lane exchanges, the waves' in wave order through LDS.  12288 x 4096:
+// 8.6 us (9.2 with 32 rows and four waves, 11.0 with 32 and eight; the conversions
+// left out, the time is the same).
+constexpr int kGemvK = 8192;
+
 template <typename Elt, int NW>
 __global__ __launch_bounds__(NW * 64) void mx4_gemv_kernel(Mx4Gemv p) {
     typedef typename Elt::scalar scalar;
     typedef typename Elt::vec2 vec2;
-    __shared__ float red[NW * 16];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = blockIdx.x * 16;
+    constexpr int NS = 3;
+    constexpr int BN = 16;
+    constexpr int CODES = BN * 128, STAGE = CODES + kMx4Tile;
+    constexpr int L = CODES / 1024 + 1;            // loads of a k-tile
+    __shared__ int4_t stages[NW * NS * STAGE / 16];
+    __shared__ uint4_t xs[kGemvK / 8];
+    __shared__ float red[NW * BN];
+    const int t = threadIdx.x;
+    const int lane = t & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int n0 = blockIdx.x * BN;
     const int fr = lane & 15, fq = lane >> 4;
-    const int rows_b = min(16, p.N - n0);
+    const int fsw = swz_pp(fr);
+    const int rows_b = min(BN, p.N - n0);
     const uint32_t srow = (uint32_t)p.nkt * kMx4Tile;
     const __amdgpu_buffer_rsrc_t rb =
         make_rsrc(p.B + (int64_t)n0 * p.ldb, (uint32_t)((rows_b - 1) * p.ldb + p.rowbytes));
     const __amdgpu_buffer_rsrc_t rsb = make_rsrc(p.SB + (int64_t)(n0 / 64) * srow, srow);
-    const uint32_t voff_b = (uint32_t)(fr * p.ldb) + fq * 32;
-    const uint32_t voff_s = lane * 8 + ((n0 >> 4) & 3) * 2;
-    const bool aligned = (reinterpret_cast<uintptr_t>(p.x) & 15) == 0;
+    uint32_t voff[CODES / 1024];
+    const int pos = (lane & 7) ^ swz_pp(lane >> 3);    // chunk of the k-tile at this place
+#pragma unroll
+    for (int j = 0; j < CODES / 1024; ++j)
+        voff[j] = (uint32_t)((j * 8 + (lane >> 3)) * p.ldb) + ((pos & 3) * 2 + (pos >> 2)) * 16;
+    int4_t* const mine = stages + wave * (NS * STAGE / 16);
+    auto load = [&](int kt, int stage) {
+        int4_t* at = mine + stage * (STAGE / 16);
+#pragma unroll
+        for (int j = 0; j < CODES / 1024; ++j) dma16(rb, at + j * 64, voff[j] + (uint32_t)kt * 128, 0);
+        if (lane < 32) dma16(rsb, at + CODES / 16, lane * 16, kt * kMx4Tile);
+    };
+
     float sum = 0.0f;
-    for (int kt = wave; kt < p.nkt; kt += NW) {
-        int4_t w[2];
-        w[0] = __builtin_bit_cast(int4_t,
-                                  __builtin_amdgcn_raw_buffer_load_b128(rb, voff_b + kt * 128, 0, 0));
-        w[1] = __builtin_bit_cast(
-            int4_t, __builtin_amdgcn_raw_buffer_load_b128(rb, voff_b + 16 + kt * 128, 0, 0));
-        const int sc =
-            (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsb, voff_s, kt * kMx4Tile, 0);
-        const int k0 = kt * 256 + fq * 64;
+    for (int k0 = 0; k0 < p.nkt; k0 += kGemvK / 256) {
+        const int n1 = min(p.nkt - k0, kGemvK / 256);   // k-tiles of this turn
+        const int n = (n1 - wave + NW - 1) / NW;        // this wave's
+        for (int j = 0; j < min(n, NS); ++j) load(k0 + wave + j * NW, j);
+        if (k0 > 0) __syncthreads();                    // xs has been read
+        for (int i = t; i < n1 * 32; i += NW * 64)
+            xs[i] = mx4_load8(p.x + (int64_t)k0 * 256 + i * 8, p.K - k0 * 256 - i * 8);
+        wait_lds();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+        int stage = 0;
+        for (int j = 0; j < n; ++j) {
+            const int younger = min(n - 1 - j, NS - 1);
+            if (younger == 2)
+                wait_global_loads<2 * L>();
+            else if (younger == 1)
+                wait_global_loads<L>();
+            else
+                wait_global_loads<0>();
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("" ::: "memory");
+            const int4_t* at = mine + stage * (STAGE / 16);
+            int4_t w[2];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int kb = k0 + s * 32;
-            const int valid = p.K - kb;
-            if (valid <= 0) continue;
-            uint4_t xv[4];
-            if (aligned && valid >= 32) {
+            for (int s = 0; s < 2; ++s) w[s] = at[fr * 8 + ((4 * s + fq) ^ fsw)];
+            const uint32_t sc =
+                reinterpret_cast<const uint16_t*>(at + CODES / 16)[lane * 4 + ((n0 >> 4) & 3)];
+            wait_lds();
+            __builtin_amdgcn_sched_barrier(0);
+            if (j + NS < n) load(k0 + wave + (j + NS) * NW, stage);
+            const uint4_t* xk = xs + (wave + j * NW) * 32 + fq * 8;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    xv[c] = *reinterpret_cast<const uint4_t*>(p.x + kb + 8 * c);
-            } else {
+            for (int s = 0; s < 2; ++s) {
+                float part = 0.0f;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
+                    const uint4_t xv = xk[s * 4 + c];
 #pragma unroll
                     for (int d = 0; d < 4; ++d) {
-                        const int k = 8 * c + 2 * d;
-                        const uint32_t lo = k < valid ? p.x[kb + k] : 0u;
-                        const uint32_t hi = k + 1 < valid ? p.x[kb + k + 1] : 0u;
-                        xv[c][d] = lo | (hi << 16);
+                        const uint32_t xw = xv[d];
+                        part = Elt::dot2(Elt::codes((uint32_t)w[s][c], d),
+                                         __builtin_bit_cast(vec2, xw), part);
                     }
-            }
-            float part = 0.0f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const uint32_t xw = xv[c][d];
-                    part = Elt::dot2(Elt::codes((uint32_t)w[s][c], d), __builtin_bit_cast(vec2, xw), part);
                 }
-            sum += part * mx4_scale_value((sc >> (8 * s)) & 255);
+                sum += part * mx4_scale_value((sc >> (8 * s)) & 255);
+            }
+            stage = stage + 1 == NS ? 0 : stage + 1;
         }
     }
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
-    if (lane < 16) red[wave * 16 + lane] = sum;
+    if (lane < 16) red[wave * BN + lane] = sum;
     __syncthreads();
-    if (threadIdx.x < rows_b) {
-        float s = red[threadIdx.x];
+    if (t < rows_b) {
+        float s = red[t];
 #pragma unroll
-        for (int w = 1; w < NW; ++w) s += red[w * 16 + threadIdx.x];
+        for (int w = 1; w < NW; ++w) s += red[w * BN + t];
         const scalar v = (scalar)s;
-        p.y[n0 + threadIdx.x] = __builtin_bit_cast(uint16_t, v);
+        p.y[n0 + t] = __builtin_bit_cast(uint16_t, v);
     }
 }
 
