@@ -395,6 +395,17 @@ __device__ __forceinline__ int uniform_load(const int32_t* p) {
         reinterpret_cast<uint64_t>(p));
 }
 
+// LDS place of a row's 16-byte chunks: chunk c (block c of the k-tile) of row r is
+// kept at c ^ mx4_swz(r).  A fragment read of half s takes chunk 2 g + s in quarter
+// g; its bank pattern is that of the 16-bit kernels (chunk 4 s + g at 4 s + g ^
+// swz_pp(r)) with the places' three bits turned round, so it is as free of
+// conflicts.  Chunks in order (and not halves first) matter to the loads: four
+// neighbouring lanes fetch one aligned 64 bytes; fetching every other chunk they
+// took twice the time (a 128 x 128 k-tile's loads 1080 clocks).
+__device__ __forceinline__ int mx4_swz(int row) {
+    return ((row & 1) ? 1 : 0) ^ ((row & 2) ? 3 : 0) ^ ((row & 4) ? 6 : 0);
+}
+
 // acc += B_frag . A_frag^T over one 128-deep half; BYTE_A, BYTE_B pick the
 // lane's scale bytes.
 template <int BYTE_B, int BYTE_A>
@@ -480,8 +491,8 @@ __device__ __forceinline__ void mx4_skinny_body(const Mx4Gemm& p, char* smem, in
 
     __amdgpu_buffer_rsrc_t rb[MATS], rsb[MATS];
     uint32_t voff_b[MATS][B_BYTES / 1024], voff_a[A_BYTES / 1024];
-    const int pos = (lane & 7) ^ swz_pp(lane >> 3);   // chunk of the k-tile at this place
-    const uint32_t chunk = ((pos & 3) * 2 + (pos >> 2)) * 16;
+    const int pos = (lane & 7) ^ mx4_swz(lane >> 3);   // chunk of the k-tile at this place
+    const uint32_t chunk = pos * 16;
 #pragma unroll
     for (int m = 0; m < MATS; ++m) {
         const uint8_t* q = m == 0 ? p.B + e * p.eqb : p.B2 + e * p.eqb2;
@@ -530,7 +541,7 @@ __device__ __forceinline__ void mx4_skinny_body(const Mx4Gemm& p, char* smem, in
             for (int j = 0; j < NMB; ++j) acc[m][i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 
     const int n = (p.nkt - wave + NW - 1) / NW;   // this wave's k-tiles (0 or less: none)
-    const int fsw = swz_pp(fr);
+    const int fsw = mx4_swz(fr);
     for (int j = 0; j < min(n, NS); ++j) load(wave + j * NW, j);
     int stage = 0;
     for (int j = 0; j < n; ++j) {
@@ -547,7 +558,7 @@ __device__ __forceinline__ void mx4_skinny_body(const Mx4Gemm& p, char* smem, in
         int4_t fb[MATS][2][PB], fa[2][NMB];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int c = (4 * s + fq) ^ fsw;
+            const int c = (2 * fq + s) ^ fsw;
 #pragma unroll
             for (int m = 0; m < MATS; ++m)
 #pragma unroll
@@ -805,9 +816,7 @@ __device__ __forceinline__ void mx4_store_quantized(const Mx4Gemm& p, const floa
 
 // The tiled product: output tiles of BM x BN, WM x WN waves of 16x16x128 MFMAs.
 // A stage holds the codes of BM + BN rows x 128 bytes and their scale tiles,
-// loaded straight into LDS; NS stages.  16-byte chunk 2 g + s of row r (block
-// 2 g + s of the k-tile) is kept at position (4 s + g) ^ swz_pp(r), so a fragment
-// read of half s has the conflict-free pattern of the 16-bit kernels.
+// loaded straight into LDS; NS stages.  A row's chunks lie as mx4_swz says.
 //
 // A workgroup takes tiles in turn, its k-tiles one stream: once the fragments of a
 // k-tile are in registers the loads of the one NS further on go into its stage,
@@ -939,17 +948,17 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
 #pragma unroll
     for (int j = 0; j < A_DMA; ++j) {
         const int row = (wave * A_DMA + j) * 8 + (lane >> 3);
-        const int pos = (lane & 7) ^ swz_pp(row);
-        voff_a[j] = (uint32_t)(row * p.lda) + ((pos & 3) * 2 + (pos >> 2)) * 16;
+        const int pos = (lane & 7) ^ mx4_swz(row);
+        voff_a[j] = (uint32_t)(row * p.lda) + pos * 16;
     }
 #pragma unroll
     for (int j = 0; j < B_DMA; ++j) {
         const int row = (wave * B_DMA + j) * 8 + (lane >> 3);
-        const int pos = (lane & 7) ^ swz_pp(row);
+        const int pos = (lane & 7) ^ mx4_swz(row);
         // gated: LDS rows 64 w + 32 h + i are row 32 w + i of matrix h
         const int src = GATED ? (row >> 6) * 32 + (row & 31) : row;
         voff_b[j] = (uint32_t)(src * (GATED && (row & 32) ? p.ldb2 : p.ldb)) +
-                    ((pos & 3) * 2 + (pos >> 2)) * 16;
+                    pos * 16;
     }
     Place at = locate(tile), next_at = at;        // the tile that is multiplied, that is loaded
     int load_kt = 0;
@@ -1020,7 +1029,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
     };
 
     const int frow = lane & 15, fq = lane >> 4;
-    const int fsw = swz_pp(frow);
+    const int fsw = mx4_swz(frow);
     const int a_row0 = wave_m * WTM + frow;
     const int b_row0 = A_UNITS / 8 + wave_n * WTN + frow;
     constexpr int SAW = FM / 2, SBW = FN / 2;     // scale dwords per lane (two parts each)
@@ -1030,7 +1039,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
     };
     auto read_half = [&](int stage, int s, Frags& f) {
         const int4_t* base = smem + stage * STAGE;
-        const int chunk = (4 * s + fq) ^ fsw;
+        const int chunk = (2 * fq + s) ^ fsw;
 #pragma unroll
         for (int j = 0; j < FM; ++j) f.a[s][j] = base[(a_row0 + j * 16) * 8 + chunk];
 #pragma unroll
@@ -1210,17 +1219,17 @@ __global__ __launch_bounds__(NW * 64) void mx4_gemv_kernel(Mx4Gemv p) {
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int n0 = blockIdx.x * BN;
     const int fr = lane & 15, fq = lane >> 4;
-    const int fsw = swz_pp(fr);
+    const int fsw = mx4_swz(fr);
     const int rows_b = min(BN, p.N - n0);
     const uint32_t srow = (uint32_t)p.nkt * kMx4Tile;
     const __amdgpu_buffer_rsrc_t rb =
         make_rsrc(p.B + (int64_t)n0 * p.ldb, (uint32_t)((rows_b - 1) * p.ldb + p.rowbytes));
     const __amdgpu_buffer_rsrc_t rsb = make_rsrc(p.SB + (int64_t)(n0 / 64) * srow, srow);
     uint32_t voff[CODES / 1024];
-    const int pos = (lane & 7) ^ swz_pp(lane >> 3);    // chunk of the k-tile at this place
+    const int pos = (lane & 7) ^ mx4_swz(lane >> 3);    // chunk of the k-tile at this place
 #pragma unroll
     for (int j = 0; j < CODES / 1024; ++j)
-        voff[j] = (uint32_t)((j * 8 + (lane >> 3)) * p.ldb) + ((pos & 3) * 2 + (pos >> 2)) * 16;
+        voff[j] = (uint32_t)((j * 8 + (lane >> 3)) * p.ldb) + pos * 16;
     int4_t* const mine = stages + wave * (NS * STAGE / 16);
     auto load = [&](int kt, int stage) {
         int4_t* at = mine + stage * (STAGE / 16);
@@ -1254,7 +1263,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_gemv_kernel(Mx4Gemv p) {
             const int4_t* at = mine + stage * (STAGE / 16);
             int4_t w[2];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) w[s] = at[fr * 8 + ((4 * s + fq) ^ fsw)];
+            for (int s = 0; s < 2; ++s) w[s] = at[fr * 8 + ((2 * fq + s) ^ fsw)];
             const uint32_t sc =
                 reinterpret_cast<const uint16_t*>(at + CODES / 16)[lane * 4 + ((n0 >> 4) & 3)];
             wait_lds();

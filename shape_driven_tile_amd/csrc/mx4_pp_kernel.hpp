@@ -65,8 +65,8 @@ __global__ __launch_bounds__(512) void mx4_pp_kernel(Mx4Gemm p) {
 #pragma unroll
     for (int j = 0; j < DMA; ++j) {
         const int row = lw * 64 + j * 8 + (lane >> 3);
-        const int pos = (lane & 7) ^ swz_pp(row);
-        voff[j] = (uint32_t)(row * ld) + ((pos & 3) * 2 + (pos >> 2)) * 16;
+        const int pos = (lane & 7) ^ mx4_swz(row);
+        voff[j] = (uint32_t)(row * ld) + pos * 16;
     }
     // The k offset moves the descriptor: rows past M or N and the last row's
     // bytes past its blocks lie past its end and read as zero.
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(512) void mx4_pp_kernel(Mx4Gemm p) {
         for (int j = 0; j < FM; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 
     const int frow = lane & 15, fq = lane >> 4;
-    const int fsw = swz_pp(frow);
+    const int fsw = mx4_swz(frow);
     const int a_row0 = wave_m * WTM + frow;
     const int b_row0 = wave_n * WTN + frow;
     int4_t fa[2][FM], fb[2][FN];
@@ -111,7 +111,7 @@ __global__ __launch_bounds__(512) void mx4_pp_kernel(Mx4Gemm p) {
         const int4_t* bbase = smem + B_BASE + sb * UNITS;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int chunk = (4 * h + fq) ^ fsw;
+            const int chunk = (2 * fq + h) ^ fsw;
 #pragma unroll
             for (int j = 0; j < FM; ++j) fa[h][j] = abase[(a_row0 + j * 16) * 8 + chunk];
 #pragma unroll
