@@ -1009,13 +1009,24 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
         }
     };
     auto advance = [&]() {
-        if (++load_kt == nkt) {
-            load_kt = 0;
-            tile += turn;
-            loads = tile < last;
-            if (loads) {
-                next_at = locate(tile);
-                describe(next_at);
+        if (++load_kt < nkt) return;
+        load_kt = 0;
+        if (!loads) return;
+        tile += turn;
+        loads = tile < last;
+        if (loads) {
+            next_at = locate(tile);
+            describe(next_at);
+        } else {
+            // Nothing is left: the loads go on, so that the loop has no branch for
+            // them, from empty descriptors (zeros, to stages that are not read).
+            ra = make_rsrc(p.A, 0);
+            rb = make_rsrc(p.B, 0);
+            rsa = make_rsrc(p.SA, 0);
+            rsb = make_rsrc(p.SB, 0);
+            if constexpr (GATED) {
+                rb2 = make_rsrc(p.B, 0);
+                rsb2 = make_rsrc(p.SB, 0);
             }
         }
     };
@@ -1123,16 +1134,13 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
         return;
     }
     describe(at);
-    for (int j = 0; j < NS && loads; ++j) {
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
         load_codes(j);
         load_scales(j);
         advance();
     }
-    // k-tile 0 has landed (the others may still be on their way)
-    if (loads)
-        wait_global_loads<(NS - 1) * L>();
-    else
-        wait_global_loads<0>();
+    wait_global_loads<(NS - 1) * L>();            // k-tile 0 has landed
     barrier();
     // One k-tile a turn: `kt` of tile `at`, landed in stage s.
     int kt = 0, s = 0;
@@ -1147,37 +1155,31 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
         mfma_half(std::integral_constant<int, 0>{}, f);
         pin();
         barrier();                                // every wave has read stage s
-        const bool full = loads;                  // NS - 1 younger k-tiles than the next will fly
-        if (loads) {
-            load_codes(s);
-            mfma_half(std::integral_constant<int, 1>{}, f);
-            // a load between every two MFMAs (masks: 0x020 global read, 0x008 MFMA)
+        load_codes(s);
+        mfma_half(std::integral_constant<int, 1>{}, f);
+        // a load between every two MFMAs (masks: 0x020 global read, 0x008 MFMA)
 #pragma unroll
-            for (int m = 0; m < A_DMA + B_DMA; ++m) {
-                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, FM * FN / (A_DMA + B_DMA), 0);
-            }
-            pin();
-            load_scales(s);
-            advance();
-        } else {
-            mfma_half(std::integral_constant<int, 1>{}, f);
-            pin();
+        for (int m = 0; m < A_DMA + B_DMA; ++m) {
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, FM * FN / (A_DMA + B_DMA), 0);
         }
+        pin();
+        load_scales(s);
+        advance();
         s = (s + 1 == NS) ? 0 : s + 1;
         if (++kt == nkt) {
             store();
-            if (!more) return;
+            if (!more) break;
             kt = 0;
             at = next_at;
             clear();
         }
-        if (full)
-            wait_global_loads<(NS - 1) * L>();    // stores, if any, only make it longer
-        else
-            wait_global_loads<0>();
-        barrier();                                // the next k-tile has landed
+        // the next k-tile has landed: at most the NS - 1 after it are on their way
+        // (stores, younger, only make the wait longer)
+        wait_global_loads<(NS - 1) * L>();
+        barrier();
     }
+    wait_global_loads<0>();
 }
 
 // ---- 16-bit activations, MX4 weights, one token -------------------------------------
