@@ -19,6 +19,7 @@ namespace {
 
 constexpr int64_t kMaxK = int64_t(1) << 23;
 constexpr int64_t kMaxLd = (int64_t(1) << 22) + 16;   // bytes, exclusive
+constexpr int64_t kMaxRows = INT_MAX - 255;           // the last tile's end fits 32 bits
 
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
@@ -40,7 +41,7 @@ int check_mx4(int64_t rows, int64_t K, const void* Q, int64_t ldq, const void* S
     if (rows == 0 || K == 0) return SDT_OK;
     if (!Q || !S) return SDT_ERR_INVALID_ARG;
     if (ldq < row_bytes(K)) return SDT_ERR_INVALID_ARG;
-    if (K > kMaxK || rows > INT_MAX || ldq >= kMaxLd) return SDT_ERR_UNSUPPORTED;
+    if (K > kMaxK || rows > kMaxRows || ldq >= kMaxLd) return SDT_ERR_UNSUPPORTED;
     if (misaligned(Q, 16) || misaligned(S, 16) || ldq % 16 != 0) return SDT_ERR_UNSUPPORTED;
     return SDT_OK;
 }
@@ -141,7 +142,7 @@ int gemm(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void
     if (rc == SDT_OK) rc = check_mx4(M, K, A, lda, SA);
     if (rc == SDT_OK) rc = check_mx4(N, K, B, ldb, SB);
     if (rc != SDT_OK) return rc;
-    if (M > INT_MAX || N > INT_MAX) return SDT_ERR_UNSUPPORTED;
+    if (M > kMaxRows || N > kMaxRows) return SDT_ERR_UNSUPPORTED;
     DeviceInfo dev;
     rc = device_info(&dev);
     if (rc != SDT_OK) return rc;
@@ -151,8 +152,8 @@ int gemm(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void
     p.B = static_cast<const uint8_t*>(B);
     p.SB = static_cast<const uint8_t*>(SB);
     p.C = static_cast<uint16_t*>(C);
-    p.lda = lda;
-    p.ldb = ldb;
+    p.lda = (uint32_t)lda;
+    p.ldb = (uint32_t)ldb;
     p.ldc = ldc;
     p.M = (int)M;
     p.N = (int)N;
@@ -180,7 +181,7 @@ int gemv(int64_t N, int64_t K, const void* x, const void* B, int64_t ldb, const 
     if (!y || (!x && K > 0)) return SDT_ERR_INVALID_ARG;
     int rc = check_mx4(N, K, B, ldb, SB);
     if (rc != SDT_OK) return rc;
-    if (N > INT_MAX || misaligned(x, 2) || misaligned(y, 2)) return SDT_ERR_UNSUPPORTED;
+    if (N > kMaxRows || misaligned(x, 2) || misaligned(y, 2)) return SDT_ERR_UNSUPPORTED;
     Mx4Gemv p;
     p.x = static_cast<const uint16_t*>(x);
     p.B = static_cast<const uint8_t*>(B);
@@ -341,7 +342,7 @@ int moe_gemm(const sdt_moe_plan* plan, int64_t N, int64_t K, const void* A, int6
     if (!out.q) rc = check_out(rows, N, C, ldc);
     if (rc == SDT_OK) rc = check_mx4(rows, K, A, lda, SA);
     if (rc != SDT_OK) return rc;
-    if (N > INT_MAX) return SDT_ERR_UNSUPPORTED;
+    if (N > kMaxRows) return SDT_ERR_UNSUPPORTED;
     DeviceInfo dev;
     rc = device_info(&dev);
     if (rc != SDT_OK) return rc;
@@ -351,8 +352,8 @@ int moe_gemm(const sdt_moe_plan* plan, int64_t N, int64_t K, const void* A, int6
     p.B = static_cast<const uint8_t*>(B->q);
     p.SB = static_cast<const uint8_t*>(B->s);
     p.C = static_cast<uint16_t*>(C);
-    p.lda = lda;
-    p.ldb = B->ldq;
+    p.lda = (uint32_t)lda;
+    p.ldb = (uint32_t)B->ldq;
     p.ldc = ldc;
     p.M = (int)rows;
     p.N = (int)N;
@@ -367,7 +368,7 @@ int moe_gemm(const sdt_moe_plan* plan, int64_t N, int64_t K, const void* A, int6
     if (up) {
         p.B2 = static_cast<const uint8_t*>(up->q);
         p.SB2 = static_cast<const uint8_t*>(up->s);
-        p.ldb2 = up->ldq;
+        p.ldb2 = (uint32_t)up->ldq;
         p.eqb2 = up->q_expert;
         p.esb2 = up->s_expert;
     }
@@ -590,7 +591,7 @@ extern "C" int mx4_pack_scales(int64_t rows, int64_t K, const void* R, int64_t l
     if (rows == 0 || K == 0) return SDT_OK;
     const int64_t nb = ceil_div(K, 32);
     if (!R || !S || ldr < nb) return SDT_ERR_INVALID_ARG;
-    if (K > kMaxK || rows > INT_MAX || misaligned(S, 16)) return SDT_ERR_UNSUPPORTED;
+    if (K > kMaxK || rows > kMaxRows || misaligned(S, 16)) return SDT_ERR_UNSUPPORTED;
     const int64_t grid = ceil_div(rows, 64) * k_tiles(K);
     if (grid > INT_MAX) return SDT_ERR_UNSUPPORTED;
     const uint8_t* r = static_cast<const uint8_t*>(R);

@@ -375,7 +375,8 @@ struct Mx4Gemm {
     const uint8_t *A, *B, *B2;     // codes (B2: the gated product's second matrix)
     const uint8_t *SA, *SB, *SB2;  // tiled scales
     uint16_t* C;
-    int64_t lda, ldb, ldb2, ldc;   // bytes; ldc elements
+    uint32_t lda, ldb, ldb2;       // bytes
+    int64_t ldc;                   // elements
     int M, N;
     int rowbytes, nkt;             // codes of one row; k-tiles
     int gm, gn, nxcd;              // output tiles (grouped: gm 64-row tiles of the plan)
@@ -452,12 +453,11 @@ __device__ __forceinline__ bool mx4_group(const Mx4Gemm& p, int g, int& e, int64
     return rows > 0;
 }
 
-// Two values rounded to the type, packed.
+// Two values rounded to the type, packed (one instruction).
 template <typename Elt>
 __device__ __forceinline__ uint32_t mx4_pack2(float a, float b) {
-    typedef typename Elt::scalar scalar;
-    const scalar lo = (scalar)a, hi = (scalar)b;
-    return __builtin_bit_cast(uint16_t, lo) | ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
+    const floatx2_t v = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, typename Elt::vec2));
 }
 
 // The few-row product: BN columns of C (gated: of each matrix) and up to 64 rows
@@ -497,8 +497,8 @@ __device__ __forceinline__ void mx4_skinny_body(const Mx4Gemm& p, char* smem, in
     for (int m = 0; m < MATS; ++m) {
         const uint8_t* q = m == 0 ? p.B + e * p.eqb : p.B2 + e * p.eqb2;
         const uint8_t* sc = m == 0 ? p.SB + e * p.esb : p.SB2 + e * p.esb2;
-        const int64_t ld = m == 0 ? p.ldb : p.ldb2;
-        rb[m] = make_rsrc(q + (int64_t)n0 * ld, (uint32_t)((rows_b - 1) * ld + p.rowbytes));
+        const uint32_t ld = m == 0 ? p.ldb : p.ldb2;
+        rb[m] = make_rsrc(q + (uint64_t)(uint32_t)n0 * ld, (uint32_t)((rows_b - 1) * ld + p.rowbytes));
         rsb[m] = make_rsrc(sc + (int64_t)(n0 / 64) * srow, srow);
 #pragma unroll
         for (int j = 0; j < B_BYTES / 1024; ++j)
@@ -726,18 +726,18 @@ __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
     b = r[1];
 }
 
-// A wave's FN x FM parts, rows mb .. (of M), columns nb .. (of N): 16-byte stores,
-// 64 bytes of 16 rows at a time.  Whole in columns they go through a descriptor
-// that drops the rows past M.
+// A wave's FN x FM parts, `left` rows from mb, columns nb .. (of N): 16-byte
+// stores, 64 bytes of 16 rows at a time.  Whole in columns they go through a
+// descriptor that drops the rows past the last.
 template <typename Elt, int FN, int FM>
 __device__ __forceinline__ void mx4_store(uint16_t* C, int64_t ldc, const floatx4_t (&acc)[FN][FM],
-                                          int64_t mb, int64_t M, int64_t nb, int N, int lane) {
+                                          uint32_t mb, int left, uint32_t nb, int N, int lane) {
     const int fr = lane & 15, fq = lane >> 4;
-    const int64_t left = M - mb;
     if (left <= 0) return;
-    const int rows = (int)min(left, (int64_t)(FM * 16));
-    const bool whole = nb + FN * 16 <= N && ldc < (1 << 24);
-    C += mb * ldc + nb;
+    const int rows = min(left, FM * 16);
+    const int columns = N - (int)nb;              // to the right of nb (none where nb is past N)
+    const bool whole = columns >= FN * 16 && ldc < (1 << 24);
+    C += (int64_t)mb * ldc + nb;
     const __amdgpu_buffer_rsrc_t r = make_rsrc(C, (uint32_t)((rows - 1) * ldc + FN * 16) * 2);
     const int n = (fq & 1) * 16 + (fq >> 1) * 8;
     const uint32_t off = (uint32_t)(fr * (int)ldc + n) * 2;
@@ -760,7 +760,7 @@ __device__ __forceinline__ void mx4_store(uint16_t* C, int64_t ldc, const floatx
 #pragma unroll
                 for (int d = 0; d < 8; ++d) {
                     const uint32_t w = v[d >> 1];
-                    if (nb + i * 16 + n + d < N) c[d] = (uint16_t)(w >> (16 * (d & 1)));
+                    if (i * 16 + n + d < columns) c[d] = (uint16_t)(w >> (16 * (d & 1)));
                 }
             }
         }
@@ -772,12 +772,12 @@ __device__ __forceinline__ void mx4_store(uint16_t* C, int64_t ldc, const floatx
 // through memory.  `rows`: rows of the tile that exist.
 template <typename Elt, int FM>
 __device__ __forceinline__ void mx4_store_quantized(const Mx4Gemm& p, const floatx4_t (&out)[2][FM],
-                                                    int64_t m0, int64_t n0, int rows, int wave_m,
+                                                    uint32_t m0, uint32_t n0, int rows, int wave_m,
                                                     int wave_n, int lane) {
     static_assert(FM == 2 || FM == 4, "a wave's rows: half of or a whole scale tile");
     const int fr = lane & 15, fq = lane >> 4;
-    const int64_t block = n0 / 32 + wave_n;
-    const bool in = block < (p.N + 31) / 32;
+    const uint32_t block = n0 / 32 + wave_n;
+    const bool in = block < (uint32_t)(p.N + 31) / 32;
     uint32_t q[4] = {0, 0, 0, 0};
     int e = 0;                                        // of row 16 fq + fr of the wave's
 #pragma unroll
@@ -803,14 +803,14 @@ __device__ __forceinline__ void mx4_store_quantized(const Mx4Gemm& p, const floa
     if (in && r < rows) {
         const uint4_t v = {(q[0] & 0xffffu) | (q[1] << 16), (q[2] & 0xffffu) | (q[3] << 16),
                            (q[0] >> 16) | (q[1] & 0xffff0000u), (q[2] >> 16) | (q[3] & 0xffff0000u)};
-        *reinterpret_cast<uint4_t*>(p.QO + (m0 + r) * p.ldqo + block * 16) = v;
+        *reinterpret_cast<uint4_t*>(p.QO + (int64_t)(m0 + r) * p.ldqo + block * 16) = v;
     }
     // a byte per row and block; the last columns' workgroup also clears the quarters
     // past them, whose blocks hold nothing
     const int g0 = (int)(n0 / 64) & 3;
-    uint8_t* tile = p.SO + ((m0 + r) / 64 * p.nkto + n0 / 256) * kMx4Tile;
+    uint8_t* tile = p.SO + ((int64_t)((m0 + r) / 64) * p.nkto + n0 / 256) * kMx4Tile;
     tile[mx4_scale_offset(r & 63, 2 * g0 + wave_n)] = in && r < rows ? (uint8_t)e : 0;
-    if (n0 + 64 >= p.N)
+    if (n0 + 64 >= (uint32_t)p.N)
         for (int g = g0 + 1; g < 4; ++g) tile[mx4_scale_offset(r & 63, 2 * g + wave_n)] = 0;
 }
 
@@ -900,18 +900,20 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
     const int last = (xcd + 1) * (total / p.nxcd) + min(xcd + 1, total % p.nxcd);
     int tile = xcd * (total / p.nxcd) + min(xcd, total % p.nxcd) + blockIdx.x / p.nxcd;
     if (tile >= last) return;
+    // grouped: row and column tile, and how far a turn moves them
+    int tm = tile / p.gn, tn = tile - tm * p.gn;
+    const int turn_m = turn / p.gn, turn_n = turn - turn_m * p.gn;
 
     struct Place {
-        int64_t m0, n0;
+        uint32_t m0, n0;
         int rows;                                 // of the tile that exist
         int e;
     };
-    auto locate = [&](int l) {
+    auto locate = [&]() {
         Place x;
         x.e = 0;
         if constexpr (GROUPED) {
-            const int tm = l / p.gn;
-            x.n0 = (int64_t)(l - tm * p.gn) * BNO;
+            x.n0 = (uint32_t)tn * BNO;
             int before = 0;                       // the pairs whose tiles all lie before tm
             for (int c = 0; 2 * c < p.experts; c += 64) {
                 const bool in = 2 * (c + lane) < p.experts && upto[c + lane] <= tm;
@@ -928,18 +930,28 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
             const bool second = tm - t0 >= first;
             t0 += second ? first : 0;
             x.e += second ? 1 : 0;
-            const int count = second ? c1 : c0;
-            const int64_t row0 = second ? o1 : o0;
-            x.m0 = row0 + (int64_t)(tm - t0) * BM;
-            x.rows = min(count - (tm - t0) * BM, BM);
+            x.m0 = (uint32_t)(second ? o1 : o0) + (uint32_t)(tm - t0) * BM;
+            x.rows = min((second ? c1 : c0) - (tm - t0) * BM, BM);
         } else {
             GemmParams gp;
             gp.gm = p.gm;
             gp.gn = p.gn;
-            grouped_origin(gp, l, BM, BNO, x.m0, x.n0);
-            x.rows = (int)min((int64_t)p.M - x.m0, (int64_t)BM);
+            int64_t m0, n0;
+            grouped_origin(gp, tile, BM, BNO, m0, n0);
+            x.m0 = (uint32_t)m0;
+            x.n0 = (uint32_t)n0;
+            x.rows = min(p.M - (int)x.m0, BM);
         }
         return x;
+    };
+    auto next_tile = [&]() {
+        tile += turn;
+        tm += turn_m;
+        tn += turn_n;
+        if (tn >= p.gn) {
+            tn -= p.gn;
+            ++tm;
+        }
     };
 
     // ---- the stream of k-tiles: the loads' position ------------------------------------
@@ -960,23 +972,23 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
         voff_b[j] = (uint32_t)(src * (GATED && (row & 32) ? p.ldb2 : p.ldb)) +
                     pos * 16;
     }
-    Place at = locate(tile), next_at = at;        // the tile that is multiplied, that is loaded
+    Place at = locate(), next_at = at;        // the tile that is multiplied, that is loaded
     int load_kt = 0;
     bool loads = nkt > 0;                         // loads are left
     __amdgpu_buffer_rsrc_t ra, rb, rb2, rsa, rsb, rsb2;
     auto describe = [&](const Place& x) {
-        const int rows_b = (int)min((int64_t)BNO, (int64_t)p.N - x.n0);
+        const int rows_b = min(BNO, p.N - (int)x.n0);
         const uint32_t sa = (uint32_t)((x.rows + 63) / 64) * srow;
         const uint32_t sb = (uint32_t)((rows_b + 63) / 64) * srow;
-        ra = make_rsrc(p.A + x.m0 * p.lda, (uint32_t)((x.rows - 1) * p.lda + p.rowbytes));
-        rb = make_rsrc(p.B + x.e * p.eqb + x.n0 * p.ldb,
-                       (uint32_t)((rows_b - 1) * p.ldb + p.rowbytes));
-        rsa = make_rsrc(p.SA + (x.m0 / 64) * srow, sa);
-        rsb = make_rsrc(p.SB + x.e * p.esb + (x.n0 / 64) * srow, sb);
+        const uint32_t last_b = (uint32_t)(rows_b - 1);
+        ra = make_rsrc(p.A + (uint64_t)x.m0 * p.lda, (uint32_t)(x.rows - 1) * p.lda + p.rowbytes);
+        rb = make_rsrc(p.B + x.e * p.eqb + (uint64_t)x.n0 * p.ldb, last_b * p.ldb + p.rowbytes);
+        rsa = make_rsrc(p.SA + (uint64_t)(x.m0 / 64) * srow, sa);
+        const uint64_t s0 = (uint64_t)(x.n0 / 64) * srow;
+        rsb = make_rsrc(p.SB + x.e * p.esb + s0, sb);
         if constexpr (GATED) {
-            rb2 = make_rsrc(p.B2 + x.e * p.eqb2 + x.n0 * p.ldb2,
-                            (uint32_t)((rows_b - 1) * p.ldb2 + p.rowbytes));
-            rsb2 = make_rsrc(p.SB2 + x.e * p.esb2 + (x.n0 / 64) * srow, sb);
+            rb2 = make_rsrc(p.B2 + x.e * p.eqb2 + (uint64_t)x.n0 * p.ldb2, last_b * p.ldb2 + p.rowbytes);
+            rsb2 = make_rsrc(p.SB2 + x.e * p.esb2 + s0, sb);
         }
     };
     auto load_codes = [&](int stage) {
@@ -1012,10 +1024,10 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
         if (++load_kt < nkt) return;
         load_kt = 0;
         if (!loads) return;
-        tile += turn;
+        next_tile();
         loads = tile < last;
         if (loads) {
-            next_at = locate(tile);
+            next_at = locate();
             describe(next_at);
         } else {
             // Nothing is left: the loads go on, so that the loop has no branch for
@@ -1105,7 +1117,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
     };
     auto store = [&]() {
-        const int64_t mb = at.m0 + wave_m * WTM, M = at.m0 + at.rows;
+        const uint32_t mb = at.m0 + wave_m * WTM;
+        const int left = at.rows - wave_m * WTM;
         if constexpr (GATED) {
             floatx4_t out[FN / 2][FM];
 #pragma unroll
@@ -1118,17 +1131,17 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
             if constexpr (QOUT)
                 mx4_store_quantized<Elt, FM>(p, out, at.m0, at.n0, at.rows, wave_m, wave_n, lane);
             else
-                mx4_store<Elt, FN / 2, FM>(p.C, p.ldc, out, mb, M, at.n0 + wave_n * (WTN / 2), p.N,
+                mx4_store<Elt, FN / 2, FM>(p.C, p.ldc, out, mb, left, at.n0 + wave_n * (WTN / 2), p.N,
                                            lane);
         } else {
-            mx4_store<Elt, FN, FM>(p.C, p.ldc, acc, mb, M, at.n0 + wave_n * WTN, p.N, lane);
+            mx4_store<Elt, FN, FM>(p.C, p.ldc, acc, mb, left, at.n0 + wave_n * WTN, p.N, lane);
         }
     };
 
     clear();
     if (nkt == 0) {                               // every sum is empty
-        for (; tile < last; tile += turn) {
-            at = locate(tile);
+        for (; tile < last; next_tile()) {
+            at = locate();
             store();
         }
         return;
