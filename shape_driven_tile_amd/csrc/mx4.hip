@@ -133,6 +133,30 @@ int launch_skinny(Mx4Gemm p, int64_t groups, int num_cu, void* stream) {
                   4 * 64, p, stream);
 }
 
+// Which kernel a product runs, from the number of output tiles of each against
+// the CUs (us measured on MI355X, K = 4096 where not named):
+//   few rows (M <= 64, or <= 128 with at most one 64 x 64 tile a CU): the weights
+//   are streamed (100x4096: 8.3 against 9.8 with 64 x 64 tiles; 256x4096: 10.4
+//   against 9.4);
+//   at most one 64 x 64 tile a CU: those (1024^3: 4.9, with 128 x 128 6.3);
+//   at most one 64 x 128 tile a CU: those (512x4096: 11.6, with 64 x 64 12.1, with
+//   128 x 128 14.1; just past it, 256x12288: 15.6 against 14.6);
+//   else 128 x 128, two workgroups a CU in turn, or 256 x 256, one, by the estimate
+//   below.
+// A CU's time: a round of 256 x 256 tiles that fills the chip takes 1.7 us a
+// k-tile and 7.5 besides, one that does not 1.25 a k-tile; a 128 x 128 tile 0.58
+// and 1.6, and 3 once.  2560x4096: 27.9 (256) against 32.5 (128); 4096x5120: 57.9
+// against 51.7; 1024x8192x8192: 46.3 against 40.0; 6000x6000x500: 44.5 against
+// 27.9; 4096x4096x1024: 15.9 against 18.3; 8192^3: 246 against 301.
+bool large_tiles_win(int64_t M, int64_t N, int64_t nkt, int64_t cu) {
+    const int64_t t256 = ceil_div(M, 256) * ceil_div(N, 256);
+    const int64_t t128 = ceil_div(M, 128) * ceil_div(N, 128);
+    const double k = (double)nkt;
+    const double large = (double)(t256 / cu) * (1.7 * k + 7.5) + (t256 % cu ? 1.25 * k + 7.5 : 0.0);
+    const double small = (double)t128 / (double)cu * (0.58 * k + 1.6) + 3.0;
+    return t128 > cu && large < small;
+}
+
 template <typename Elt>
 int gemm(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA, const void* B,
          int64_t ldb, const void* SB, void* C, int64_t ldc, void* stream) {
@@ -160,17 +184,21 @@ int gemm(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void
     p.rowbytes = (int)row_bytes(K);
     p.nkt = (int)k_tiles(K);
     p.nxcd = dev.nxcd;
-    if (M <= 64) return launch_skinny<Elt, false, false>(p, 1, dev.num_cu, stream);
-    if (ceil_div(M, 256) * ceil_div(N, 256) >= dev.num_cu / 2) {
+    const int64_t cu = dev.num_cu;
+    const int64_t t64 = ceil_div(M, 64) * ceil_div(N, 64);
+    if (M <= 64 || (M <= 128 && t64 <= cu))
+        return launch_skinny<Elt, false, false>(p, ceil_div(M, 64), dev.num_cu, stream);
+    if (large_tiles_win(M, N, p.nkt, cu)) {
         p.gm = (int)ceil_div(M, 256);
         p.gn = (int)ceil_div(N, 256);
         return launch(reinterpret_cast<const void*>(&mx4_pp_kernel<Elt>), (int64_t)p.gm * p.gn, 512,
                       p, stream);
     }
-    if (ceil_div(M, 128) * ceil_div(N, 128) >= dev.num_cu / 2)
-        return launch_tile<Elt, 128, 128, 2, 2, 2, false, false>(p, ceil_div(M, 128), dev.num_cu,
-                                                                 stream);
-    return launch_tile<Elt, 64, 64, 2, 2, 4, false, false>(p, ceil_div(M, 64), dev.num_cu, stream);
+    if (t64 <= cu)
+        return launch_tile<Elt, 64, 64, 2, 2, 4, false, false>(p, ceil_div(M, 64), dev.num_cu, stream);
+    if (ceil_div(M, 64) * ceil_div(N, 128) <= cu)
+        return launch_tile<Elt, 64, 128, 2, 2, 3, false, false>(p, ceil_div(M, 64), dev.num_cu, stream);
+    return launch_tile<Elt, 128, 128, 2, 2, 2, false, false>(p, ceil_div(M, 128), dev.num_cu, stream);
 }
 
 template <typename Elt>
@@ -308,7 +336,11 @@ int check_experts(int64_t N, int64_t K, const sdt_mx4_experts* B) {
 int64_t rows_per_expert(const sdt_moe_plan* plan) {
     return plan->tokens * plan->topk / plan->experts;
 }
-constexpr int64_t kSkinnyRows = 16;   // up to these the weights are streamed
+// Up to these the weights are streamed, up to 64 they meet 64 x 128 tiles, above
+// 128 x 128 (layers of 16 experts, 2048 x 1024, us: 8 rows 32.9 streamed and 34.4
+// in 64 x 128 tiles, 16 rows 37.2 and 35.0; 64 rows 39.8 and in 128 x 128 40.8, 128
+// rows 49.0 and 45.2).
+constexpr int64_t kSkinnyRows = 12;
 
 template <typename Elt, int BM, int BN, int NS>
 int launch_grouped_tile(const Mx4Gemm& p, const sdt_moe_plan* plan, bool gated, int num_cu,
