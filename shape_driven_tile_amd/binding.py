@@ -359,15 +359,17 @@ def _stream_handle(stream):
 
 
 def _rows(t, name, dtype=None):
-    import torch
-    dtype = torch.float16 if dtype is None else dtype
+    if dtype is None:
+        import torch
+        dtype = torch.float16
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise TypeError(f"{name} must be a device tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
         raise ValueError(f"{name} must be 2-D with unit stride along its rows")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1]))
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else max(stride[0], shape[1]))
 
 
 def gemm_f16(A, B, C, stream=None) -> None:
@@ -704,9 +706,14 @@ class Mx4:
         return self.q.stride(-2) if self.rows > 1 else max(self.q.stride(-2), mx4_row_bytes(self.K))
 
     def _one(self, name):
-        if self.q.dim() != 2:
+        q = self.q
+        stride = q.stride()
+        if len(stride) != 2:
             raise ValueError(f"{name} must be one matrix, not one per expert")
-        return self.q.data_ptr(), self.ldq(), self.s.data_ptr()
+        ld = stride[0]
+        if self.rows <= 1:
+            ld = max(ld, -(-self.K // 32) * 16)
+        return q.data_ptr(), ld, self.s.data_ptr()
 
     def _experts(self, experts, name) -> SdtMx4Experts:
         if self.q.dim() != 3 or self.q.shape[0] != experts:

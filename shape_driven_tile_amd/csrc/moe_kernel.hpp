@@ -390,16 +390,17 @@ struct SlotQuad {
 };
 
 __global__ __launch_bounds__(1024) void moe_plan_kernel(PlanParams p) {
+    constexpr int NW = 16;
     __shared__ int hist[kMaxExperts];
-    __shared__ int wcount[16], wbefore[16];
+    __shared__ int wcount[NW], wbefore[NW];
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int e = blockIdx.x;
-    for (int i = t; i < p.E; i += 1024) hist[i] = 0;
+    for (int i = t; i < p.E; i += NW * 64) hist[i] = 0;
     __syncthreads();
     // this wave's quads of slots
     const int quads = (int)(((int64_t)p.R + 3) / 4);
-    const int per = (quads + 15) / 16;
+    const int per = (quads + NW - 1) / NW;
     const int first = min(wave * per, quads), last = min(first + per, quads);
     auto load = [&](int q0, SlotQuad (&v)[kPlanLoads]) {
 #pragma unroll
@@ -415,8 +416,8 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(PlanParams p) {
         }
     };
     int mine = 0;                              // slots of this wave that chose e
+    SlotQuad v[kPlanLoads];
     for (int q0 = first; q0 < last; q0 += 64 * kPlanLoads) {
-        SlotQuad v[kPlanLoads];
         load(q0, v);
 #pragma unroll
         for (int u = 0; u < kPlanLoads; ++u) {
@@ -440,13 +441,13 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(PlanParams p) {
     __syncthreads();
     // rows before this expert's
     int before = 0;
-    for (int i = t; i < e; i += 1024) before += (hist[i] + 63) & ~63;
+    for (int i = t; i < e; i += NW * 64) before += (hist[i] + 63) & ~63;
 #pragma unroll
     for (int m = 32; m > 0; m >>= 1) before += __shfl_xor(before, m);
     if (lane == 0) wbefore[wave] = before;
     __syncthreads();
     int start = 0, row0 = 0, count = 0;
-    for (int w = 0; w < 16; ++w) {
+    for (int w = 0; w < NW; ++w) {
         start += wbefore[w];
         if (w < wave) row0 += wcount[w];
         count += wcount[w];
@@ -457,18 +458,17 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(PlanParams p) {
         p.offsets[e] = start;
         if (e == p.E - 1) p.offsets[p.E] = end;
     }
-    for (int i = start + count + t; i < end; i += 1024) p.rows[i] = -1;
-    for (int i = start / 64 + t; i < end / 64; i += 1024) p.tiles[i] = e;
+    for (int i = start + count + t; i < end; i += NW * 64) p.rows[i] = -1;
+    for (int i = start / 64 + t; i < end / 64; i += NW * 64) p.tiles[i] = e;
     if (e == p.E - 1) {
-        for (int i = end + t; i < p.cap; i += 1024) p.rows[i] = -1;
-        for (int i = end / 64 + t; i < p.cap / 64; i += 1024) p.tiles[i] = -1;
+        for (int i = end + t; i < p.cap; i += NW * 64) p.rows[i] = -1;
+        for (int i = end / 64 + t; i < p.cap / 64; i += NW * 64) p.tiles[i] = -1;
     }
     if (mine == 0) return;
     int row = start + row0;                    // of this wave's next slot
     const uint64_t below = (1ull << lane) - 1;
     for (int q0 = first; q0 < last; q0 += 64 * kPlanLoads) {
-        SlotQuad v[kPlanLoads];
-        load(q0, v);
+        if (last - first > 64 * kPlanLoads) load(q0, v);   // else they are still there
 #pragma unroll
         for (int u = 0; u < kPlanLoads; ++u) {
             if (q0 + u * 64 >= last) break;
@@ -503,9 +503,11 @@ struct CombineParams {
     int topk, N, nch;      // nch: chunks of 8 columns
 };
 
-// Eight columns of one token per thread.
+// Eight columns of one token per thread, the rows of four slots loaded together.
+// Bound by reading D (4096 tokens, 6 rows of 2048 each: 19 us, 5.2 TB/s).
 template <typename S>
 __global__ __launch_bounds__(256) void moe_combine_kernel(CombineParams p) {
+    constexpr int G = 4;
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t t = id / p.nch;
     if (t >= p.T) return;
@@ -513,19 +515,37 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(CombineParams p) {
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     typedef S vec8 __attribute__((ext_vector_type(8)));
     typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-    for (int j = 0; j < p.topk; ++j) {
-        const int row = p.pos[t * p.topk + j];
-        if (row < 0) continue;
-        const float w = p.weights[t * p.topk + j];
-        const uint16_t* d = p.D + row * p.ldd + n;
+    for (int j0 = 0; j0 < p.topk; j0 += G) {
+        int row[G];
+        float w[G];
+#pragma unroll
+        for (int u = 0; u < G; ++u) {
+            const bool in = j0 + u < p.topk;
+            row[u] = in ? p.pos[t * p.topk + j0 + u] : -1;
+            w[u] = in ? p.weights[t * p.topk + j0 + u] : 0.0f;
+        }
         if (n + 7 < p.N) {
-            const vec8 v = __builtin_bit_cast(vec8, *reinterpret_cast<const u4*>(d));
+            u4 v[G];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) acc[c] += w * (float)v[c];
+            for (int u = 0; u < G; ++u) {
+                v[u] = u4{0, 0, 0, 0};
+                if (row[u] >= 0) v[u] = *reinterpret_cast<const u4*>(p.D + row[u] * p.ldd + n);
+            }
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+                if (row[u] >= 0) {
+                    const vec8 x = __builtin_bit_cast(vec8, v[u]);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) acc[c] += w[u] * (float)x[c];
+                }
         } else {
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (n + c < p.N) acc[c] += w * (float)__builtin_bit_cast(S, d[c]);
+            for (int u = 0; u < G; ++u)
+                if (row[u] >= 0)
+                    for (int c = 0; c < 8; ++c)
+                        if (n + c < p.N) {
+                            const uint16_t d = p.D[row[u] * p.ldd + n + c];
+                            acc[c] += w[u] * (float)__builtin_bit_cast(S, d);
+                        }
         }
     }
     uint16_t h[8];

@@ -468,7 +468,10 @@ __device__ __forceinline__ uint32_t mx4_pack2(float a, float b) {
 // a lane to a row, each instruction touches 64 lines: 5.8 bytes a clock and CU,
 // a third of what memory gives.)  Few rows (NMB = 1: 16) leave the LDS to more
 // stages.  The waves' partial sums are added in wave order.
-constexpr int kSkinnyWaveLds = 35 * 1024;
+// A wave's LDS: grouped products have many short tiles, and three workgroups a CU
+// with two stages pass them faster than two with three (64 tokens of 32 experts:
+// 44.2 -> 41.8 and 27.6 -> 24.6 us; 8 tokens of 64: 21.3 -> 19.7 and 13.5 -> 11.8).
+constexpr int skinny_wave_lds(bool grouped) { return (grouped ? 23 : 35) * 1024; }
 
 template <typename Elt, bool GROUPED, bool GATED, bool QOUT, int NW, int NMB>
 __device__ __forceinline__ void mx4_skinny_body(const Mx4Gemm& p, char* smem, int e, int64_t m0,
@@ -479,10 +482,11 @@ __device__ __forceinline__ void mx4_skinny_body(const Mx4Gemm& p, char* smem, in
     constexpr int PB = BN / 16;                   // 16-column parts of a matrix
     constexpr int B_BYTES = BN * 128, A_BYTES = NMB * 16 * 128;
     constexpr int STAGE = MATS * (B_BYTES + kMx4Tile) + A_BYTES + kMx4Tile;
-    constexpr int NS = kSkinnyWaveLds / STAGE >= 3 ? 3 : 2;
+    constexpr int kWaveLds = skinny_wave_lds(GROUPED);
+    constexpr int NS = kWaveLds / STAGE >= 3 ? 3 : kWaveLds / STAGE;
     constexpr int L = MATS * (B_BYTES / 1024 + 1) + A_BYTES / 1024 + 1;
-    static_assert(NS * STAGE <= kSkinnyWaveLds, "a wave's stages");
-    static_assert(MATS * PB * NMB * 1024 <= kSkinnyWaveLds, "a wave's sums");
+    static_assert(NS >= 1 && NS * STAGE <= kWaveLds, "a wave's stages");
+    static_assert(MATS * PB * NMB * 1024 <= kWaveLds, "a wave's sums");
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fr = lane & 15, fq = lane >> 4;
@@ -511,7 +515,7 @@ __device__ __forceinline__ void mx4_skinny_body(const Mx4Gemm& p, char* smem, in
     for (int j = 0; j < A_BYTES / 1024; ++j)
         voff_a[j] = (uint32_t)((j * 8 + (lane >> 3)) * p.lda) + chunk;
 
-    char* const mine = smem + wave * kSkinnyWaveLds;
+    char* const mine = smem + wave * kWaveLds;
     auto load = [&](int kt, int stage) {
         int4_t* at = reinterpret_cast<int4_t*>(mine + stage * STAGE);
         // in the lane offset, which the descriptor's range check covers
@@ -548,7 +552,7 @@ __device__ __forceinline__ void mx4_skinny_body(const Mx4Gemm& p, char* smem, in
         const int younger = min(n - 1 - j, NS - 1);   // k-tiles that may stay in flight
         if (NS > 2 && younger == 2)
             wait_global_loads<NS == 3 ? 2 * L : 0>();
-        else if (younger == 1)
+        else if (NS > 1 && younger == 1)
             wait_global_loads<L>();
         else
             wait_global_loads<0>();
@@ -627,7 +631,7 @@ __device__ __forceinline__ void mx4_skinny_body(const Mx4Gemm& p, char* smem, in
         floatx4_t s = *reinterpret_cast<const floatx4_t*>(at);
 #pragma unroll
         for (int w = 1; w < NW; ++w)
-            s += *reinterpret_cast<const floatx4_t*>(at + w * kSkinnyWaveLds);
+            s += *reinterpret_cast<const floatx4_t*>(at + w * kWaveLds);
         return s;
     };
     auto output = [&](int i, int j) {             // part (i, j): row fr, columns 4 fq .. + 3
@@ -689,7 +693,7 @@ __device__ __forceinline__ void mx4_skinny_body(const Mx4Gemm& p, char* smem, in
 
 template <typename Elt, bool GROUPED, bool GATED, bool QOUT, int NW>
 __global__ __launch_bounds__(NW * 64) void mx4_skinny_kernel(Mx4Gemm p) {
-    __shared__ int4_t smem[NW * kSkinnyWaveLds / 16];
+    __shared__ int4_t smem[NW * skinny_wave_lds(GROUPED) / 16];
     const int l = xcd_remap(blockIdx.x, gridDim.x, p.nxcd);
     const int g = l / p.gn, nt = l - g * p.gn;
     const int n0 = nt * (GATED ? 32 : 64);
