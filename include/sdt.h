@@ -306,12 +306,12 @@ int64_t sdt_mx4_row_bytes(int64_t K);
 int64_t sdt_mx4_scale_bytes(int64_t rows, int64_t K);
 
 /* Q, S = X (rows x K, row stride ldx >= K elements, any alignment of the
- * element type; 16-byte aligned rows load fastest).  Per block: e = floor(log2(max |x|)) - 2 + 127
+ * element type; rows on 128-byte lines load fastest).  Per block: e = floor(log2(max |x|)) - 2 + 127
  * clamped to [0, 254], each element x / 2^(e - 127) rounded to the nearest
  * code, ties to the even one, saturated at 6 (sign kept, also of zeros); a
  * block of zeros has e = 0; a block that holds an infinity or a NaN has e = 255
  * and zero codes.  rows == 0 or K == 0 is a no-op.  Limits: as above, rows at
- * most 2^31 - 1. */
+ * most 2^31 - 256 (also of the products' matrices). */
 int mx4_quantize_f16(int64_t rows, int64_t K, const void* X, int64_t ldx,
                      void* Q, int64_t ldq, void* S, void* stream);
 int mx4_quantize_bf16(int64_t rows, int64_t K, const void* X, int64_t ldx,
@@ -345,10 +345,11 @@ int mx4_pack_scales(int64_t rows, int64_t K, const void* R, int64_t ldr, void* S
 /* C = A . B^T for MX4 matrices A (M x K) and B (N x K): the exact products of
  * the values, accumulated in fp32 on the scaled MFMAs, rounded once to the
  * type of the name.  C as gemm_f16's: 16-byte aligned, ldc >= N a multiple of 8.  M == 0 or
- * N == 0 is a no-op; K == 0 writes zeros.  Deterministic.  Few rows (M <= 64
- * where the tiles would leave the device idle) stream B once through a kernel
- * without LDS staging; others run 64 x 64, 128 x 128 or 256 x 256 tiles by the
- * output-block count, as the 16-bit products do. */
+ * N == 0 is a no-op; K == 0 writes zeros.  Deterministic.  Few rows (M <= 64, or
+ * <= 128 where 64 x 64 tiles would leave CUs idle) stream B once; others run 64 x
+ * 64, 64 x 128, 128 x 128 or 256 x 256 tiles, by the number of tiles a CU and an
+ * estimate of their time.  Rows that start on 128-byte lines (ldq a multiple of
+ * 128) load fastest. */
 int gemm_mx4_f16(int64_t M, int64_t N, int64_t K,
                  const void* A, int64_t lda, const void* SA,
                  const void* B, int64_t ldb, const void* SB,
@@ -482,9 +483,10 @@ int moe_combine_bf16(const sdt_moe_plan* plan, int64_t N, const void* D, int64_t
 /* A layer of gated experts in one call: Y = sum over a token's experts of
  * weight * (silu(x G_e^T) * (x U_e^T)) D_e^T, x and the gated product quantised
  * to MX4 before each product (the gated product and the experts' outputs are
- * rounded to the type of the name first).  The calls above in order: moe_plan,
- * mx4_quantize_rows, moe_gemm_mx4 with `up`, mx4_quantize_rows, moe_gemm_mx4,
- * moe_combine; the results are theirs, bit for bit.  X (tokens x K, stride ldx
+ * rounded to the type of the name first).  The results are bit for bit those of
+ * the calls above in order: moe_plan, mx4_quantize_rows, moe_gemm_mx4 with `up`,
+ * mx4_quantize_rows, moe_gemm_mx4, moe_combine (the layer reads and quantises a
+ * token once, and the gated product comes out of its kernel quantised).  X (tokens x K, stride ldx
  * elements), gate and up (N x K), down (K x N), Y (tokens x K, ldy a multiple
  * of 8, 16-byte aligned).  workspace: device memory, 16-byte aligned, at least
  * sdt_moe_experts_workspace_size bytes (fewer: SDT_ERR_INVALID_ARG); no

@@ -9,6 +9,10 @@
 // loads, group 0 those of A (two 32 KB stages), group 1 those of B (three).
 // The 160 KB are full, so scales go from memory into registers, one k-tile
 // ahead: 8 bytes a lane per 64 rows, three coalesced 512-byte loads a wave.
+// 8192^3: 228-250 us (4.4-4.8 PFLOP/s), MFMAs busy 58% of the clocks; bound by the
+// power limit (a register-only loop of these MFMAs on random codes: 6.15-7.15
+// PFLOP/s) and by the stage loads (197 us with them left out).  128 x 128 tiles,
+// two workgroups a CU, take 301 us there.
 #pragma once
 
 #include "mx4_kernel.hpp"
