@@ -675,17 +675,20 @@ class Mx4:
     def __init__(self, q, s, rows: int, K: int):
         import torch
         rows, K = int(rows), int(K)
-        if q.dtype is not torch.uint8 or s.dtype is not torch.uint8:
+        u8 = torch.uint8
+        if q.dtype is not u8 or s.dtype is not u8:
             raise TypeError("Mx4: codes and scales must be uint8")
-        if not q.is_cuda or s.device != q.device:
+        where = q.get_device() if q.is_cuda else -1
+        if where < 0 or not s.is_cuda or s.get_device() != where:
             raise TypeError("Mx4: codes and scales must be on one device")
-        if q.dim() not in (2, 3) or s.dim() != q.dim() - 1 or q.shape[:-2] != s.shape[:-1]:
-            raise ValueError(f"Mx4: codes {tuple(q.shape)} and scales {tuple(s.shape)} do not match")
-        if q.shape[-2] != rows or q.shape[-1] < mx4_row_bytes(K) or \
-                s.shape[-1] < mx4_scale_bytes(rows, K):
-            raise ValueError(f"Mx4: codes {tuple(q.shape)} and scales {tuple(s.shape)} cannot hold "
+        qs, ss = q.shape, s.shape
+        if len(qs) not in (2, 3) or len(ss) != len(qs) - 1 or (len(qs) == 3 and qs[0] != ss[0]):
+            raise ValueError(f"Mx4: codes {tuple(qs)} and scales {tuple(ss)} do not match")
+        if qs[-2] != rows or qs[-1] < -(-K // 32) * 16 or \
+                ss[-1] < -(-rows // 64) * -(-K // 256) * 512:
+            raise ValueError(f"Mx4: codes {tuple(qs)} and scales {tuple(ss)} cannot hold "
                              f"{rows} x {K}")
-        if q.stride(-1) != 1 or s.stride(-1) != 1:
+        if q.stride()[-1] != 1 or s.stride()[-1] != 1:
             raise ValueError("Mx4: unit stride along rows of codes and along the scales")
         self.q, self.s, self.rows, self.K = q, s, rows, K
 
@@ -729,7 +732,7 @@ def _check(rc: int, where: str) -> None:
 
 def _quantize(entry, X, out, dtype, stream):
     px, ldx = _rows(X, "X", dtype)
-    if tuple(X.shape) != (out.rows, out.K):
+    if X.shape != (out.rows, out.K):
         raise ValueError(f"shape mismatch X{tuple(X.shape)} out ({out.rows}, {out.K})")
     q, ldq, s = out._one("out")
     _check(getattr(lib(), entry)(out.rows, out.K, px, ldx, q, ldq, s, _stream_handle(stream)), entry)
@@ -772,7 +775,7 @@ def mx4_quantize_rows_bf16(X, index, divisor: int, out: Mx4, stream=None) -> Non
 
 def _dequantize(entry, m, Y, dtype, stream):
     py, ldy = _rows(Y, "Y", dtype)
-    if tuple(Y.shape) != (m.rows, m.K):
+    if Y.shape != (m.rows, m.K):
         raise ValueError(f"shape mismatch matrix ({m.rows}, {m.K}) Y{tuple(Y.shape)}")
     q, ldq, s = m._one("matrix")
     _check(getattr(lib(), entry)(m.rows, m.K, q, ldq, s, py, ldy, _stream_handle(stream)), entry)
@@ -806,7 +809,7 @@ def mx4_pack_scales(scales, out: Mx4, stream=None) -> None:
 
 
 def _gemm_mx4(entry, A, B, C, dtype, stream):
-    if A.K != B.K or tuple(C.shape) != (A.rows, B.rows):
+    if A.K != B.K or C.shape != (A.rows, B.rows):
         raise ValueError(f"shape mismatch A({A.rows}, {A.K}) B({B.rows}, {B.K}) C{tuple(C.shape)}")
     pa, lda, sa = A._one("A")
     pb, ldb, sb = B._one("B")
@@ -831,7 +834,7 @@ def _gemv_mx4(entry, x, B, y, dtype, stream):
         raise TypeError(f"x and y must be {dtype}")
     if not x.is_cuda or not y.is_cuda:
         raise TypeError("x and y must be device tensors")
-    if x.dim() != 1 or y.dim() != 1 or x.stride(0) != 1 or y.stride(0) != 1:
+    if x.stride() != (1,) or y.stride() != (1,):
         raise ValueError("x and y must be contiguous vectors")
     if x.shape[0] != B.K or y.shape[0] != B.rows:
         raise ValueError(f"shape mismatch x{tuple(x.shape)} B({B.rows}, {B.K}) y{tuple(y.shape)}")
@@ -889,10 +892,14 @@ def _floats(t, name):
 
 def _logit_type(t, name):
     import torch
-    kinds = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
-    if t.dtype not in kinds:
-        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    return kinds[t.dtype]
+    dtype = t.dtype
+    if dtype is torch.float32:
+        return "f32"
+    if dtype is torch.float16:
+        return "f16"
+    if dtype is torch.bfloat16:
+        return "bf16"
+    raise TypeError(f"{name} must be float32, float16 or bfloat16, got {dtype}")
 
 
 def moe_route(logits, idx, weights, cfg: SdtRoute, bias=None, stream=None) -> None:
@@ -901,7 +908,8 @@ def moe_route(logits, idx, weights, cfg: SdtRoute, bias=None, stream=None) -> No
     kind = _logit_type(logits, "logits")
     p, ld = _rows(logits, "logits", logits.dtype)
     T, E = logits.shape
-    if tuple(idx.shape) != (T, cfg.topk) or tuple(weights.shape) != (T, cfg.topk):
+    chosen = (T, cfg.topk)
+    if idx.shape != chosen or weights.shape != chosen:
         raise ValueError(f"shape mismatch logits{tuple(logits.shape)} topk {cfg.topk} "
                          f"idx{tuple(idx.shape)} weights{tuple(weights.shape)}")
     if bias is not None and tuple(bias.shape) != (E,):
