@@ -220,9 +220,9 @@ int gemv(int64_t N, int64_t K, const void* x, const void* B, int64_t ldb, const 
     p.K = (int)K;
     p.rowbytes = (int)row_bytes(K);
     p.nkt = (int)k_tiles(K);
-    constexpr int NW = 8;
-    return launch(reinterpret_cast<const void*>(&mx4_gemv_kernel<Elt, NW>), ceil_div(N, 16), NW * 64,
-                  p, stream);
+    const void* k = K <= 4096 ? reinterpret_cast<const void*>(&mx4_gemv_kernel<Elt, 8, 2, 4096>)
+                              : reinterpret_cast<const void*>(&mx4_gemv_kernel<Elt, 8, 3, 8192>);
+    return launch(k, ceil_div(N, 16), 8 * 64, p, stream);
 }
 
 // ---- experts ---------------------------------------------------------------------------

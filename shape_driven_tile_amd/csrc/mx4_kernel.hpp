@@ -1213,25 +1213,23 @@ struct Mx4Gemv {
 // y of 16 rows of B per workgroup, whose NW waves split the k-tiles.  Bound by the
 // stream of B, which comes as in mx4_skinny_body: straight into LDS of each wave,
 // eight lanes to a row's 128 bytes, NS k-tiles in flight.  The activations are in
-// LDS, kGemvK of them at a time, zeros past K.  Lane l takes row l % 16, blocks
+// LDS, XK of them at a time, zeros past K.  Lane l takes row l % 16, blocks
 // 2 (l / 16) and + 1 of a k-tile: the codes are converted two at a time to
 // the activations' type (exact) and multiplied by pairs into an fp32 sum per
 // block, which the block's scale then multiplies once.  The four quarters' sums
 // are added by lane exchanges, the waves' in wave order through LDS.  12288 x 4096:
-// 8.6 us (9.2 with 32 rows and four waves, 11.0 with 32 and eight; the conversions
-// left out, the time is the same).
-constexpr int kGemvK = 8192;
-
-template <typename Elt, int NW>
+// 8.0 us with NS = 2 and XK = 4096, which lets three workgroups share a CU, and 9.0
+// with NS = 3 and XK = 8192; 4096 x 12288: 9.8 and 9.4 (32 rows a workgroup: 9.2 with
+// four waves, 11.0 with eight; the conversions left out, the time is the same).
+template <typename Elt, int NW, int NS, int XK>
 __global__ __launch_bounds__(NW * 64) void mx4_gemv_kernel(Mx4Gemv p) {
     typedef typename Elt::scalar scalar;
     typedef typename Elt::vec2 vec2;
-    constexpr int NS = 3;
     constexpr int BN = 16;
     constexpr int CODES = BN * 128, STAGE = CODES + kMx4Tile;
     constexpr int L = CODES / 1024 + 1;            // loads of a k-tile
     __shared__ int4_t stages[NW * NS * STAGE / 16];
-    __shared__ uint4_t xs[kGemvK / 8];
+    __shared__ uint4_t xs[XK / 8];
     __shared__ float red[NW * BN];
     const int t = threadIdx.x;
     const int lane = t & 63;
@@ -1258,8 +1256,8 @@ __global__ __launch_bounds__(NW * 64) void mx4_gemv_kernel(Mx4Gemv p) {
     };
 
     float sum = 0.0f;
-    for (int k0 = 0; k0 < p.nkt; k0 += kGemvK / 256) {
-        const int n1 = min(p.nkt - k0, kGemvK / 256);   // k-tiles of this turn
+    for (int k0 = 0; k0 < p.nkt; k0 += XK / 256) {
+        const int n1 = min(p.nkt - k0, XK / 256);   // k-tiles of this turn
         const int n = (n1 - wave + NW - 1) / NW;        // this wave's
         for (int j = 0; j < min(n, NS); ++j) load(k0 + wave + j * NW, j);
         if (k0 > 0) __syncthreads();                    // xs has been read
@@ -1271,7 +1269,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_gemv_kernel(Mx4Gemv p) {
         int stage = 0;
         for (int j = 0; j < n; ++j) {
             const int younger = min(n - 1 - j, NS - 1);
-            if (younger == 2)
+            if (NS > 2 && younger == 2)
                 wait_global_loads<2 * L>();
             else if (younger == 1)
                 wait_global_loads<L>();
