@@ -418,9 +418,24 @@ int moe_gemm(const sdt_moe_plan* plan, int64_t N, int64_t K, const void* A, int6
                      : launch_grouped_tile<Elt, 128, 128, 2>(p, plan, up, dev.num_cu, stream);
 }
 
+PlanParams plan_params(const int32_t* idx, const sdt_moe_plan* plan, int64_t rows) {
+    PlanParams p;
+    p.idx = idx;
+    p.counts = plan->counts;
+    p.offsets = plan->offsets;
+    p.rows = plan->rows;
+    p.pos = plan->pos;
+    p.tiles = plan->tiles;
+    p.R = (int)(plan->tokens * plan->topk);
+    p.E = plan->experts;
+    p.cap = (int)rows;
+    return p;
+}
+
+// The plan and its rows of X, quantised.
 template <typename Elt>
-int quantize_tokens(const sdt_moe_plan* plan, int64_t K, const void* X, int64_t ldx, void* Q,
-                    int64_t ldq, void* S, void* stream) {
+int plan_and_quantize(const int32_t* idx, const sdt_moe_plan* plan, int64_t rows, int64_t K,
+                      const void* X, int64_t ldx, void* Q, int64_t ldq, void* S, void* stream) {
     Mx4QuantTokens p;
     p.X = static_cast<const uint16_t*>(X);
     p.ldx = ldx;
@@ -432,8 +447,19 @@ int quantize_tokens(const sdt_moe_plan* plan, int64_t K, const void* X, int64_t 
     p.topk = plan->topk;
     p.K = (int)K;
     p.nkt = (int)k_tiles(K);
-    return launch(reinterpret_cast<const void*>(&mx4_quantize_tokens_kernel<Elt>),
-                  ceil_div(p.tokens, 16) * p.nkt, 256, p, stream);
+    const int64_t grid = ceil_div(p.tokens, 16) * p.nkt;
+    if (plan->tokens * plan->topk <= kPlanQuantizeSlots) {
+        PlanParams q = plan_params(idx, plan, rows);
+        void* args[] = {&q, &p};
+        return launched(hipLaunchKernel(reinterpret_cast<const void*>(&moe_plan_quantize_kernel<Elt>),
+                                        dim3((unsigned)grid), dim3(256), args, 0,
+                                        static_cast<hipStream_t>(stream)));
+    }
+    const int rc = moe_plan(idx, plan, stream);
+    if (rc != SDT_OK) return rc;
+    if (plan->topk > kMaxTopk)
+        return quantize<Elt>(rows, K, X, plan->tokens, ldx, plan->rows, plan->topk, Q, ldq, S, stream);
+    return launch(reinterpret_cast<const void*>(&mx4_quantize_tokens_kernel<Elt>), grid, 256, p, stream);
 }
 
 template <typename S>
@@ -517,13 +543,9 @@ int moe_layer(const sdt_moe_layer* layer, const int32_t* idx, const float* weigh
     }
     if (misaligned(idx, 4) || misaligned(weights, 4)) return SDT_ERR_UNSUPPORTED;
     uint8_t* w = static_cast<uint8_t*>(workspace);
-    rc = moe_plan(idx, plan, stream);
-    if (rc != SDT_OK || K == 0) return rc;
+    if (K == 0) return moe_plan(idx, plan, stream);
     // Every token is read and quantised once; the gated product comes out quantised.
-    rc = plan->topk <= kMaxTopk
-             ? quantize_tokens<Elt>(plan, K, X, ldx, w + l.xq, l.ldx, w + l.xs, stream)
-             : quantize<Elt>(rows, K, X, T, ldx, plan->rows, plan->topk, w + l.xq, l.ldx, w + l.xs,
-                             stream);
+    rc = plan_and_quantize<Elt>(idx, plan, rows, K, X, ldx, w + l.xq, l.ldx, w + l.xs, stream);
     const Mx4Out hq = {w + l.hq, w + l.hs, l.ldhq};
     if (rc == SDT_OK)
         rc = moe_gemm<Elt>(plan, N, K, w + l.xq, l.ldx, w + l.xs, &layer->gate, &layer->up, nullptr, 0,
@@ -648,16 +670,7 @@ extern "C" int moe_plan(const int32_t* idx, const sdt_moe_plan* plan, void* stre
     if (rc != SDT_OK) return rc;
     if (plan->tokens > 0 && !idx) return SDT_ERR_INVALID_ARG;
     if (misaligned(idx, 4)) return SDT_ERR_UNSUPPORTED;
-    PlanParams p;
-    p.idx = idx;
-    p.counts = plan->counts;
-    p.offsets = plan->offsets;
-    p.rows = plan->rows;
-    p.pos = plan->pos;
-    p.tiles = plan->tiles;
-    p.R = (int)(plan->tokens * plan->topk);
-    p.E = plan->experts;
-    p.cap = (int)rows;
+    PlanParams p = plan_params(idx, plan, rows);
     return launch(reinterpret_cast<const void*>(&moe_plan_kernel), p.E, 1024, p, stream);
 }
 

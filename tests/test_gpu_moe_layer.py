@@ -123,3 +123,32 @@ def test_layer_of_many_slots_a_token():
     want = by_parts(parts, x, idx, w, "bf16")
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("T,topk,E", [(1, 1, 1), (1, 8, 64), (3, 5, 7), (17, 15, 33), (64, 4, 32),
+                                      (4, 64, 1024), (128, 2, 60), (129, 2, 60), (2, 100, 9),
+                                      (1, 64, 1024), (16, 4, 33), (64, 1, 1024), (21, 3, 5), (13, 5, 64)])
+def test_layer_fills_its_plan(T, topk, E):
+    """The plan that the layer leaves is moe_plan's, with few slots and many."""
+    import torch
+
+    import mx4_reference as ref
+    sdt = _sdt()
+    N, K = 32, 288
+    layer, parts = make_layer(E, N, K, "bf16", 6)
+    rng = np.random.default_rng(T * topk)
+    ids = rng.integers(-1, E + 1, (T, topk)).astype(np.int32)
+    x = torch.from_numpy(rng.standard_normal((T, K))).bfloat16().to(DEV)
+    w = dev(rng.random((T, topk)).astype(np.float32))
+    p = sdt.MoePlan.empty(T, topk, E, device=DEV)
+    for a in (p.counts, p.offsets, p.rows, p.pos, p.tiles):
+        a.fill_(-77)
+    say(f"layer's plan T {T} topk {topk} E {E}")
+    y = layer(x, dev(ids), w, plan=p)
+    torch.cuda.synchronize()
+    for got, want, what in zip((p.counts, p.offsets, p.rows, p.pos, p.tiles), ref.plan(ids, E),
+                               ("counts", "offsets", "rows", "pos", "tiles")):
+        assert np.array_equal(got.cpu().numpy(), want), what
+    want = by_parts(parts, x, dev(ids), w, "bf16")
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
