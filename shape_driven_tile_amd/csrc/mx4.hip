@@ -52,6 +52,9 @@ int check_out(int64_t rows, int64_t N, const void* C, int64_t ldc) {
     return SDT_OK;
 }
 
+// 16-bit rows x K of 64 MB or more: twice the L2 caches' 32.
+bool past_caches(int64_t rows, int64_t K) { return rows * K >= int64_t(1) << 25; }
+
 template <typename Elt>
 int quantize(int64_t rows, int64_t K, const void* X, int64_t xrows, int64_t ldx,
              const int32_t* index, int divisor, void* Q, int64_t ldq, void* S, void* stream) {
@@ -73,7 +76,13 @@ int quantize(int64_t rows, int64_t K, const void* X, int64_t xrows, int64_t ldx,
     p.rows = rows;
     p.K = (int)K;
     p.nkt = (int)k_tiles(K);
-    return launch(reinterpret_cast<const void*>(&mx4_quantize_kernel<Elt>),
+    DeviceInfo dev;
+    rc = device_info(&dev);
+    if (rc != SDT_OK) return rc;
+    const bool large = past_caches(rows, K);
+    p.nxcd = large ? dev.nxcd : 1;
+    return launch(large ? reinterpret_cast<const void*>(&mx4_quantize_kernel<Elt, true>)
+                        : reinterpret_cast<const void*>(&mx4_quantize_kernel<Elt, false>),
                   ceil_div(rows, 64) * p.nkt, 256, p, stream);
 }
 
@@ -96,6 +105,10 @@ int dequantize(int64_t rows, int64_t K, const void* Q, int64_t ldq, const void* 
     p.rows = rows;
     p.K = (int)K;
     p.nkt = (int)k_tiles(K);
+    DeviceInfo dev;
+    rc = device_info(&dev);
+    if (rc != SDT_OK) return rc;
+    p.nxcd = past_caches(rows, K) ? dev.nxcd : 1;
     return launch(reinterpret_cast<const void*>(&mx4_dequantize_kernel<OUT>),
                   ceil_div(rows, 64) * p.nkt, 256, p, stream);
 }
