@@ -128,7 +128,7 @@ __device__ __forceinline__ int best_lane(uint64_t k) {
 // logits in fp32 or (WIDE), with a bias or worths summed over two, from scores in
 // 64 bits, so that two experts tie only where their definitions do.  Bound by
 // the rounds' instructions: 16384 tokens, 8 of 128 experts (bf16): 35 us with
-// lane exchanges through LDS on 64-bit keys, 10 us so.
+// lane exchanges through LDS on 64-bit keys, 11.5 us so.
 template <typename T, int EPL, bool WIDE>
 __global__ __launch_bounds__(256) void moe_route_kernel(RouteParams p) {
     typedef std::conditional_t<WIDE, uint64_t, uint32_t> Key;
@@ -292,7 +292,8 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteParams p) {
 // = scale / S * (dw_j - sum_i dw_i p_i), or scale * dw_j; a sigmoid's dl = s (1 -
 // s) ds.  Softmax: dl = s (ds - sum ds s); renormalised, that sum is zero by
 // construction and s_j / S = p_j, so dl_j = scale p_j (dw_j - sum dw p) on the
-// chosen and exactly zero elsewhere.
+// chosen and exactly zero elsewhere.  16384 tokens, 8 of 128 experts (bf16): 9.8
+// us, bound by its instructions (memory alone would be 2).
 template <typename T, int EPL>
 __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteParams p) {
     const int lane = threadIdx.x & 63;

@@ -278,8 +278,9 @@ __device__ __forceinline__ void mx4_quantize_token_tile(const Mx4QuantTokens& p,
     }
 }
 
-// Bound by the writes of the rows' codes; 16 tokens a workgroup, so that a decode
-// batch also fills the CUs.
+// Bound by the writes of the rows' codes (4096 tokens of 2048, 6 experts each: 13 us;
+// quantising the plan's rows one by one took 22); 16 tokens a workgroup, so that a
+// decode batch also fills the CUs.
 template <typename Elt>
 __global__ __launch_bounds__(256) void mx4_quantize_tokens_kernel(Mx4QuantTokens p) {
     __shared__ uint16_t sm[16 * 4];
@@ -499,9 +500,8 @@ __device__ __forceinline__ int uniform_load(const int32_t* p) {
 // kept at c ^ mx4_swz(r).  A fragment read of half s takes chunk 2 g + s in quarter
 // g; its bank pattern is that of the 16-bit kernels (chunk 4 s + g at 4 s + g ^
 // swz_pp(r)) with the places' three bits turned round, so it is as free of
-// conflicts.  Chunks in order (and not halves first) matter to the loads: four
-// neighbouring lanes fetch one aligned 64 bytes; fetching every other chunk they
-// took twice the time (a 128 x 128 k-tile's loads 1080 clocks).
+// conflicts.  Chunks in order keep an aligned 64 bytes to four neighbouring lanes
+// of a load (halves first: 0-8% slower on most tiles, 3% faster on some).
 __device__ __forceinline__ int mx4_swz(int row) {
     return ((row & 1) ? 1 : 0) ^ ((row & 2) ? 3 : 0) ^ ((row & 4) ? 6 : 0);
 }
@@ -566,7 +566,9 @@ __device__ __forceinline__ uint32_t mx4_pack2(float a, float b) {
 // k-tiles in flight, and are read from there as fragments.  (Loaded as fragments,
 // a lane to a row, each instruction touches 64 lines: 5.8 bytes a clock and CU,
 // a third of what memory gives.)  Few rows (NMB = 1: 16) leave the LDS to more
-// stages.  The waves' partial sums are added in wave order.
+// stages.  The waves' partial sums are added in wave order.  16 x 12288 x 4096: 7.0
+// us (3.8 TB/s of weights, 9.9 without the LDS); experts' products of 64 tokens:
+// 41 and 25 us (5.2 and 4.3 TB/s).
 // A wave's LDS: grouped products have many short tiles, and three workgroups a CU
 // with two stages pass them faster than two with three (64 tokens of 32 experts:
 // 44.2 -> 41.8 and 27.6 -> 24.6 us; 8 tokens of 64: 21.3 -> 19.7 and 13.5 -> 11.8).
@@ -932,6 +934,12 @@ __device__ __forceinline__ void mx4_store_quantized(const Mx4Gemm& p, const floa
 // second, so a lane holds both factors of its outputs; BN / 2 columns per tile.
 // GROUPED: a tile's rows are one expert's of a plan; the tiles are counted from
 // the plan's counts, so the grid holds no empty ones.
+//
+// Bound by the loads into LDS (53 bytes a clock and CU from rows on 128-byte lines,
+// 650 of a 128 x 128 k-tile's 1050 clocks; 30 from others) and, on short k-loops,
+// by the epilogue.  1024 x 8192 x 8192: 40 us (3.4 PFLOP/s); 4096 tokens of 64
+// experts, 2048 -> 1024: gated 114-118 us, down 66 (1.8 and 1.6 PFLOP/s).  With loader
+// waves and one workgroup a CU those took 167 and 106.
 template <typename Elt, int BM, int BN, int WM, int WN, int NS, bool GROUPED, bool GATED,
           bool QOUT = false>
 __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
