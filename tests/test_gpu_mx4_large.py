@@ -175,3 +175,20 @@ def test_gemm_full_round_empty_k():
     sdt.gemm_mx4_f16(sdt.Mx4.empty(M, 0, device=DEV), sdt.Mx4.empty(N, 0, device=DEV), c)
     torch.cuda.synchronize()
     assert bool((c == 0).all())
+
+
+# between one 64 x 64 and one 64 x 128 tile a CU; few rows in two groups
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [(500, 4000, 33), (500, 4000, 300), (449, 3970, 700),
+                                   (512, 4096, 1100), (500, 4000, 2100), (65, 1000, 600),
+                                   (100, 4001, 1300), (128, 8000, 257)])
+def test_gemm_middle_sizes(dtype, M, N, K):
+    import torch
+    rng = np.random.default_rng(M + N + 2 * K)
+    ca, sa = random_matrix(M, K, rng, whole=True)
+    cb, sb = random_matrix(N, K, rng, whole=True)
+    say(f"middle sizes {dtype} {M}x{N}x{K}")
+    got = run_gemm(dtype, device_matrix(ca, sa, M, K, 16), device_matrix(cb, sb, N, K, 48), M, N)
+    want = torch.from_numpy(ref.values(ca, sa, K).astype(np.float32)
+                            @ ref.values(cb, sb, K).astype(np.float32).T)
+    assert torch.equal(got, want.to(_t(dtype)))
