@@ -15,7 +15,9 @@ class Mx4Experts:
     """The experts' weights (gate and up: N x K, down: K x N, one matrix per
     expert) and the layer's work buffer, which grows to the largest call's need
     and is used by one stream at a time: work of the layer on another stream is
-    ordered after it by the caller."""
+    ordered after it by the caller.  What a call allocates it allocates on the
+    stream that runs it, and the buffer is recorded on every stream that uses it,
+    so the allocator gives none of it away before that work is done."""
 
     def __init__(self, gate: sdt.Mx4, up: sdt.Mx4, down: sdt.Mx4):
         if gate.q.dim() != 3 or (up.rows, up.K) != (gate.rows, gate.K) or \
@@ -29,24 +31,43 @@ class Mx4Experts:
                                      up._experts(self.experts, "up"),
                                      down._experts(self.experts, "down"))
         self._workspace = None
-        self._holds = None                       # the sizes that the buffer was last checked for
+        self._streams = set()                    # that the allocator knows to use the buffer
+        self._holds = None                       # the sizes and stream it was last checked for
 
     def workspace(self, tokens: int, topk: int):
+        """The buffer for a call on the current stream."""
         import torch
-        if self._holds == (tokens, topk):
+        handle = sdt._stream_handle(None)
+        if self._holds == (tokens, topk, handle):
             return self._workspace
         need = sdt.moe_experts_workspace_size(tokens, topk, self.experts, self.N, self.K)
         if self._workspace is None or self._workspace.numel() < need:
             self._workspace = torch.empty(max(need, 16), dtype=torch.uint8,
                                           device=self.weights[0].q.device)
-        self._holds = (tokens, topk)
+            self._streams = {handle}
+        elif handle not in self._streams:
+            self._workspace.record_stream(torch.cuda.current_stream())
+            self._streams.add(handle)
+        self._holds = (tokens, topk, handle)
         return self._workspace
 
     def __call__(self, x, idx, weights, plan: sdt.MoePlan | None = None, out=None, stream=None):
         """y [T, K] of x [T, K] (float16 or bfloat16), the experts idx [T, topk]
         (int32) of each token and their weights [T, topk] (float32).  `plan`: a
         MoePlan of these sizes to fill (made here if absent); `out`: y's memory,
-        rows a multiple of 8 elements apart."""
+        rows a multiple of 8 elements apart; `stream`: instead of the current
+        one, ordered with it by the caller."""
+        import torch
+        if stream is None or stream.cuda_stream == sdt._stream_handle(None):
+            return self._run(x, idx, weights, plan, out)
+        current = torch.cuda.current_stream()
+        with torch.cuda.stream(stream):
+            y = self._run(x, idx, weights, plan, out)
+        if out is None:
+            y.record_stream(current)             # where the caller goes on with it
+        return y
+
+    def _run(self, x, idx, weights, plan, out):
         import torch
         T, topk = idx.shape
         if plan is None:
@@ -58,7 +79,7 @@ class Mx4Experts:
             out = torch.empty(T, ld, dtype=x.dtype, device=x.device)
             if ld != self.K:
                 out = out[:, :self.K]
-        sdt.moe_experts_mx4(self.layer, x, idx, weights, plan, out, self.workspace(T, topk), stream)
+        sdt.moe_experts_mx4(self.layer, x, idx, weights, plan, out, self.workspace(T, topk))
         return out
 
 
