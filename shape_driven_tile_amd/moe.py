@@ -17,7 +17,9 @@ class Mx4Experts:
     and is used by one stream at a time: work of the layer on another stream is
     ordered after it by the caller.  What a call allocates it allocates on the
     stream that runs it, and the buffer is recorded on every stream that uses it,
-    so the allocator gives none of it away before that work is done."""
+    so the allocator gives none of it away before that work is done.  A buffer
+    that a graph was captured with is kept as long as the layer, also when a
+    larger one replaces it for later calls."""
 
     def __init__(self, gate: sdt.Mx4, up: sdt.Mx4, down: sdt.Mx4):
         if gate.q.dim() != 3 or (up.rows, up.K) != (gate.rows, gate.K) or \
@@ -31,6 +33,8 @@ class Mx4Experts:
                                      up._experts(self.experts, "up"),
                                      down._experts(self.experts, "down"))
         self._workspace = None
+        self._captured = False                   # a graph holds the buffer's address
+        self._kept = []                          # replaced buffers that graphs hold
         self._streams = set()                    # that the allocator knows to use the buffer
         self._holds = None                       # the sizes and stream it was last checked for
 
@@ -38,10 +42,19 @@ class Mx4Experts:
         """The buffer for a call on the current stream."""
         import torch
         handle = sdt._stream_handle(None)
-        if self._holds == (tokens, topk, handle):
-            return self._workspace
+        if self._holds != (tokens, topk, handle):
+            self._hold(tokens, topk, handle)
+        if not self._captured and torch.cuda.is_current_stream_capturing():
+            self._captured = True
+        return self._workspace
+
+    def _hold(self, tokens: int, topk: int, handle: int) -> None:
+        import torch
         need = sdt.moe_experts_workspace_size(tokens, topk, self.experts, self.N, self.K)
         if self._workspace is None or self._workspace.numel() < need:
+            if self._captured:
+                self._kept.append(self._workspace)
+                self._captured = False
             self._workspace = torch.empty(max(need, 16), dtype=torch.uint8,
                                           device=self.weights[0].q.device)
             self._streams = {handle}
@@ -49,7 +62,6 @@ class Mx4Experts:
             self._workspace.record_stream(torch.cuda.current_stream())
             self._streams.add(handle)
         self._holds = (tokens, topk, handle)
-        return self._workspace
 
     def __call__(self, x, idx, weights, plan: sdt.MoePlan | None = None, out=None, stream=None):
         """y [T, K] of x [T, K] (float16 or bfloat16), the experts idx [T, topk]

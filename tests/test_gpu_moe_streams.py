@@ -68,3 +68,33 @@ def test_streams_in_turn():
     torch.cuda.synchronize()
     for y, w in zip(got, want):
         assert torch.equal(y, w)
+
+
+def test_graph_keeps_its_buffer():
+    """A graph captured with a small buffer, replayed after larger eager calls have
+    replaced it and other tensors have taken and filled memory of its size."""
+    import torch
+
+    from shape_driven_tile_amd import binding as sdt
+    E, topk, N, K = 8, 2, 96, 160
+    layer, parts = make_layer(E, N, K, "bf16", 13)
+    small, large = inputs(50, topk, E, K, 1), inputs(700, topk, E, K, 2)
+    say("layer in a graph, larger calls between replays")
+    layer(*small)
+    y = torch.zeros(50, K, dtype=torch.bfloat16, device=DEV)
+    plan = sdt.MoePlan.empty(50, topk, E, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer(*small, plan=plan, out=y)
+    need = sdt.moe_experts_workspace_size(50, topk, E, N, K)
+    want = by_parts(parts, *small, "bf16")
+    want_large = by_parts(parts, *large, "bf16")
+    torch.cuda.synchronize()
+    for _ in range(3):
+        assert torch.equal(layer(*large), want_large)
+        filled = [torch.full((need,), 0x7f, dtype=torch.uint8, device=DEV) for _ in range(4)]
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        assert all(bool((f == 0x7f).all()) for f in filled)

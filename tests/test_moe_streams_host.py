@@ -44,6 +44,7 @@ class Streams:
         monkeypatch.setattr(torch, "empty", make)
         monkeypatch.setattr(torch.cuda, "stream", on)
         monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: self.current[-1])
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
         monkeypatch.setattr(torch.Tensor, "record_stream",
                             lambda t, s: self.known[t.data_ptr()].add(s.cuda_stream))
         monkeypatch.setattr(sdt, "_stream_handle", lambda s: (s or self.current[-1]).cuda_stream)
@@ -123,3 +124,25 @@ def test_given_memory_stays_the_callers(streams):
     c = streams.calls[-1]
     assert c.stream == streams.side.cuda_stream and c.out == out.data_ptr()
     assert c.plan == plan.counts.data_ptr()
+
+
+def test_buffer_of_a_captured_call_is_kept(streams, monkeypatch):
+    """A graph holds the buffer's address: a larger buffer that replaces it for
+    later calls must not free it, and buffers of no graph are not kept."""
+    import weakref
+
+    import torch
+    capturing = [False]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    run = layer()
+
+    def buffer(T, capture):
+        capturing[0] = capture
+        run(*tokens(T))
+        return weakref.ref(run._workspace)
+
+    refs = [buffer(5, False), buffer(500, False), buffer(500, True), buffer(2000, False),
+            buffer(9000, True), buffer(20000, False)]
+    streams.keep.clear()
+    alive = [r() is not None for r in refs]
+    assert alive == [False, True, True, False, True, True]
