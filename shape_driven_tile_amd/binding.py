@@ -670,7 +670,7 @@ class Mx4:
     bytes `s` [mx4_scale_bytes(rows, K)].  With a leading dimension on both, one
     matrix per expert."""
 
-    __slots__ = ("q", "s", "rows", "K")
+    __slots__ = ("q", "s", "rows", "K", "device")      # device: its index, -1 the host
 
     def __init__(self, q, s, rows: int, K: int):
         import torch
@@ -690,7 +690,7 @@ class Mx4:
                              f"{rows} x {K}")
         if q.stride()[-1] != 1 or s.stride()[-1] != 1:
             raise ValueError("Mx4: unit stride along rows of codes and along the scales")
-        self.q, self.s, self.rows, self.K = q, s, rows, K
+        self.q, self.s, self.rows, self.K, self.device = q, s, rows, K, where
 
     @classmethod
     def empty(cls, rows: int, K: int, experts: int | None = None, device="cuda") -> "Mx4":
@@ -701,7 +701,7 @@ class Mx4:
         m.q = torch.empty(lead + (rows, -(-K // 32) * 16), dtype=torch.uint8, device=device)
         m.s = torch.empty(lead + (-(-rows // 64) * -(-K // 256) * 512,), dtype=torch.uint8,
                           device=device)
-        m.rows, m.K = rows, K
+        m.rows, m.K, m.device = rows, K, m.q.get_device()
         return m
 
     def ldq(self) -> int:
@@ -730,10 +730,18 @@ def _check(rc: int, where: str) -> None:
         raise SdtError(rc, where)
 
 
+def _apart(where: str, *devices: int):
+    """Operands of different devices (-1: the host): the C ABI takes addresses, which
+    do not tell, so no call is made with them."""
+    return TypeError(f"{where}: operands must be on one device, not on {devices} (-1: the host)")
+
+
 def _quantize(entry, X, out, dtype, stream):
     px, ldx = _rows(X, "X", dtype)
     if X.shape != (out.rows, out.K):
         raise ValueError(f"shape mismatch X{tuple(X.shape)} out ({out.rows}, {out.K})")
+    if out.device != X.get_device():
+        raise _apart(entry, X.get_device(), out.device)
     q, ldq, s = out._one("out")
     _check(getattr(lib(), entry)(out.rows, out.K, px, ldx, q, ldq, s, _stream_handle(stream)), entry)
 
@@ -756,6 +764,8 @@ def _quantize_rows(entry, X, index, divisor, out, dtype, stream):
         raise ValueError(f"shape mismatch X{tuple(X.shape)} index{tuple(index.shape)} out "
                          f"({out.rows}, {out.K})")
     _ints(index, "index")
+    if not (out.device == X.get_device() == index.get_device()):
+        raise _apart(entry, X.get_device(), index.get_device(), out.device)
     q, ldq, s = out._one("out")
     _check(getattr(lib(), entry)(out.rows, out.K, px, X.shape[0], ldx, index.data_ptr(),
                                  int(divisor), q, ldq, s, _stream_handle(stream)), entry)
@@ -777,6 +787,8 @@ def _dequantize(entry, m, Y, dtype, stream):
     py, ldy = _rows(Y, "Y", dtype)
     if Y.shape != (m.rows, m.K):
         raise ValueError(f"shape mismatch matrix ({m.rows}, {m.K}) Y{tuple(Y.shape)}")
+    if m.device != Y.get_device():
+        raise _apart(entry, m.device, Y.get_device())
     q, ldq, s = m._one("matrix")
     _check(getattr(lib(), entry)(m.rows, m.K, q, ldq, s, py, ldy, _stream_handle(stream)), entry)
 
@@ -803,6 +815,8 @@ def mx4_pack_scales(scales, out: Mx4, stream=None) -> None:
     p, ld = _rows(scales, "scales", torch.uint8)
     if tuple(scales.shape) != (out.rows, -(-out.K // 32)):
         raise ValueError(f"shape mismatch scales{tuple(scales.shape)} out ({out.rows}, {out.K})")
+    if out.device != scales.get_device():
+        raise _apart("mx4_pack_scales", scales.get_device(), out.device)
     _, _, s = out._one("out")
     _check(lib().mx4_pack_scales(out.rows, out.K, p, ld, s, _stream_handle(stream)),
            "mx4_pack_scales")
@@ -814,6 +828,8 @@ def _gemm_mx4(entry, A, B, C, dtype, stream):
     pa, lda, sa = A._one("A")
     pb, ldb, sb = B._one("B")
     pc, ldc = _rows(C, "C", dtype)
+    if not (A.device == B.device == C.get_device()):
+        raise _apart(entry, A.device, B.device, C.get_device())
     _check(getattr(lib(), entry)(A.rows, B.rows, A.K, pa, lda, sa, pb, ldb, sb, pc, ldc,
                                  _stream_handle(stream)), entry)
 
@@ -838,6 +854,8 @@ def _gemv_mx4(entry, x, B, y, dtype, stream):
         raise ValueError("x and y must be contiguous vectors")
     if x.shape[0] != B.K or y.shape[0] != B.rows:
         raise ValueError(f"shape mismatch x{tuple(x.shape)} B({B.rows}, {B.K}) y{tuple(y.shape)}")
+    if not (B.device == x.get_device() == y.get_device()):
+        raise _apart(entry, x.get_device(), B.device, y.get_device())
     pb, ldb, sb = B._one("B")
     _check(getattr(lib(), entry)(B.rows, B.K, x.data_ptr(), pb, ldb, sb, y.data_ptr(),
                                  _stream_handle(stream)), entry)
@@ -916,6 +934,11 @@ def moe_route(logits, idx, weights, cfg: SdtRoute, bias=None, stream=None) -> No
         raise ValueError(f"bias must hold {E} values")
     b = None if bias is None else _floats(bias, "bias")
     entry = "moe_route_" + kind
+    where = logits.get_device()
+    if not (idx.get_device() == weights.get_device() == where) or \
+            (bias is not None and bias.get_device() != where):
+        raise _apart(entry, where, idx.get_device(), weights.get_device(),
+                     where if bias is None else bias.get_device())
     _check(getattr(lib(), entry)(T, E, p, ld, b, ctypes.byref(cfg), _ints(idx, "idx"),
                                  _floats(weights, "weights"), _stream_handle(stream)), entry)
 
@@ -932,6 +955,9 @@ def moe_route_backward(logits, idx, dweights, dlogits, cfg: SdtRoute, stream=Non
                          f"idx{tuple(idx.shape)} dweights{tuple(dweights.shape)} "
                          f"dlogits{tuple(dlogits.shape)}")
     entry = "moe_route_backward_" + kind
+    where = logits.get_device()
+    if not (idx.get_device() == dweights.get_device() == dlogits.get_device() == where):
+        raise _apart(entry, where, idx.get_device(), dweights.get_device(), dlogits.get_device())
     _check(getattr(lib(), entry)(T, E, p, ld, ctypes.byref(cfg), _ints(idx, "idx"),
                                  _floats(dweights, "dweights"), d, ldd, _stream_handle(stream)),
            entry)
@@ -950,7 +976,7 @@ class MoePlan:
     each out of `experts`: int32 device tensors counts, offsets, rows, pos, tiles."""
 
     __slots__ = ("tokens", "topk", "experts", "size", "counts", "offsets", "rows", "pos", "tiles",
-                 "_struct")
+                 "device", "_struct")
 
     @classmethod
     def empty(cls, tokens: int, topk: int, experts: int, device="cuda") -> "MoePlan":
@@ -961,6 +987,7 @@ class MoePlan:
         sizes = (experts, experts + 1, size, tokens * topk, size // 64)
         flat = torch.empty(sum(sizes), dtype=torch.int32, device=device)
         p.counts, p.offsets, p.rows, p.pos, p.tiles = flat.split(sizes)
+        p.device = flat.get_device()         # its index, -1 the host
         at = flat.data_ptr()
         offsets = at + 4 * experts
         rows = offsets + 4 * experts + 4
@@ -974,6 +1001,8 @@ def moe_plan(idx, plan: MoePlan, stream=None) -> None:
     """Fills plan from idx [tokens, topk]: the slots sorted by expert."""
     if tuple(idx.shape) != (plan.tokens, plan.topk):
         raise ValueError(f"idx must be ({plan.tokens}, {plan.topk}), got {tuple(idx.shape)}")
+    if plan.device != idx.get_device():
+        raise _apart("moe_plan", idx.get_device(), plan.device)
     _check(lib().moe_plan(_ints(idx, "idx"), ctypes.byref(plan._struct), _stream_handle(stream)),
            "moe_plan")
 
@@ -987,6 +1016,10 @@ def _moe_gemm_mx4(entry, plan, A, B, C, up, dtype, stream):
     pc, ldc = _rows(C, "C", dtype)
     b = B._experts(plan.experts, "B")
     u = None if up is None else ctypes.byref(up._experts(plan.experts, "up"))
+    if not (plan.device == A.device == B.device == C.get_device()) or \
+            (up is not None and up.device != plan.device):
+        raise _apart(entry, plan.device, A.device, B.device, C.get_device(),
+                     B.device if up is None else up.device)
     _check(getattr(lib(), entry)(ctypes.byref(plan._struct), B.rows, B.K, pa, lda, sa,
                                  ctypes.byref(b), u, pc, ldc, _stream_handle(stream)), entry)
 
@@ -1012,6 +1045,8 @@ def _moe_combine(entry, plan, D, weights, Y, dtype, stream):
             tuple(weights.shape) != (plan.tokens, plan.topk):
         raise ValueError(f"shape mismatch plan {plan.size} rows D{tuple(D.shape)} "
                          f"weights{tuple(weights.shape)} Y{tuple(Y.shape)}")
+    if not (plan.device == D.get_device() == weights.get_device() == Y.get_device()):
+        raise _apart(entry, plan.device, D.get_device(), weights.get_device(), Y.get_device())
     _check(getattr(lib(), entry)(ctypes.byref(plan._struct), N, pd, ldd,
                                  _floats(weights, "weights"), py, ldy, _stream_handle(stream)), entry)
 
@@ -1051,6 +1086,12 @@ def moe_experts_mx4(layer: SdtMoeLayer, X, idx, weights, plan: MoePlan, Y, works
                          f"weights{tuple(weights.shape)}")
     px, ldx = _rows(X, "X", X.dtype)
     py, ldy = _rows(Y, "Y", X.dtype)
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise TypeError("workspace must be contiguous uint8")
+    devices = (X.get_device(), idx.get_device(), weights.get_device(), plan.device,
+               Y.get_device(), workspace.get_device())
+    if devices.count(devices[0]) != 6:
+        raise _apart(entry, *devices)
     _check(getattr(lib(), entry)(ctypes.byref(layer), _ints(idx, "idx"),
                                  _floats(weights, "weights"), ctypes.byref(plan._struct), px, ldx,
                                  py, ldy, workspace.data_ptr(), workspace.numel(),
