@@ -487,7 +487,8 @@ int moe_combine_bf16(const sdt_moe_plan* plan, int64_t N, const void* D, int64_t
  * the calls above in order: moe_plan, mx4_quantize_rows, moe_gemm_mx4 with `up`,
  * mx4_quantize_rows, moe_gemm_mx4, moe_combine (the layer reads and quantises a
  * token once, and the gated product comes out of its kernel quantised).  X (tokens x K, stride ldx
- * elements), gate and up (N x K), down (K x N), Y (tokens x K, ldy a multiple
+ * elements), gate and up (N x K), down (K x N), a matrix of each for every
+ * expert of the plan, Y (tokens x K, ldy a multiple
  * of 8, 16-byte aligned).  workspace: device memory, 16-byte aligned, at least
  * sdt_moe_experts_workspace_size bytes (fewer: SDT_ERR_INVALID_ARG); no
  * initialisation; calls that share it must be ordered on one stream. */

@@ -84,13 +84,29 @@ class SdtMoePlan(ctypes.Structure):
 
 
 class SdtMx4Experts(ctypes.Structure):
+    """sdt_mx4_experts.  Made from an Mx4 it knows how many matrices its addresses
+    hold and where they lie; a struct of plain addresses does not."""
+    experts = device = None
     _fields_ = [("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("q_expert", ctypes.c_int64),
                 ("s", ctypes.c_void_p), ("s_expert", ctypes.c_int64)]
 
 
 class SdtMoeLayer(ctypes.Structure):
+    """sdt_moe_layer, with what its matrices know of themselves: moe_experts_mx4
+    refuses a plan of other experts, and operands of another device."""
+    experts = device = None
     _fields_ = [("N", ctypes.c_int64), ("K", ctypes.c_int64), ("gate", SdtMx4Experts),
                 ("up", SdtMx4Experts), ("down", SdtMx4Experts)]
+
+    def __init__(self, *args, **kw):
+        super().__init__(*args, **kw)
+        matrices = [m for m in (*args[2:], *kw.values()) if isinstance(m, SdtMx4Experts)]
+        for what in ("experts", "device"):
+            known = {getattr(m, what) for m in matrices} - {None}
+            if len(known) > 1:
+                raise TypeError(f"the layer's matrices do not agree: {what} {sorted(known)}")
+            if known:
+                setattr(self, what, known.pop())
 
 
 class SdtError(RuntimeError):
@@ -721,8 +737,10 @@ class Mx4:
     def _experts(self, experts, name) -> SdtMx4Experts:
         if self.q.dim() != 3 or self.q.shape[0] != experts:
             raise ValueError(f"{name} must hold one matrix for each of {experts} experts")
-        return SdtMx4Experts(self.q.data_ptr(), self.ldq(), self.q.stride(0), self.s.data_ptr(),
-                             self.s.stride(0))
+        given = SdtMx4Experts(self.q.data_ptr(), self.ldq(), self.q.stride(0), self.s.data_ptr(),
+                              self.s.stride(0))
+        given.experts, given.device = experts, self.device
+        return given
 
 
 def _check(rc: int, where: str) -> None:
@@ -730,7 +748,7 @@ def _check(rc: int, where: str) -> None:
         raise SdtError(rc, where)
 
 
-def _apart(where: str, *devices: int):
+def _apart(where: str, *devices):
     """Operands of different devices (-1: the host): the C ABI takes addresses, which
     do not tell, so no call is made with them."""
     return TypeError(f"{where}: operands must be on one device, not on {devices} (-1: the host)")
@@ -1074,7 +1092,8 @@ def moe_experts_workspace_size(tokens: int, topk: int, experts: int, N: int, K: 
 def moe_experts_mx4(layer: SdtMoeLayer, X, idx, weights, plan: MoePlan, Y, workspace,
                     stream=None) -> None:
     """A layer of gated MX4 experts in one call (moe.Mx4Experts keeps the layer);
-    workspace: a uint8 device tensor of moe_experts_workspace_size bytes."""
+    workspace: a uint8 device tensor of moe_experts_workspace_size bytes.  A layer
+    made of plain addresses has to hold as many matrices as the plan has experts."""
     import torch
     entry = {torch.float16: "moe_experts_mx4_f16", torch.bfloat16: "moe_experts_mx4_bf16"}.get(X.dtype)
     if entry is None:
@@ -1084,14 +1103,16 @@ def moe_experts_mx4(layer: SdtMoeLayer, X, idx, weights, plan: MoePlan, Y, works
             tuple(idx.shape) != (plan.tokens, plan.topk) or tuple(weights.shape) != tuple(idx.shape):
         raise ValueError(f"shape mismatch X{tuple(X.shape)} Y{tuple(Y.shape)} idx{tuple(idx.shape)} "
                          f"weights{tuple(weights.shape)}")
+    if layer.experts is not None and layer.experts != plan.experts:
+        raise ValueError(f"a plan of {plan.experts} experts for a layer of {layer.experts}")
     px, ldx = _rows(X, "X", X.dtype)
     py, ldy = _rows(Y, "Y", X.dtype)
     if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise TypeError("workspace must be contiguous uint8")
     devices = (X.get_device(), idx.get_device(), weights.get_device(), plan.device,
                Y.get_device(), workspace.get_device())
-    if devices.count(devices[0]) != 6:
-        raise _apart(entry, *devices)
+    if devices.count(devices[0]) != 6 or layer.device not in (None, devices[0]):
+        raise _apart(entry, *devices, layer.device)
     _check(getattr(lib(), entry)(ctypes.byref(layer), _ints(idx, "idx"),
                                  _floats(weights, "weights"), ctypes.byref(plan._struct), px, ldx,
                                  py, ldy, workspace.data_ptr(), workspace.numel(),

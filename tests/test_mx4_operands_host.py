@@ -169,3 +169,41 @@ def test_layer_workspace_is_plain_bytes(library):
         with pytest.raises((TypeError, ValueError)):
             call(bad)
         assert not library.calls
+
+
+def test_layer_and_plan_are_of_the_same_experts(library):
+    """A plan of more experts than the layer's matrices hold would send the products
+    past the last one."""
+    import torch
+
+    from shape_driven_tile_amd import moe
+
+    def matrices(experts, device=0):
+        return (matrix(N, K, device, experts), matrix(N, K, device, experts),
+                matrix(K, N, device, experts))
+
+    def call(given, experts=E):
+        need = sdt.moe_experts_workspace_size(T, TOPK, 8, N, K)
+        sdt.moe_experts_mx4(given, Tensor(T, K, dtype=torch.bfloat16),
+                            Tensor(T, TOPK, dtype=torch.int32), Tensor(T, TOPK, dtype=torch.float32),
+                            plan(0), Tensor(T, K, dtype=torch.bfloat16),
+                            Tensor(need, dtype=torch.uint8))
+    call(moe.Mx4Experts(*matrices(E)).layer)
+    assert library.calls.pop() == "moe_experts_mx4_bf16"
+    for experts in (E - 1, E + 1):
+        given = moe.Mx4Experts(*matrices(experts)).layer
+        with pytest.raises(ValueError):
+            call(given)
+    given = moe.Mx4Experts(*matrices(E, 1)).layer
+    with pytest.raises(TypeError):
+        call(given)
+    gate, up, down = matrices(E)
+    for mixed in ((matrix(N, K, 1, E), up, down), (gate, matrix(N, K, 1, E), down),
+                  (gate, up, matrix(K, N, 1, E))):
+        with pytest.raises(TypeError):
+            moe.Mx4Experts(*mixed)
+    # a struct of addresses: its caller knows what they hold
+    experts = sdt.SdtMx4Experts(0x10000, 64, 64 * 64, 0x10000, 512)
+    assert not library.calls
+    call(sdt.SdtMoeLayer(N, K, experts, experts, experts))
+    assert library.calls.pop() == "moe_experts_mx4_bf16"
