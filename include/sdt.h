@@ -389,9 +389,12 @@ typedef struct sdt_route {
  * without a bias: the sum of the two largest scores in 64 bits).  Largest
  * first; ties go to the lower index, groups likewise.  Weights: the scores
  * (never the bias) of the chosen, over their sum where renormalize is set,
- * times scale.  A NaN logit counts as -infinity, whose score is 0; a row with
- * nothing but these has zero weights (its choice follows the ties); +infinity
- * takes the whole softmax, shared evenly.  A NaN of score + bias counts as
+ * times scale.  Renormalised weights keep the ratios of scores of any size, as far
+ * as 64 bits hold the scores: a softmax score 745 below the row's largest logit
+ * and the sigmoid of a logit below -709 are 0 (a logit of its type's lowest value
+ * is a mask).  A NaN logit counts as -infinity, whose score is 0; a row that
+ * chooses nothing but scores of 0 has zero weights (its choice follows the ties);
+ * +infinity takes the whole softmax, shared evenly.  A NaN of score + bias counts as
  * -infinity.  SDT_ERR_INVALID_ARG: E < 1, topk outside [1, min(64, groups_kept *
  * E / groups)], groups not a divisor of E, groups_kept outside [1, groups],
  * group_top not 1 or 2 or larger than a group, a score or flag outside its

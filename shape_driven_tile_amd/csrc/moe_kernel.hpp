@@ -121,9 +121,24 @@ __device__ __forceinline__ int best_lane(uint64_t k) {
     return __builtin_ctzll(__ballot(hi == tophi && (uint32_t)k == toplo));
 }
 
+// The score of a logit x over exp(m), from exponentials of differences, so that scores
+// far below 1 keep their ratios: m is 0 or the largest logit that it is compared
+// with (softmax: scores over exp(top) too, top the row's largest, without their sum;
+// sigmoid: where m < 0).  Zero where 64 bits hold no more of the score itself, a
+// softmax 745 below the row's largest and a sigmoid below -709: a logit of a type's
+// lowest value is a mask, whatever it is compared with.
+__device__ __forceinline__ float softmax_share(float x, float top, float m) {
+    if (x == -__builtin_inff() || x - top < -745.0f) return 0.0f;
+    return x == m ? 1.0f : expf(x - m);            // x == m: also an infinite one
+}
+__device__ __forceinline__ float sigmoid_share(float x, float m) {
+    if (x < -709.0f) return 0.0f;
+    return expf(fminf(x, 0.0f) - fminf(m, 0.0f)) / (1.0f + expf(-fabsf(x)));
+}
+
 // One wave per token; lane l holds experts l EPL .. + EPL - 1, so the lowest
-// lane among equals has the lowest expert.  Every score is formed from the
-// logits in registers; the choice is topk rounds of a wave-wide maximum, six
+// lane among equals has the lowest expert.  The weights are formed from the
+// chosen logits, a lane each; the choice is topk rounds of a wave-wide maximum, six
 // steps of lane-crossing operands (DPP) on 32-bit keys.  Keys come from the
 // logits in fp32 or (WIDE), with a bias or worths summed over two, from scores in
 // 64 bits, so that two experts tie only where their definitions do.  Bound by
@@ -147,22 +162,19 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteParams p) {
         if (x[j] != x[j]) x[j] = ninf;
         top = fmaxf(top, x[j]);
     }
-    // scores: softmax's numerators (the largest logit's is 1, also an infinite
-    // one's) or sigmoids
-    float s[EPL];
+    // softmax: the row's largest logit and, where a weight is a score itself, the sum
+    // of the numerators (the largest logit's is 1, also an infinite one's)
+    float inv = 1.0f;
     double sd[WIDE ? EPL : 1];
     if (p.score == 0) {
         top = wave_max(top);
-        float total = 0.0f;
+        if (!p.renormalize) {
+            float total = 0.0f;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            s[j] = x[j] == ninf ? 0.0f : x[j] == top ? 1.0f : expf(x[j] - top);
-            total += s[j];
+            for (int j = 0; j < EPL; ++j) total += softmax_share(x[j], top, top);
+            total = wave_sum(total);
+            inv = total > 0.0f ? 1.0f / total : 0.0f;
         }
-        total = wave_sum(total);
-        const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) s[j] *= inv;
         if constexpr (WIDE) {
             double totald = 0.0;
 #pragma unroll
@@ -174,12 +186,9 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteParams p) {
 #pragma unroll
             for (int j = 0; j < EPL; ++j) sd[j] = totald > 0.0 ? sd[j] / totald : 0.0;
         }
-    } else {
+    } else if constexpr (WIDE) {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            s[j] = x[j] == ninf ? 0.0f : 1.0f / (1.0f + expf(-x[j]));
-            if constexpr (WIDE) sd[j] = x[j] == ninf ? 0.0 : 1.0 / (1.0 + exp(-(double)x[j]));
-        }
+        for (int j = 0; j < EPL; ++j) sd[j] = x[j] == ninf ? 0.0 : 1.0 / (1.0 + exp(-(double)x[j]));
     }
     Key key[EPL];
 #pragma unroll
@@ -252,34 +261,39 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteParams p) {
             }
         }
     }
-    // topk rounds over the lanes' best; lane r keeps the r-th choice
+    // topk rounds over the lanes' best; lane r keeps the r-th choice and its logit
     int mine = 0;
-    float w = 0.0f;
+    float xr = ninf;
     for (int r = 0; r < p.topk; ++r) {
         Key best = key[0];
         int at = 0;
-        float sv = s[0];
+        float xv = x[0];
 #pragma unroll
         for (int j = 1; j < EPL; ++j)
             if (key[j] > best) {
                 best = key[j];
                 at = j;
-                sv = s[j];
+                xv = x[j];
             }
         const int l = best_lane(best);
         const int e = l * EPL + (int)lane_value((uint32_t)at, l);
-        sv = lane_value(sv, l);
+        xv = lane_value(xv, l);
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
             if (e0 + j == e) key[j] = 0;
         if (lane == r) {
             mine = e;
-            w = sv;
+            xr = xv;
         }
     }
+    float w;
     if (p.renormalize) {
+        const float m = wave_max(xr);
+        w = p.score == 0 ? softmax_share(xr, top, m) : sigmoid_share(xr, m);
         const float sum = wave_sum(w);
         w = sum > 0.0f ? w / sum : 0.0f;
+    } else {
+        w = p.score == 0 ? softmax_share(xr, top, top) * inv : sigmoid_share(xr, 0.0f);
     }
     if (lane < p.topk) {
         p.idx[t * p.topk + lane] = mine;
