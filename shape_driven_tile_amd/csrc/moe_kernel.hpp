@@ -301,13 +301,22 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteParams p) {
     }
 }
 
+// 1 - sigmoid(x), not as a difference.
+__device__ __forceinline__ float sigmoid_complement(float x) {
+    const float e = expf(-fabsf(x));
+    return (x >= 0.0f ? e : 1.0f) / (1.0f + e);
+}
+
 // The gradient of the logits, one wave per token (lanes hold experts as above).
-// With p_j the chosen scores over their sum S (renormalised) or the scores: ds_j
-// = scale / S * (dw_j - sum_i dw_i p_i), or scale * dw_j; a sigmoid's dl = s (1 -
-// s) ds.  Softmax: dl = s (ds - sum ds s); renormalised, that sum is zero by
-// construction and s_j / S = p_j, so dl_j = scale p_j (dw_j - sum dw p) on the
-// chosen and exactly zero elsewhere.  16384 tokens, 8 of 128 experts (bf16): 9.8
-// us, bound by its instructions (memory alone would be 2).
+// With dw_j the weights' gradients of expert j (their mean u_j over its n_j slots
+// where it was chosen more than once) and p_j the chosen scores over their sum:
+//   renormalised: scale n_j p_j (u_j - sum_i n_i p_i u_i), for a sigmoid times 1 -
+//   s_j, and exactly zero on experts that were not chosen (softmax: s_j / S = p_j);
+//   softmax: scale s_j (dw_j - sum_i s_i dw_i); sigmoid: scale s_j (1 - s_j) dw_j.
+// The sums' weights add up to 1, so any constant may be taken from all dw: with the
+// one of the largest score nothing is left to cancel where that score is next to 1.
+// 16384 tokens, 8 of 128 experts (bf16): 9.8 us, bound by its instructions (memory
+// alone would be 2).
 template <typename T, int EPL>
 __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteParams p) {
     const int lane = threadIdx.x & 63;
@@ -321,7 +330,7 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteParams p) 
         e_r = p.idx[t * p.topk + lane];
         dw_r = p.dweights[t * p.topk + lane];
     }
-    float x[EPL], s[EPL], ds[EPL];
+    float x[EPL], ds[EPL];
     float top = ninf;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
@@ -330,25 +339,8 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteParams p) 
         top = fmaxf(top, x[j]);
         ds[j] = 0.0f;
     }
-    if (p.score == 0) {
-        top = wave_max(top);
-        float total = 0.0f;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            s[j] = x[j] == ninf ? 0.0f : x[j] == top ? 1.0f : expf(x[j] - top);
-            total += s[j];
-        }
-        total = wave_sum(total);
-        const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) s[j] *= inv;
-    } else {
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) s[j] = x[j] == ninf ? 0.0f : 1.0f / (1.0f + expf(-x[j]));
-    }
     // the weights' gradients to their experts' lanes (an expert named twice
-    // gets the sum, in slot order), and the chosen scores' sums
-    float S = 0.0f, inner = 0.0f;
+    // gets the sum, in slot order)
     float n[EPL];                          // times an expert was chosen
 #pragma unroll
     for (int j = 0; j < EPL; ++j) n[j] = 0.0f;
@@ -361,25 +353,60 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteParams p) 
             if (e == e0 + j) {
                 ds[j] += dw;
                 n[j] += 1.0f;
-                S += s[j];
-                inner += dw * s[j];
             }
     }
-    float out[EPL];
-    inner = wave_sum(inner);
+    if (p.score == 0) top = wave_max(top);
+    // the largest logit among those that the sums run over, and its gradient
+    const bool all = !p.renormalize;
+    float m = ninf;
     if (p.renormalize) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            if (n[j] > 1.0f) ds[j] /= n[j];
+            if (n[j] > 0.0f) m = fmaxf(m, x[j]);
+        }
+        m = wave_max(m);
+    } else {
+        m = top;
+    }
+    float pivot = 0.0f;
+    if (p.renormalize || p.score == 0) {
+        bool here = false;
+        float d = 0.0f;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            if ((all || n[j] > 0.0f) && x[j] == m && !here) {
+                here = true;
+                d = ds[j];
+            }
+        const uint64_t mask = __ballot(here);
+        if (mask != 0) pivot = lane_value(d, __builtin_ctzll(mask));
+    }
+    float out[EPL];
+    if (p.renormalize || p.score == 0) {
+        float S = 0.0f, inner = 0.0f;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            float q = p.score == 0 ? softmax_share(x[j], top, m) : sigmoid_share(x[j], m);
+            if (p.renormalize) q = n[j] > 0.0f ? n[j] * q : 0.0f;
+            ds[j] -= pivot;
+            S += q;
+            inner += q * ds[j];
+            out[j] = q;
+        }
         S = wave_sum(S);
+        inner = wave_sum(inner);
         const float inv = S > 0.0f ? 1.0f / S : 0.0f;
         const float mean = inner * inv;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            const float d = p.scale * (s[j] * inv) * (ds[j] - n[j] * mean);
-            out[j] = p.score == 0 ? d : d * (1.0f - s[j]);
+            out[j] = p.scale * (out[j] * inv) * (ds[j] - mean);
+            if (p.score != 0) out[j] *= sigmoid_complement(x[j]);
         }
     } else {
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-            out[j] = p.scale * (p.score == 0 ? s[j] * (ds[j] - inner) : s[j] * (1.0f - s[j]) * ds[j]);
+            out[j] = p.scale * (sigmoid_share(x[j], 0.0f) * sigmoid_complement(x[j])) * ds[j];
     }
 #pragma unroll
     for (int j = 0; j < EPL; ++j)

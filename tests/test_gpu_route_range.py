@@ -98,3 +98,76 @@ def test_route_masks_stay_masks(score):
         assert idx[1, 0] == 4 and idx[2, 0] == 7
         assert np.array_equal(w[1:], [[1, 0, 0, 0]] * 2)
         assert np.array_equal(w[0], [0.25] * 4 if score == "softmax" else [0.0] * 4)
+
+
+def mean_difference(p, ds):
+    """ds_j - sum_i p_i ds_i where the p add up to 1, as sum_i p_i (ds_j - ds_i): the
+    first form loses to cancellation what lies 2^-64 below ds where a p is next to 1."""
+    return (p[:, None, :] * (ds[:, :, None] - ds[:, None, :])).sum(axis=2)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_backward_far_scores(score, renormalize, dtype):
+    """Every gradient relative to its own score (and complement).  The differences of
+    the weights' gradients are taken from that of the row's largest score, so a
+    bound counts |dw_j - dw_top| and their mean, each off by the steps of a score."""
+    import torch
+    sdt = _sdt()
+    x = rows(dtype)
+    x64 = x.double().numpy()
+    T = x64.shape[0]
+    scale = 2.5
+    rng = np.random.default_rng(3)
+    cases = {"chosen": ref.route(x64, topk=TOPK, score=score)[0],
+             "others": np.argsort(x64, axis=1)[:, :TOPK].astype(np.int32)[:, ::-1].copy(),
+             "any": np.stack([rng.permutation(E)[:TOPK] for _ in range(T)]).astype(np.int32)}
+    for name, idx in cases.items():
+        dw = rng.standard_normal(idx.shape).astype(np.float32)
+        out = torch.full((T, E), float("nan"), dtype=_t(dtype), device=DEV)
+        say(f"route backward far scores {score} {renormalize} {dtype} {name}")
+        sdt.moe_route_backward(x.to(DEV), dev(idx), dev(dw), out,
+                               sdt.route_cfg(topk=TOPK, score=score, renormalize=renormalize,
+                                             scale=scale))
+        torch.cuda.synchronize()
+        got = out.double().cpu().numpy()
+        s, c = scores(x64, score)
+        at = np.arange(T)[:, None], idx
+        chosen = np.zeros((T, E), dtype=bool)
+        chosen[at] = True
+        ds = np.zeros((T, E), dtype=np.longdouble)
+        ds[at] = dw
+        # exponentials of differences as large as these (a softmax of less than 2^-160
+        # is left to the bound's last term)
+        reach = 2 * (far(x64, idx, score, renormalize) if renormalize or score == "sigmoid"
+                     else 160.0)
+        if renormalize:
+            p = np.where(chosen, s, 0)
+            p = p / p.sum(axis=1, keepdims=True)
+            pivot = np.take_along_axis(ds, p.argmax(axis=1)[:, None], axis=1)
+            off = np.where(chosen, np.abs(ds - pivot), 0)
+            want = scale * p * mean_difference(p, ds)
+            size = scale * p * (off + (p * off).sum(axis=1, keepdims=True))
+            if score == "sigmoid":
+                want, size = want * c, size * c
+            steps = reach + 2 * TOPK + 32
+            assert not np.any(got[~chosen]), "a gradient where nothing was chosen"
+        elif score == "sigmoid":
+            want = scale * ds * s * c
+            size = np.abs(want)
+            steps = reach + 32
+        else:
+            pivot = np.take_along_axis(ds, s.argmax(axis=1)[:, None], axis=1)
+            off = np.abs(ds - pivot)
+            want = scale * s * mean_difference(s, ds)
+            size = scale * s * (off + (s * off).sum(axis=1, keepdims=True))
+            steps = reach + 2 * E + 32
+        want, size = want.astype(np.float64), size.astype(np.float64)
+        # the smallest scores: fp32 holds them to 2^-149, which dw and the scale multiply
+        least = scale * np.abs(dw).max() * 8 * 2.0 ** -149
+        least = least + {"f32": 2.0 ** -150, "f16": 2.0 ** -25, "bf16": 2.0 ** -134}[dtype]
+        tol = steps * STEP * size
+        tol = tol + torch.finfo(_t(dtype)).eps / 2 * (np.abs(want) + tol) + least
+        bad = np.argwhere(np.abs(got - want) > tol)
+        assert bad.size == 0, (name, len(bad), bad[:4], got[tuple(bad[0])], want[tuple(bad[0])])
