@@ -121,29 +121,43 @@ __device__ __forceinline__ int best_lane(uint64_t k) {
     return __builtin_ctzll(__ballot(hi == tophi && (uint32_t)k == toplo));
 }
 
-// The score of a logit x over exp(m), from exponentials of differences, so that scores
-// far below 1 keep their ratios: m is 0 or the largest logit that it is compared
-// with (softmax: scores over exp(top) too, top the row's largest, without their sum;
-// sigmoid: where m < 0).  Zero where 64 bits hold no more of the score itself, a
-// softmax 745 below the row's largest and a sigmoid below -709: a logit of a type's
-// lowest value is a mask, whatever it is compared with.
-__device__ __forceinline__ float softmax_share(float x, float top, float m) {
-    if (x == -__builtin_inff() || x - top < -745.0f) return 0.0f;
-    return x == m ? 1.0f : expf(x - m);            // x == m: also an infinite one
+// Scores.  A softmax's numerator: the largest logit's is 1, also an infinite one's.
+__device__ __forceinline__ float softmax_numerator(float x, float top) {
+    return x == -__builtin_inff() ? 0.0f : x == top ? 1.0f : expf(x - top);
 }
-__device__ __forceinline__ float sigmoid_share(float x, float m) {
-    if (x < -709.0f) return 0.0f;
-    return expf(fminf(x, 0.0f) - fminf(m, 0.0f)) / (1.0f + expf(-fabsf(x)));
+// A sigmoid and 1 - it, from e = exp(-|x|) in [0, 1], so that neither overflows or is
+// a difference (the reciprocal, of a number in [1, 2], is a step off at most).
+struct Sigmoid {
+    float s, c;
+};
+__device__ __forceinline__ Sigmoid sigmoid(float x) {
+    const float e = expf(-fabsf(x));
+    const float r = __builtin_amdgcn_rcpf(1.0f + e);
+    return x >= 0.0f ? Sigmoid{r, e * r} : Sigmoid{e * r, r};
+}
+// A score for a sum that it is divided by: over a common factor, exp(m - top) / sum
+// for a softmax and exp(m) for sigmoids of an m < 0, with m the largest logit in the
+// sum (top: of the row), so that scores far below 1 keep their ratios.  Zero where 64
+// bits hold no more of the score itself, a softmax 745 below the row's largest and
+// a sigmoid below -709: a logit of a type's lowest value is a mask, whatever it is
+// compared with.
+__device__ __forceinline__ float softmax_share(float x, float top, float m) {
+    return x - top < -745.0f ? 0.0f : softmax_numerator(x, m);
+}
+__device__ __forceinline__ float sigmoid_share(float x, float m, const Sigmoid& g) {
+    if (!(m < 0.0f)) return g.s;
+    return x < -709.0f ? 0.0f : expf(x - m) * g.c;   // 1 / (1 + exp(x)) = 1 - sigmoid(x)
 }
 
 // One wave per token; lane l holds experts l EPL .. + EPL - 1, so the lowest
-// lane among equals has the lowest expert.  The weights are formed from the
-// chosen logits, a lane each; the choice is topk rounds of a wave-wide maximum, six
-// steps of lane-crossing operands (DPP) on 32-bit keys.  Keys come from the
+// lane among equals has the lowest expert.  Renormalised weights are formed from
+// the chosen logits, a lane each; the choice is topk rounds of a wave-wide maximum,
+// six steps of lane-crossing operands (DPP) on 32-bit keys.  Keys come from the
 // logits in fp32 or (WIDE), with a bias or worths summed over two, from scores in
 // 64 bits, so that two experts tie only where their definitions do.  Bound by
 // the rounds' instructions: 16384 tokens, 8 of 128 experts (bf16): 35 us with
-// lane exchanges through LDS on 64-bit keys, 11.5 us so.
+// lane exchanges through LDS on 64-bit keys, 9.8 us so (a score for every expert
+// instead of the chosen: 10.4).
 template <typename T, int EPL, bool WIDE>
 __global__ __launch_bounds__(256) void moe_route_kernel(RouteParams p) {
     typedef std::conditional_t<WIDE, uint64_t, uint32_t> Key;
@@ -162,18 +176,25 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteParams p) {
         if (x[j] != x[j]) x[j] = ninf;
         top = fmaxf(top, x[j]);
     }
-    // softmax: the row's largest logit and, where a weight is a score itself, the sum
-    // of the numerators (the largest logit's is 1, also an infinite one's)
-    float inv = 1.0f;
+    // what the chosen take to their weights: the score, or the logit where the scores
+    // are renormalised
+    float v[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) v[j] = x[j];
     double sd[WIDE ? EPL : 1];
     if (p.score == 0) {
         top = wave_max(top);
         if (!p.renormalize) {
             float total = 0.0f;
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) total += softmax_share(x[j], top, top);
+            for (int j = 0; j < EPL; ++j) {
+                v[j] = softmax_numerator(x[j], top);
+                total += v[j];
+            }
             total = wave_sum(total);
-            inv = total > 0.0f ? 1.0f / total : 0.0f;
+            const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) v[j] *= inv;
         }
         if constexpr (WIDE) {
             double totald = 0.0;
@@ -186,9 +207,14 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteParams p) {
 #pragma unroll
             for (int j = 0; j < EPL; ++j) sd[j] = totald > 0.0 ? sd[j] / totald : 0.0;
         }
-    } else if constexpr (WIDE) {
+    } else {
+        if (!p.renormalize)
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) sd[j] = x[j] == ninf ? 0.0 : 1.0 / (1.0 + exp(-(double)x[j]));
+            for (int j = 0; j < EPL; ++j) v[j] = sigmoid(x[j]).s;
+        if constexpr (WIDE)
+#pragma unroll
+            for (int j = 0; j < EPL; ++j)
+                sd[j] = x[j] == ninf ? 0.0 : 1.0 / (1.0 + exp(-(double)x[j]));
     }
     Key key[EPL];
 #pragma unroll
@@ -261,39 +287,37 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteParams p) {
             }
         }
     }
-    // topk rounds over the lanes' best; lane r keeps the r-th choice and its logit
+    // topk rounds over the lanes' best; lane r keeps the r-th choice
     int mine = 0;
-    float xr = ninf;
+    float w = ninf;
     for (int r = 0; r < p.topk; ++r) {
         Key best = key[0];
         int at = 0;
-        float xv = x[0];
+        float chosen = v[0];
 #pragma unroll
         for (int j = 1; j < EPL; ++j)
             if (key[j] > best) {
                 best = key[j];
                 at = j;
-                xv = x[j];
+                chosen = v[j];
             }
         const int l = best_lane(best);
         const int e = l * EPL + (int)lane_value((uint32_t)at, l);
-        xv = lane_value(xv, l);
+        chosen = lane_value(chosen, l);
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
             if (e0 + j == e) key[j] = 0;
         if (lane == r) {
             mine = e;
-            xr = xv;
+            w = chosen;
         }
     }
-    float w;
     if (p.renormalize) {
-        const float m = wave_max(xr);
-        w = p.score == 0 ? softmax_share(xr, top, m) : sigmoid_share(xr, m);
-        const float sum = wave_sum(w);
+        // without a bias the first choice has the largest logit
+        const float m = p.bias == nullptr ? lane_value(w, 0) : wave_max(w);
+        w = p.score == 0 ? softmax_share(w, top, m) : sigmoid_share(w, m, sigmoid(w));
+        const float sum = wave_sum(w);           // lanes past topk: of -infinity, 0
         w = sum > 0.0f ? w / sum : 0.0f;
-    } else {
-        w = p.score == 0 ? softmax_share(xr, top, top) * inv : sigmoid_share(xr, 0.0f);
     }
     if (lane < p.topk) {
         p.idx[t * p.topk + lane] = mine;
@@ -301,22 +325,22 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteParams p) {
     }
 }
 
-// 1 - sigmoid(x), not as a difference.
-__device__ __forceinline__ float sigmoid_complement(float x) {
-    const float e = expf(-fabsf(x));
-    return (x >= 0.0f ? e : 1.0f) / (1.0f + e);
-}
-
-// The gradient of the logits, one wave per token (lanes hold experts as above).
-// With dw_j the weights' gradients of expert j (their mean u_j over its n_j slots
-// where it was chosen more than once) and p_j the chosen scores over their sum:
-//   renormalised: scale n_j p_j (u_j - sum_i n_i p_i u_i), for a sigmoid times 1 -
-//   s_j, and exactly zero on experts that were not chosen (softmax: s_j / S = p_j);
-//   softmax: scale s_j (dw_j - sum_i s_i dw_i); sigmoid: scale s_j (1 - s_j) dw_j.
+// The gradient of the logits, one wave per token.  With p_r the chosen scores over
+// their sum and dw_r their weights' gradients:
+//   renormalised: the logit of slot r gets scale p_r (dw_r - sum_i p_i dw_i), for a
+//   sigmoid times 1 - s_r (softmax: s_r / sum = p_r), other logits exactly zero;
+//   sigmoid: scale s_r (1 - s_r) dw_r, others zero;
+//   softmax: every logit gets scale s_j (dw_j - sum_i s_i dw_i), dw_j = 0 where not
+//   chosen, the sum of its slots' where chosen more than once.
 // The sums' weights add up to 1, so any constant may be taken from all dw: with the
 // one of the largest score nothing is left to cancel where that score is next to 1.
-// 16384 tokens, 8 of 128 experts (bf16): 9.8 us, bound by its instructions (memory
-// alone would be 2).
+// The first two are worked out a slot a lane and then go to the lanes that hold the
+// experts' outputs (EPL each, in order), in slot order.
+// 16384 tokens, 8 of 128 experts (bf16): 8.2 us, bound by its instructions (memory
+// alone would be 2).  A softmax needs the row's largest logit, so the row is there,
+// and up to four logits a lane a slot's comes from its lane (65536 tokens, 2 of 200:
+// 26.3 us, from memory 28.1); a sigmoid reads the slots' alone (16384, 8 of 256: 9.9
+// us, the rows 10.6).
 template <typename T, int EPL>
 __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteParams p) {
     const int lane = threadIdx.x & 63;
@@ -324,89 +348,97 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteParams p) 
     if (t >= p.T) return;
     const float ninf = -__builtin_inff();
     const int e0 = lane * EPL;
-    int e_r = -1;
-    float dw_r = 0.0f;
+    int er = -1;                               // this lane's slot
+    float dw = 0.0f, xr = ninf;
     if (lane < p.topk) {
-        e_r = p.idx[t * p.topk + lane];
-        dw_r = p.dweights[t * p.topk + lane];
-    }
-    float x[EPL], ds[EPL];
-    float top = ninf;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        x[j] = e0 + j < p.E ? route_load<T>(p.logits, t * p.ld + e0 + j) : ninf;
-        if (x[j] != x[j]) x[j] = ninf;
-        top = fmaxf(top, x[j]);
-        ds[j] = 0.0f;
-    }
-    // the weights' gradients to their experts' lanes (an expert named twice
-    // gets the sum, in slot order)
-    float n[EPL];                          // times an expert was chosen
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) n[j] = 0.0f;
-    for (int r = 0; r < p.topk; ++r) {
-        const int e = (int)lane_value((uint32_t)e_r, r);
-        const float dw = lane_value(dw_r, r);
-        if (e < 0 || e >= p.E) continue;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if (e == e0 + j) {
-                ds[j] += dw;
-                n[j] += 1.0f;
-            }
-    }
-    if (p.score == 0) top = wave_max(top);
-    // the largest logit among those that the sums run over, and its gradient
-    const bool all = !p.renormalize;
-    float m = ninf;
-    if (p.renormalize) {
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            if (n[j] > 1.0f) ds[j] /= n[j];
-            if (n[j] > 0.0f) m = fmaxf(m, x[j]);
-        }
-        m = wave_max(m);
-    } else {
-        m = top;
-    }
-    float pivot = 0.0f;
-    if (p.renormalize || p.score == 0) {
-        bool here = false;
-        float d = 0.0f;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if ((all || n[j] > 0.0f) && x[j] == m && !here) {
-                here = true;
-                d = ds[j];
-            }
-        const uint64_t mask = __ballot(here);
-        if (mask != 0) pivot = lane_value(d, __builtin_ctzll(mask));
+        er = p.idx[t * p.topk + lane];
+        dw = p.dweights[t * p.topk + lane];
+        if (er < 0 || er >= p.E) er = -1;
     }
     float out[EPL];
-    if (p.renormalize || p.score == 0) {
-        float S = 0.0f, inner = 0.0f;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            float q = p.score == 0 ? softmax_share(x[j], top, m) : sigmoid_share(x[j], m);
-            if (p.renormalize) q = n[j] > 0.0f ? n[j] * q : 0.0f;
-            ds[j] -= pivot;
-            S += q;
-            inner += q * ds[j];
-            out[j] = q;
+    for (int j = 0; j < EPL; ++j) out[j] = 0.0f;
+    // v of every slot to its expert
+    auto scatter = [&](float v) {
+        for (int r = 0; r < p.topk; ++r) {
+            const int e = (int)lane_value((uint32_t)er, r);
+            const float vr = lane_value(v, r);
+#pragma unroll
+            for (int j = 0; j < EPL; ++j)
+                if (e == e0 + j) out[j] += vr;
         }
-        S = wave_sum(S);
-        inner = wave_sum(inner);
+    };
+    // the slots' gradients from their scores q over the largest, which has the logit m
+    auto renormalized = [&](float q, float m, float factor) {
+        const uint64_t largest = __ballot(er >= 0 && xr == m);
+        const float d = dw - (largest ? lane_value(dw, __builtin_ctzll(largest)) : 0.0f);
+        if (er < 0) q = 0.0f;
+        const float S = wave_sum(q);
+        const float inner = wave_sum(er >= 0 ? q * d : 0.0f);
         const float inv = S > 0.0f ? 1.0f / S : 0.0f;
-        const float mean = inner * inv;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            out[j] = p.scale * (out[j] * inv) * (ds[j] - mean);
-            if (p.score != 0) out[j] *= sigmoid_complement(x[j]);
+        scatter(p.scale * factor * (q * inv) * (d - inner * inv));
+    };
+    auto slot_from_memory = [&]() {
+        if (er >= 0) xr = route_load<T>(p.logits, t * p.ld + er);
+        if (xr != xr) xr = ninf;
+    };
+    if (p.score != 0) {
+        slot_from_memory();
+        const Sigmoid g = sigmoid(xr);
+        if (p.renormalize) {
+            const float m = wave_max(xr);
+            renormalized(sigmoid_share(xr, m, g), m, g.c);
+        } else {
+            scatter(p.scale * (g.s * g.c) * dw);
         }
     } else {
+        float x[EPL];
+        float top = ninf;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            out[j] = p.scale * (sigmoid_share(x[j], 0.0f) * sigmoid_complement(x[j])) * ds[j];
+        for (int j = 0; j < EPL; ++j) {
+            x[j] = e0 + j < p.E ? route_load<T>(p.logits, t * p.ld + e0 + j) : ninf;
+            if (x[j] != x[j]) x[j] = ninf;
+            top = fmaxf(top, x[j]);
+        }
+        top = wave_max(top);
+        if (p.renormalize) {
+            if constexpr (EPL <= 4) {          // the logit is in the lane of its expert
+#pragma unroll
+                for (int j = 0; j < EPL; ++j) {
+                    const float got = __shfl(x[j], er < 0 ? 0 : er / EPL);
+                    if (er >= 0 && er % EPL == j) xr = got;
+                }
+            } else {
+                slot_from_memory();
+            }
+            const float m = wave_max(xr);
+            renormalized(softmax_share(xr, top, m), m, 1.0f);
+        } else {
+            scatter(dw);
+            bool largest = false;
+            float pivot = 0.0f;
+#pragma unroll
+            for (int j = EPL - 1; j >= 0; --j)
+                if (x[j] == top) {
+                    largest = true;
+                    pivot = out[j];
+                }
+            pivot = lane_value(pivot, __builtin_ctzll(__ballot(largest)));
+            float S = 0.0f, inner = 0.0f;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) {
+                x[j] = softmax_numerator(x[j], top);
+                out[j] -= pivot;
+                S += x[j];
+                inner += x[j] * out[j];
+            }
+            S = wave_sum(S);
+            inner = wave_sum(inner);
+            const float inv = S > 0.0f ? 1.0f / S : 0.0f;
+            const float mean = inner * inv;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) out[j] = p.scale * (x[j] * inv) * (out[j] - mean);
+        }
     }
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
