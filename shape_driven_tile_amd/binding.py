@@ -367,11 +367,15 @@ def check_gemv_kn_args(N, K, x_ptr, B_ptr, ldb, y_ptr) -> int:
 
 def _stream_handle(stream):
     """The HIP stream of `stream`, or the current one of the current device (asked
-    for its handle: a torch.cuda.Stream object would cost 2.8 us a call)."""
+    for its handle where torch has the calls: a torch.cuda.Stream object would cost
+    2.8 us a call)."""
     if stream is not None:
         return stream.cuda_stream
     import torch
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    try:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
 
 
 def _rows(t, name, dtype=None):

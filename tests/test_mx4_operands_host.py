@@ -207,3 +207,17 @@ def test_layer_and_plan_are_of_the_same_experts(library):
     assert not library.calls
     call(sdt.SdtMoeLayer(N, K, experts, experts, experts))
     assert library.calls.pop() == "moe_experts_mx4_bf16"
+
+
+@pytest.mark.parametrize("missing", ["_cuda_getCurrentRawStream", "_cuda_getDevice"])
+def test_stream_handle_without_torchs_own_call(monkeypatch, missing):
+    """torch's unnamed call for the current stream's handle may go: the public one
+    then serves."""
+    import types
+
+    import torch
+    monkeypatch.delattr(torch._C, missing)
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda *a: types.SimpleNamespace(cuda_stream=77))
+    assert sdt._stream_handle(None) == 77
+    assert sdt._stream_handle(types.SimpleNamespace(cuda_stream=5)) == 5
