@@ -1102,9 +1102,8 @@ def moe_experts_mx4(layer: SdtMoeLayer, X, idx, weights, plan: MoePlan, Y, works
     entry = {torch.float16: "moe_experts_mx4_f16", torch.bfloat16: "moe_experts_mx4_bf16"}.get(X.dtype)
     if entry is None:
         raise TypeError(f"X must be float16 or bfloat16, got {X.dtype}")
-    shape = (plan.tokens, layer.K)
-    if tuple(X.shape) != shape or tuple(Y.shape) != shape or \
-            tuple(idx.shape) != (plan.tokens, plan.topk) or tuple(weights.shape) != tuple(idx.shape):
+    shape, chosen = (plan.tokens, layer.K), (plan.tokens, plan.topk)
+    if X.shape != shape or Y.shape != shape or idx.shape != chosen or weights.shape != chosen:
         raise ValueError(f"shape mismatch X{tuple(X.shape)} Y{tuple(Y.shape)} idx{tuple(idx.shape)} "
                          f"weights{tuple(weights.shape)}")
     if layer.experts is not None and layer.experts != plan.experts:
@@ -1113,10 +1112,11 @@ def moe_experts_mx4(layer: SdtMoeLayer, X, idx, weights, plan: MoePlan, Y, works
     py, ldy = _rows(Y, "Y", X.dtype)
     if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise TypeError("workspace must be contiguous uint8")
-    devices = (X.get_device(), idx.get_device(), weights.get_device(), plan.device,
-               Y.get_device(), workspace.get_device())
-    if devices.count(devices[0]) != 6 or layer.device not in (None, devices[0]):
-        raise _apart(entry, *devices, layer.device)
+    where = X.get_device()
+    if not (idx.get_device() == weights.get_device() == plan.device == Y.get_device() ==
+            workspace.get_device() == where) or layer.device not in (None, where):
+        raise _apart(entry, where, idx.get_device(), weights.get_device(), plan.device,
+                     Y.get_device(), workspace.get_device(), layer.device)
     _check(getattr(lib(), entry)(ctypes.byref(layer), _ints(idx, "idx"),
                                  _floats(weights, "weights"), ctypes.byref(plan._struct), px, ldx,
                                  py, ldy, workspace.data_ptr(), workspace.numel(),

@@ -44,7 +44,8 @@ class Mx4Experts:
         handle = sdt._stream_handle(None)
         if self._holds != (tokens, topk, handle):
             self._hold(tokens, topk, handle)
-        if not self._captured and torch.cuda.is_current_stream_capturing():
+        # (the default stream, 0, cannot be captured)
+        if handle != 0 and not self._captured and torch.cuda.is_current_stream_capturing():
             self._captured = True
         return self._workspace
 
@@ -70,17 +71,13 @@ class Mx4Experts:
         rows a multiple of 8 elements apart; `stream`: instead of the current
         one, ordered with it by the caller."""
         import torch
-        if stream is None or stream.cuda_stream == sdt._stream_handle(None):
-            return self._run(x, idx, weights, plan, out)
-        current = torch.cuda.current_stream()
-        with torch.cuda.stream(stream):
-            y = self._run(x, idx, weights, plan, out)
-        if out is None:
-            y.record_stream(current)             # where the caller goes on with it
-        return y
-
-    def _run(self, x, idx, weights, plan, out):
-        import torch
+        if stream is not None and stream.cuda_stream != sdt._stream_handle(None):
+            current = torch.cuda.current_stream()
+            with torch.cuda.stream(stream):
+                y = self(x, idx, weights, plan, out)
+            if out is None:
+                y.record_stream(current)         # where the caller goes on with it
+            return y
         T, topk = idx.shape
         if plan is None:
             plan = sdt.MoePlan.empty(T, topk, self.experts, device=x.device)
