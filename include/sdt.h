@@ -361,7 +361,8 @@ int gemm_mx4_bf16(int64_t M, int64_t N, int64_t K,
 
 /* y(n) = sum_k x(k) * B(n, k): the M = 1 product of K 16-bit activations (type
  * of the name, any alignment of it) with an MX4 weight matrix; fp32
- * accumulation, y in the type of the name.  N == 0 is a no-op, K == 0 writes
+ * accumulation (32 products x * code, below 192 max |x|, before their block's scale
+ * multiplies them), y in the type of the name.  N == 0 is a no-op, K == 0 writes
  * zeros.  Deterministic. */
 int gemv_mx4_m1_f16(int64_t N, int64_t K, const void* x,
                     const void* B, int64_t ldb, const void* SB, void* y, void* stream);

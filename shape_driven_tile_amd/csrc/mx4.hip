@@ -133,7 +133,8 @@ int launch_tile(Mx4Gemm p, int64_t row_tiles, int num_cu, void* stream) {
 
 // Waves that split the k-tiles: two where the workgroups outnumber the CUs (two of
 // them share one: 64 tokens of 32 experts, 50 -> 45 and 35 -> 28 us against four),
-// four where not (64 x 4096 x 4096, 64 workgroups: 7.5 us against 9.0 with two).
+// four where not (64 x 4096 x 4096, 64 workgroups: 7.5 us against 9.0 with two).  64
+// columns a workgroup at any N: 12288 gives 192 workgroups and leaves 64 CUs idle.
 template <typename Elt, bool GROUPED, bool GATED, bool QOUT = false>
 int launch_skinny(Mx4Gemm p, int64_t groups, int num_cu, void* stream) {
     p.gm = (int)groups;
@@ -352,7 +353,9 @@ int64_t rows_per_expert(const sdt_moe_plan* plan) {
 // Up to these the weights are streamed, up to 64 they meet 64 x 128 tiles, above
 // 128 x 128 (layers of 16 experts, 2048 x 1024, us: 8 rows 32.9 streamed and 34.4
 // in 64 x 128 tiles, 16 rows 37.2 and 35.0; 64 rows 39.8 and in 128 x 128 40.8, 128
-// rows 49.0 and 45.2).
+// rows 49.0 and 45.2).  The host does not know the choice: where the tokens reach few
+// of many experts this streams weights that tiles would share (256 experts, 256
+// tokens of 8: all on eight experts 148 us and 40 in tiles, spread evenly 176 and 191).
 constexpr int64_t kSkinnyRows = 12;
 
 template <typename Elt, int BM, int BN, int NS>

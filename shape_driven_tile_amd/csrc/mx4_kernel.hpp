@@ -938,8 +938,9 @@ __device__ __forceinline__ void mx4_store_quantized(const Mx4Gemm& p, const floa
 // Bound by the loads into LDS (53 bytes a clock and CU from rows on 128-byte lines,
 // 650 of a 128 x 128 k-tile's 1050 clocks; 30 from others) and, on short k-loops,
 // by the epilogue.  1024 x 8192 x 8192: 40 us (3.4 PFLOP/s); 4096 tokens of 64
-// experts, 2048 -> 1024: gated 114-118 us, down 66 (1.8 and 1.6 PFLOP/s).  With loader
-// waves and one workgroup a CU those took 167 and 106.
+// experts, 2048 -> 1024: gated 114-118 us, down 66 (1.8 and 1.6 PFLOP/s), of which the
+// epilogues and the stores are 20 and 18 (left out, for timing alone: 94 and 49).
+// With loader waves and one workgroup a CU those took 167 and 106.
 template <typename Elt, int BM, int BN, int WM, int WN, int NS, bool GROUPED, bool GATED,
           bool QOUT = false>
 __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
@@ -1299,7 +1300,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
             clear();
         }
         // the next k-tile has landed: at most the NS - 1 after it are on their way
-        // (stores, younger, only make the wait longer)
+        // (after a tile's stores, which are younger and counted too, the wait is also
+        // for loads of those)
         wait_global_loads<(NS - 1) * L>();
         barrier();
     }

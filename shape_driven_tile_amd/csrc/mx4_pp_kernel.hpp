@@ -12,7 +12,8 @@
 // 8192^3: 228-250 us (4.4-4.8 PFLOP/s), MFMAs busy 58% of the clocks; bound by the
 // power limit (a register-only loop of these MFMAs on random codes: 6.15-7.15
 // PFLOP/s) and by the stage loads (197 us with them left out).  128 x 128 tiles,
-// two workgroups a CU, take 301 us there.
+// two workgroups a CU, take 301 us there.  The accumulators and fragments fill the
+// 256 registers; four more spill to 16 bytes of scratch a lane.
 #pragma once
 
 #include "mx4_kernel.hpp"
