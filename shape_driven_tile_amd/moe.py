@@ -2,9 +2,9 @@
 
     python -m shape_driven_tile_amd.moe [--tokens T]
 
-quantises random weights, routes random tokens and runs the layer once through
-the library's operators (route, plan, quantise, the experts' products, combine),
-printing its time.
+quantises random weights, routes random tokens (by a 16-bit product: ranking experts
+is where a 4-bit one's error shows first) and runs the layer through the library's
+operators (route, plan, quantise, the experts' products, combine), printing its time.
 """
 from __future__ import annotations
 
@@ -115,24 +115,23 @@ def main(argv=None) -> None:
             sdt.mx4_quantize_bf16(w.bfloat16(), sdt.Mx4(m.q[e], m.s[e], rows, K))
         return m
 
+    def rows(n, width):                          # from multiples of 8 elements, as products take them
+        return torch.empty(n, -(-width // 8) * 8, dtype=torch.bfloat16, device=dev)[:, :width]
+
     layer = Mx4Experts(matrices(a.inter, a.hidden), matrices(a.inter, a.hidden),
                        matrices(a.hidden, a.inter))
-    x = torch.randn(a.tokens, a.hidden, device=dev, generator=g).bfloat16()
-    router = sdt.Mx4.empty(a.experts, a.hidden, device=dev)
-    sdt.mx4_quantize_bf16(torch.randn(a.experts, a.hidden, device=dev, generator=g).bfloat16(),
-                          router)
-    xq = sdt.Mx4.empty(a.tokens, a.hidden, device=dev)
-    logits = torch.empty(a.tokens, -(-a.experts // 8) * 8, dtype=torch.bfloat16,
-                         device=dev)[:, :a.experts]
+    x, router = rows(a.tokens, a.hidden), rows(a.experts, a.hidden)
+    x.copy_(torch.randn(x.shape, device=dev, generator=g))
+    router.copy_(torch.randn(router.shape, device=dev, generator=g) * a.hidden ** -0.5)
+    logits = rows(a.tokens, a.experts)
     cfg = sdt.route_cfg(topk=a.topk)
     idx = torch.empty(a.tokens, a.topk, dtype=torch.int32, device=dev)
     weights = torch.empty(a.tokens, a.topk, device=dev)
     plan = sdt.MoePlan.empty(a.tokens, a.topk, a.experts, device=dev)
-    y = torch.empty(a.tokens, -(-a.hidden // 8) * 8, dtype=torch.bfloat16, device=dev)[:, :a.hidden]
+    y = rows(a.tokens, a.hidden)
 
     def step():
-        sdt.mx4_quantize_bf16(x, xq)
-        sdt.gemm_mx4_bf16(xq, router, logits)
+        sdt.gemm_bf16(x, router, logits)
         sdt.moe_route(logits, idx, weights, cfg)
         layer(x, idx, weights, plan=plan, out=y)
 
