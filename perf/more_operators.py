@@ -229,10 +229,10 @@ def _like(t):
     return torch.empty(rows, -(-K // 8) * 8, dtype=t.dtype, device=t.device)[:, :K]
 
 
-def _work_buffer(s, need):
+def _work_buffer(s, size):
     """A work buffer, kept with the state as a program keeps it with its layer."""
     if "buffer" not in s:
-        s["buffer"] = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+        s["buffer"] = torch.empty(max(size(), 16), dtype=torch.uint8, device=DEV)
     return s["buffer"]
 
 
@@ -252,7 +252,7 @@ def _run_own(s):
         sdt.rms_norm(x, s["weight"], y=y, residual=s["residual"], total=total, rstd=rstd, eps=EPS)
         dx, dweight = _like(x), torch.empty(K, device=x.device)
         sdt.rms_norm_backward(total, s["weight"], rstd, s["dy"], dx, dweight,
-                              _work_buffer(s, sdt.rms_norm_workspace_size(rows, K)),
+                              _work_buffer(s, lambda: sdt.rms_norm_workspace_size(rows, K)),
                               dtotal=s["dtotal"])
         return total, y, dx, dweight
     if op == "linear":
@@ -280,15 +280,19 @@ def _run_own(s):
         sdt.gated_ff(x, gate, up, h, act=s["act"], g=g, u=u)
         dx, dgate, dup = _like(x), _like(gate), _like(up)
         sdt.gated_ff_backward(x, gate, up, g, u, s["dh"], dx, dgate, dup,
-                              _work_buffer(s, sdt.gated_ff_workspace_size(M, N, K)), act=s["act"])
+                              _work_buffer(s, lambda: sdt.gated_ff_workspace_size(M, N, K)),
+                              act=s["act"])
         return h, dx, dgate, dup
     da, db = _like(s["a"]), _like(s["b"])
+    M, N, K = s["M"], s["N"], s["K"]
+    buffer = _work_buffer(s, lambda: max(sdt.gemm_turned_workspace_size(M, K, N),
+                                         sdt.gemm_turned_workspace_size(N, K, M)))
     if f16:
-        sdt.gemm_f16_nn(s["dc"], s["b"], da)
-        sdt.gemm_f16_tn(s["dc"], s["a"], db)
+        sdt.gemm_f16_nn(s["dc"], s["b"], da, buffer)
+        sdt.gemm_f16_tn(s["dc"], s["a"], db, buffer)
     else:
-        sdt.gemm_bf16_nn(s["dc"], s["b"], da)
-        sdt.gemm_bf16_tn(s["dc"], s["a"], db)
+        sdt.gemm_bf16_nn(s["dc"], s["b"], da, buffer)
+        sdt.gemm_bf16_tn(s["dc"], s["a"], db, buffer)
     return da, db
 
 
