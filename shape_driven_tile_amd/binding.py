@@ -42,10 +42,19 @@ EXPORTS = (
     "sdt_moe_plan_rows", "moe_plan", "moe_gemm_mx4_f16", "moe_gemm_mx4_bf16",
     "moe_combine_f16", "moe_combine_bf16",
     "sdt_moe_experts_workspace_size", "moe_experts_mx4_f16", "moe_experts_mx4_bf16",
+    "fp8_quantize_f16", "fp8_quantize_bf16",
+    "fp8_dequantize_f16", "fp8_dequantize_bf16", "fp8_dequantize_f32",
+    "gemm_fp8_f16", "gemm_fp8_bf16",
+    "rms_norm_f16", "rms_norm_bf16", "rms_norm_backward_f16", "rms_norm_backward_bf16",
+    "sdt_rms_norm_workspace_size",
+    "gated_ff_f16", "gated_ff_bf16", "gated_ff_backward_f16", "gated_ff_backward_bf16",
+    "sdt_gated_ff_workspace_size",
+    "gemm_f16_nn", "gemm_bf16_nn", "gemm_f16_tn", "gemm_bf16_tn",
+    "sdt_gemm_turned_workspace_size",
 )
 
 # The include/sdt.h version these structures and signatures follow.
-ABI_VERSION = 6
+ABI_VERSION = 7
 
 
 class SdtTile(ctypes.Structure):
@@ -107,6 +116,34 @@ class SdtMoeLayer(ctypes.Structure):
                 raise TypeError(f"the layer's matrices do not agree: {what} {sorted(known)}")
             if known:
                 setattr(self, what, known.pop())
+
+
+def _fields(text):
+    """ctypes fields from "name type" words: p a pointer, i an int64, n an int, f a float."""
+    kinds = {"p": ctypes.c_void_p, "i": ctypes.c_int64, "n": ctypes.c_int, "f": ctypes.c_float}
+    words = text.split()
+    return [(name, kinds[kind]) for name, kind in zip(words[::2], words[1::2])]
+
+
+class SdtNorm(ctypes.Structure):
+    _fields_ = _fields("rows i K i x p ldx i residual p ldr i weight p eps f total p ldt i y p ldy i "
+                       "q p ldq i s p lds i rstd p")
+
+
+class SdtNormGrad(ctypes.Structure):
+    _fields_ = _fields("rows i K i total p ldt i weight p rstd p dy p lddy i dtotal p lddt i "
+                       "dx p lddx i dweight p workspace p workspace_bytes i")
+
+
+class SdtGatedFf(ctypes.Structure):
+    _fields_ = _fields("M i N i K i x p ldx i gate p ldgate i up p ldup i act n h p ldh i "
+                       "g p ldg i u p ldu i wide n")
+
+
+class SdtGatedFfGrad(ctypes.Structure):
+    _fields_ = _fields("M i N i K i x p ldx i gate p ldgate i up p ldup i act n g p ldg i u p ldu i "
+                       "wide n dh p lddh i dx p lddx i dgate p lddgate i dup p lddup i "
+                       "workspace p workspace_bytes i")
 
 
 class SdtError(RuntimeError):
@@ -196,6 +233,7 @@ def lib():
                  "sdt_mfma_ceiling"):
         getattr(L, name).restype = _int
     _declare_mx4(L)
+    _declare_ffn(L)
     if L.sdt_abi_version() != ABI_VERSION:
         raise RuntimeError(f"{LIB_PATH} has ABI version {L.sdt_abi_version()}, this binding "
                            f"expects {ABI_VERSION}: rebuild the library")
@@ -229,11 +267,33 @@ def _declare_mx4(L):
         getattr(L, f"moe_route_{t}").argtypes = [_i64, _i64, _vp, _i64, _vp, route, _vp, _vp, _vp]
         getattr(L, f"moe_route_backward_{t}").argtypes = [_i64, _i64, _vp, _i64, route, _vp, _vp,
                                                           _vp, _i64, _vp]
-    for name in EXPORTS[EXPORTS.index("sdt_mx4_row_bytes"):]:
+    for name in EXPORTS[EXPORTS.index("sdt_mx4_row_bytes"):EXPORTS.index("fp8_quantize_f16")]:
         getattr(L, name).restype = _int
     for name in ("sdt_mx4_row_bytes", "sdt_mx4_scale_bytes", "sdt_moe_plan_rows",
                  "sdt_moe_experts_workspace_size"):
         getattr(L, name).restype = _i64
+
+
+def _declare_ffn(L):
+    for t in ("f16", "bf16"):
+        getattr(L, f"fp8_quantize_{t}").argtypes = [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int,
+                                                    _vp]
+        getattr(L, f"gemm_fp8_{t}").argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                                _i64, _vp, _i64, _vp]
+        for layout in ("nn", "tn"):
+            getattr(L, f"gemm_{t}_{layout}").argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp,
+                                                         _i64, _vp, _i64, _vp]
+        for entry, args in (("rms_norm", SdtNorm), ("rms_norm_backward", SdtNormGrad),
+                            ("gated_ff", SdtGatedFf), ("gated_ff_backward", SdtGatedFfGrad)):
+            getattr(L, f"{entry}_{t}").argtypes = [ctypes.POINTER(args), _vp]
+    for t in ("f32", "f16", "bf16"):
+        getattr(L, f"fp8_dequantize_{t}").argtypes = [_i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64,
+                                                      _vp]
+    L.sdt_rms_norm_workspace_size.argtypes = [_i64, _i64]
+    L.sdt_gated_ff_workspace_size.argtypes = [_i64, _i64, _i64]
+    L.sdt_gemm_turned_workspace_size.argtypes = [_i64, _i64, _i64]
+    for name in EXPORTS[EXPORTS.index("fp8_quantize_f16"):]:
+        getattr(L, name).restype = _i64 if name.startswith("sdt_") else _int
 
 
 # ---- host-only helpers ------------------------------------------------------
@@ -1121,3 +1181,355 @@ def moe_experts_mx4(layer: SdtMoeLayer, X, idx, weights, plan: MoePlan, Y, works
                                  _floats(weights, "weights"), ctypes.byref(plan._struct), px, ldx,
                                  py, ldy, workspace.data_ptr(), workspace.numel(),
                                  _stream_handle(stream)), entry)
+
+
+# ---- 8-bit matrices with a scale for each block of 128 ------------------------------
+
+class Fp8:
+    """An 8-bit matrix on the device (the format: include/sdt.h): float8_e4m3fn codes
+    `q` [rows, K], rows a multiple of 16 bytes apart, and float32 scales `s`: of each
+    row and block of 128 k, [ceil(K / 128), rows] (block 1, activations), or of each
+    block of 128 rows x 128 k, [ceil(rows / 128), ceil(K / 128)] (block 128, weights)."""
+
+    __slots__ = ("q", "s", "rows", "K", "block", "device")      # device: its index, -1 the host
+
+    def __init__(self, q, s, block: int = 1):
+        import torch
+        if block not in (1, 128):
+            raise ValueError(f"Fp8: block must be 1 or 128, got {block}")
+        if q.dtype is not torch.float8_e4m3fn or s.dtype is not torch.float32:
+            raise TypeError(f"Fp8: codes must be float8_e4m3fn and scales float32, got {q.dtype} and "
+                            f"{s.dtype}")
+        where = q.get_device() if q.is_cuda else -1
+        if where < 0 or not s.is_cuda or s.get_device() != where:
+            raise TypeError("Fp8: codes and scales must be on one device")
+        if q.dim() != 2 or s.dim() != 2:
+            raise ValueError(f"Fp8: codes {tuple(q.shape)} and scales {tuple(s.shape)} must be 2-D")
+        rows, K = q.shape
+        kb = -(-K // 128)
+        fits = (kb, rows) if block == 1 else (-(-rows // 128), kb)
+        if tuple(s.shape) != fits:
+            raise ValueError(f"Fp8: a {rows} x {K} matrix of block {block} has scales {fits}, not "
+                             f"{tuple(s.shape)}")
+        if (K > 1 and q.stride(1) != 1) or (fits[1] > 1 and s.stride(1) != 1):
+            raise ValueError("Fp8: unit stride along rows of codes and of scales")
+        self.q, self.s, self.rows, self.K, self.block, self.device = q, s, rows, K, block, where
+
+    @classmethod
+    def empty(cls, rows: int, K: int, block: int = 1, device="cuda") -> "Fp8":
+        import torch
+        if block not in (1, 128):
+            raise ValueError(f"Fp8: block must be 1 or 128, got {block}")
+        m = cls.__new__(cls)                 # tensors that fit by construction: no checks
+        kb, ld = -(-K // 128), -(-K // 16) * 16
+        q = torch.empty(rows, ld, dtype=torch.float8_e4m3fn, device=device)
+        m.q = q if ld == K else q[:, :K]
+        m.s = torch.empty((kb, rows) if block == 1 else (-(-rows // 128), kb), dtype=torch.float32,
+                          device=device)
+        m.rows, m.K, m.block, m.device = rows, K, block, q.get_device()
+        return m
+
+    def _args(self):
+        """Codes, bytes from row to row, scales, floats from row to row of them."""
+        q, s = self.q, self.s
+        ld, lds = q.stride(0), s.stride(0)
+        if self.rows <= 1:
+            ld = max(ld, self.K)
+        return q.data_ptr(), ld, s.data_ptr(), max(lds, s.shape[1])
+
+
+def _quantize8(entry, X, out, dtype, stream):
+    px, ldx = _rows(X, "X", dtype)
+    if X.shape != (out.rows, out.K):
+        raise ValueError(f"shape mismatch X{tuple(X.shape)} out ({out.rows}, {out.K})")
+    if out.device != X.get_device():
+        raise _apart(entry, X.get_device(), out.device)
+    q, ldq, s, lds = out._args()
+    _check(getattr(lib(), entry)(out.rows, out.K, px, ldx, q, ldq, s, lds, out.block,
+                                 _stream_handle(stream)), entry)
+
+
+def fp8_quantize_f16(X, out: Fp8, stream=None) -> None:
+    """out = X [rows, K] in 8 bits."""
+    import torch
+    _quantize8("fp8_quantize_f16", X, out, torch.float16, stream)
+
+
+def fp8_quantize_bf16(X, out: Fp8, stream=None) -> None:
+    import torch
+    _quantize8("fp8_quantize_bf16", X, out, torch.bfloat16, stream)
+
+
+def _dequantize8(entry, m, Y, dtype, stream):
+    py, ldy = _rows(Y, "Y", dtype)
+    if Y.shape != (m.rows, m.K):
+        raise ValueError(f"shape mismatch matrix ({m.rows}, {m.K}) Y{tuple(Y.shape)}")
+    if m.device != Y.get_device():
+        raise _apart(entry, m.device, Y.get_device())
+    q, ldq, s, lds = m._args()
+    _check(getattr(lib(), entry)(m.rows, m.K, q, ldq, s, lds, m.block, py, ldy, _stream_handle(stream)),
+           entry)
+
+
+def fp8_dequantize_f16(m: Fp8, Y, stream=None) -> None:
+    """Y [rows, K] = the values of an 8-bit matrix."""
+    import torch
+    _dequantize8("fp8_dequantize_f16", m, Y, torch.float16, stream)
+
+
+def fp8_dequantize_bf16(m: Fp8, Y, stream=None) -> None:
+    import torch
+    _dequantize8("fp8_dequantize_bf16", m, Y, torch.bfloat16, stream)
+
+
+def fp8_dequantize_f32(m: Fp8, Y, stream=None) -> None:
+    import torch
+    _dequantize8("fp8_dequantize_f32", m, Y, torch.float32, stream)
+
+
+def _gemm_fp8(entry, A, B, C, dtype, stream):
+    if A.K != B.K or C.shape != (A.rows, B.rows):
+        raise ValueError(f"shape mismatch A({A.rows}, {A.K}) B({B.rows}, {B.K}) C{tuple(C.shape)}")
+    if A.block != 1 or B.block != 128:
+        raise ValueError(f"A must have blocks of 1 x 128 and B of 128 x 128, not {A.block} and {B.block}")
+    pc, ldc = _rows(C, "C", dtype)
+    if not (A.device == B.device == C.get_device()):
+        raise _apart(entry, A.device, B.device, C.get_device())
+    _check(getattr(lib(), entry)(A.rows, B.rows, A.K, *A._args(), *B._args(), pc, ldc,
+                                 _stream_handle(stream)), entry)
+
+
+def gemm_fp8_f16(A: Fp8, B: Fp8, C, stream=None) -> None:
+    """C[M, N] = A[M, K] . B[N, K]^T for 8-bit matrices (A of block 1, B of block
+    128), fp32 accumulate, fp16 out."""
+    import torch
+    _gemm_fp8("gemm_fp8_f16", A, B, C, torch.float16, stream)
+
+
+def gemm_fp8_bf16(A: Fp8, B: Fp8, C, stream=None) -> None:
+    import torch
+    _gemm_fp8("gemm_fp8_bf16", A, B, C, torch.bfloat16, stream)
+
+
+# ---- the norm and the gated feed-forward block ------------------------------------------
+
+def _kind16(t, name):
+    """The suffix of the entry points for tensors of t's type."""
+    import torch
+    if t.dtype is torch.float16:
+        return "f16"
+    if t.dtype is torch.bfloat16:
+        return "bf16"
+    raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+
+
+def _matrix(t, name, shape, dtype, where):
+    """Address and row stride of a matrix that a call needs in this shape and place."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    got = _rows(t, name, dtype)
+    if t.get_device() != where:
+        raise _apart(name, where, t.get_device())
+    return got
+
+
+def _vector(t, name, n, dtype, where):
+    if tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous values, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != where:
+        raise _apart(name, where, t.get_device())
+    return t.data_ptr()
+
+
+def _buffer(t, where):
+    """Address and bytes of a work buffer (None: none)."""
+    import torch
+    if t is None:
+        return None, 0
+    if t.dtype is not torch.uint8 or not t.is_contiguous():
+        raise TypeError("workspace must be contiguous uint8")
+    if t.get_device() != where:
+        raise _apart("workspace", where, t.get_device())
+    return t.data_ptr(), t.numel()
+
+
+def rms_norm(x, weight, y=None, q: Fp8 | None = None, residual=None, total=None, rstd=None,
+             eps: float = 1e-6, stream=None) -> None:
+    """y [rows, K] = t * rstd * weight with t = x + residual rounded to the type and
+    rstd = 1 / sqrt(mean(t^2) + eps).  float16 or bfloat16 x, residual, weight [K]
+    (None: ones), y and total (t); q: y in 8 bits; rstd [rows] float32, for the
+    gradient.  At least one of y, q, total and rstd is given."""
+    import torch
+    kind = _kind16(x, "x")
+    px, ldx = _rows(x, "x", x.dtype)
+    shape, dtype, where = x.shape, x.dtype, x.get_device()
+    rows, K = shape
+    none = (None, 0)
+    pr, ldr = none if residual is None else _matrix(residual, "residual", shape, dtype, where)
+    pt, ldt = none if total is None else _matrix(total, "total", shape, dtype, where)
+    py, ldy = none if y is None else _matrix(y, "y", shape, dtype, where)
+    pw = None if weight is None else _vector(weight, "weight", K, dtype, where)
+    ps = None if rstd is None else _vector(rstd, "rstd", rows, torch.float32, where)
+    if q is None:
+        codes = (None, 0, None, 0)
+    else:
+        if (q.rows, q.K) != (rows, K) or q.block != 1:
+            raise ValueError(f"q must be {rows} x {K} of block 1, got {q.rows} x {q.K} of {q.block}")
+        if q.device != where:
+            raise _apart("rms_norm", where, q.device)
+        codes = q._args()
+    entry = "rms_norm_" + kind
+    args = SdtNorm(rows, K, px, ldx, pr, ldr, pw, eps, pt, ldt, py, ldy, *codes, ps)
+    _check(getattr(lib(), entry)(ctypes.byref(args), _stream_handle(stream)), entry)
+
+
+def rms_norm_workspace_size(rows: int, K: int) -> int:
+    """Workspace bytes of rms_norm_backward with dweight."""
+    v = int(lib().sdt_rms_norm_workspace_size(int(rows), int(K)))
+    if v < 0:
+        raise SdtError(SDT_ERR_INVALID_ARG, "sdt_rms_norm_workspace_size")
+    return v
+
+
+def rms_norm_backward(total, weight, rstd, dy, dx, dweight=None, workspace=None, dtotal=None,
+                      stream=None) -> None:
+    """dx [rows, K], the gradient of x (and of the residual), and dweight [K] float32,
+    from dy and, where t has a gradient besides, dtotal.  workspace: a uint8 device
+    tensor of rms_norm_workspace_size bytes, where dweight is given."""
+    import torch
+    kind = _kind16(total, "total")
+    pt, ldt = _rows(total, "total", total.dtype)
+    shape, dtype, where = total.shape, total.dtype, total.get_device()
+    rows, K = shape
+    py, ldy = _matrix(dy, "dy", shape, dtype, where)
+    px, ldx = _matrix(dx, "dx", shape, dtype, where)
+    pd, ldd = (None, 0) if dtotal is None else _matrix(dtotal, "dtotal", shape, dtype, where)
+    pw = None if weight is None else _vector(weight, "weight", K, dtype, where)
+    pg = None if dweight is None else _vector(dweight, "dweight", K, torch.float32, where)
+    ps = _vector(rstd, "rstd", rows, torch.float32, where)
+    wp, wn = _buffer(workspace, where)
+    entry = "rms_norm_backward_" + kind
+    args = SdtNormGrad(rows, K, pt, ldt, pw, ps, py, ldy, pd, ldd, px, ldx, pg, wp, wn)
+    _check(getattr(lib(), entry)(ctypes.byref(args), _stream_handle(stream)), entry)
+
+
+_ACTS = {"silu": 0, "gelu": 1}
+
+
+def _act(act):
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    return _ACTS[act]
+
+
+def _factors(g, u, shape, dtype, where):
+    """The kept factors' addresses, strides and whether they are float32."""
+    import torch
+    if g is None and u is None:
+        return None, 0, None, 0, 0
+    if g is None or u is None:
+        raise ValueError("g and u are given together")
+    kept = torch.float32 if g.dtype is torch.float32 else dtype
+    return (*_matrix(g, "g", shape, kept, where), *_matrix(u, "u", shape, kept, where),
+            1 if kept is torch.float32 else 0)
+
+
+def gated_ff(x, gate, up, h, act: str = "silu", g=None, u=None, stream=None) -> None:
+    """h [M, N] = a(x . gate^T) * (x . up^T) for x [M, K], gate and up [N, K], float16 or
+    bfloat16; a: silu, or gelu in its tanh form.  g and u [M, N], float32 or the type:
+    the two products, kept for gated_ff_backward."""
+    kind = _kind16(x, "x")
+    px, ldx = _rows(x, "x", x.dtype)
+    dtype, where = x.dtype, x.get_device()
+    (M, K), N = x.shape, gate.shape[0]
+    pg, ldg = _matrix(gate, "gate", (N, K), dtype, where)
+    pu, ldu = _matrix(up, "up", (N, K), dtype, where)
+    ph, ldh = _matrix(h, "h", (M, N), dtype, where)
+    entry = "gated_ff_" + kind
+    args = SdtGatedFf(M, N, K, px, ldx, pg, ldg, pu, ldu, _act(act), ph, ldh,
+                      *_factors(g, u, (M, N), dtype, where))
+    _check(getattr(lib(), entry)(ctypes.byref(args), _stream_handle(stream)), entry)
+
+
+def gated_ff_workspace_size(M: int, N: int, K: int) -> int:
+    """Workspace bytes of gated_ff_backward."""
+    v = int(lib().sdt_gated_ff_workspace_size(int(M), int(N), int(K)))
+    if v < 0:
+        raise SdtError(SDT_ERR_INVALID_ARG, "sdt_gated_ff_workspace_size")
+    return v
+
+
+def gated_ff_backward(x, gate, up, g, u, dh, dx, dgate, dup, workspace, act: str = "silu",
+                      stream=None) -> None:
+    """dx [M, K], dgate and dup [N, K] from dh [M, N] and the kept g and u (dx, or
+    dgate and dup together, None: not wanted).  workspace: a uint8 device tensor of
+    gated_ff_workspace_size bytes."""
+    kind = _kind16(x, "x")
+    px, ldx = _rows(x, "x", x.dtype)
+    dtype, where = x.dtype, x.get_device()
+    (M, K), N = x.shape, gate.shape[0]
+    pg, ldg = _matrix(gate, "gate", (N, K), dtype, where)
+    pu, ldu = _matrix(up, "up", (N, K), dtype, where)
+    pd, ldd = _matrix(dh, "dh", (M, N), dtype, where)
+    if g is None:
+        raise ValueError("g and u, as gated_ff kept them, are needed")
+    factors = _factors(g, u, (M, N), dtype, where)
+    none = (None, 0)
+    ox = none if dx is None else _matrix(dx, "dx", (M, K), dtype, where)
+    og = none if dgate is None else _matrix(dgate, "dgate", (N, K), dtype, where)
+    ou = none if dup is None else _matrix(dup, "dup", (N, K), dtype, where)
+    entry = "gated_ff_backward_" + kind
+    args = SdtGatedFfGrad(M, N, K, px, ldx, pg, ldg, pu, ldu, _act(act), *factors, pd, ldd, *ox, *og,
+                          *ou, *_buffer(workspace, where))
+    _check(getattr(lib(), entry)(ctypes.byref(args), _stream_handle(stream)), entry)
+
+
+# ---- products of operands stored along the other dimension ---------------------------------
+
+def gemm_turned_workspace_size(M: int, N: int, K: int) -> int:
+    """Workspace bytes that let gemm_*_nn and gemm_*_tn split a C [M, N] along K (0: no split)."""
+    v = int(lib().sdt_gemm_turned_workspace_size(int(M), int(N), int(K)))
+    if v < 0:
+        raise SdtError(SDT_ERR_INVALID_ARG, "sdt_gemm_turned_workspace_size")
+    return v
+
+
+def _gemm_turned(entry, A, B, C, workspace, dtype, stream):
+    M, K = A.shape if entry.endswith("nn") else A.shape[::-1]
+    N = B.shape[1]
+    if B.shape[0] != K or C.shape != (M, N):
+        raise ValueError(f"shape mismatch A{tuple(A.shape)} B{tuple(B.shape)} C{tuple(C.shape)}")
+    pa, lda = _rows(A, "A", dtype)
+    pb, ldb = _rows(B, "B", dtype)
+    pc, ldc = _rows(C, "C", dtype)
+    where = A.get_device()
+    if not (B.get_device() == C.get_device() == where):
+        raise _apart(entry, where, B.get_device(), C.get_device())
+    _check(getattr(lib(), entry)(M, N, K, pa, lda, pb, ldb, pc, ldc, *_buffer(workspace, where),
+                                 _stream_handle(stream)), entry)
+
+
+def gemm_f16_nn(A, B, C, workspace=None, stream=None) -> None:
+    """C[M, N] = A[M, K] . B[K, N], fp32 accumulate, fp16 out (of a product a . b^T, the
+    gradient of a: dC . b).  workspace: a uint8 device tensor, see
+    gemm_turned_workspace_size."""
+    import torch
+    _gemm_turned("gemm_f16_nn", A, B, C, workspace, torch.float16, stream)
+
+
+def gemm_bf16_nn(A, B, C, workspace=None, stream=None) -> None:
+    import torch
+    _gemm_turned("gemm_bf16_nn", A, B, C, workspace, torch.bfloat16, stream)
+
+
+def gemm_f16_tn(A, B, C, workspace=None, stream=None) -> None:
+    """C[M, N] = A[K, M]^T . B[K, N] (of a product a . b^T, the gradient of b: dC^T . a)."""
+    import torch
+    _gemm_turned("gemm_f16_tn", A, B, C, workspace, torch.float16, stream)
+
+
+def gemm_bf16_tn(A, B, C, workspace=None, stream=None) -> None:
+    import torch
+    _gemm_turned("gemm_bf16_tn", A, B, C, workspace, torch.bfloat16, stream)

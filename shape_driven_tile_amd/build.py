@@ -24,7 +24,7 @@ LIB = os.path.join(HERE, "libsdt.so")
 ARCH = "gfx950"
 
 SOURCES = [os.path.join(CSRC, "sdt.hip"), os.path.join(CSRC, "mx4.hip"),
-           os.path.join(CSRC, "launcher.cpp")]
+           os.path.join(CSRC, "ffn.hip"), os.path.join(CSRC, "launcher.cpp")]
 
 # Packed fp32 vector ops are switched off for every device compile.
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
@@ -114,7 +114,7 @@ def resource_summary(path: str) -> str:
     registers, spills, LDS, occupancy) to `path`."""
     import re
     report = ""
-    for source in SOURCES[:2]:
+    for source in [s for s in SOURCES if s.endswith(".hip")]:
         cmd = [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
                "-I", INCLUDE, "-I", CSRC] + DEVICE_FLAGS + [
                "-Rpass-analysis=kernel-resource-usage", "--cuda-device-only", "-c",
@@ -137,7 +137,7 @@ def resource_summary(path: str) -> str:
                            capture_output=True, text=True).stdout.splitlines()
     out = ["# Kernel resources: every instantiation in libsdt.so (gfx950)", "",
            "The compiler's own report (`-Rpass-analysis=kernel-resource-usage`) for the",
-           "device code of `shape_driven_tile_amd/csrc/sdt.hip` and `mx4.hip`, written by", "",
+           "device code of `shape_driven_tile_amd/csrc/sdt.hip`, `mx4.hip` and `ffn.hip`, written by", "",
            "    python -m shape_driven_tile_amd.build --resource-summary "
            "profiles/kernel_resource_usage.md", "",
            "VGPRs and AGPRs are per lane (the two files are allocated together on",

@@ -1,0 +1,603 @@
+// C ABI of the feed-forward entry points (declared in sdt.h): 8-bit matrices and
+// their products, the norm, the gated block, products of operands stored along
+// the other dimension.  Argument checks on the host, the choice of a kernel, the
+// launch.  Allocates nothing.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "launcher.hpp"
+#include "runtime.hpp"
+#include "sdt.h"
+#include "tile_kernel.hpp"
+
+namespace sdt {
+namespace {
+
+constexpr int64_t kMaxK = int64_t(1) << 23;
+constexpr int64_t kMaxLd = int64_t(1) << 22;          // elements, exclusive (gemm_f16's)
+constexpr int64_t kMaxRows = INT_MAX - 255;           // the last tile's end fits 32 bits
+constexpr int64_t kMaxNorm = 32768;                   // elements of a normed row
+constexpr int kSplitTarget = 256;                     // workgroups that a split aims at
+constexpr int kNormParts = 512;                       // workgroups of the norm's gradient
+
+bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+int launched(hipError_t e) { return e == hipSuccess ? SDT_OK : fail_hip(e); }
+
+template <typename P>
+int launch(const void* kernel, int64_t grid, int threads, P& params, void* stream) {
+    if (grid > INT_MAX) return SDT_ERR_UNSUPPORTED;
+    if (grid == 0) return SDT_OK;
+    void* args[] = {&params};
+    return launched(hipLaunchKernel(kernel, dim3((unsigned)grid), dim3((unsigned)threads), args, 0,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+// ---- 8-bit matrices -------------------------------------------------------------------
+
+// Codes and scales of a rows x K matrix (both > 0).
+int check_fp8(int64_t rows, int64_t K, const void* Q, int64_t ldq, const void* S, int64_t lds, int block) {
+    if (block != 1 && block != 128) return SDT_ERR_INVALID_ARG;
+    if (!Q || !S) return SDT_ERR_INVALID_ARG;
+    if (ldq < K || lds < (block == 1 ? rows : ceil_div(K, 128))) return SDT_ERR_INVALID_ARG;
+    if (K > kMaxK || rows > kMaxRows || ldq >= 2 * kMaxLd || lds > INT_MAX) return SDT_ERR_UNSUPPORTED;
+    if (misaligned(Q, 16) || misaligned(S, 4) || (rows > 1 && ldq % 16 != 0)) return SDT_ERR_UNSUPPORTED;
+    return SDT_OK;
+}
+
+// Rows a workgroup takes: eight loads in flight a lane where that still gives every
+// CU two workgroups, else one (a token: latency).
+bool many_rows(int64_t rows, int64_t nct, int num_cu) { return rows * nct >= int64_t(16) * num_cu; }
+
+template <typename Elt>
+int quantize8(int64_t rows, int64_t K, const void* X, int64_t ldx, void* Q, int64_t ldq, float* S,
+              int64_t lds, int block, void* stream) {
+    if (rows < 0 || K < 0) return SDT_ERR_INVALID_ARG;
+    if (block != 1 && block != 128) return SDT_ERR_INVALID_ARG;
+    if (rows == 0 || K == 0) return SDT_OK;
+    if (!X || ldx < K) return SDT_ERR_INVALID_ARG;
+    int rc = check_fp8(rows, K, Q, ldq, S, lds, block);
+    if (rc != SDT_OK) return rc;
+    if (misaligned(X, 2)) return SDT_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    rc = device_info(&dev);
+    if (rc != SDT_OK) return rc;
+    Fp8Quant p;
+    p.X = static_cast<const uint16_t*>(X);
+    p.ldx = ldx;
+    p.Q = static_cast<uint8_t*>(Q);
+    p.ldq = ldq;
+    p.S = S;
+    p.lds = lds;
+    p.rows = rows;
+    p.K = (int)K;
+    if (block == 128) {
+        p.nct = (int)ceil_div(K, 128);
+        return launch(reinterpret_cast<const void*>(&fp8_quantize_blocks_kernel<Elt>),
+                      ceil_div(rows, 128) * p.nct, 256, p, stream);
+    }
+    p.nct = (int)ceil_div(K, 2048);
+    if (many_rows(rows, p.nct, dev.num_cu))
+        return launch(reinterpret_cast<const void*>(&fp8_quantize_rows_kernel<Elt, 8>),
+                      ceil_div(rows, 8) * p.nct, 256, p, stream);
+    return launch(reinterpret_cast<const void*>(&fp8_quantize_rows_kernel<Elt, 1>), rows * p.nct, 256, p,
+                  stream);
+}
+
+template <typename Out>
+int dequantize8(int64_t rows, int64_t K, const void* Q, int64_t ldq, const float* S, int64_t lds, int block,
+                void* Y, int64_t ldy, void* stream) {
+    if (rows < 0 || K < 0) return SDT_ERR_INVALID_ARG;
+    if (block != 1 && block != 128) return SDT_ERR_INVALID_ARG;
+    if (rows == 0 || K == 0) return SDT_OK;
+    if (!Y || ldy < K) return SDT_ERR_INVALID_ARG;
+    int rc = check_fp8(rows, K, Q, ldq, S, lds, block);
+    if (rc != SDT_OK) return rc;
+    if (misaligned(Y, std::is_same_v<Out, float> ? 4 : 2)) return SDT_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    rc = device_info(&dev);
+    if (rc != SDT_OK) return rc;
+    Fp8Dequant p;
+    p.Q = static_cast<const uint8_t*>(Q);
+    p.ldq = ldq;
+    p.S = S;
+    p.lds = lds;
+    p.block = block;
+    p.Y = Y;
+    p.ldy = ldy;
+    p.rows = rows;
+    p.K = (int)K;
+    p.nct = (int)ceil_div(K, 2048);
+    if (many_rows(rows, p.nct, dev.num_cu))
+        return launch(reinterpret_cast<const void*>(&fp8_dequantize_kernel<Out, 8>), ceil_div(rows, 8) * p.nct,
+                      256, p, stream);
+    return launch(reinterpret_cast<const void*>(&fp8_dequantize_kernel<Out, 1>), rows * p.nct, 256, p, stream);
+}
+
+// ---- products ---------------------------------------------------------------------------
+
+int check_out(int64_t rows, int64_t N, const void* C, int64_t ldc) {
+    if (!C || ldc < N) return SDT_ERR_INVALID_ARG;
+    if (misaligned(C, 16) || (rows > 1 && ldc % 8 != 0)) return SDT_ERR_UNSUPPORTED;
+    return SDT_OK;
+}
+
+// A 16-bit operand of `rows` rows of K (> 0) elements, as gemm_f16's.
+int check_in(int64_t rows, int64_t K, const void* A, int64_t lda) {
+    if (!A || lda < K) return SDT_ERR_INVALID_ARG;
+    if (lda >= kMaxLd) return SDT_ERR_UNSUPPORTED;
+    if (misaligned(A, 16) || (rows > 1 && lda % 8 != 0)) return SDT_ERR_UNSUPPORTED;
+    return SDT_OK;
+}
+
+TileGemm product(int64_t M, int64_t N, int64_t L, int z, int nxcd) {
+    TileGemm p = {};
+    p.M = (int)M;
+    p.N = (int)N;
+    p.L = (int)L;
+    p.nkt = (int)ceil_div(L * z, 128);
+    p.products = p.batch = p.splits = 1;
+    p.nxcd = nxcd;
+    return p;
+}
+
+template <typename Elt, bool FP8, int BM, int BN, int WM, int WN, int NS, bool TA, bool TB, bool GATED>
+int launch_tile(TileGemm& p, void* stream) {
+    p.gm = (int)ceil_div(p.M, BM);
+    p.gn = (int)ceil_div(p.N, GATED ? BN / 2 : BN);
+    const int64_t grid = (int64_t)p.gm * p.gn * p.batch * p.splits;
+    const int rc = launch(
+        reinterpret_cast<const void*>(&tile_gemm_kernel<Elt, FP8, BM, BN, WM, WN, NS, TA, TB, GATED>), grid,
+        WM * WN * 64, p, stream);
+    if (rc != SDT_OK || p.splits == 1) return rc;
+    return launch(reinterpret_cast<const void*>(&tile_reduce_kernel<Elt, BM, BN, WM, WN>),
+                  (int64_t)p.gm * p.gn * p.batch, WM * WN * 64, p, stream);
+}
+
+template <typename Elt, bool FP8, bool GATED, int PB, int NMB, int NS>
+int launch_rows(TileGemm& p, void* stream) {
+    p.gm = (int)ceil_div(p.M, NMB * 16);
+    p.gn = (int)ceil_div(p.N, PB * 16);
+    return launch(reinterpret_cast<const void*>(&rows_gemm_kernel<Elt, FP8, GATED, 4, PB, NMB, NS>),
+                  (int64_t)p.gm * p.gn, 256, p, stream);
+}
+
+template <typename Elt>
+int gemm8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* SA, int64_t ldsa,
+          const void* B, int64_t ldb, const float* SB, int64_t ldsb, void* C, int64_t ldc, void* stream) {
+    if (M < 0 || N < 0 || K < 0) return SDT_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return SDT_OK;
+    int rc = check_out(M, N, C, ldc);
+    if (rc == SDT_OK && K > 0) rc = check_fp8(M, K, A, lda, SA, ldsa, 1);
+    if (rc == SDT_OK && K > 0) rc = check_fp8(N, K, B, ldb, SB, ldsb, 128);
+    if (rc != SDT_OK) return rc;
+    if (M > kMaxRows || N > kMaxRows) return SDT_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    rc = device_info(&dev);
+    if (rc != SDT_OK) return rc;
+    TileGemm p = product(M, N, K, 1, dev.nxcd);
+    p.A[0] = static_cast<const uint8_t*>(A);
+    p.B[0] = static_cast<const uint8_t*>(B);
+    p.SA = SA;
+    p.SB = SB;
+    p.C[0] = static_cast<uint16_t*>(C);
+    p.lda[0] = lda;
+    p.ldb[0] = ldb;
+    p.ldsa = ldsa;
+    p.ldsb = ldsb;
+    p.ldc[0] = ldc;
+    const int64_t cu = dev.num_cu;
+    if (M <= 16) return launch_rows<Elt, true, false, 2, 1, 3>(p, stream);
+    if (M <= 64) return launch_rows<Elt, true, false, 2, 4, 2>(p, stream);
+    if (ceil_div(M, 128) * ceil_div(N, 128) >= cu)
+        return launch_tile<Elt, true, 128, 128, 2, 2, 2, false, false, false>(p, stream);
+    return launch_tile<Elt, true, 64, 64, 2, 2, 4, false, false, false>(p, stream);
+}
+
+// How a product with a workspace is laid out: its tiles' side and the workgroups
+// along each tile's k-tiles.
+struct Split {
+    int side, splits;
+    int64_t bytes;
+};
+Split plan_split(int64_t M, int64_t N, int64_t kt, int batch) {
+    Split s;
+    const int64_t t128 = ceil_div(M, 128) * ceil_div(N, 128) * batch;
+    s.side = t128 >= kSplitTarget * 3 / 4 ? 128 : 64;
+    const int64_t tiles = ceil_div(M, s.side) * ceil_div(N, s.side) * batch;
+    int64_t n = tiles > 0 ? kSplitTarget / tiles : 1;
+    n = std::min(n, kt / 8);
+    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(n, 16));
+    s.bytes = s.splits > 1 ? tiles * s.splits * s.side * s.side * 4 : 0;
+    return s;
+}
+
+template <typename Elt, bool TA, bool TB>
+int launch_split(TileGemm& p, void* ws, int64_t ws_bytes, void* stream) {
+    const Split s = plan_split(p.M, p.N, (int64_t)p.nkt * p.products, p.batch);
+    if (s.splits > 1 && ws_bytes >= s.bytes) {
+        p.splits = s.splits;
+        p.ws = static_cast<float*>(ws);
+    }
+    return s.side == 128 ? launch_tile<Elt, false, 128, 128, 2, 2, 2, TA, TB, false>(p, stream)
+                         : launch_tile<Elt, false, 64, 64, 2, 2, 4, TA, TB, false>(p, stream);
+}
+
+// C (M x N) = A . B, A (M x L) or, TA, A^T with A (L x M); B (L x N).
+template <typename Elt, bool TA>
+int gemm_turned(int64_t M, int64_t N, int64_t L, const void* A, int64_t lda, const void* B, int64_t ldb,
+                void* C, int64_t ldc, void* ws, int64_t ws_bytes, void* stream) {
+    if (M < 0 || N < 0 || L < 0 || ws_bytes < 0 || (ws_bytes > 0 && !ws)) return SDT_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return SDT_OK;
+    int rc = check_out(M, N, C, ldc);
+    if (rc == SDT_OK && L > 0) rc = TA ? check_in(L, M, A, lda) : check_in(M, L, A, lda);
+    if (rc == SDT_OK && L > 0) rc = check_in(L, N, B, ldb);
+    if (rc != SDT_OK) return rc;
+    if (M > kMaxRows || N > kMaxRows || L > kMaxRows || misaligned(ws, 16)) return SDT_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    rc = device_info(&dev);
+    if (rc != SDT_OK) return rc;
+    TileGemm p = product(M, N, L, 2, dev.nxcd);
+    p.A[0] = static_cast<const uint8_t*>(A);
+    p.B[0] = static_cast<const uint8_t*>(B);
+    p.C[0] = static_cast<uint16_t*>(C);
+    p.lda[0] = lda * 2;
+    p.ldb[0] = ldb * 2;
+    p.ldc[0] = ldc;
+    return launch_split<Elt, TA, true>(p, ws, ws_bytes, stream);
+}
+
+// ---- the norm ---------------------------------------------------------------------------
+
+// Threads and chunks of a row of K: one wave up to 512 elements.
+template <template <typename, int, int> class K, typename Elt>
+const void* norm_kernel(int64_t n, int* threads) {
+    if (n <= 512) return *threads = 64, K<Elt, 64, 1>::get();
+    if (n <= 2048) return *threads = 256, K<Elt, 256, 1>::get();
+    if (n <= 4096) return *threads = 256, K<Elt, 256, 2>::get();
+    if (n <= 8192) return *threads = 256, K<Elt, 256, 4>::get();
+    if (n <= 16384) return *threads = 512, K<Elt, 512, 4>::get();
+    return *threads = 1024, K<Elt, 1024, 4>::get();
+}
+template <typename Elt, int T, int CH>
+struct Forward {
+    static const void* get() { return reinterpret_cast<const void*>(&rms_norm_kernel<Elt, T, CH>); }
+};
+template <typename Elt, int T, int CH>
+struct Backward {
+    static const void* get() { return reinterpret_cast<const void*>(&rms_norm_backward_kernel<Elt, T, CH>); }
+};
+
+// A 16-bit matrix of the norm: any alignment of its elements.
+int check_rows(int64_t K, const void* X, int64_t ld, bool needed) {
+    if (!X) return needed ? SDT_ERR_INVALID_ARG : SDT_OK;
+    if (ld < K) return SDT_ERR_INVALID_ARG;
+    return misaligned(X, 2) ? SDT_ERR_UNSUPPORTED : SDT_OK;
+}
+
+template <typename Elt>
+int norm(const sdt_norm* a, void* stream) {
+    if (!a || a->rows < 0 || a->K < 0 || !std::isfinite(a->eps) || a->eps < 0.0f) return SDT_ERR_INVALID_ARG;
+    if (a->rows == 0 || a->K == 0) return SDT_OK;
+    if (!a->total && !a->y && !a->q && !a->rstd) return SDT_ERR_INVALID_ARG;
+    int rc = check_rows(a->K, a->x, a->ldx, true);
+    if (rc == SDT_OK) rc = check_rows(a->K, a->residual, a->ldr, false);
+    if (rc == SDT_OK) rc = check_rows(a->K, a->weight, a->K, false);
+    if (rc == SDT_OK) rc = check_rows(a->K, a->total, a->ldt, false);
+    if (rc == SDT_OK) rc = check_rows(a->K, a->y, a->ldy, false);
+    if (rc == SDT_OK && a->q) rc = check_fp8(a->rows, a->K, a->q, a->ldq, a->s, a->lds, 1);
+    if (rc != SDT_OK) return rc;
+    if (misaligned(a->rstd, 4) || a->K > kMaxNorm || a->rows > kMaxRows) return SDT_ERR_UNSUPPORTED;
+    Norm p = {};
+    p.X = static_cast<const uint16_t*>(a->x);
+    p.ldx = a->ldx;
+    p.R = static_cast<const uint16_t*>(a->residual);
+    p.ldr = a->ldr;
+    p.W = static_cast<const uint16_t*>(a->weight);
+    p.T = static_cast<uint16_t*>(a->total);
+    p.ldt = a->ldt;
+    p.Y = static_cast<uint16_t*>(a->y);
+    p.ldy = a->ldy;
+    p.Q = static_cast<uint8_t*>(a->q);
+    p.ldq = a->ldq;
+    p.S = a->s;
+    p.lds = a->lds;
+    p.rstd = a->rstd;
+    p.rows = a->rows;
+    p.K = (int)a->K;
+    p.eps = a->eps;
+    int threads;
+    const void* k = norm_kernel<Forward, Elt>(a->K, &threads);
+    return threads == 64 ? launch(k, ceil_div(a->rows, 4), 256, p, stream)
+                         : launch(k, a->rows, threads, p, stream);
+}
+
+// Workgroups of the gradient: each keeps the weight's gradient of its rows.
+int64_t norm_parts(int64_t rows, int64_t K) {
+    return std::min<int64_t>(K <= 512 ? ceil_div(rows, 4) : rows, kNormParts);
+}
+
+template <typename Elt>
+int norm_backward(const sdt_norm_grad* a, void* stream) {
+    if (!a || a->rows < 0 || a->K < 0) return SDT_ERR_INVALID_ARG;
+    if (a->K == 0) return SDT_OK;
+    if (a->rows == 0 && !a->dweight) return SDT_OK;
+    if (misaligned(a->dweight, 4) || a->K > kMaxNorm || a->rows > kMaxRows) return SDT_ERR_UNSUPPORTED;
+    Norm p = {};
+    p.rows = a->rows;
+    p.K = (int)a->K;
+    const int64_t parts = norm_parts(a->rows, a->K);
+    if (a->rows > 0) {
+        int rc = check_rows(a->K, a->total, a->ldt, true);
+        if (rc == SDT_OK) rc = check_rows(a->K, a->weight, a->K, false);
+        if (rc == SDT_OK) rc = check_rows(a->K, a->dy, a->lddy, true);
+        if (rc == SDT_OK) rc = check_rows(a->K, a->dtotal, a->lddt, false);
+        if (rc == SDT_OK) rc = check_rows(a->K, a->dx, a->lddx, true);
+        if (rc != SDT_OK) return rc;
+        if (!a->rstd) return SDT_ERR_INVALID_ARG;
+        if (a->dweight && (!a->workspace || a->workspace_bytes < parts * a->K * 4)) return SDT_ERR_INVALID_ARG;
+        if (misaligned(a->rstd, 4) || (a->dweight && misaligned(a->workspace, 16))) return SDT_ERR_UNSUPPORTED;
+        p.X = static_cast<const uint16_t*>(a->total);
+        p.ldx = a->ldt;
+        p.W = static_cast<const uint16_t*>(a->weight);
+        p.rstd_in = a->rstd;
+        p.DY = static_cast<const uint16_t*>(a->dy);
+        p.lddy = a->lddy;
+        p.DT = static_cast<const uint16_t*>(a->dtotal);
+        p.lddt = a->lddt;
+        p.DX = static_cast<uint16_t*>(a->dx);
+        p.lddx = a->lddx;
+        p.dw_part = a->dweight ? static_cast<float*>(a->workspace) : nullptr;
+        int threads;
+        const void* k = norm_kernel<Backward, Elt>(a->K, &threads);
+        rc = launch(k, parts, threads == 64 ? 256 : threads, p, stream);
+        if (rc != SDT_OK) return rc;
+    }
+    if (!a->dweight) return SDT_OK;
+    ColumnSum c;                                  // no rows: no parts, zeros
+    c.part = static_cast<const float*>(a->workspace);
+    c.out = a->dweight;
+    c.parts = (int)parts;
+    c.K = (int)a->K;
+    return launch(reinterpret_cast<const void*>(&column_sum_kernel), ceil_div(a->K, 64), 1024, c, stream);
+}
+
+// ---- the gated block ----------------------------------------------------------------------
+
+// Both factors, kept for the gradients: fp32 or 16 bits.
+int check_factors(int64_t M, int64_t N, const void* g, int64_t ldg, const void* u, int64_t ldu, int wide) {
+    if ((wide | 1) != 1) return SDT_ERR_INVALID_ARG;
+    if (!g || !u || ldg < N || ldu < N) return SDT_ERR_INVALID_ARG;
+    const int unit = wide ? 4 : 8;
+    if (misaligned(g, 16) || misaligned(u, 16)) return SDT_ERR_UNSUPPORTED;
+    return M > 1 && (ldg % unit != 0 || ldu % unit != 0) ? SDT_ERR_UNSUPPORTED : SDT_OK;
+}
+
+template <typename Elt>
+int gated(const sdt_gated_ff* a, void* stream) {
+    if (!a || a->M < 0 || a->N < 0 || a->K < 0 || (a->act | 1) != 1) return SDT_ERR_INVALID_ARG;
+    if (a->M == 0 || a->N == 0) return SDT_OK;
+    const int64_t M = a->M, N = a->N, K = a->K;
+    int rc = check_out(M, N, a->h, a->ldh);
+    if (rc == SDT_OK && K > 0) rc = check_in(M, K, a->x, a->ldx);
+    if (rc == SDT_OK && K > 0) rc = check_in(N, K, a->gate, a->ldgate);
+    if (rc == SDT_OK && K > 0) rc = check_in(N, K, a->up, a->ldup);
+    if (rc == SDT_OK && (a->g || a->u)) rc = check_factors(M, N, a->g, a->ldg, a->u, a->ldu, a->wide);
+    if (rc != SDT_OK) return rc;
+    if (M > kMaxRows || N > kMaxRows || K > kMaxK) return SDT_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    rc = device_info(&dev);
+    if (rc != SDT_OK) return rc;
+    TileGemm p = product(M, N, K, 2, dev.nxcd);
+    p.A[0] = static_cast<const uint8_t*>(a->x);
+    p.B[0] = static_cast<const uint8_t*>(a->gate);
+    p.B[1] = static_cast<const uint8_t*>(a->up);
+    p.C[0] = static_cast<uint16_t*>(a->h);
+    p.lda[0] = a->ldx * 2;
+    p.ldb[0] = a->ldgate * 2;
+    p.ldb[1] = a->ldup * 2;
+    p.ldc[0] = a->ldh;
+    p.G = a->g;
+    p.U = a->u;
+    p.ldg = a->ldg;
+    p.ldu = a->ldu;
+    p.wide = a->wide;
+    p.act = a->act;
+    if (M <= 16) return launch_rows<Elt, false, true, 1, 1, 4>(p, stream);
+    if (M <= 64) return launch_rows<Elt, false, true, 1, 4, 2>(p, stream);
+    if (ceil_div(M, 128) * ceil_div(N, 64) >= dev.num_cu)
+        return launch_tile<Elt, false, 128, 128, 2, 2, 2, false, false, true>(p, stream);
+    return launch_tile<Elt, false, 64, 128, 2, 2, 3, false, false, true>(p, stream);
+}
+
+// The backward's buffer: dg and du side by side (rows of 2 N' elements), then the
+// splits' sums of the product that needs most.
+struct GatedLayout {
+    int64_t ld, at, bytes;                        // elements of a row; the sums' offset
+};
+GatedLayout gated_layout(int64_t M, int64_t N, int64_t K) {
+    GatedLayout l;
+    const int64_t np = ceil_div(N, 8) * 8;
+    l.ld = 2 * np;
+    l.at = ceil_div(M * l.ld * 2, 256) * 256;
+    l.bytes = l.at + std::max(plan_split(M, K, 2 * ceil_div(N, 64), 1).bytes,
+                              plan_split(N, K, ceil_div(M, 64), 2).bytes);
+    return l;
+}
+
+template <typename Elt>
+int gated_backward(const sdt_gated_ff_grad* a, void* stream) {
+    if (!a || a->M < 0 || a->N < 0 || a->K < 0 || (a->act | 1) != 1) return SDT_ERR_INVALID_ARG;
+    const int64_t M = a->M, N = a->N, K = a->K;
+    if (!a->dx && !a->dgate && !a->dup) return SDT_ERR_INVALID_ARG;
+    if ((a->dgate == nullptr) != (a->dup == nullptr)) return SDT_ERR_INVALID_ARG;
+    if (K == 0 || (M == 0 && N == 0)) return SDT_OK;
+    int rc = SDT_OK;
+    const bool input = a->dx && M > 0, weights = a->dgate && N > 0;
+    if (input) rc = check_out(M, K, a->dx, a->lddx);
+    if (rc == SDT_OK && weights) rc = check_out(N, K, a->dgate, a->lddgate);
+    if (rc == SDT_OK && weights) rc = check_out(N, K, a->dup, a->lddup);
+    if (rc != SDT_OK) return rc;
+    const GatedLayout l = gated_layout(M, N, K);
+    if (M > 0 && N > 0) {
+        if (weights) rc = check_in(M, K, a->x, a->ldx);
+        if (rc == SDT_OK && input) rc = check_in(N, K, a->gate, a->ldgate);
+        if (rc == SDT_OK && input) rc = check_in(N, K, a->up, a->ldup);
+        if (rc == SDT_OK) rc = check_factors(M, N, a->g, a->ldg, a->u, a->ldu, a->wide);
+        if (rc == SDT_OK) rc = check_rows(N, a->dh, a->lddh, true);
+        if (rc != SDT_OK) return rc;
+        if (!a->workspace || a->workspace_bytes < l.bytes) return SDT_ERR_INVALID_ARG;
+        if (misaligned(a->workspace, 16) || l.ld >= kMaxLd) return SDT_ERR_UNSUPPORTED;
+    }
+    if (M > kMaxRows || N > kMaxRows || K > kMaxRows) return SDT_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    rc = device_info(&dev);
+    if (rc != SDT_OK) return rc;
+    uint16_t* const dg = static_cast<uint16_t*>(a->workspace);
+    uint16_t* const du = dg ? dg + l.ld / 2 : nullptr;
+    char* const ws = dg ? static_cast<char*>(a->workspace) + l.at : nullptr;
+    if (M > 0 && N > 0) {
+        GatedGrad p;
+        p.G = a->g;
+        p.U = a->u;
+        p.ldg = a->ldg;
+        p.ldu = a->ldu;
+        p.DH = static_cast<const uint16_t*>(a->dh);
+        p.lddh = a->lddh;
+        p.DG = dg;
+        p.DU = du;
+        p.ldd = l.ld;
+        p.M = M;
+        p.N = (int)N;
+        p.nct = (int)ceil_div(N, 2048);
+        p.wide = a->wide;
+        p.act = a->act;
+        rc = many_rows(M, p.nct, dev.num_cu)
+                 ? launch(reinterpret_cast<const void*>(&gated_grad_kernel<Elt, 4>), ceil_div(M, 4) * p.nct, 256,
+                          p, stream)
+                 : launch(reinterpret_cast<const void*>(&gated_grad_kernel<Elt, 1>), M * p.nct, 256, p, stream);
+        if (rc != SDT_OK) return rc;
+    }
+    if (input) {                                  // dx = dg . gate + du . up
+        TileGemm p = product(M, K, N, 2, dev.nxcd);
+        p.A[0] = reinterpret_cast<const uint8_t*>(dg);
+        p.A[1] = reinterpret_cast<const uint8_t*>(du);
+        p.B[0] = static_cast<const uint8_t*>(a->gate);
+        p.B[1] = static_cast<const uint8_t*>(a->up);
+        p.C[0] = static_cast<uint16_t*>(a->dx);
+        p.lda[0] = p.lda[1] = l.ld * 2;
+        p.ldb[0] = a->ldgate * 2;
+        p.ldb[1] = a->ldup * 2;
+        p.ldc[0] = a->lddx;
+        p.products = 2;
+        rc = launch_split<Elt, false, true>(p, ws, l.bytes - l.at, stream);
+        if (rc != SDT_OK) return rc;
+    }
+    if (weights) {                                // dgate = dg^T . x, dup = du^T . x
+        TileGemm p = product(N, K, M, 2, dev.nxcd);
+        p.A[0] = reinterpret_cast<const uint8_t*>(dg);
+        p.A[1] = reinterpret_cast<const uint8_t*>(du);
+        p.B[0] = p.B[1] = static_cast<const uint8_t*>(a->x);
+        p.C[0] = static_cast<uint16_t*>(a->dgate);
+        p.C[1] = static_cast<uint16_t*>(a->dup);
+        p.lda[0] = p.lda[1] = l.ld * 2;
+        p.ldb[0] = p.ldb[1] = a->ldx * 2;
+        p.ldc[0] = a->lddgate;
+        p.ldc[1] = a->lddup;
+        p.batch = 2;
+        rc = launch_split<Elt, true, true>(p, ws, l.bytes - l.at, stream);
+    }
+    return rc;
+}
+
+}  // namespace
+}  // namespace sdt
+
+using sdt::BF16;
+using sdt::F16;
+
+extern "C" {
+
+int fp8_quantize_f16(int64_t rows, int64_t K, const void* X, int64_t ldx, void* Q, int64_t ldq, float* S,
+                     int64_t lds, int block, void* stream) {
+    return sdt::quantize8<F16>(rows, K, X, ldx, Q, ldq, S, lds, block, stream);
+}
+int fp8_quantize_bf16(int64_t rows, int64_t K, const void* X, int64_t ldx, void* Q, int64_t ldq, float* S,
+                      int64_t lds, int block, void* stream) {
+    return sdt::quantize8<BF16>(rows, K, X, ldx, Q, ldq, S, lds, block, stream);
+}
+int fp8_dequantize_f16(int64_t rows, int64_t K, const void* Q, int64_t ldq, const float* S, int64_t lds,
+                       int block, void* Y, int64_t ldy, void* stream) {
+    return sdt::dequantize8<F16>(rows, K, Q, ldq, S, lds, block, Y, ldy, stream);
+}
+int fp8_dequantize_bf16(int64_t rows, int64_t K, const void* Q, int64_t ldq, const float* S, int64_t lds,
+                        int block, void* Y, int64_t ldy, void* stream) {
+    return sdt::dequantize8<BF16>(rows, K, Q, ldq, S, lds, block, Y, ldy, stream);
+}
+int fp8_dequantize_f32(int64_t rows, int64_t K, const void* Q, int64_t ldq, const float* S, int64_t lds,
+                       int block, void* Y, int64_t ldy, void* stream) {
+    return sdt::dequantize8<float>(rows, K, Q, ldq, S, lds, block, Y, ldy, stream);
+}
+int gemm_fp8_f16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* SA, int64_t ldsa,
+                 const void* B, int64_t ldb, const float* SB, int64_t ldsb, void* C, int64_t ldc,
+                 void* stream) {
+    return sdt::gemm8<F16>(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, stream);
+}
+int gemm_fp8_bf16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* SA, int64_t ldsa,
+                  const void* B, int64_t ldb, const float* SB, int64_t ldsb, void* C, int64_t ldc,
+                  void* stream) {
+    return sdt::gemm8<BF16>(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, stream);
+}
+
+int rms_norm_f16(const sdt_norm* args, void* stream) { return sdt::norm<F16>(args, stream); }
+int rms_norm_bf16(const sdt_norm* args, void* stream) { return sdt::norm<BF16>(args, stream); }
+int rms_norm_backward_f16(const sdt_norm_grad* args, void* stream) {
+    return sdt::norm_backward<F16>(args, stream);
+}
+int rms_norm_backward_bf16(const sdt_norm_grad* args, void* stream) {
+    return sdt::norm_backward<BF16>(args, stream);
+}
+int64_t sdt_rms_norm_workspace_size(int64_t rows, int64_t K) {
+    if (rows < 0 || K < 0 || K > sdt::kMaxNorm) return -1;
+    return sdt::norm_parts(rows, K) * K * 4;
+}
+
+int gated_ff_f16(const sdt_gated_ff* args, void* stream) { return sdt::gated<F16>(args, stream); }
+int gated_ff_bf16(const sdt_gated_ff* args, void* stream) { return sdt::gated<BF16>(args, stream); }
+int gated_ff_backward_f16(const sdt_gated_ff_grad* args, void* stream) {
+    return sdt::gated_backward<F16>(args, stream);
+}
+int gated_ff_backward_bf16(const sdt_gated_ff_grad* args, void* stream) {
+    return sdt::gated_backward<BF16>(args, stream);
+}
+int64_t sdt_gated_ff_workspace_size(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0 || M > sdt::kMaxRows || N > sdt::kMaxRows || K > sdt::kMaxRows) return -1;
+    return sdt::gated_layout(M, N, K).bytes;
+}
+
+int gemm_f16_nn(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B, int64_t ldb,
+                void* C, int64_t ldc, void* workspace, int64_t workspace_bytes, void* stream) {
+    return sdt::gemm_turned<F16, false>(M, N, K, A, lda, B, ldb, C, ldc, workspace, workspace_bytes, stream);
+}
+int gemm_bf16_nn(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B, int64_t ldb,
+                 void* C, int64_t ldc, void* workspace, int64_t workspace_bytes, void* stream) {
+    return sdt::gemm_turned<BF16, false>(M, N, K, A, lda, B, ldb, C, ldc, workspace, workspace_bytes, stream);
+}
+int gemm_f16_tn(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B, int64_t ldb,
+                void* C, int64_t ldc, void* workspace, int64_t workspace_bytes, void* stream) {
+    return sdt::gemm_turned<F16, true>(M, N, K, A, lda, B, ldb, C, ldc, workspace, workspace_bytes, stream);
+}
+int gemm_bf16_tn(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B, int64_t ldb,
+                 void* C, int64_t ldc, void* workspace, int64_t workspace_bytes, void* stream) {
+    return sdt::gemm_turned<BF16, true>(M, N, K, A, lda, B, ldb, C, ldc, workspace, workspace_bytes, stream);
+}
+int64_t sdt_gemm_turned_workspace_size(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0 || M > sdt::kMaxRows || N > sdt::kMaxRows || K > sdt::kMaxRows) return -1;
+    return sdt::plan_split(M, N, sdt::ceil_div(K, 64), 1).bytes;
+}
+
+}  // extern "C"

@@ -15,15 +15,10 @@
 // is masked in it.
 #pragma once
 
-#include "gemm_kernel.hpp"
+#include "lanes.hpp"
 #include "moe_kernel.hpp"
 
 namespace sdt {
-
-typedef int int8v_t __attribute__((ext_vector_type(8)));
-typedef int int2_t __attribute__((ext_vector_type(2)));
-typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
-typedef float floatx2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kMx4Tile = 512;      // bytes of a scale tile: 64 rows x 8 blocks
 
@@ -105,28 +100,6 @@ struct Mx4Quant {
     int nxcd;              // 1: tiles in launch order
 };
 
-// Sixteen-byte accesses at any alignment of the element: the memory system takes
-// them, and a row that starts off 16 bytes costs no more than the lines it
-// straddles.
-typedef uint4_t __attribute__((aligned(2))) uint4_any_t;
-
-// Eight elements from x, of which `valid` lie below K: none past K is read.
-template <bool ONCE = false>
-__device__ __forceinline__ uint4_t mx4_load8(const uint16_t* x, int valid) {
-    if (valid >= 8) {
-        if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const uint4_any_t*>(x));
-        return *reinterpret_cast<const uint4_any_t*>(x);
-    }
-    uint4_t v = {0, 0, 0, 0};
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        const uint32_t lo = 2 * d < valid ? x[2 * d] : 0u;
-        const uint32_t hi = 2 * d + 1 < valid ? x[2 * d + 1] : 0u;
-        v[d] = lo | (hi << 16);
-    }
-    return v;
-}
-
 // The largest magnitude of packed elements, as a 16-bit pattern without its
 // sign: the patterns' order is the magnitudes' (an infinity or a NaN lies at or
 // above the infinity's).
@@ -189,7 +162,7 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(Mx4Quant p) {
         }
         have[i] = ok;
         v[i] = uint4_t{0, 0, 0, 0};
-        if (ok) v[i] = mx4_load8<LARGE>(p.X + src * p.ldx + k, valid);
+        if (ok) v[i] = load8<LARGE>(p.X + src * p.ldx + k, valid);
     }
     if (t < kMx4Tile / 4) reinterpret_cast<uint32_t*>(sm)[t] = 0;
     __syncthreads();
@@ -242,7 +215,7 @@ __device__ __forceinline__ void mx4_quantize_token_tile(const Mx4QuantTokens& p,
     for (int i = 0; i < 2; ++i) {
         const int64_t row = first + (t >> 5) + 8 * i;
         v[i] = uint4_t{0, 0, 0, 0};
-        if (row < p.tokens) v[i] = mx4_load8(p.X + row * p.ldx + k, valid);
+        if (row < p.tokens) v[i] = load8(p.X + row * p.ldx + k, valid);
     }
     const int slots = (int)min((int64_t)16, p.tokens - first) * p.topk;
     prepare(slots);
@@ -490,12 +463,6 @@ struct Mx4Gemm {
     int nkto;
 };
 
-// A value that no work of this kernel writes, from a uniform address, by a scalar load.
-__device__ __forceinline__ int uniform_load(const int32_t* p) {
-    return *reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(
-        reinterpret_cast<uint64_t>(p));
-}
-
 // LDS place of a row's 16-byte chunks: chunk c (block c of the k-tile) of row r is
 // kept at c ^ mx4_swz(r).  A fragment read of half s takes chunk 2 g + s in quarter
 // g; its bank pattern is that of the 16-bit kernels (chunk 4 s + g at 4 s + g ^
@@ -522,27 +489,6 @@ __device__ __forceinline__ floatx4_t mx4_mfma_part(int4_t b, int4_t a, floatx4_t
     return mx4_mfma<2 * (PB & 1) + S, 2 * (PA & 1) + S>(b, a, c, sb, sa);
 }
 
-// silu(g) * u = g / (1 + exp(-g)) * u of the gated product, in fp32: 2^t by the
-// hardware instruction (one step off), t = -g log2(e) in two parts so that the
-// rounding of t does not grow with g, and the hardware reciprocal (one step off).
-// Limited to +-88, where 2^t is still finite and 1 / (1 + 2^t) already below the
-// normal numbers.  The library's expf and division took 3 us of a
-// 128 x 64 tile's 11.  The empty asm keeps the product an fp32 value: left to
-// itself the compiler rounds s * u straight to fp16 in some kernels and not in
-// others, and the layer's results would depend on which ran.
-__device__ __forceinline__ float silu_mul(float g, float u) {
-    constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147182f;
-    const float x = -__builtin_amdgcn_fmed3f(g, -88.0f, 88.0f);
-    const float t = x * kLog2e;
-    const float low = __builtin_fmaf(x, kLog2e, -t) + x * kLog2eLow;
-    const float z = __builtin_amdgcn_exp2f(t);
-    const float ez = __builtin_fmaf(z * kLn2, low, z);
-    const float s = g * __builtin_amdgcn_rcpf(1.0f + ez);
-    float r = s * u;
-    asm("" : "+v"(r));
-    return r;
-}
-
 // Expert, first row and rows of 64-row tile `g` of a plan; false where it has none.
 __device__ __forceinline__ bool mx4_group(const Mx4Gemm& p, int g, int& e, int64_t& m0, int& rows) {
     e = uniform_load(p.tiles + g);
@@ -550,13 +496,6 @@ __device__ __forceinline__ bool mx4_group(const Mx4Gemm& p, int g, int& e, int64
     m0 = (int64_t)g * 64;
     rows = min(uniform_load(p.offsets + e) + uniform_load(p.counts + e) - g * 64, 64);
     return rows > 0;
-}
-
-// Two values rounded to the type, packed (one instruction).
-template <typename Elt>
-__device__ __forceinline__ uint32_t mx4_pack2(float a, float b) {
-    const floatx2_t v = {a, b};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, typename Elt::vec2));
 }
 
 // The few-row product: BN columns of C (gated: of each matrix) and up to 64 rows
@@ -751,8 +690,8 @@ __device__ __forceinline__ void mx4_skinny_body(const Mx4Gemm& p, char* smem, in
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const floatx4_t s = output(i, j);
-                w[2 * i] = mx4_pack2<Elt>(s[0], s[1]);
-                w[2 * i + 1] = mx4_pack2<Elt>(s[2], s[3]);
+                w[2 * i] = pack2<Elt>(s[0], s[1]);
+                w[2 * i + 1] = pack2<Elt>(s[2], s[3]);
             }
             uint32_t top = mx4_top(w[0], w[1], w[2], w[3]);
             top = max(top, (uint32_t)__shfl_xor((int)top, 16));
@@ -780,7 +719,7 @@ __device__ __forceinline__ void mx4_skinny_body(const Mx4Gemm& p, char* smem, in
             uint16_t* c = p.C + (m0 + m) * p.ldc + c0;
             if (c0 + 3 < p.N) {
                 *reinterpret_cast<uint2_t*>(c) =
-                    uint2_t{mx4_pack2<Elt>(s[0], s[1]), mx4_pack2<Elt>(s[2], s[3])};
+                    uint2_t{pack2<Elt>(s[0], s[1]), pack2<Elt>(s[2], s[3])};
             } else {
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
@@ -813,65 +752,6 @@ __global__ __launch_bounds__(NW * 64) void mx4_skinny_kernel(Mx4Gemm p) {
         mx4_skinny_body<Elt, GROUPED, GATED, QOUT, NW, 4>(p, lds, e, m0, n0, rows);
 }
 
-// ---- epilogues in registers ------------------------------------------------------------
-// Lane l holds, of the 16 x 16 part (i, j) of a wave's outputs, row l % 16 and
-// columns 4 (l / 16) .. + 3.  Lanes of different quarters swap registers
-// (v_permlane16_swap: rows 1, 3 of the first operand against rows 0, 2 of the
-// second; v_permlane32_swap: its upper half against the lower) until each holds
-// 16 bytes of one row, so that no LDS is needed beside the stages in flight.
-
-__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
-    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-    a = r[0];
-    b = r[1];
-}
-__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
-    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-    a = r[0];
-    b = r[1];
-}
-
-// A wave's FN x FM parts, `left` rows from mb, columns nb .. (of N): 16-byte
-// stores, 64 bytes of 16 rows at a time.  Whole in columns they go through a
-// descriptor that drops the rows past the last.
-template <typename Elt, int FN, int FM>
-__device__ __forceinline__ void mx4_store(uint16_t* C, int64_t ldc, const floatx4_t (&acc)[FN][FM],
-                                          uint32_t mb, int left, uint32_t nb, int N, int lane) {
-    const int fr = lane & 15, fq = lane >> 4;
-    if (left <= 0) return;
-    const int rows = min(left, FM * 16);
-    const int columns = N - (int)nb;              // to the right of nb (none where nb is past N)
-    const bool whole = columns >= FN * 16 && ldc < (1 << 24);
-    C += (int64_t)mb * ldc + nb;
-    const __amdgpu_buffer_rsrc_t r = make_rsrc(C, (uint32_t)((rows - 1) * ldc + FN * 16) * 2);
-    const int n = (fq & 1) * 16 + (fq >> 1) * 8;
-    const uint32_t off = (uint32_t)(fr * (int)ldc + n) * 2;
-#pragma unroll
-    for (int j = 0; j < FM; ++j) {
-#pragma unroll
-        for (int i = 0; i < FN; i += 2) {
-            uint32_t a0 = mx4_pack2<Elt>(acc[i][j][0], acc[i][j][1]);
-            uint32_t a1 = mx4_pack2<Elt>(acc[i][j][2], acc[i][j][3]);
-            uint32_t b0 = mx4_pack2<Elt>(acc[i + 1][j][0], acc[i + 1][j][1]);
-            uint32_t b1 = mx4_pack2<Elt>(acc[i + 1][j][2], acc[i + 1][j][3]);
-            swap16(a0, b0);                           // quarters 0, 2: part i; 1, 3: part i + 1
-            swap16(a1, b1);
-            const uint4_t v = {a0, a1, b0, b1};
-            if (whole) {
-                __builtin_amdgcn_raw_buffer_store_b128(v, r, off + (uint32_t)(j * 32 * (int)ldc) + i * 32,
-                                                       0, 0);
-            } else if (j * 16 + fr < rows) {
-                uint16_t* c = C + (j * 16 + fr) * ldc + n + i * 16;
-#pragma unroll
-                for (int d = 0; d < 8; ++d) {
-                    const uint32_t w = v[d >> 1];
-                    if (i * 16 + n + d < columns) c[d] = (uint16_t)(w >> (16 * (d & 1)));
-                }
-            }
-        }
-    }
-}
-
 // A wave's 32 columns of the gated product (block n0 / 32 + wave_n) rounded to the
 // type, quantised and stored: what mx4_quantize makes of it, without its way
 // through memory.  `rows`: rows of the tile that exist.
@@ -890,7 +770,7 @@ __device__ __forceinline__ void mx4_store_quantized(const Mx4Gemm& p, const floa
         uint32_t w[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            w[c] = mx4_pack2<Elt>(out[c >> 1][j][2 * (c & 1)], out[c >> 1][j][2 * (c & 1) + 1]);
+            w[c] = pack2<Elt>(out[c >> 1][j][2 * (c & 1)], out[c >> 1][j][2 * (c & 1) + 1]);
         uint32_t top = mx4_top(w[0], w[1], w[2], w[3]);
         top = max(top, (uint32_t)__shfl_xor((int)top, 16));
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
@@ -1243,10 +1123,10 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_gemm_kernel(Mx4Gemm p) {
             if constexpr (QOUT)
                 mx4_store_quantized<Elt, FM>(p, out, at.m0, at.n0, at.rows, wave_m, wave_n, lane);
             else
-                mx4_store<Elt, FN / 2, FM>(p.C, p.ldc, out, mb, left, at.n0 + wave_n * (WTN / 2), p.N,
+                store_parts<Elt, FN / 2, FM>(p.C, p.ldc, out, mb, left, at.n0 + wave_n * (WTN / 2), p.N,
                                            lane);
         } else {
-            mx4_store<Elt, FN, FM>(p.C, p.ldc, acc, mb, left, at.n0 + wave_n * WTN, p.N, lane);
+            store_parts<Elt, FN, FM>(p.C, p.ldc, acc, mb, left, at.n0 + wave_n * WTN, p.N, lane);
         }
     };
 
@@ -1371,7 +1251,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_gemv_kernel(Mx4Gemv p) {
         for (int j = 0; j < min(n, NS); ++j) load(k0 + wave + j * NW, j);
         if (k0 > 0) __syncthreads();                    // xs has been read
         for (int i = t; i < n1 * 32; i += NW * 64)
-            xs[i] = mx4_load8(p.x + (int64_t)k0 * 256 + i * 8, p.K - k0 * 256 - i * 8);
+            xs[i] = load8(p.x + (int64_t)k0 * 256 + i * 8, p.K - k0 * 256 - i * 8);
         wait_lds();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");

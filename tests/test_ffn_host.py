@@ -1,0 +1,193 @@
+"""Refusals and sizes of the 8-bit, norm, gated feed-forward and turned-product entry
+points, on the host: every call here is refused (or has nothing to do) before
+anything is enqueued."""
+import ctypes
+
+import pytest
+
+from shape_driven_tile_amd import binding as sdt
+
+OK, INVALID, UNSUPPORTED = sdt.SDT_OK, sdt.SDT_ERR_INVALID_ARG, sdt.SDT_ERR_UNSUPPORTED
+P = 0x10000          # an address that is never read
+
+
+def call(name, *args):
+    return int(getattr(sdt.lib(), name)(*args))
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("change, want", [
+    ({}, None), ({"rows": -1}, INVALID), ({"K": -1}, INVALID), ({"ldx": 199}, INVALID),
+    ({"X": None}, INVALID), ({"Q": None}, INVALID), ({"S": None}, INVALID), ({"block": 64}, INVALID),
+    ({"ldq": 192}, INVALID), ({"ldq": 200}, UNSUPPORTED), ({"lds": 9}, INVALID),
+    ({"block": 128, "lds": 1}, INVALID), ({"X": P + 1}, UNSUPPORTED), ({"Q": P + 8}, UNSUPPORTED),
+    ({"S": P + 2}, UNSUPPORTED), ({"ldq": 1 << 23}, UNSUPPORTED),
+    ({"K": 1 << 24, "ldx": 1 << 24, "ldq": 1 << 24}, UNSUPPORTED), ({"lds": 1 << 31}, UNSUPPORTED),
+    ({"rows": 0}, OK), ({"K": 0}, OK), ({"rows": 0, "block": 3}, INVALID),
+])
+def test_quantize_refusals(t, change, want):
+    a = dict(rows=10, K=200, X=P, ldx=200, Q=P, ldq=208, S=P, lds=10, block=1)
+    a.update(change)
+    if want is None:
+        return            # the base case would launch: the GPU tests run it
+    assert call(f"fp8_quantize_{t}", *a.values(), None) == want
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("change, want", [
+    ({"rows": -1}, INVALID), ({"ldy": 199}, INVALID), ({"Y": None}, INVALID), ({"S": None}, INVALID),
+    ({"Y": P + 1}, UNSUPPORTED), ({"ldq": 207}, UNSUPPORTED), ({"rows": 0}, OK), ({"K": 0}, OK),
+])
+def test_dequantize_refusals(t, change, want):
+    a = dict(rows=10, K=200, Q=P, ldq=208, S=P, lds=10, block=1, Y=P, ldy=200)
+    a.update(change)
+    assert call(f"fp8_dequantize_{t}", *a.values(), None) == want
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("change, want", [
+    ({"M": -1}, INVALID), ({"K": -1}, INVALID), ({"C": None}, INVALID), ({"ldc": 299}, INVALID),
+    ({"ldc": 300}, UNSUPPORTED), ({"C": P + 8}, UNSUPPORTED), ({"A": None}, INVALID),
+    ({"lda": 192}, INVALID), ({"lda": 200}, UNSUPPORTED), ({"ldsa": 9}, INVALID), ({"ldsb": 1}, INVALID),
+    ({"B": P + 4}, UNSUPPORTED), ({"SB": P + 1}, UNSUPPORTED), ({"M": 0}, OK), ({"N": 0}, OK),
+    ({"M": 2 ** 31 - 200, "ldsa": 2 ** 31 - 1}, UNSUPPORTED),
+])
+def test_gemm_refusals(t, change, want):
+    a = dict(M=10, N=300, K=200, A=P, lda=208, SA=P, ldsa=10, B=P, ldb=208, SB=P, ldsb=2, C=P, ldc=304)
+    a.update(change)
+    assert call(f"gemm_fp8_{t}", *a.values(), None) == want
+
+
+def _struct(kind, base, change):
+    a = dict(base)
+    a.update(change)
+    return ctypes.byref(kind(**a))
+
+
+NORM = dict(rows=4, K=100, x=P, ldx=100, residual=P, ldr=100, weight=P, eps=1e-6, total=P, ldt=100, y=P,
+            ldy=100, q=P, ldq=112, s=P, lds=4, rstd=P)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("change, want", [
+    ({"rows": -1}, INVALID), ({"K": -1}, INVALID), ({"x": None}, INVALID), ({"ldx": 99}, INVALID),
+    ({"ldr": 99}, INVALID), ({"ldt": 99}, INVALID), ({"ldy": 99}, INVALID), ({"ldq": 96}, INVALID),
+    ({"s": None}, INVALID), ({"lds": 3}, INVALID), ({"eps": float("nan")}, INVALID),
+    ({"eps": -1.0}, INVALID), ({"total": None, "y": None, "q": None, "rstd": None}, INVALID),
+    ({"x": P + 1}, UNSUPPORTED), ({"weight": P + 1}, UNSUPPORTED), ({"rstd": P + 2}, UNSUPPORTED),
+    ({"q": P + 8}, UNSUPPORTED), ({"ldq": 104}, UNSUPPORTED), ({"rows": 0}, OK), ({"K": 0}, OK),
+    ({"K": 32769, **{k: 1 << 20 for k in ("ldx", "ldr", "ldt", "ldy", "ldq")}}, UNSUPPORTED),
+])
+def test_norm_refusals(t, change, want):
+    assert call(f"rms_norm_{t}", _struct(sdt.SdtNorm, NORM, change), None) == want
+
+
+def test_null_structs():
+    for name in ("rms_norm_f16", "rms_norm_backward_bf16", "gated_ff_f16", "gated_ff_backward_bf16"):
+        assert call(name, None, None) == INVALID
+
+
+NORM_GRAD = dict(rows=4, K=100, total=P, ldt=100, weight=P, rstd=P, dy=P, lddy=100, dtotal=P, lddt=100,
+                 dx=P, lddx=100, dweight=P, workspace=P, workspace_bytes=1600)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("change, want", [
+    ({"rows": -1}, INVALID), ({"total": None}, INVALID), ({"rstd": None}, INVALID), ({"dy": None}, INVALID),
+    ({"dx": None}, INVALID), ({"lddx": 99}, INVALID), ({"lddt": 99}, INVALID),
+    ({"workspace": None}, INVALID), ({"workspace_bytes": 399}, INVALID), ({"workspace": P + 8}, UNSUPPORTED),
+    ({"dweight": P + 2}, UNSUPPORTED), ({"dy": P + 1}, UNSUPPORTED), ({"K": 0}, OK),
+    ({"rows": 0, "dweight": None}, OK),
+])
+def test_norm_backward_refusals(t, change, want):
+    assert call(f"rms_norm_backward_{t}", _struct(sdt.SdtNormGrad, NORM_GRAD, change), None) == want
+
+
+GATED = dict(M=10, N=300, K=200, x=P, ldx=200, gate=P, ldgate=200, up=P, ldup=208, act=0, h=P, ldh=304,
+             g=P, ldg=300, u=P, ldu=300, wide=1)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("change, want", [
+    ({"M": -1}, INVALID), ({"act": 2}, INVALID), ({"act": -1}, INVALID), ({"x": None}, INVALID),
+    ({"up": None}, INVALID), ({"h": None}, INVALID), ({"ldx": 199}, INVALID), ({"ldup": 204}, UNSUPPORTED),
+    ({"ldh": 300}, UNSUPPORTED), ({"h": P + 2}, UNSUPPORTED), ({"gate": P + 8}, UNSUPPORTED),
+    ({"g": None}, INVALID), ({"ldu": 299}, INVALID), ({"wide": 2}, INVALID), ({"ldg": 301}, UNSUPPORTED),
+    ({"wide": 0}, UNSUPPORTED), ({"ldgate": 1 << 22}, UNSUPPORTED), ({"M": 0}, OK), ({"N": 0}, OK),
+])
+def test_gated_refusals(t, change, want):
+    assert call(f"gated_ff_{t}", _struct(sdt.SdtGatedFf, GATED, change), None) == want
+
+
+GATED_GRAD = dict(M=10, N=300, K=200, x=P, ldx=200, gate=P, ldgate=200, up=P, ldup=208, act=0, g=P, ldg=300,
+                  u=P, ldu=300, wide=1, dh=P, lddh=300, dx=P, lddx=200, dgate=P, lddgate=200, dup=P,
+                  lddup=200, workspace=P, workspace_bytes=1 << 30)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("change, want", [
+    ({"N": -1}, INVALID), ({"act": 2}, INVALID), ({"dgate": None}, INVALID),
+    ({"dx": None, "dgate": None, "dup": None}, INVALID), ({"g": None}, INVALID), ({"dh": None}, INVALID),
+    ({"lddh": 299}, INVALID), ({"lddx": 196}, INVALID), ({"lddup": 204}, UNSUPPORTED),
+    ({"workspace": None}, INVALID), ({"workspace_bytes": 100}, INVALID), ({"workspace": P + 4}, UNSUPPORTED),
+    ({"gate": P + 8}, UNSUPPORTED), ({"dh": P + 1}, UNSUPPORTED), ({"K": 0}, OK), ({"M": 0, "N": 0}, OK),
+])
+def test_gated_backward_refusals(t, change, want):
+    assert call(f"gated_ff_backward_{t}", _struct(sdt.SdtGatedFfGrad, GATED_GRAD, change), None) == want
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("layout, change, want", [
+    ("nn", {"M": -1}, INVALID), ("tn", {"K": -1}, INVALID), ("nn", {"lda": 40}, INVALID),
+    ("tn", {"lda": 32}, INVALID), ("nn", {"ldb": 56}, INVALID), ("nn", {"lda": 52}, UNSUPPORTED),
+    ("tn", {"ldb": 1 << 22}, UNSUPPORTED), ("nn", {"A": P + 8}, UNSUPPORTED), ("tn", {"C": None}, INVALID),
+    ("tn", {"B": None}, INVALID), ("nn", {"ws": None, "bytes": 4}, INVALID), ("nn", {"bytes": -1}, INVALID),
+    ("nn", {"ws": P + 4}, UNSUPPORTED), ("nn", {"M": 0}, OK), ("tn", {"N": 0}, OK),
+])
+def test_turned_refusals(t, layout, change, want):
+    a = dict(M=40, N=60, K=50, A=P, lda=56, B=P, ldb=64, C=P, ldc=64, ws=P, bytes=1 << 20)
+    a.update(change)
+    assert call(f"gemm_{t}_{layout}", *a.values(), None) == want
+
+
+def test_workspace_sizes():
+    assert sdt.rms_norm_workspace_size(0, 4096) == 0
+    assert sdt.rms_norm_workspace_size(1, 4096) == 4096 * 4
+    assert sdt.rms_norm_workspace_size(10 ** 6, 4096) == sdt.rms_norm_workspace_size(10 ** 5, 4096)
+    for bad in ((-1, 8), (8, -1), (8, 32769)):
+        with pytest.raises(sdt.SdtError):
+            sdt.rms_norm_workspace_size(*bad)
+    # both factors' gradients, in 16 bits, are held at least
+    assert sdt.gated_ff_workspace_size(100, 300, 200) >= 100 * 2 * 304 * 2
+    assert sdt.gated_ff_workspace_size(0, 300, 200) >= 0
+    with pytest.raises(sdt.SdtError):
+        sdt.gated_ff_workspace_size(1, -1, 1)
+    assert sdt.gemm_turned_workspace_size(8192, 8192, 8192) == 0        # tiles enough
+    assert sdt.gemm_turned_workspace_size(64, 64, 8192) > 0             # one tile, long
+    assert sdt.gemm_turned_workspace_size(64, 64, 100) == 0             # and short
+    with pytest.raises(sdt.SdtError):
+        sdt.gemm_turned_workspace_size(1, 1, -1)
+
+
+def test_host_tensors_are_refused():
+    """No address of the host's goes to the device."""
+    import torch
+    x, v = torch.zeros(4, 128, dtype=torch.float16), torch.zeros(128, dtype=torch.float16)
+    with pytest.raises(TypeError):
+        sdt.rms_norm(x, v, y=x)
+    with pytest.raises(TypeError):
+        sdt.gated_ff(x, x, x, torch.zeros(4, 4, dtype=torch.float16))
+    with pytest.raises(TypeError):
+        sdt.gemm_f16_nn(x, torch.zeros(128, 4, dtype=torch.float16), torch.zeros(4, 4, dtype=torch.float16))
+    with pytest.raises(TypeError):
+        sdt.Fp8(torch.zeros(4, 128, dtype=torch.float8_e4m3fn), torch.ones(1, 4))
+    with pytest.raises(TypeError):
+        sdt.Fp8(torch.zeros(4, 128), torch.ones(1, 4))
+    with pytest.raises(ValueError):
+        sdt.Fp8.empty(4, 128, block=64, device="cpu")
+    with pytest.raises(TypeError):
+        sdt.fp8_quantize_f16(x, sdt.Fp8.empty(4, 128, device="cpu"))
+    with pytest.raises(TypeError):
+        sdt.rms_norm(x.float(), v, y=x)
+    with pytest.raises(TypeError):
+        sdt.rms_norm_backward(x, v, torch.zeros(4), x, x)

@@ -1,0 +1,747 @@
+"""8-bit matrices and products, the norm, the gated block and turned products on the
+GPU against their 64-bit definitions.  Codes, scales and values are compared bit for
+bit.  Other bounds count roundings: an fp32 sum of n terms is off by at most n steps
+of 2^-24 of the sum of magnitudes, a result of its type by half a step of it
+(finfo.eps / 2), the activations (two hardware functions, each one step off, in a
+handful of operations) by 16 steps of 2^-24 of the value.  Products of small whole
+numbers are exact before the last rounding and compared bit for bit."""
+import numpy as np
+import pytest
+
+import ffn_reference as ref
+from gpu_helpers import DEV, say
+
+pytestmark = pytest.mark.gpu
+
+TYPES = ["f16", "bf16"]
+U = 2.0 ** -24
+
+
+def _t(name):
+    import torch
+    return {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}[name]
+
+
+def _sdt():
+    from shape_driven_tile_amd import binding
+    return binding
+
+
+def rows_of(t, pad=0, align=8):
+    """A device copy of t [rows, K] whose rows are a multiple of `align` elements apart,
+    `pad` more than they need, NaN between them; and the whole buffer."""
+    import torch
+    rows, K = t.shape
+    full = torch.full((rows, -(-(K + pad) // align) * align), float("nan"), dtype=t.dtype, device=DEV)
+    full[:, :K] = t
+    return full[:, :K], full
+
+
+def out_like(rows, K, dtype, pad=0, align=8):
+    import torch
+    return rows_of(torch.full((rows, K), float("nan"), dtype=dtype), pad, align)
+
+
+def half(dtype):
+    import torch
+    return torch.finfo(dtype).eps / 2
+
+
+def tiny(dtype):
+    """Half a step among the smallest values."""
+    import torch
+    return 2.0 ** -25 if dtype is torch.float16 else 2.0 ** -134
+
+
+def check(got, want, bound, what):
+    """|got - want| <= bound + half a step of got's type, everywhere; what lies past the
+    type's largest value by half a step and more rounds to infinity, by its definition."""
+    import torch
+    g = got.double()
+    lim = bound + half(got.dtype) * (want.abs() + bound) + tiny(got.dtype) if \
+        got.dtype is not torch.float32 else bound + U * want.abs() + 2.0 ** -149
+    bad = ~((g - want).abs() <= lim)
+    top = torch.finfo(got.dtype).max * (1 + half(got.dtype) / 2)     # max + half its step
+    beyond = want.abs() - bound >= top
+    bad = torch.where(beyond, g != torch.sign(want) * float("inf"),
+                      bad & ~((want.abs() + bound >= top) & (g == torch.sign(want) * float("inf"))))
+    if bool(bad.any()):
+        at = bad.nonzero()[0].tolist()
+        i = tuple(at)
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {at}: {g[i].item()} for "
+                             f"{want[i].item()}, limit {lim[i].item()}")
+
+
+def untouched(full, K):
+    import torch
+    return bool(torch.isnan(full[:, K:].float()).all())
+
+
+def gen(seed):
+    import torch
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def normal(shape, dtype, seed, std=1.0):
+    import torch
+    return (torch.randn(shape, device=DEV, generator=gen(seed)) * std).to(dtype)
+
+
+def whole(shape, dtype, seed, most=3):
+    """Whole numbers in [-most, most]."""
+    import torch
+    return torch.randint(-most, most + 1, shape, device=DEV, generator=gen(seed)).to(dtype)
+
+
+# ---- 8-bit matrices ----------------------------------------------------------------
+
+
+def values_to_quantize(rows, K, dtype, seed):
+    """Rows with ties, wide ranges, zero blocks, and blocks at both ends of the type."""
+    x = normal((rows, K), dtype, seed)
+    x[:, ::7] *= 12
+    flat = x.view(-1)
+    flat[::97] = 0
+    if K > 128:
+        x[0, :128] = 0
+        x[-1, 128:] *= 2.0 ** (-14 if dtype == _t("f16") else -120)
+    return x
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("rows, K, pad", [(1, 1, 0), (1, 128, 0), (3, 129, 0), (5, 1000, 8), (130, 2050, 3),
+                                          (129, 4100, 0), (700, 300, 0)])
+def test_quantize(dtype, block, rows, K, pad):
+    import torch
+    say(f"quantize {dtype} block {block} {rows}x{K}+{pad}")
+    sdt, t = _sdt(), _t(dtype)
+    x, _ = rows_of(values_to_quantize(rows, K, t, 1), pad, align=1)       # any alignment
+    m = sdt.Fp8.empty(rows, K, block=block, device=DEV)
+    full = m.q if m.q.shape[1] == m.q.stride(0) else m.q.as_strided((rows, m.q.stride(0)), m.q.stride())
+    full.view(torch.uint8).fill_(0x55)
+    m.s.fill_(-1)
+    getattr(sdt, f"fp8_quantize_{dtype}")(x, m)
+    codes, scales = ref.quantize(x.double().cpu().numpy(), block)
+    assert np.array_equal(m.s.cpu().numpy(), scales)
+    assert np.array_equal(m.q.float().cpu().numpy(), codes.astype(np.float32))
+    if full.shape[1] > K:
+        assert bool((full.view(torch.uint8)[:, K:] == 0x55).all())        # bytes past K
+    want = codes.astype(np.float32) * ref.scale_map(scales, block, rows, K)
+    for out in ("f32", "f16", "bf16"):
+        y, rest = out_like(rows, K, _t(out), pad, align=1)
+        getattr(sdt, f"fp8_dequantize_{out}")(m, y)
+        assert torch.equal(y, torch.from_numpy(want).to(DEV).to(_t(out))), out
+        assert untouched(rest, K)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_quantize_every_value(dtype):
+    """Every finite value of the type, in blocks of random company."""
+    import torch
+    sdt, t = _sdt(), _t(dtype)
+    every = torch.from_numpy(np.random.default_rng(2).permutation(65536).astype(np.uint16).view(np.int16))
+    x = every.to(DEV).view(t)
+    x = x[torch.isfinite(x.float())]
+    x = x[:len(x) // 512 * 512].view(-1, 512).contiguous()
+    order = torch.sort(x.float().abs().flatten()).indices
+    for case in (x, x.flatten()[order].view(-1, 512).contiguous()):       # of like magnitude too
+        m = sdt.Fp8.empty(case.shape[0], 512, device=DEV)
+        getattr(sdt, f"fp8_quantize_{dtype}")(case, m)
+        codes, scales = ref.quantize(case.double().cpu().numpy(), 1)
+        assert np.array_equal(m.s.cpu().numpy(), scales)
+        assert np.array_equal(m.q.float().cpu().numpy(), codes.astype(np.float32))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_quantize_not_finite(dtype, block, value):
+    """Only the block that holds the value is lost."""
+    import torch
+    sdt, t = _sdt(), _t(dtype)
+    x = normal((200, 300), t, 3)
+    x[150, 140] = value
+    m = sdt.Fp8.empty(200, 300, block=block, device=DEV)
+    getattr(sdt, f"fp8_quantize_{dtype}")(x, m)
+    codes, scales = ref.quantize(x.double().cpu().numpy(), block)
+    assert int(np.isnan(scales).sum()) == 1
+    assert np.array_equal(m.s.cpu().numpy(), scales, equal_nan=True)
+    assert np.array_equal(m.q.float().cpu().numpy(), codes.astype(np.float32))
+    y = torch.empty_like(x)
+    getattr(sdt, f"fp8_dequantize_{dtype}")(m, y)
+    assert int(torch.isnan(y).sum()) == (128 if block == 1 else 72 * 128)
+
+
+def test_no_rows():
+    import torch
+    sdt = _sdt()
+    for rows, K in ((0, 256), (4, 0)):
+        m = sdt.Fp8.empty(rows, K, device=DEV)
+        x = torch.empty(rows, K, dtype=torch.float16, device=DEV)
+        sdt.fp8_quantize_f16(x, m)
+        sdt.fp8_dequantize_f16(m, x)
+        sdt.rms_norm(x, torch.ones(K, dtype=torch.float16, device=DEV), y=x)
+
+
+# ---- 8-bit products --------------------------------------------------------------------
+
+
+def fp8_matrix(rows, K, block, seed, plain=False):
+    """A random 8-bit matrix (rows 16 bytes and more apart, NaN codes between them) and
+    its values; plain: whole numbers, scales of powers of two."""
+    import torch
+    sdt = _sdt()
+    g = gen(seed)
+    ld = -(-K // 16) * 16 + 16
+    full = torch.full((rows, ld), 0x7F, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    if plain:
+        v = torch.randint(-3, 4, (rows, K), device=DEV, generator=g).float()
+    else:
+        v = torch.randn(rows, K, device=DEV, generator=g) * 60
+    full[:, :K] = v.clamp(-448, 448).to(torch.float8_e4m3fn)
+    kb = -(-K // 128)
+    shape = (kb, rows) if block == 1 else (-(-rows // 128), kb)
+    wide = torch.full((shape[0], shape[1] + 3), float("nan"), device=DEV)  # scales' own stride
+    s = wide[:, :shape[1]]
+    e = torch.randint(-1, 2, shape, device=DEV, generator=g).float()
+    s.copy_(torch.exp2(e) * (1.0 if plain else 0.75 + 0.5 * torch.rand(shape, device=DEV, generator=g)))
+    m = sdt.Fp8(full[:, :K], s, block=block)
+    scale = torch.from_numpy(ref.scale_map(s.cpu().numpy(), block, rows, K)).to(DEV)
+    return m, m.q.double() * scale.double()
+
+
+def mfma_bound(a, b):
+    """What the 8-bit MFMAs drop: of the eight products of consecutive k the bits below
+    2^-13 of the largest (each product cut towards zero where it passes the alignment to
+    the largest one's exponents), so less than 8 * 2^-13 max |a b| <= 2^-10 max |a| max |b|
+    for each eight."""
+    import torch
+
+    def tops(v):
+        n = -(-v.shape[1] // 8)
+        return torch.nn.functional.pad(v.abs(), (0, n * 8 - v.shape[1])).view(v.shape[0], n, 8).amax(dim=2)
+    return 2.0 ** -10 * (tops(a) @ tops(b).t())
+
+
+SIZES = [(1, 1, 1), (1, 300, 200), (2, 64, 128), (16, 130, 1000), (17, 33, 129), (64, 100, 4000), (65, 64, 64),
+         (100, 129, 383), (128, 128, 128), (200, 700, 640), (1000, 257, 100), (2100, 2050, 700)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M, N, K", SIZES)
+@pytest.mark.parametrize("plain", [True, False])
+def test_gemm_fp8(dtype, M, N, K, plain):
+    import torch
+    say(f"gemm_fp8 {dtype} {M}x{N}x{K} plain {plain}")
+    sdt, t = _sdt(), _t(dtype)
+    a, av = fp8_matrix(M, K, 1, 1, plain)
+    b, bv = fp8_matrix(N, K, 128, 2, plain)
+    c, full = out_like(M, N, t, pad=8)
+    getattr(sdt, f"gemm_fp8_{dtype}")(a, b, c)
+    want = av @ bv.t()
+    if plain:
+        # products up to 9 * 4 in quarters: sums below 2^24 quarters are exact in fp32
+        assert torch.equal(c, want.float().to(t))
+    else:
+        check(c, want, (K + 4) * U * (av.abs() @ bv.abs().t()) + mfma_bound(av, bv), "gemm_fp8")
+    assert untouched(full, N)
+
+
+def test_gemm_fp8_all_codes():
+    """Every pair of finite codes in a product of one term, subnormals among them."""
+    import torch
+    sdt = _sdt()
+    every = torch.arange(256, dtype=torch.uint8, device=DEV)
+    every = every[(every & 0x7F) != 0x7F].view(torch.float8_e4m3fn)
+    n = every.numel()
+    for M in (n, 40):
+        q = torch.zeros(n, 128, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+        q[:, 5] = every
+        a = sdt.Fp8(q[:M], torch.full((1, M), 2.0 ** -6, device=DEV))
+        b = sdt.Fp8(q, torch.ones(2, 1, device=DEV), block=128)
+        c = torch.empty(M, 256, dtype=torch.float16, device=DEV)[:, :n]
+        sdt.gemm_fp8_f16(a, b, c)
+        want = (every[:M].float()[:, None] * every.float()[None, :] * 2.0 ** -6).half()
+        assert torch.equal(c, want)
+
+
+@pytest.mark.parametrize("M", [3, 70, 300])
+def test_gemm_fp8_nan_block(M):
+    """A NaN scale of one block of A reaches its row, of B its 128 columns, no other."""
+    import torch
+    sdt = _sdt()
+    a, _ = fp8_matrix(M, 300, 1, 1)
+    b, _ = fp8_matrix(300, 300, 128, 2)
+    a.s[1, 2] = float("nan")
+    b.s[1, 0] = float("nan")
+    c = torch.empty(M, 304, dtype=torch.bfloat16, device=DEV)[:, :300]
+    sdt.gemm_fp8_bf16(a, b, c)
+    nan = torch.isnan(c)
+    assert bool(nan[2].all()) and bool(nan[:, 128:256].all())
+    nan[2] = False
+    nan[:, 128:256] = False
+    assert not bool(nan.any())
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_no_sum(M):
+    """K == 0 is the empty sum."""
+    import torch
+    sdt = _sdt()
+    f = dict(dtype=torch.float16, device=DEV)
+    c = torch.full((M, 64), 5.0, **f)
+    sdt.gemm_fp8_f16(sdt.Fp8.empty(M, 0, device=DEV), sdt.Fp8.empty(64, 0, block=128, device=DEV), c)
+    assert not c.any()
+    for act in ("silu", "gelu"):
+        c.fill_(5.0)
+        g, u = torch.full((M, 64), 5.0, device=DEV), torch.full((M, 64), 5.0, device=DEV)
+        sdt.gated_ff(torch.empty(M, 0, **f), torch.empty(64, 0, **f), torch.empty(64, 0, **f), c, act=act,
+                     g=g, u=u)
+        assert not c.any() and not g.any() and not u.any()
+    c.fill_(5.0)
+    sdt.gemm_f16_nn(torch.empty(M, 0, **f), torch.empty(0, 64, **f), c)
+    assert not c.any()
+    c.fill_(5.0)
+    sdt.gemm_f16_tn(torch.empty(0, M, **f), torch.empty(0, 64, **f), c)
+    assert not c.any()
+
+
+# ---- the norm ----------------------------------------------------------------------------
+
+NORM_SIZES = [(1, 1), (1, 8), (3, 100), (5, 512), (2, 513), (7, 1000), (4, 2048), (3, 4097), (2, 8170), (2, 8200),
+              (3, 16390), (2, 32768), (600, 300), (1100, 700)]
+
+
+def norm_reference(x, r, w, eps):
+    t = x if r is None else (x.double() + r.double()).to(x.dtype)
+    d = t.double()
+    rstd = 1 / (d.square().mean(dim=1) + eps).sqrt()
+    n = d * rstd[:, None]
+    return t, rstd, n, n if w is None else n * w.double()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows, K", NORM_SIZES)
+@pytest.mark.parametrize("residual, weight, pad", [(True, True, 0), (False, True, 3), (True, False, 8)])
+def test_norm(dtype, rows, K, residual, weight, pad):
+    import torch
+    say(f"norm {dtype} {rows}x{K} {residual} {weight} +{pad}")
+    sdt, t = _sdt(), _t(dtype)
+    x, _ = rows_of(normal((rows, K), t, 1), pad, align=1)
+    r = rows_of(normal((rows, K), t, 2, 3.0), pad, align=1)[0] if residual else None
+    w = normal((K,), t, 3) if weight else None
+    eps = 1e-5
+    total, tf = out_like(rows, K, t, pad, align=1)
+    y, yf = out_like(rows, K, t, pad, align=1)
+    rstd = torch.full((rows,), float("nan"), device=DEV)
+    q = sdt.Fp8.empty(rows, K, device=DEV)
+    sdt.rms_norm(x, w, y=y, q=q, residual=r, total=total, rstd=rstd, eps=eps)
+    want_t, want_r, n, want = norm_reference(x, r, w, eps)
+    # t: x + r in fp32, whose own rounding is one half step of 2^-24 before the type's
+    check(total, x.double() + (0 if r is None else r.double()), U * want_t.double().abs(), "total")
+    # what is normed is the t that was written
+    _, want_r, n, want = norm_reference(total, None, w, eps)
+    # the squares' sum: at most 32 + 16 additions a thread and its joins, and three operations
+    rel = (K / 64 + 64) * U
+    check(rstd, want_r, rel * want_r, "rstd")
+    check(y, want, (rel + 4 * U) * want.abs(), "y")
+    assert untouched(tf, K) and untouched(yf, K)
+    # 8 bits: the scale is off as y is, a value by half a step of e4m3 (2^-4; 2^-10
+    # scales where it is subnormal) around what y's error makes of it
+    v = torch.empty(rows, K, device=DEV)
+    sdt.fp8_dequantize_f32(q, v)
+    kb = -(-K // 128)
+    padded = torch.zeros(rows, kb * 128, dtype=torch.float64, device=DEV)
+    padded[:, :K] = want
+    top = padded.view(rows, kb, 128).abs().amax(dim=2)
+    s = q.s.double().t()
+    assert bool(((s - top / 448).abs() <= (rel + 6 * U) * top / 448 + 2.0 ** -126).all())
+    scale = s.repeat_interleave(128, dim=1)[:, :K]
+    off = (rel + 8 * U) * want.abs()
+    lim = off + (2.0 ** -4) * (want.abs() + off) + 2.0 ** -10 * scale
+    assert bool(((v.double() - want).abs() <= lim).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("K", [300, 4096, 9000])
+def test_norm_codes(dtype, K):
+    """8 bits of rows whose norm is exact (rstd a power of two, weights ones): bit for
+    bit the quantisation of the rows."""
+    import torch
+    sdt, t = _sdt(), _t(dtype)
+    sign = torch.where(torch.rand(9, K, device=DEV, generator=gen(4)) < 0.5, -1.0, 1.0)
+    x = (sign * 2.0).to(t)
+    w = normal((K,), t, 5)
+    q, q2 = sdt.Fp8.empty(9, K, device=DEV), sdt.Fp8.empty(9, K, device=DEV)
+    sdt.rms_norm(x, w, q=q, eps=0.0)
+    getattr(sdt, f"fp8_quantize_{dtype}")((sign.to(t) * w), q2)
+    assert torch.equal(q.s, q2.s) and torch.equal(q.q.view(torch.uint8), q2.q.view(torch.uint8))
+
+
+def test_norm_special_rows():
+    """Zero rows have rstd 1 / sqrt(eps); a row with a NaN or an infinity keeps to itself."""
+    import torch
+    sdt = _sdt()
+    x = normal((4, 1000), torch.bfloat16, 1)
+    x[1] = 0
+    x[2, 5] = float("nan")
+    x[3, 7] = float("inf")
+    y, rstd = torch.empty_like(x), torch.empty(4, device=DEV)
+    q = sdt.Fp8.empty(4, 1000, device=DEV)
+    sdt.rms_norm(x, None, y=y, q=q, rstd=rstd, eps=2.0 ** -20)
+    assert not y[1].any() and not q.q[1].float().any() and bool((q.s[:, 1] == 2.0 ** -126).all())
+    assert rstd[1].item() == 1024.0
+    assert bool(torch.isnan(y[2]).all()) and bool(torch.isfinite(y[:2]).all())
+    assert bool(torch.isnan(q.s[:, 2]).all()) and bool(torch.isfinite(q.s[:, :2]).all())
+    assert bool(torch.isnan(y[3, 7])) and not y[3, :7].any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows, K", NORM_SIZES)
+@pytest.mark.parametrize("weight, extra, pad", [(True, True, 0), (False, False, 3)])
+def test_norm_backward(dtype, rows, K, weight, extra, pad):
+    import torch
+    say(f"norm backward {dtype} {rows}x{K} {weight} {extra} +{pad}")
+    sdt, t = _sdt(), _t(dtype)
+    x, _ = rows_of(normal((rows, K), t, 1), pad, align=1)
+    dy, _ = rows_of(normal((rows, K), t, 2), pad, align=1)
+    dt = rows_of(normal((rows, K), t, 3), pad, align=1)[0] if extra else None
+    w = normal((K,), t, 4) if weight else None
+    _, rstd, n, _ = norm_reference(x, None, None, 1e-6)
+    rstd32 = rstd.float()
+    dx, full = out_like(rows, K, t, pad, align=1)
+    dw = torch.full((K,), float("nan"), device=DEV)
+    ws = torch.empty(max(16, sdt.rms_norm_workspace_size(rows, K)), dtype=torch.uint8, device=DEV)
+    sdt.rms_norm_backward(x, w, rstd32, dy, dx, dw, ws, dtotal=dt)
+    n = x.double() * rstd32.double()[:, None]
+    dn = dy.double() * (1 if w is None else w.double())
+    inner = (dn * n).mean(dim=1, keepdim=True)
+    r = rstd32.double()[:, None]
+    want = r * (dn - n * inner) + (0 if dt is None else dt.double())
+    mags = (dn * n).abs().mean(dim=1, keepdim=True)
+    bound = (K / 64 + 64) * U * r * n.abs() * mags + 8 * U * (r * (dn.abs() + n.abs() * inner.abs()) +
+                                                             (0 if dt is None else dt.double().abs()))
+    check(dx, want, bound, "dx")
+    assert untouched(full, K)
+    terms = (dy.double() * n)
+    check(dw, terms.sum(dim=0), (rows + 4) * U * terms.abs().sum(dim=0), "dweight")
+
+
+def test_norm_gradient_by_differences():
+    """The gradients against central differences of the 64-bit norm itself."""
+    import torch
+    sdt = _sdt()
+    rows, K, eps = 3, 40, 1e-3
+    x, dy, w = (normal(s, torch.float16, i) for i, s in enumerate([(rows, K), (rows, K), (K,)]))
+    rstd = torch.empty(rows, device=DEV)
+    y = torch.empty_like(x)
+    sdt.rms_norm(x, w, y=y, rstd=rstd, eps=eps)
+    dx, dw = torch.empty_like(x), torch.empty(K, device=DEV)
+    ws = torch.empty(sdt.rms_norm_workspace_size(rows, K), dtype=torch.uint8, device=DEV)
+    sdt.rms_norm_backward(x, w, rstd, dy, dx, dw, ws)
+
+    def loss(xd, wd):
+        return (xd / (xd.square().mean(dim=1, keepdim=True) + eps).sqrt() * wd * dy.double()).sum().item()
+    xd, wd, h = x.double(), w.double(), 1e-5
+
+    def slope(of, i):
+        up, down = of.clone().flatten(), of.clone().flatten()
+        up[i] += h
+        down[i] -= h
+        return up.view_as(of), down.view_as(of)
+    for i in range(0, rows * K, 11):
+        a, b = slope(xd, i)
+        d = (loss(a, wd) - loss(b, wd)) / (2 * h)
+        # differences: h^2 of the third derivative and 1e-15 / h of the sum, below 1e-7
+        assert abs(dx.flatten()[i].item() - d) <= 2.0 ** -11 * abs(d) + 1e-5
+    for i in range(0, K, 7):
+        a, b = slope(wd, i)
+        d = (loss(xd, a) - loss(xd, b)) / (2 * h)
+        assert abs(dw[i].item() - d) <= 1e-5 * (1 + abs(d))
+
+
+def test_norm_in_place():
+    """total over the residual, y over x; dx over dtotal."""
+    import torch
+    sdt = _sdt()
+    x, r, w = (normal(s, torch.bfloat16, i) for i, s in enumerate([(50, 1000), (50, 1000), (1000,)]))
+    y, t = torch.empty_like(x), torch.empty_like(x)
+    rstd = torch.empty(50, device=DEV)
+    sdt.rms_norm(x, w, y=y, residual=r, total=t, rstd=rstd)
+    x2, r2 = x.clone(), r.clone()
+    sdt.rms_norm(x2, w, y=x2, residual=r2, total=r2)
+    assert torch.equal(x2, y) and torch.equal(r2, t)
+    dx, d2 = torch.empty_like(x), r.clone()
+    sdt.rms_norm_backward(t, w, rstd, x, dx, dtotal=r)
+    sdt.rms_norm_backward(t, w, rstd, x, d2, dtotal=d2)
+    assert torch.equal(dx, d2)
+
+
+def test_norm_no_rows_weight_gradient():
+    import torch
+    sdt = _sdt()
+    e = torch.empty(0, 100, dtype=torch.float16, device=DEV)
+    dw = torch.full((100,), 7.0, device=DEV)
+    sdt.rms_norm_backward(e, None, torch.empty(0, device=DEV), e, e, dw, None)
+    assert not dw.any()
+
+
+# ---- the gated block -----------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M, N, K", [s for s in SIZES])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("kept", [None, "wide", "type"])
+def test_gated(dtype, M, N, K, act, kept):
+    import torch
+    say(f"gated {dtype} {M}x{N}x{K} {act} {kept}")
+    sdt, t = _sdt(), _t(dtype)
+    x, _ = rows_of(normal((M, K), t, 1), 8)
+    gate, _ = rows_of(normal((N, K), t, 2, K ** -0.5), 0)
+    up, _ = rows_of(normal((N, K), t, 3, K ** -0.5), 16)
+    h, full = out_like(M, N, t, pad=8)
+    kt = torch.float32 if kept == "wide" else t
+    g, gf = out_like(M, N, kt, pad=4) if kept else (None, None)
+    u, uf = out_like(M, N, kt, pad=12) if kept else (None, None)
+    sdt.gated_ff(x, gate, up, h, act=act, g=g, u=u)
+    xd, gd, ud = x.double(), gate.double(), up.double()
+    G, V = xd @ gd.t(), xd @ ud.t()
+    eg = (K + 1) * U * (xd.abs() @ gd.abs().t())
+    ev = (K + 1) * U * (xd.abs() @ ud.abs().t())
+    a, da = ref.act(G, act)
+    # |a'| <= 1.13 for both; 16 steps for the activation itself
+    ea = 1.13 * eg + 16 * U * a.abs() + 2.0 ** -120
+    check(h, a * V, (ea * (V.abs() + ev) + a.abs() * ev) + 4 * U * (a * V).abs(), "h")
+    assert untouched(full, N)
+    if kept:
+        check(g, G, eg, "g")
+        check(u, V, ev, "u")
+        assert untouched(gf, N) and untouched(uf, N)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gated_far_arguments(act):
+    """Arguments at which exp over- or underflows."""
+    import torch
+    sdt = _sdt()
+    v = torch.tensor([0.0, -0.0, 1.0, -1.0, 5.0, -5.0, 20.0, -20.0, 87.0, -87.0, 90.0, -90.0, 200.0, -200.0, 3e4,
+                      -3e4, 1e10, -1e10, 1e19, -1e19], device=DEV).bfloat16()
+    n = v.numel()
+    x = torch.zeros(n, 8, dtype=torch.bfloat16, device=DEV)
+    x[:, 0] = v
+    x[:, 1] = 1
+    gate, up = torch.zeros_like(x[:1]), torch.zeros_like(x[:1])
+    gate[0, 0] = 1
+    up[0, 1] = 1
+    h = torch.empty(n, 1, dtype=torch.bfloat16, device=DEV)
+    full = torch.empty(n, 8, dtype=torch.bfloat16, device=DEV)
+    h = full[:, :1]
+    g, u = torch.empty(n, 4, device=DEV)[:, :1], torch.empty(n, 4, device=DEV)[:, :1]
+    sdt.gated_ff(x, gate, up, h, act=act, g=g, u=u)
+    a, da = ref.act(v.double(), act)
+    check(h[:, 0], a, 16 * U * a.abs() + 2.0 ** -100, "a")
+    # the slope through the gradient of the up-projected one
+    dx = torch.empty(n, 8, dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(sdt.gated_ff_workspace_size(n, 1, 8), dtype=torch.uint8, device=DEV)
+    ones = torch.ones(n, 8, dtype=torch.bfloat16, device=DEV)[:, :1]
+    sdt.gated_ff_backward(x, gate, up, g, u, ones, dx, None, None, ws, act=act)
+    # Where exp(-|t|) is below e^-88 it counts as 0: a and a' lose at most (1 + |g| dt/dg)
+    # e^-88 there, 89 e^-88 = 5.4e-37 for silu (t = g = 88, falling beyond) and 235 e^-88 =
+    # 1.5e-36 for gelu (g = 10.1, dt/dg = 23.3), less than 2^-118
+    ok = v.float().abs() < 1e4
+    check(dx[ok, 0], da[ok], 64 * U * da[ok].abs() + 64 * U * a[ok].abs().clamp(max=1) + 2.0 ** -118, "slope")
+    assert bool((dx[~ok, 0] == (v[~ok] > 0)).all())
+
+
+GRAD_SIZES = [(1, 1, 1), (3, 70, 40), (64, 64, 64), (100, 129, 383), (500, 257, 130), (2000, 200, 100),
+              (130, 2050, 700), (2100, 600, 1030)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M, N, K", GRAD_SIZES)
+@pytest.mark.parametrize("act, kept", [("silu", "wide"), ("gelu", "type")])
+def test_gated_backward(dtype, M, N, K, act, kept):
+    import torch
+    say(f"gated backward {dtype} {M}x{N}x{K} {act} {kept}")
+    sdt, t = _sdt(), _t(dtype)
+    x, _ = rows_of(normal((M, K), t, 1), 8)
+    gate, _ = rows_of(normal((N, K), t, 2, K ** -0.5), 0)
+    up, _ = rows_of(normal((N, K), t, 3, K ** -0.5), 16)
+    dh, _ = rows_of(normal((M, N), t, 4), 1, align=1)
+    kt = torch.float32 if kept == "wide" else t
+    g, _ = rows_of(normal((M, N), kt, 5), 4)
+    u, _ = rows_of(normal((M, N), kt, 6), 12)
+    dx, xf = out_like(M, K, t, pad=8)
+    dgate, gf = out_like(N, K, t)
+    dup, uf = out_like(N, K, t, pad=24)
+    ws = torch.full((sdt.gated_ff_workspace_size(M, N, K),), 0xFF, dtype=torch.uint8, device=DEV)
+    sdt.gated_ff_backward(x, gate, up, g, u, dh, dx, dgate, dup, ws, act=act)
+    xd, wg, wu = x.double(), gate.double(), up.double()
+    a, da = ref.act(g.double(), act)
+    dg, du = dh.double() * u.double() * da, dh.double() * a
+    # each is rounded to the type before the products; a' is a sum of terms up to 1.2
+    step = half(t) + 32 * U
+    eg = step * dg.abs() + 32 * U * (dh.double() * u.double()).abs() + tiny(t)
+    eu = step * du.abs() + tiny(t)
+
+    def bound(n, parts):
+        return sum(ea @ b.abs() + (n + 2) * U * ((va.abs() + ea) @ b.abs()) for va, ea, b in parts)
+    check(dx, dg @ wg + du @ wu, bound(2 * N, [(dg, eg, wg), (du, eu, wu)]), "dx")
+    check(dgate, dg.t() @ xd, bound(M, [(dg.t(), eg.t(), xd)]), "dgate")
+    check(dup, du.t() @ xd, bound(M, [(du.t(), eu.t(), xd)]), "dup")
+    assert untouched(xf, K) and untouched(gf, K) and untouched(uf, K)
+    # in parts: the same bits
+    dx2, dg2, du2 = torch.empty_like(xf)[:, :K], torch.empty_like(gf)[:, :K], torch.empty_like(uf)[:, :K]
+    sdt.gated_ff_backward(x, gate, up, g, u, dh, dx2, None, None, ws, act=act)
+    sdt.gated_ff_backward(x, gate, up, g, u, dh, None, dg2, du2, ws, act=act)
+    assert torch.equal(dx, dx2) and torch.equal(dgate, dg2) and torch.equal(dup, du2)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gated_gradient_by_differences(act):
+    """dx, dgate and dup against central differences of the 64-bit block."""
+    import torch
+    sdt = _sdt()
+    M, N, K = 5, 24, 16
+    x, gate, up, dh = (normal(s, torch.float16, i) for i, s in enumerate([(M, K), (N, K), (N, K), (M, N)]))
+    gate, up = gate * 0.25, up * 0.25
+    h = torch.empty(M, N, dtype=torch.float16, device=DEV)
+    g, u = torch.empty(M, N, device=DEV), torch.empty(M, N, device=DEV)
+    sdt.gated_ff(x, gate, up, h, act=act, g=g, u=u)
+    dx, dg, du = torch.empty_like(x), torch.empty_like(gate), torch.empty_like(up)
+    ws = torch.empty(sdt.gated_ff_workspace_size(M, N, K), dtype=torch.uint8, device=DEV)
+    sdt.gated_ff_backward(x, gate, up, g, u, dh, dx, dg, du, ws, act=act)
+    xs = [x.double(), gate.double(), up.double()]
+
+    def loss(v):
+        return (ref.act(v[0] @ v[1].t(), act)[0] * (v[0] @ v[2].t()) * dh.double()).sum().item()
+    eps = 1e-5
+    for which, got in enumerate((dx, dg, du)):
+        for i in range(0, got.numel(), 13):
+            v = [t.clone() for t in xs]
+            v[which].view(-1)[i] += eps
+            hi = loss(v)
+            v[which].view(-1)[i] -= 2 * eps
+            d = (hi - loss(v)) / (2 * eps)
+            # 24 terms at most, each rounded to 16 bits before the product: 2^-11 of up to
+            # |dh u a'| |w| < 4, and the result's own half step
+            assert abs(got.view(-1)[i].item() - d) <= 2.0 ** -11 * abs(d) + 24 * 2.0 ** -11
+
+
+# ---- turned products ------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("layout", ["nn", "tn"])
+@pytest.mark.parametrize("M, N, K, split", [(*s, False) for s in SIZES] + [
+    (64, 64, 5000, False), (100, 30, 4097, False), (2048, 1540, 256, False), (64, 64, 5000, True),
+    (100, 30, 4097, True), (1, 8, 1024, True), (700, 300, 1030, True)])
+def test_turned(dtype, layout, M, N, K, split):
+    import torch
+    say(f"{layout} {dtype} {M}x{N}x{K} split {split}")
+    sdt, t = _sdt(), _t(dtype)
+    need = sdt.gemm_turned_workspace_size(M, N, K)
+    assert need > 0 or not split
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV) if split else None
+    run = getattr(sdt, f"gemm_{dtype}_{layout}")
+    for plain in (True, False):
+        make = whole if plain else normal
+        a = make((M, K) if layout == "nn" else (K, M), t, 1)
+        a, b = rows_of(a, 8)[0], rows_of(make((K, N), t, 2), 16)[0]
+        c, full = out_like(M, N, t, pad=8)
+        run(a, b, c, workspace=ws)
+        ad = a.double() if layout == "nn" else a.double().t()
+        want = ad @ b.double()
+        if plain:
+            assert torch.equal(c, want.float().to(t))          # whole sums below 2^24
+        else:
+            check(c, want, (K + 2) * U * (ad.abs() @ b.double().abs()), layout)
+        assert untouched(full, N)
+
+
+# ---- streams and graphs ------------------------------------------------------------------------
+
+
+def block(sdt, s):
+    """The operators one after another, as a layer uses them."""
+    sdt.rms_norm(s["x"], s["w"], y=s["n"], residual=s["r"], total=s["t"], rstd=s["rstd"])
+    sdt.gated_ff(s["n"], s["gate"], s["up"], s["h"], g=s["g"], u=s["u"])
+    sdt.gemm_bf16(s["h"], s["down"], s["y"])
+    sdt.gemm_bf16_nn(s["dy"], s["down"], s["dh"], s["ws"])
+    sdt.gemm_bf16_tn(s["dy"], s["h"], s["ddown"], s["ws"])
+    sdt.gated_ff_backward(s["n"], s["gate"], s["up"], s["g"], s["u"], s["dh"], s["dn"], s["dgate"], s["dup"],
+                          s["ws"])
+    sdt.rms_norm_backward(s["t"], s["w"], s["rstd"], s["dn"], s["dx"], s["dw"], s["ws"], dtotal=s["dy"])
+    sdt.fp8_quantize_bf16(s["n"], s["n8"])
+    sdt.gemm_fp8_bf16(s["n8"], s["w8"], s["y8"])
+
+
+def block_state(M=70, N=200, K=136):
+    import torch
+    sdt, t = _sdt(), torch.bfloat16
+    e = lambda *s: torch.empty(s, dtype=t, device=DEV)       # noqa: E731
+    s = {"x": normal((M, K), t, 1), "r": normal((M, K), t, 2), "w": normal((K,), t, 3),
+         "gate": normal((N, K), t, 4, K ** -0.5), "up": normal((N, K), t, 5, K ** -0.5),
+         "down": normal((K, N), t, 6, N ** -0.5), "dy": normal((M, K), t, 7)}
+    s.update(n=e(M, K), t=e(M, K), h=e(M, N), y=e(M, K), dh=e(M, N), ddown=e(K, N), dn=e(M, K), dgate=e(N, K),
+             dup=e(N, K), dx=e(M, K), y8=e(M, N), rstd=torch.empty(M, device=DEV),
+             g=torch.empty(M, N, device=DEV), u=torch.empty(M, N, device=DEV), dw=torch.empty(K, device=DEV),
+             n8=sdt.Fp8.empty(M, K, device=DEV), w8=sdt.Fp8.empty(N, K, block=128, device=DEV))
+    need = max(sdt.gated_ff_workspace_size(M, N, K), sdt.rms_norm_workspace_size(M, K),
+               sdt.gemm_turned_workspace_size(M, N, K), sdt.gemm_turned_workspace_size(K, N, M))
+    s["ws"] = torch.empty(need, dtype=torch.uint8, device=DEV)
+    sdt.fp8_quantize_bf16(s["gate"], s["w8"])
+    return s
+
+
+OUTPUTS = ["n", "t", "h", "y", "dh", "ddown", "dn", "dgate", "dup", "dx", "dw", "y8", "g", "u", "rstd"]
+
+
+def test_run_together_in_a_graph():
+    """Captured on a stream and replayed among eager work: every replay's outputs are
+    those of the eager calls, on the inputs that it finds."""
+    import torch
+    sdt = _sdt()
+    s, e = block_state(), block_state()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        block(sdt, s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        block(sdt, s)
+    for turn in range(4):
+        new = normal(s["x"].shape, torch.bfloat16, 50 + turn)
+        for state in (s, e):
+            state["x"].copy_(new)
+            for name in OUTPUTS:
+                state[name].fill_(float("nan"))
+        graph.replay()
+        block(sdt, e)
+        torch.cuda.synchronize()
+        for name in OUTPUTS:
+            assert torch.equal(s[name], e[name]), (turn, name)
+            assert bool(torch.isfinite(s[name].float()).all()), name
+
+
+def test_run_together_on_streams():
+    """Two states on two streams at once, by the stream argument."""
+    import torch
+    sdt = _sdt()
+    want = block_state()
+    block(sdt, want)
+    torch.cuda.synchronize()
+    states = [block_state() for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, stream in zip(states, streams):
+            with torch.cuda.stream(stream):
+                block(sdt, s)
+    torch.cuda.synchronize()
+    for s in states:
+        for name in OUTPUTS:
+            assert torch.equal(s[name], want[name]), name
