@@ -13,6 +13,7 @@
 #include "runtime.hpp"
 #include "sdt.h"
 #include "tile_kernel.hpp"
+#include "tile_pp_kernel.hpp"
 
 namespace sdt {
 namespace {
@@ -158,6 +159,17 @@ int launch_tile(TileGemm& p, void* stream) {
                   (int64_t)p.gm * p.gn * p.batch, WM * WN * 64, p, stream);
 }
 
+template <typename Elt, bool TA, bool TB, bool GATED>
+int launch_pp(TileGemm& p, void* stream) {
+    p.gm = (int)ceil_div(p.M, 256);
+    p.gn = (int)ceil_div(p.N, GATED ? 128 : 256);
+    return launch(reinterpret_cast<const void*>(&tile_pp_kernel<Elt, TA, TB, GATED>),
+                  (int64_t)p.gm * p.gn * p.batch, 512, p, stream);
+}
+
+// Whether 256 x 256 tiles, a workgroup a CU, beat 128 x 128 ones, two.
+bool large_tiles(int64_t t256, int64_t cu) { return t256 >= cu; }
+
 template <typename Elt, bool FP8, bool GATED, int PB, int NMB, int NS>
 int launch_rows(TileGemm& p, void* stream) {
     p.gm = (int)ceil_div(p.M, NMB * 16);
@@ -217,8 +229,11 @@ Split plan_split(int64_t M, int64_t N, int64_t kt, int batch) {
 }
 
 template <typename Elt, bool TA, bool TB>
-int launch_split(TileGemm& p, void* ws, int64_t ws_bytes, void* stream) {
+int launch_split(TileGemm& p, void* ws, int64_t ws_bytes, int num_cu, void* stream) {
     const Split s = plan_split(p.M, p.N, (int64_t)p.nkt * p.products, p.batch);
+    const bool strides = p.products == 1 || (p.lda[0] == p.lda[1] && p.ldb[0] == p.ldb[1]);
+    if (strides && large_tiles(ceil_div(p.M, 256) * ceil_div(p.N, 256) * p.batch, num_cu))
+        return launch_pp<Elt, TA, TB, false>(p, stream);
     if (s.splits > 1 && ws_bytes >= s.bytes) {
         p.splits = s.splits;
         p.ws = static_cast<float*>(ws);
@@ -248,7 +263,7 @@ int gemm_turned(int64_t M, int64_t N, int64_t L, const void* A, int64_t lda, con
     p.lda[0] = lda * 2;
     p.ldb[0] = ldb * 2;
     p.ldc[0] = ldc;
-    return launch_split<Elt, TA, true>(p, ws, ws_bytes, stream);
+    return launch_split<Elt, TA, true>(p, ws, ws_bytes, dev.num_cu, stream);
 }
 
 // ---- the norm ---------------------------------------------------------------------------
@@ -409,6 +424,8 @@ int gated(const sdt_gated_ff* a, void* stream) {
     p.act = a->act;
     if (M <= 16) return launch_rows<Elt, false, true, 1, 1, 4>(p, stream);
     if (M <= 64) return launch_rows<Elt, false, true, 1, 4, 2>(p, stream);
+    if (large_tiles(ceil_div(M, 256) * ceil_div(N, 128), dev.num_cu))
+        return launch_pp<Elt, false, false, true>(p, stream);
     if (ceil_div(M, 128) * ceil_div(N, 64) >= dev.num_cu)
         return launch_tile<Elt, false, 128, 128, 2, 2, 2, false, false, true>(p, stream);
     return launch_tile<Elt, false, 64, 128, 2, 2, 3, false, false, true>(p, stream);
@@ -494,7 +511,7 @@ int gated_backward(const sdt_gated_ff_grad* a, void* stream) {
         p.ldb[1] = a->ldup * 2;
         p.ldc[0] = a->lddx;
         p.products = 2;
-        rc = launch_split<Elt, false, true>(p, ws, l.bytes - l.at, stream);
+        rc = launch_split<Elt, false, true>(p, ws, l.bytes - l.at, dev.num_cu, stream);
         if (rc != SDT_OK) return rc;
     }
     if (weights) {                                // dgate = dg^T . x, dup = du^T . x
@@ -509,7 +526,7 @@ int gated_backward(const sdt_gated_ff_grad* a, void* stream) {
         p.ldc[0] = a->lddgate;
         p.ldc[1] = a->lddup;
         p.batch = 2;
-        rc = launch_split<Elt, true, true>(p, ws, l.bytes - l.at, stream);
+        rc = launch_split<Elt, true, true>(p, ws, l.bytes - l.at, dev.num_cu, stream);
     }
     return rc;
 }

@@ -21,7 +21,6 @@
 namespace sdt {
 
 typedef short short4_t __attribute__((ext_vector_type(4)));
-typedef short short8_t __attribute__((ext_vector_type(8)));
 
 struct TileGemm {
     const uint8_t *A[2], *B[2];    // two pairs: of products that are added, of a
@@ -126,22 +125,28 @@ struct Operand {
         }
         return make_rsrc(base + kt * 128, (uint32_t)((rows - 1) * ld + ((L * z + 3) & ~3) - kt * 128));
     }
-    // Half h of the fragment of part P (16 rows): eight values, or 16 codes.
-    static __device__ __forceinline__ int4_t fragment(const int4_t* stage, int P, int h, int lane) {
+    // Where the lane reads half 0 of the fragment of part P (16 rows), in bytes of a
+    // stage; part P + j (P a multiple of the parts j runs over) and half h from it.
+    static __device__ __forceinline__ int place(int P, int lane) {
         const int fr = lane & 15, fq = lane >> 4;
         if constexpr (TURNED) {
-            typedef __attribute__((address_space(3))) short4_t* lds4;
-            const int r4 = fr >> 2, c = fr & 3;
-            const int k = 8 * fq + r4;                   // + 32 h + 4 t: the same swizzle
-            const int unit = (2 * P + (c >> 1)) ^ turned_swz<UPR>(k);
-            const char* at = reinterpret_cast<const char*>(stage) + (k + 32 * h) * (UPR * 16) +
-                             unit * 16 + (c & 1) * 8;
-            const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)at);
-            const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + 4 * UPR * 16));
-            const short8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            return __builtin_bit_cast(int4_t, v);
+            const int k = 8 * fq + (fr >> 2), c = fr & 3;    // + 32 h + 4 t: the same swizzle
+            return k * (UPR * 16) + ((P * 32) ^ (turned_swz<UPR>(k) * 16)) + c * 8;
         }
-        return stage[(P * 16 + fr) * 8 + ((4 * h + fq) ^ swz_pp(fr))];
+        return (P * 16 + fr) * 128 + (fq ^ swz_pp(fr)) * 16;
+    }
+    // Eight values, or 16 codes.
+    static __device__ __forceinline__ int4_t fragment(const int4_t* stage, int at, int j, int h) {
+        const char* base = reinterpret_cast<const char*>(stage);
+        if constexpr (TURNED) {
+            typedef __attribute__((address_space(3))) short4_t* lds4;
+            const char* from = base + (at ^ (j * 32)) + h * 32 * (UPR * 16);
+            const int2_t lo = __builtin_bit_cast(int2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)from));
+            const int2_t hi = __builtin_bit_cast(
+                int2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(from + 4 * (UPR * 16))));
+            return int4_t{lo[0], lo[1], hi[0], hi[1]};
+        }
+        return *reinterpret_cast<const int4_t*>(base + (at ^ (h * 64)) + j * 2048);
     }
 };
 
@@ -190,7 +195,7 @@ __device__ __forceinline__ void dma4(const float* from, float* lds_wave_base) {
 
 // A wave's parts of both factors, in fp32, `left` rows from mb and columns nb .. of N.
 template <int FN, int FM>
-__device__ __forceinline__ void store_wide(float* C, int64_t ldc, const floatx4_t (*acc)[FM], int64_t mb,
+__device__ __forceinline__ void store_wide(float* C, int64_t ldc, const floatx4_t (&acc)[FN][FM], int64_t mb,
                                            int left, int nb, int N, int lane) {
     const int fr = lane & 15, fq = lane >> 4;
 #pragma unroll
@@ -219,27 +224,26 @@ __device__ __forceinline__ void tile_store(const TileGemm& p, int batch, const f
                                            uint32_t mb, int left, uint32_t nb, int lane) {
     if constexpr (GATED) {
         constexpr int H = FN / 2;
+        // references to the two halves
+        const floatx4_t(&g)[H][FM] = *reinterpret_cast<const floatx4_t(*)[H][FM]>(&acc[0]);
+        const floatx4_t(&u)[H][FM] = *reinterpret_cast<const floatx4_t(*)[H][FM]>(&acc[H]);
+        if (p.G) {
+            if (p.wide) {
+                store_wide<H, FM>(static_cast<float*>(p.G), p.ldg, g, mb, left, nb, p.N, lane);
+                store_wide<H, FM>(static_cast<float*>(p.U), p.ldu, u, mb, left, nb, p.N, lane);
+            } else {
+                store_parts<Elt, H, FM>(static_cast<uint16_t*>(p.G), p.ldg, g, mb, left, nb, p.N, lane);
+                store_parts<Elt, H, FM>(static_cast<uint16_t*>(p.U), p.ldu, u, mb, left, nb, p.N, lane);
+            }
+        }
         floatx4_t out[H][FM];
 #pragma unroll
         for (int i = 0; i < H; ++i)
 #pragma unroll
             for (int j = 0; j < FM; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    out[i][j][e] = act_mul(acc[i][j][e], acc[i + H][j][e], p.act);
+                for (int e = 0; e < 4; ++e) out[i][j][e] = act_mul(g[i][j][e], u[i][j][e], p.act);
         store_parts<Elt, H, FM>(p.C[0], p.ldc[0], out, mb, left, nb, p.N, lane);
-        if (p.G) {
-            if (p.wide) {
-                store_wide<H, FM>(static_cast<float*>(p.G), p.ldg, acc, mb, left, nb, p.N, lane);
-                store_wide<H, FM>(static_cast<float*>(p.U), p.ldu, acc + H, mb, left, nb, p.N, lane);
-            } else {
-                // references to the two halves
-                const floatx4_t(&g)[H][FM] = *reinterpret_cast<const floatx4_t(*)[H][FM]>(&acc[0]);
-                const floatx4_t(&u)[H][FM] = *reinterpret_cast<const floatx4_t(*)[H][FM]>(&acc[H]);
-                store_parts<Elt, H, FM>(static_cast<uint16_t*>(p.G), p.ldg, g, mb, left, nb, p.N, lane);
-                store_parts<Elt, H, FM>(static_cast<uint16_t*>(p.U), p.ldu, u, mb, left, nb, p.N, lane);
-            }
-        }
     } else {
         store_parts<Elt, FN, FM>(p.C[batch], p.ldc[batch], acc, mb, left, nb, p.N, lane);
     }
@@ -365,6 +369,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
 #pragma unroll
         for (int j = 0; j < FM; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 
+    const int at_a = OpA::place(wave_m * FM, lane), at_b = OpB::place(wave_n * FN, lane);
     int4_t fa[FM][2], fb[FN][2];
     float scale[FM];
     auto read = [&](int stage) {
@@ -372,10 +377,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int j = 0; j < FM; ++j) fa[j][h] = OpA::fragment(base, wave_m * FM + j, h, lane);
+            for (int j = 0; j < FM; ++j) fa[j][h] = OpA::fragment(base, at_a, j, h);
 #pragma unroll
-            for (int i = 0; i < FN; ++i)
-                fb[i][h] = OpB::fragment(base + OpA::UNITS, wave_n * FN + i, h, lane);
+            for (int i = 0; i < FN; ++i) fb[i][h] = OpB::fragment(base + OpA::UNITS, at_b, i, h);
         }
         if constexpr (FP8) {
             const float* sc = reinterpret_cast<const float*>(base + OpA::UNITS + OpB::UNITS);
@@ -563,6 +567,7 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
 #pragma unroll
             for (int j = 0; j < NMB; ++j) acc[m][i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 
+    const int place = OpA::place(0, lane);        // the same in B's rows
     const int n = (p.nkt - wave + NW - 1) / NW;   // this wave's k-tiles (0 or less: none)
     for (int j = 0; j < min(n, NS); ++j) load(wave + j * NW, j);
     int stage = 0;
@@ -583,12 +588,12 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int i = 0; i < NMB; ++i) fa[i][h] = OpA::fragment(at, i, h, lane);
+            for (int i = 0; i < NMB; ++i) fa[i][h] = OpA::fragment(at, place, i, h);
 #pragma unroll
             for (int m = 0; m < MATS; ++m)
 #pragma unroll
                 for (int i = 0; i < PB; ++i)
-                    fb[m][i][h] = OpB::fragment(at + A_UNITS + m * B_UNITS, i, h, lane);
+                    fb[m][i][h] = OpB::fragment(at + A_UNITS + m * B_UNITS, place, i, h);
         }
         float scale[NMB];
         if constexpr (FP8) {
