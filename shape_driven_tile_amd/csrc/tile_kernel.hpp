@@ -113,18 +113,42 @@ struct Operand {
         const int row = u >> 3;
         return (uint32_t)(src(row) * ld) + ((u & 7) ^ swz_pp(row)) * 16;
     }
-    // The descriptor of a k-tile: `rows` of the operand's rows exist from its first
-    // one at `base` on.  Bytes past the last row's end read as zero; the end is
-    // rounded up to the 4 bytes that its last value lies in.
-    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t describe(const uint8_t* base, int64_t ld,
-                                                                      int rows, int kt, int L, int z) {
-        if constexpr (TURNED) {
-            const int left = min(64, L - kt * 64);
-            return make_rsrc(base + (int64_t)kt * 64 * ld,
-                             (uint32_t)((left - 1) * ld + ((rows * 2 + 3) & ~3)));
+    // The k-tiles of the operand in turn, by scalar arithmetic alone (a load of the
+    // pointers in the loop would hold up the loads that follow it).  `rows` of the
+    // operand's rows exist from its first one (or column) at `base` on.  Bytes past the
+    // last row's end read as zero; the end is rounded up to the 4 bytes that its last
+    // value lies in.
+    struct Stream {
+        const uint8_t* at;
+        int64_t ld;
+        int end;                                         // bytes of the last row
+        int left;                                        // TURNED: k-rows left
+        uint32_t bytes;
+        __device__ __forceinline__ void start(const uint8_t* base, int64_t stride, int rows, int k, int L,
+                                              int z) {
+            ld = stride;
+            if constexpr (TURNED) {
+                at = base + (int64_t)k * 64 * ld;
+                left = L - k * 64;
+                end = (rows * 2 + 3) & ~3;
+            } else {
+                at = base + (int64_t)k * 128;
+                bytes = (uint32_t)((rows - 1) * ld + ((L * z + 3) & ~3) - k * 128);
+            }
         }
-        return make_rsrc(base + kt * 128, (uint32_t)((rows - 1) * ld + ((L * z + 3) & ~3) - kt * 128));
-    }
+        __device__ __forceinline__ __amdgpu_buffer_rsrc_t next() {
+            if constexpr (TURNED) {
+                const __amdgpu_buffer_rsrc_t r = make_rsrc(at, (uint32_t)((min(64, left) - 1) * (int)ld + end));
+                at += 64 * ld;
+                left -= 64;
+                return r;
+            }
+            const __amdgpu_buffer_rsrc_t r = make_rsrc(at, bytes);
+            at += 128;
+            bytes -= 128;
+            return r;
+        }
+    };
     // Where the lane reads half 0 of the fragment of part P (16 rows), in bytes of a
     // stage; part P + j (P a multiple of the parts j runs over) and half h from it.
     static __device__ __forceinline__ int place(int P, int lane) {
@@ -320,9 +344,23 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
             }
         }
     };
-    // the pair of k-tile kt: of the products added, or of the batch
-    auto pair_of = [&](int kt) { return batch + (kt >= p.nkt ? 1 : 0); };
-    offsets(pair_of(first));
+    // The k-tile that the next load takes.  The pointers of both pairs stay at hand.
+    typename OpA::Stream sa;
+    typename OpB::Stream sb, sb2;
+    const uint8_t* const a1 = p.A[1];
+    const uint8_t* const b1 = p.B[1];
+    const int64_t lda1 = p.lda[1], ldb1 = p.ldb[1];
+    int load_k = first >= p.nkt ? first - p.nkt : first;
+    auto start = [&](bool second) {
+        const int64_t lda = second ? lda1 : p.lda[0], ldb = second ? ldb1 : p.ldb[0];
+        sa.start((second ? a1 : p.A[0]) + (TA ? m0 * 2 : m0 * lda), lda, TA ? (int)(p.M - m0) : rows_a, load_k,
+                 p.L, Z);
+        const int columns = TB ? (int)(p.N - n0) : rows_b;
+        sb.start((second ? b1 : p.B[0]) + (TB ? n0 * 2 : n0 * ldb), ldb, columns, load_k, p.L, Z);
+        if constexpr (GATED) sb2.start(b1 + n0 * ldb1, ldb1, columns, load_k, p.L, Z);
+        offsets(second ? 1 : 0);
+    };
+    start(batch == 1 || first >= p.nkt);
     // the scales this lane loads: a row's (lanes 0-31) or the columns' block's
     const float* scale_at = nullptr;
     int64_t scale_step = 0;
@@ -332,22 +370,16 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
         scale_step = lane < 32 ? p.ldsa : 1;
     }
 
-    auto load = [&](int kt, int stage) {
+    auto load = [&](int stage) {
         int4_t* base = smem + stage * STAGE;
-        const int pair = pair_of(kt);
-        const int k = kt >= p.nkt ? kt - p.nkt : kt;
-        if (kt == p.nkt && kt != first) offsets(pair);    // the second product's strides
-        const int64_t lda = p.lda[pair], ldb = p.ldb[GATED ? 0 : pair];
-        const __amdgpu_buffer_rsrc_t ra = OpA::describe(p.A[pair] + (TA ? m0 * 2 : m0 * lda), lda,
-                                                        TA ? (int)(p.M - m0) : rows_a, k, p.L, Z);
-        const int columns = TB ? (int)(p.N - n0) : rows_b;
-        const __amdgpu_buffer_rsrc_t rb = OpB::describe(
-            p.B[GATED ? 0 : pair] + (TB ? n0 * 2 : n0 * ldb), ldb, columns, k, p.L, Z);
+        if constexpr (FP8)
+            dma4(scale_at + load_k * scale_step,
+                 reinterpret_cast<float*>(base + OpA::UNITS + OpB::UNITS + wave * 16));
+        const __amdgpu_buffer_rsrc_t ra = sa.next(), rb = sb.next();
 #pragma unroll
         for (int j = 0; j < OpA::DMA; ++j) dma16(ra, base + (wave * OpA::DMA + j) * 64, voff_a[j], 0);
         if constexpr (GATED) {
-            const __amdgpu_buffer_rsrc_t r2 =
-                OpB::describe(p.B[1] + n0 * p.ldb[1], p.ldb[1], columns, k, p.L, Z);
+            const __amdgpu_buffer_rsrc_t r2 = sb2.next();
 #pragma unroll
             for (int j = 0; j < OpB::DMA; ++j) {
                 const bool second = ((wave * OpB::DMA + j) * 8) % WTN >= WTN / 2;
@@ -358,9 +390,10 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
             for (int j = 0; j < OpB::DMA; ++j)
                 dma16(rb, base + OpA::UNITS + (wave * OpB::DMA + j) * 64, voff_b[j], 0);
         }
-        if constexpr (FP8)
-            dma4(scale_at + k * scale_step,
-                 reinterpret_cast<float*>(base + OpA::UNITS + OpB::UNITS + wave * 16));
+        if (++load_k == p.nkt && p.products == 2) {       // on to the second product
+            load_k = 0;
+            start(true);
+        }
     };
 
     floatx4_t acc[FN][FM];
@@ -430,7 +463,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
     };
 
     const bool ragged = (!TA || !TB) && (p.L * Z) % 128 != 0;
-    for (int j = 0; j < NS && first + j < end; ++j) load(first + j, j);
+    for (int j = 0; j < NS && first + j < end; ++j) load(j);
     int s = 0;
     for (int kt = first; kt < end; ++kt) {
         // k-tile kt has landed; the one or more after it may be on their way
@@ -452,7 +485,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
         mma(0, FN / 2);
         pin();
         barrier();                                // every wave has read stage s
-        if (kt + NS < end) load(kt + NS, s);
+        if (kt + NS < end) load(s);
         mma(FN / 2, FN);
         pin();
         s = (s + 1 == NS) ? 0 : s + 1;
@@ -538,17 +571,22 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
     int4_t* const mine = smem + wave * MINE;
     typedef Operand<false, NMB * 16, 1> OpA;
     typedef Operand<false, BN, 1> OpB;
+    const uint8_t* const a0 = p.A[0] + m0 * p.lda[0];
+    const uint8_t* const b0[2] = {p.B[0] + n0 * p.ldb[0], GATED ? p.B[1] + n0 * p.ldb[1] : nullptr};
+    // bytes up to the last row's end, which is rounded up to 4
+    const int row_end = (p.L * Z + 3) & ~3;
+    const uint32_t a_end = (uint32_t)((rows_a - 1) * p.lda[0] + row_end);
+    const uint32_t b_end[2] = {(uint32_t)((rows_b - 1) * p.ldb[0] + row_end),
+                               (uint32_t)((rows_b - 1) * p.ldb[1] + row_end)};
     auto load = [&](int kt, int stage) {
         int4_t* at = mine + stage * STAGE;
-        const __amdgpu_buffer_rsrc_t ra =
-            OpA::describe(p.A[0] + m0 * p.lda[0], p.lda[0], rows_a, kt, p.L, Z);
+        const __amdgpu_buffer_rsrc_t ra = make_rsrc(a0 + kt * 128, a_end - kt * 128);
 #pragma unroll
         for (int j = 0; j < A_DMA; ++j) dma16(ra, at + j * 64, voff_a[j], 0);
         at += A_UNITS;
 #pragma unroll
         for (int m = 0; m < MATS; ++m) {
-            const __amdgpu_buffer_rsrc_t rb =
-                OpB::describe(p.B[m] + n0 * p.ldb[m], p.ldb[m], rows_b, kt, p.L, Z);
+            const __amdgpu_buffer_rsrc_t rb = make_rsrc(b0[m] + kt * 128, b_end[m] - kt * 128);
 #pragma unroll
             for (int j = 0; j < B_DMA; ++j) dma16(rb, at + j * 64, voff_b[m][j], 0);
             at += B_UNITS;

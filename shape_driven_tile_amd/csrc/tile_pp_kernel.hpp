@@ -64,44 +64,44 @@ __global__ __launch_bounds__(512) void tile_pp_kernel(TileGemm p) {
     const int rows_b = (int)min((int64_t)BNO, p.N - n0);
     const int all = p.products * p.nkt;
 
-    // This group's operand: group 0 loads A, group 1 B.
-    auto pair_of = [&](int kt) { return batch + (kt >= p.nkt ? 1 : 0); };
+    // This group's operand: group 0 loads A, group 1 B.  The k-tile that the next load
+    // takes; the pointers of both pairs stay at hand.
     uint32_t voff[DMA];
-    auto offsets = [&](int pair) {
 #pragma unroll
-        for (int j = 0; j < DMA; ++j) {
-            if (grp == 0) {
-                voff[j] = OpA::offset(lw, lane, j, p.lda[pair], [](int r) { return r; });
-            } else if constexpr (GATED) {
-                const bool second = ((lw * DMA + j) * 8) % WTN >= WTN / 2;
-                voff[j] = OpB::offset(lw, lane, j, second ? p.ldb[1] : p.ldb[0], [](int r) {
-                    return r / WTN * (WTN / 2) + r % (WTN / 2);
-                });
-            } else {
-                voff[j] = OpB::offset(lw, lane, j, p.ldb[pair], [](int r) { return r; });
-            }
+    for (int j = 0; j < DMA; ++j) {
+        if (grp == 0) {
+            voff[j] = OpA::offset(lw, lane, j, p.lda[0], [](int r) { return r; });
+        } else if constexpr (GATED) {
+            const bool second = ((lw * DMA + j) * 8) % WTN >= WTN / 2;
+            voff[j] = OpB::offset(lw, lane, j, second ? p.ldb[1] : p.ldb[0], [](int r) {
+                return r / WTN * (WTN / 2) + r % (WTN / 2);
+            });
+        } else {
+            voff[j] = OpB::offset(lw, lane, j, p.ldb[0], [](int r) { return r; });
         }
-    };
-    offsets(batch);
-    auto dma_a = [&](int kt, int stage) {
-        const int pair = pair_of(kt), k = kt >= p.nkt ? kt - p.nkt : kt;
-        const int64_t ld = p.lda[pair];
-        const __amdgpu_buffer_rsrc_t r = OpA::describe(p.A[pair] + (TA ? m0 * 2 : m0 * ld), ld,
-                                                       TA ? (int)(p.M - m0) : rows_a, k, p.L, 2);
+    }
+    typename OpA::Stream stream_a;
+    typename OpB::Stream stream_b, stream_u;
+    const int64_t a_at = TA ? m0 * 2 : m0 * p.lda[0], b_at = TB ? n0 * 2 : n0 * p.ldb[0];
+    const uint8_t* const a1 = p.A[1] + a_at;
+    const uint8_t* const b1 = GATED ? p.B[1] + n0 * p.ldb[1] : p.B[1] + b_at;
+    const int columns_a = TA ? (int)(p.M - m0) : rows_a, columns_b = TB ? (int)(p.N - n0) : rows_b;
+    stream_a.start(batch ? a1 : p.A[0] + a_at, p.lda[0], columns_a, 0, p.L, 2);
+    stream_b.start(batch ? b1 : p.B[0] + b_at, p.ldb[0], columns_b, 0, p.L, 2);
+    if constexpr (GATED) stream_u.start(b1, p.ldb[1], columns_b, 0, p.L, 2);
+    int load_k = 0;
+    auto dma_a = [&](int stage) {
+        const __amdgpu_buffer_rsrc_t r = stream_a.next();
         int4_t* const dst = smem + stage * UNITS + lw * DMA * 64;
 #pragma unroll
         for (int j = 0; j < DMA; ++j) dma16(r, dst + j * 64, voff[j], 0);
+        if (++load_k == p.nkt && p.products == 2) stream_a.start(a1, p.lda[0], columns_a, 0, p.L, 2);
     };
-    auto dma_b = [&](int kt, int stage) {
-        const int pair = GATED ? 0 : pair_of(kt), k = kt >= p.nkt ? kt - p.nkt : kt;
-        const int columns = TB ? (int)(p.N - n0) : rows_b;
-        const int64_t ld = p.ldb[pair];
-        const __amdgpu_buffer_rsrc_t r =
-            OpB::describe(p.B[pair] + (TB ? n0 * 2 : n0 * ld), ld, columns, k, p.L, 2);
+    auto dma_b = [&](int stage) {
+        const __amdgpu_buffer_rsrc_t r = stream_b.next();
         int4_t* const dst = smem + B_BASE + stage * UNITS + lw * DMA * 64;
         if constexpr (GATED) {
-            const __amdgpu_buffer_rsrc_t r2 =
-                OpB::describe(p.B[1] + n0 * p.ldb[1], p.ldb[1], columns, k, p.L, 2);
+            const __amdgpu_buffer_rsrc_t r2 = stream_u.next();
 #pragma unroll
             for (int j = 0; j < DMA; ++j) {
                 const bool second = ((lw * DMA + j) * 8) % WTN >= WTN / 2;
@@ -110,6 +110,7 @@ __global__ __launch_bounds__(512) void tile_pp_kernel(TileGemm p) {
         } else {
 #pragma unroll
             for (int j = 0; j < DMA; ++j) dma16(r, dst + j * 64, voff[j], 0);
+            if (++load_k == p.nkt && p.products == 2) stream_b.start(b1, p.ldb[0], columns_b, 0, p.L, 2);
         }
     };
 
@@ -121,19 +122,21 @@ __global__ __launch_bounds__(512) void tile_pp_kernel(TileGemm p) {
 
     int at_a = OpA::place(wave_m * FM, lane), at_b = OpB::place(wave_n * FN, lane);
     int4_t fa[2][FM], fb[2][FN];
-    auto read_tile = [&](int sa, int sb) {
-        // the parts' places are made from these each time: kept, they would not fit
+    auto read_a = [&](int sa) {
+        // the parts' places are made from this each time: kept, they would not fit
         // the registers
-        asm volatile("" : "+v"(at_a), "+v"(at_b));
-        const int4_t* abase = smem + sa * UNITS;
-        const int4_t* bbase = smem + B_BASE + sb * UNITS;
+        asm volatile("" : "+v"(at_a));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < FM; ++j) fa[h][j] = OpA::fragment(abase, at_a, j, h);
+            for (int j = 0; j < FM; ++j) fa[h][j] = OpA::fragment(smem + sa * UNITS, at_a, j, h);
+    };
+    auto read_b = [&](int sb) {
+        asm volatile("" : "+v"(at_b));
 #pragma unroll
-            for (int i = 0; i < FN; ++i) fb[h][i] = OpB::fragment(bbase, at_b, i, h);
-        }
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < FN; ++i) fb[h][i] = OpB::fragment(smem + B_BASE + sb * UNITS, at_b, i, h);
     };
     // The last k-tile of a product: what its K-major rows hold past their end is
     // not zero.
@@ -176,10 +179,10 @@ __global__ __launch_bounds__(512) void tile_pp_kernel(TileGemm p) {
     // ---- prologue: A(0), B(0), B(1) -------------------------------------------------
     if (all > 0) {
         if (grp == 0) {
-            dma_a(0, 0);
+            dma_a(0);
         } else {
-            dma_b(0, 0);
-            if (all > 1) dma_b(1, 1);
+            dma_b(0);
+            if (all > 1) dma_b(1);
         }
     }
     wait_global_loads<0>();
@@ -194,15 +197,24 @@ __global__ __launch_bounds__(512) void tile_pp_kernel(TileGemm p) {
         constexpr int LEFT = decltype(left)::value;       // k-tiles after this one (2: or more)
         const int sa = i & 1;
         const int sb2 = (sb == 0) ? 2 : sb - 1;   // (i + 2) % 3
-        if constexpr (G == 0 && LEFT >= 1) dma_a(i + 1, sa ^ 1);
-        if constexpr (G == 1 && LEFT >= 2) dma_b(i + 2, sb2);
-        read_tile(sa, sb);
-        // The loads among the fragment reads (masks: 0x020 global read, 0x100 LDS read).
-        constexpr int READS = 2 * (FM * (TA ? 2 : 1) + FN * (TB ? 2 : 1)) / DMA;
+        // Turned fragments first: the compiler holds back a ds_read_tr until every load
+        // into LDS that was issued before it has landed.  Those of the last read phase
+        // have; this one's would take it the phase (8192 x 4096 x 4096: nn 243 -> 194 us, tn 231 -> 202).
+        if constexpr (TB) read_b(sb);
+        if constexpr (TA) read_a(sa);
+        if constexpr (TA || TB) __builtin_amdgcn_sched_barrier(0);
+        if constexpr (G == 0 && LEFT >= 1) dma_a(sa ^ 1);
+        if constexpr (G == 1 && LEFT >= 2) dma_b(sb2);
+        if constexpr (!TB) read_b(sb);
+        if constexpr (!TA) read_a(sa);
+        // The loads among the other reads (masks: 0x020 global read, 0x100 LDS read).
+        constexpr int READS = 2 * ((TA ? 0 : FM) + (TB ? 0 : FN)) / DMA;
+        if constexpr (READS > 0) {
 #pragma unroll
-        for (int m = 0; m < DMA; ++m) {
-            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+            for (int m = 0; m < DMA; ++m) {
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+            }
         }
         if constexpr (G == 1) {
             // B(i+1) must be in LDS before group 0 reads k-tile i + 1 in the next
