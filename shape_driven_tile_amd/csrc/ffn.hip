@@ -9,6 +9,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "fp8_pp_kernel.hpp"
 #include "launcher.hpp"
 #include "runtime.hpp"
 #include "sdt.h"
@@ -205,6 +206,11 @@ int gemm8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const flo
     const int64_t cu = dev.num_cu;
     if (M <= 16) return launch_rows<Elt, true, false, 2, 1, 3>(p, stream);
     if (M <= 64) return launch_rows<Elt, true, false, 2, 4, 2>(p, stream);
+    if (large_tiles(ceil_div(M, 256) * ceil_div(N, 256), cu)) {
+        p.gm = (int)ceil_div(M, 256);
+        p.gn = (int)ceil_div(N, 256);
+        return launch(reinterpret_cast<const void*>(&fp8_pp_kernel<Elt>), (int64_t)p.gm * p.gn, 512, p, stream);
+    }
     if (ceil_div(M, 128) * ceil_div(N, 128) >= cu)
         return launch_tile<Elt, true, 128, 128, 2, 2, 2, false, false, false>(p, stream);
     return launch_tile<Elt, true, 64, 64, 2, 2, 4, false, false, false>(p, stream);
