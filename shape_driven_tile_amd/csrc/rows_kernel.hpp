@@ -21,6 +21,24 @@ __device__ __forceinline__ float widen(BF16, uint32_t bits16) {
     return __builtin_bit_cast(float, bits16 << 16);
 }
 
+// Eight elements of a row of K >= 8 from column k on, zeros past K: a partial chunk is
+// loaded as the row's last eight elements and moved down, and one past the row is that
+// load cleared, so that no load depends on a branch (with one around each, the eight of
+// a lane's rows wait for each other: 78 us for 8192 x 8192 fp16 codes).
+__device__ __forceinline__ uint4_t load_wide(const uint16_t* row, int k, int K) {
+    return *reinterpret_cast<const uint4_any_t*>(row + min(k, K - 8));
+}
+__device__ __forceinline__ uint4_t move_down(uint4_t v, int k, int K) {
+    const int s = k - (K - 8);                   // elements to move by (8 and more: none left)
+    if (s <= 0) return v;
+    if (s & 4) v = uint4_t{v[2], v[3], 0, 0};
+    if (s & 2) v = uint4_t{v[1], v[2], v[3], 0};
+    if (s & 1)
+        v = uint4_t{(v[0] >> 16) | (v[1] << 16), (v[1] >> 16) | (v[2] << 16), (v[2] >> 16) | (v[3] << 16),
+                    v[3] >> 16};
+    return s >= 8 ? uint4_t{0, 0, 0, 0} : v;
+}
+
 // Eight packed elements as fp32.
 template <typename Elt>
 __device__ __forceinline__ void unpack8(uint4_t v, float (&x)[8]) {
@@ -63,8 +81,20 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
     return max(v, turn16<1>(v));
 }
 
-// The largest magnitude of eight values as a bit pattern: the patterns' order is
-// the magnitudes', infinities and NaN above all.
+// The largest magnitude of eight packed elements, as an fp32 bit pattern: found among
+// the 16-bit patterns without their signs, whose order is the magnitudes' (infinities
+// and NaN above all).
+template <typename Elt>
+__device__ __forceinline__ uint32_t top8(uint4_t v) {
+    ushort2_t m = {0, 0};
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(ushort2_t, v[d] & 0x7fff7fffu));
+    const float x = widen(Elt{}, max(m[0], m[1]));
+    return __builtin_bit_cast(uint32_t, x);
+}
+
+// The largest magnitude of eight values as a bit pattern.
 __device__ __forceinline__ uint32_t top8(const float (&x)[8]) {
     uint32_t m = 0;
 #pragma unroll
@@ -133,18 +163,22 @@ __global__ __launch_bounds__(256) void fp8_quantize_rows_kernel(Fp8Quant p) {
     const int k = (int)(blockIdx.x % p.nct) * 2048 + t * 8;
     const int valid = p.K - k;
     uint4_t v[RPT];
+    if constexpr (RPT == 1) {                    // any K
+        v[0] = uint4_t{0, 0, 0, 0};
+        if (valid > 0) v[0] = load8(p.X + r0 * p.ldx + k, valid);
+    } else {
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-        v[i] = uint4_t{0, 0, 0, 0};
-        if (r0 + i < p.rows) v[i] = load8(p.X + (r0 + i) * p.ldx + k, valid);
+        for (int i = 0; i < RPT; ++i)
+            v[i] = load_wide(p.X + min(r0 + i, p.rows - 1) * p.ldx, k, p.K);
     }
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
         if (r0 + i >= p.rows) break;
-        float x[8];
-        unpack8<Elt>(v[i], x);
-        const float scale = fp8_scale(max16(top8(x)));
+        if constexpr (RPT > 1) v[i] = move_down(v[i], k, p.K);
+        const float scale = fp8_scale(max16(top8<Elt>(v[i])));
         if (valid > 0) {
+            float x[8];
+            unpack8<Elt>(v[i], x);
             store_codes(p.Q + (r0 + i) * p.ldq + k, fp8_codes(x, scale), valid);
             if ((t & 15) == 0) p.S[(int64_t)(k >> 7) * p.lds + r0 + i] = scale;
         }
@@ -152,7 +186,8 @@ __global__ __launch_bounds__(256) void fp8_quantize_rows_kernel(Fp8Quant p) {
 }
 
 // Scales for each block of 128 rows x 128 columns: one workgroup a block.
-template <typename Elt>
+// WIDE: rows of 8 elements and more.
+template <typename Elt, bool WIDE>
 __global__ __launch_bounds__(256) void fp8_quantize_blocks_kernel(Fp8Quant p) {
     __shared__ uint32_t tops[4];
     const int t = threadIdx.x;
@@ -164,15 +199,19 @@ __global__ __launch_bounds__(256) void fp8_quantize_blocks_kernel(Fp8Quant p) {
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int64_t row = rb * 128 + i * 16 + (t >> 4);
-        v[i] = uint4_t{0, 0, 0, 0};
-        if (row < p.rows) v[i] = load8(p.X + row * p.ldx + k, valid);
+        // rows past the last repeat it
+        const uint16_t* row = p.X + min(rb * 128 + i * 16 + (t >> 4), p.rows - 1) * p.ldx;
+        if constexpr (WIDE) {
+            v[i] = load_wide(row, k, p.K);
+        } else {
+            v[i] = uint4_t{0, 0, 0, 0};
+            if (valid > 0) v[i] = load8(row + k, valid);
+        }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float x[8];
-        unpack8<Elt>(v[i], x);
-        top = max(top, top8(x));
+        if constexpr (WIDE) v[i] = move_down(v[i], k, p.K);
+        top = max(top, top8<Elt>(v[i]));
     }
     top = max16(top);
     top = max(top, (uint32_t)__shfl_xor((int)top, 16));
@@ -214,17 +253,20 @@ __global__ __launch_bounds__(256) void fp8_dequantize_kernel(Fp8Dequant p) {
     float s[RPT];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-        const int64_t row = r0 + i;
-        c[i] = uint2_t{0, 0};
-        s[i] = 0.0f;
-        if (row >= p.rows) continue;
-        const uint8_t* q = p.Q + row * p.ldq + k;
-        if (valid >= 8) {
-            c[i] = *reinterpret_cast<const uint2_t*>(q);
+        const int64_t row = min(r0 + i, p.rows - 1);
+        const uint8_t* q = p.Q + row * p.ldq;
+        if constexpr (RPT > 1) {                 // K >= 8: as load_wide
+            typedef uint2_t __attribute__((aligned(1))) uint2_any_t;
+            c[i] = *reinterpret_cast<const uint2_any_t*>(q + min(k, p.K - 8));
         } else {
+            c[i] = uint2_t{0, 0};
+            if (valid >= 8) {
+                c[i] = *reinterpret_cast<const uint2_t*>(q + k);
+            } else {
 #pragma unroll
-            for (int d = 0; d < 8; ++d)
-                if (d < valid) c[i][d >> 2] |= (uint32_t)q[d] << (8 * (d & 3));
+                for (int d = 0; d < 8; ++d)
+                    if (d < valid) c[i][d >> 2] |= (uint32_t)q[k + d] << (8 * (d & 3));
+            }
         }
         s[i] = p.block == 1 ? p.S[(int64_t)(k >> 7) * p.lds + row]
                             : p.S[(row >> 7) * p.lds + (k >> 7)];
@@ -232,6 +274,8 @@ __global__ __launch_bounds__(256) void fp8_dequantize_kernel(Fp8Dequant p) {
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
         if (r0 + i >= p.rows) break;
+        if (RPT > 1 && valid < 8)
+            c[i] = __builtin_bit_cast(uint2_t, __builtin_bit_cast(uint64_t, c[i]) >> (8 * (8 - valid)));
         float x[8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -309,16 +353,27 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void rms_norm_kernel(Norm p) {
     for (int i = 0; i < CH; ++i) {
         const int k = (i * T + t) * 8;
         a[i] = b[i] = w[i] = uint4_t{0, 0, 0, 0};
-        if (k < p.K) {
-            a[i] = load8(p.X + row * p.ldx + k, p.K - k);
-            if (p.R) b[i] = load8(p.R + row * p.ldr + k, p.K - k);
-            if (p.W) w[i] = load8(p.W + k, p.K - k);
+        if constexpr (T == 64) {                 // any K
+            if (k < p.K) {
+                a[i] = load8(p.X + row * p.ldx + k, p.K - k);
+                if (p.R) b[i] = load8(p.R + row * p.ldr + k, p.K - k);
+                if (p.W) w[i] = load8(p.W + k, p.K - k);
+            }
+        } else {
+            a[i] = load_wide(p.X + row * p.ldx, k, p.K);
+            if (p.R) b[i] = load_wide(p.R + row * p.ldr, k, p.K);
+            if (p.W) w[i] = load_wide(p.W, k, p.K);
         }
     }
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int k = (i * T + t) * 8;
+        if constexpr (T > 64) {
+            a[i] = move_down(a[i], k, p.K);
+            b[i] = move_down(b[i], k, p.K);
+            w[i] = move_down(w[i], k, p.K);
+        }
         unpack8<Elt>(a[i], v[i]);
         if (p.R) {
             // the sum as it is kept, rounded to the type, is what is normed
@@ -379,54 +434,124 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void rms_norm_backward_kernel(No
     __shared__ float dws[PER > 1 ? PER * CH * 64 * 8 : 1];
     const int t = T == 64 ? threadIdx.x & 63 : threadIdx.x;
     const int sub = T == 64 ? threadIdx.x >> 6 : 0;
-    float dw[CH][8], g[CH][8];
+    float dw[CH][8];
+    uint4_t w[CH];                               // packed: half the registers
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int k = (i * T + t) * 8;
+        const uint32_t one = pack2<Elt>(1.0f, 1.0f);
+        w[i] = uint4_t{one, one, one, one};
+        if (p.W && k < p.K) w[i] = load8(p.W + k, p.K - k);
+#pragma unroll
+        for (int d = 0; d < 8; ++d) dw[i][d] = 0.0f;
+    }
+    const int64_t step = (int64_t)gridDim.x * PER;
+    auto load = [&](int64_t row, int i, uint4_t& a, uint4_t& b, uint4_t& c) {
+        const int k = (i * T + t) * 8;
+        a = b = c = uint4_t{0, 0, 0, 0};
+        if constexpr (T == 64) {                 // any K
+            if (k < p.K) {
+                a = load8(p.X + row * p.ldx + k, p.K - k);
+                b = load8(p.DY + row * p.lddy + k, p.K - k);
+                if (p.DT) c = load8(p.DT + row * p.lddt + k, p.K - k);
+            }
+        } else {
+            a = load_wide(p.X + row * p.ldx, k, p.K);
+            b = load_wide(p.DY + row * p.lddy, k, p.K);
+            if (p.DT) c = load_wide(p.DT + row * p.lddt, k, p.K);
+        }
+    };
+    // A chunk's n, dn and dy.
+    auto values = [&](int i, uint4_t a, uint4_t b, float rstd, float (&n)[8], float (&dn)[8], float (&dy)[8]) {
+        const int k = (i * T + t) * 8;
+        float g[8];
+        asm volatile("" : "+v"(w[i]));           // unpacked here each time
+        unpack8<Elt>(w[i], g);
+        unpack8<Elt>(T > 64 ? move_down(a, k, p.K) : a, n);
+        unpack8<Elt>(T > 64 ? move_down(b, k, p.K) : b, dy);
 #pragma unroll
         for (int d = 0; d < 8; ++d) {
-            dw[i][d] = 0.0f;
-            g[i][d] = 1.0f;
+            n[d] *= rstd;
+            dn[d] = dy[d] * g[d];
         }
-        if (p.W && k < p.K) unpack8<Elt>(load8(p.W + k, p.K - k), g[i]);
-    }
-    for (int64_t row = (int64_t)blockIdx.x * PER + sub; row < p.rows; row += (int64_t)gridDim.x * PER) {
+    };
+    auto store = [&](int64_t row, int i, uint4_t c, float rstd, float inner, const float (&n)[8],
+                     const float (&dn)[8]) {
+        const int k = (i * T + t) * 8;
+        if (k >= p.K) return;
+        float dt[8];
+        unpack8<Elt>(T > 64 ? move_down(c, k, p.K) : c, dt);
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+            dt[d] = __builtin_fmaf(rstd, __builtin_fmaf(-n[d], inner, dn[d]), dt[d]);
+        store8(p.DX + row * p.lddx + k, pack8<Elt>(dt), p.K - k);
+    };
+    int64_t row = (int64_t)blockIdx.x * PER + sub;
+    if constexpr (CH > 2) {
+        // Long rows, whose values do not fit the registers beside the sums: read again
+        // from the caches for the second pass.
+        for (; row < p.rows; row += step) {
+            const float rstd = p.rstd_in[row];
+            float inner = 0.0f;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                uint4_t a, b, c;
+                float n[8], dn[8], dy[8];
+                load(row, i, a, b, c);
+                values(i, a, b, rstd, n, dn, dy);
+#pragma unroll
+                for (int d = 0; d < 8; ++d) inner = __builtin_fmaf(dn[d], n[d], inner);
+            }
+            inner = row_sum<T>(inner, sm) / (float)p.K;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                uint4_t a, b, c;
+                float n[8], dn[8], dy[8];
+                load(row, i, a, b, c);
+                values(i, a, b, rstd, n, dn, dy);
+#pragma unroll
+                for (int d = 0; d < 8; ++d) dw[i][d] = __builtin_fmaf(dy[d], n[d], dw[i][d]);
+                store(row, i, c, rstd, inner, n, dn);
+            }
+        }
+    } else if (row < p.rows) {
+        // The next row is on its way while this one is worked on, where a wave may have
+        // the registers (8192 x 2048: 35.6 -> 32.1 us; 2048 x 16384 by 1024 threads, which
+        // spill: 77 -> 91).
+        constexpr bool AHEAD = T <= 256;
         uint4_t a[CH], b[CH], c[CH];
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int k = (i * T + t) * 8;
-            a[i] = b[i] = c[i] = uint4_t{0, 0, 0, 0};
-            if (k < p.K) {
-                a[i] = load8(p.X + row * p.ldx + k, p.K - k);
-                b[i] = load8(p.DY + row * p.lddy + k, p.K - k);
-                if (p.DT) c[i] = load8(p.DT + row * p.lddt + k, p.K - k);
+        for (int i = 0; i < CH; ++i) load(row, i, a[i], b[i], c[i]);
+        float rstd = p.rstd_in[row];
+        while (true) {
+            float n[CH][8], dn[CH][8], inner = 0.0f;
+            uint4_t dt[CH];
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                float dy[8];
+                values(i, a[i], b[i], rstd, n[i], dn[i], dy);
+                dt[i] = c[i];
+#pragma unroll
+                for (int d = 0; d < 8; ++d) {
+                    dw[i][d] = __builtin_fmaf(dy[d], n[i][d], dw[i][d]);
+                    inner = __builtin_fmaf(dn[i][d], n[i][d], inner);
+                }
             }
-        }
-        const float rstd = p.rstd_in[row];
-        float n[CH][8], dy[CH][8], inner = 0.0f;
+            const float now = rstd;
+            const int64_t next = row + step;
+            const bool more = next < p.rows;
+            auto fetch = [&]() {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            unpack8<Elt>(a[i], n[i]);
-            unpack8<Elt>(b[i], dy[i]);
+                for (int i = 0; i < CH; ++i) load(next, i, a[i], b[i], c[i]);
+                rstd = p.rstd_in[next];
+            };
+            if (AHEAD && more) fetch();
+            inner = row_sum<T>(inner, sm) / (float)p.K;
 #pragma unroll
-            for (int d = 0; d < 8; ++d) {
-                n[i][d] *= rstd;
-                dw[i][d] = __builtin_fmaf(dy[i][d], n[i][d], dw[i][d]);
-                dy[i][d] *= g[i][d];
-                inner = __builtin_fmaf(dy[i][d], n[i][d], inner);
-            }
-        }
-        inner = row_sum<T>(inner, sm) / (float)p.K;
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int k = (i * T + t) * 8;
-            if (k >= p.K) continue;
-            float dt[8];
-            unpack8<Elt>(c[i], dt);
-#pragma unroll
-            for (int d = 0; d < 8; ++d)
-                dt[d] = __builtin_fmaf(rstd, __builtin_fmaf(-n[i][d], inner, dy[i][d]), dt[d]);
-            store8(p.DX + row * p.lddx + k, pack8<Elt>(dt), p.K - k);
+            for (int i = 0; i < CH; ++i) store(row, i, dt[i], now, inner, n[i], dn[i]);
+            if (!more) break;
+            if (!AHEAD) fetch();
+            row = next;
         }
     }
     if (!p.dw_part) return;
