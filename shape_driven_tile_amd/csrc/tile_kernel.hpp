@@ -159,7 +159,8 @@ struct Operand {
         }
         return (P * 16 + fr) * 128 + (fq ^ swz_pp(fr)) * 16;
     }
-    // Eight values, or 16 codes.
+    // Eight values, or 16 codes.  (Turned fragments by the compiler's own read: it holds
+    // one back until every load into LDS issued before it has landed.)
     static __device__ __forceinline__ int4_t fragment(const int4_t* stage, int at, int j, int h) {
         const char* base = reinterpret_cast<const char*>(stage);
         if constexpr (TURNED) {
@@ -171,6 +172,44 @@ struct Operand {
             return int4_t{lo[0], lo[1], hi[0], hi[1]};
         }
         return *reinterpret_cast<const int4_t*>(base + (at ^ (h * 64)) + j * 2048);
+    }
+    // Both halves of parts 0 .. F - 1.  Turned ones two parts at a time, each in one
+    // block with its wait, so that loads for later k-tiles stay in flight.
+    template <int F>
+    static __device__ __forceinline__ void fragments(const int4_t* stage, int at, int4_t (&f)[F][2]) {
+        if constexpr (TURNED) {
+            static_assert(F % 2 == 0, "parts in pairs");
+            const uint32_t base =
+                (uint32_t) reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)stage);
+#pragma unroll
+            for (int j = 0; j < F; j += 2) {
+                int2_t v[8];
+                asm volatile(
+                    "ds_read_b64_tr_b16 %0, %8\n\t"
+                    "ds_read_b64_tr_b16 %1, %8 offset:%10\n\t"
+                    "ds_read_b64_tr_b16 %2, %8 offset:%11\n\t"
+                    "ds_read_b64_tr_b16 %3, %8 offset:%12\n\t"
+                    "ds_read_b64_tr_b16 %4, %9\n\t"
+                    "ds_read_b64_tr_b16 %5, %9 offset:%10\n\t"
+                    "ds_read_b64_tr_b16 %6, %9 offset:%11\n\t"
+                    "ds_read_b64_tr_b16 %7, %9 offset:%12\n\t"
+                    "s_waitcnt lgkmcnt(0)"
+                    : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]),
+                      "=&v"(v[6]), "=&v"(v[7])
+                    : "v"(base + (uint32_t)(at ^ (j * 32))), "v"(base + (uint32_t)(at ^ (j * 32 + 32))),
+                      "i"(4 * UPR * 16), "i"(32 * UPR * 16), "i"(36 * UPR * 16)
+                    : "memory");
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    f[j + q / 2][q % 2] =
+                        int4_t{v[2 * q][0], v[2 * q][1], v[2 * q + 1][0], v[2 * q + 1][1]};
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < F; ++j) f[j][h] = fragment(stage, at, j, h);
+        }
     }
 };
 
@@ -407,13 +446,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
     float scale[FM];
     auto read = [&](int stage) {
         const int4_t* base = smem + stage * STAGE;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int j = 0; j < FM; ++j) fa[j][h] = OpA::fragment(base, at_a, j, h);
-#pragma unroll
-            for (int i = 0; i < FN; ++i) fb[i][h] = OpB::fragment(base + OpA::UNITS, at_b, i, h);
-        }
+        OpA::template fragments<FM>(base, at_a, fa);
+        OpB::template fragments<FN>(base + OpA::UNITS, at_b, fb);
         if constexpr (FP8) {
             const float* sc = reinterpret_cast<const float*>(base + OpA::UNITS + OpB::UNITS);
             const float sb = sc[32];
@@ -464,8 +498,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
 
     const bool ragged = (!TA || !TB) && (p.L * Z) % 128 != 0;
     for (int j = 0; j < NS && first + j < end; ++j) load(j);
-    int s = 0;
-    for (int kt = first; kt < end; ++kt) {
+    int s = 0, kt = first;
+    auto step = [&](auto tail) {
         // k-tile kt has landed; the one or more after it may be on their way
         const int younger = min(end - 1 - kt, NS - 1);
         if (NS > 3 && younger == 3)
@@ -478,10 +512,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
             wait_global_loads<0>();
         barrier();
         read(s);
-        if (ragged) {
-            const int k = kt >= p.nkt ? kt - p.nkt : kt;
-            if (k == p.nkt - 1) clear_tail(k);
-        }
+        if constexpr (decltype(tail)::value) clear_tail(p.nkt - 1);
         mma(0, FN / 2);
         pin();
         barrier();                                // every wave has read stage s
@@ -489,6 +520,15 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
         mma(FN / 2, FN);
         pin();
         s = (s + 1 == NS) ? 0 : s + 1;
+        ++kt;
+    };
+    // A product's last k-tile, if it is partial, has a copy of the step of its own.
+    while (kt < end) {
+        const int stop = min(end, kt < p.nkt ? p.nkt : 2 * p.nkt) - (ragged ? 1 : 0);
+        const bool partial = ragged && (stop + 1 == p.nkt || stop + 1 == 2 * p.nkt);
+        const int whole = ragged && !partial ? stop + 1 : stop;
+        while (kt < whole) step(std::false_type{});
+        if (partial) step(std::true_type{});
     }
 
     if (p.splits > 1) {

@@ -223,10 +223,8 @@ __global__ __launch_bounds__(512) void tile_pp_kernel(TileGemm p) {
         }
         wait_lds();
         __builtin_amdgcn_sched_barrier(0);
-        if (ragged) {
-            const int k = i >= p.nkt ? i - p.nkt : i;
-            if (k == p.nkt - 1) clear_tail(k);
-        }
+        // (a first product that another is added to ends before the last k-tile)
+        if (ragged && (LEFT == 0 || (!GATED && i == p.nkt - 1))) clear_tail(p.nkt - 1);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
         mfma_tile();
