@@ -136,14 +136,17 @@ struct Operand {
                 bytes = (uint32_t)((rows - 1) * ld + ((L * z + 3) & ~3) - k * 128);
             }
         }
-        __device__ __forceinline__ __amdgpu_buffer_rsrc_t next() {
+        // `some` false: a descriptor of nothing, which the loads go through without a
+        // branch around them.
+        __device__ __forceinline__ __amdgpu_buffer_rsrc_t next(bool some = true) {
             if constexpr (TURNED) {
-                const __amdgpu_buffer_rsrc_t r = make_rsrc(at, (uint32_t)((min(64, left) - 1) * (int)ld + end));
+                const uint32_t n = (uint32_t)((min(64, left) - 1) * (int)ld + end);
+                const __amdgpu_buffer_rsrc_t r = make_rsrc(at, some ? n : 0u);
                 at += 64 * ld;
                 left -= 64;
                 return r;
             }
-            const __amdgpu_buffer_rsrc_t r = make_rsrc(at, bytes);
+            const __amdgpu_buffer_rsrc_t r = make_rsrc(at, some ? bytes : 0u);
             at += 128;
             bytes -= 128;
             return r;
@@ -320,6 +323,16 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t split_slot(const TileGemm& p, 
     return make_rsrc(p.ws + ((tile * p.splits + split) * waves + wave) * FLOATS, FLOATS * 4);
 }
 
+// Waits until at most the youngest n (<= MOST) of the k-tiles on their way, of L loads
+// each, have not landed.
+template <int MOST, int L>
+__device__ __forceinline__ void wait_tiles(int n) {
+    if constexpr (MOST > 0) {
+        if (n < MOST) return wait_tiles<MOST - 1, L>(n);
+    }
+    wait_global_loads<MOST * L>();
+}
+
 // ---- the tiled product -----------------------------------------------------------------
 // Output tiles of BM x BN by WM x WN waves, NS stages; two workgroups a CU, one's
 // reads and waits under the other's MFMAs.  The loads of the k-tile NS further on go
@@ -342,7 +355,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
     static_assert(!FP8 || (!TA && !TB && !GATED && RW <= 32 && BN <= 128), "8 bits: K-major operands");
     static_assert(!GATED || (!TB && FN % 4 == 0), "a wave's parts of both matrices, in pairs");
     static_assert(GATED || FN % 2 == 0, "parts in pairs");
-    static_assert(2 * NS * STAGE * 16 <= 160 * 1024, "two workgroups fit the LDS");
+    static_assert(NS * STAGE * 16 <= 160 * 1024, "the stages fit the LDS");
     __shared__ int4_t smem[NS * STAGE];
 
     const int t = threadIdx.x;
@@ -409,16 +422,18 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
         scale_step = lane < 32 ? p.ldsa : 1;
     }
 
+    int coming = first;                           // the k-tile that the next load takes
     auto load = [&](int stage) {
         int4_t* base = smem + stage * STAGE;
+        const bool some = coming < end;
         if constexpr (FP8)
-            dma4(scale_at + load_k * scale_step,
+            dma4(scale_at + min(load_k, p.nkt - 1) * scale_step,
                  reinterpret_cast<float*>(base + OpA::UNITS + OpB::UNITS + wave * 16));
-        const __amdgpu_buffer_rsrc_t ra = sa.next(), rb = sb.next();
+        const __amdgpu_buffer_rsrc_t ra = sa.next(some), rb = sb.next(some);
 #pragma unroll
         for (int j = 0; j < OpA::DMA; ++j) dma16(ra, base + (wave * OpA::DMA + j) * 64, voff_a[j], 0);
         if constexpr (GATED) {
-            const __amdgpu_buffer_rsrc_t r2 = sb2.next();
+            const __amdgpu_buffer_rsrc_t r2 = sb2.next(some);
 #pragma unroll
             for (int j = 0; j < OpB::DMA; ++j) {
                 const bool second = ((wave * OpB::DMA + j) * 8) % WTN >= WTN / 2;
@@ -429,7 +444,12 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
             for (int j = 0; j < OpB::DMA; ++j)
                 dma16(rb, base + OpA::UNITS + (wave * OpB::DMA + j) * 64, voff_b[j], 0);
         }
-        if (++load_k == p.nkt && p.products == 2) {       // on to the second product
+        ++coming;
+        ++load_k;
+    };
+    // The loads have come to the end of a product that another is added to.
+    auto second_product = [&]() {
+        if (load_k == p.nkt && p.products == 2) {
             load_k = 0;
             start(true);
         }
@@ -442,43 +462,49 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
         for (int j = 0; j < FM; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 
     const int at_a = OpA::place(wave_m * FM, lane), at_b = OpB::place(wave_n * FN, lane);
-    int4_t fa[FM][2], fb[FN][2];
-    float scale[FM];
-    auto read = [&](int stage) {
+    struct Frags {
+        int4_t a[FM][2], b[FN][2];
+        float sa[FM], sb;                         // scales
+    };
+    auto read_a = [&](int stage, Frags& f) {
         const int4_t* base = smem + stage * STAGE;
-        OpA::template fragments<FM>(base, at_a, fa);
-        OpB::template fragments<FN>(base + OpA::UNITS, at_b, fb);
+        OpA::template fragments<FM>(base, at_a, f.a);
         if constexpr (FP8) {
             const float* sc = reinterpret_cast<const float*>(base + OpA::UNITS + OpB::UNITS);
-            const float sb = sc[32];
+            f.sb = sc[32];
 #pragma unroll
             for (int j = 0; j < FM; ++j) {
                 const int r = (wave_m * FM + j) * 16 + (lane & 15);
-                scale[j] = sc[(r / RW) * 64 + r % RW] * sb;
+                f.sa[j] = sc[(r / RW) * 64 + r % RW];
             }
         }
+    };
+    auto read_b = [&](int stage, Frags& f) {
+        OpB::template fragments<FN>(smem + stage * STAGE + OpA::UNITS, at_b, f.b);
     };
     // The last k-tile of a product: what its K-major rows hold past their end is
     // not zero.
-    auto clear_tail = [&](int k) {
+    auto clear_tail = [&](Frags& f) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int4_t m = tail_mask(p.L * Z - k * 128 - (4 * h + (lane >> 4)) * 16);
+            const int4_t m = tail_mask(p.L * Z - (p.nkt - 1) * 128 - (4 * h + (lane >> 4)) * 16);
             if constexpr (!TA) {
 #pragma unroll
-                for (int j = 0; j < FM; ++j) fa[j][h] &= m;
+                for (int j = 0; j < FM; ++j) f.a[j][h] &= m;
             }
             if constexpr (!TB) {
 #pragma unroll
-                for (int i = 0; i < FN; ++i) fb[i][h] &= m;
+                for (int i = 0; i < FN; ++i) f.b[i][h] &= m;
             }
         }
     };
-    auto mma = [&](int i0, int i1) {
+    auto mma = [&](const Frags& f, int i0, int i1) {
 #pragma unroll
-        for (int i = i0; i < i1; ++i)
+        for (int j = 0; j < FM; ++j) {
+            const float scale = FP8 ? f.sa[j] * f.sb : 0.0f;
 #pragma unroll
-            for (int j = 0; j < FM; ++j) tile_mma<Elt, FP8>(acc[i][j], fb[i], fa[j], FP8 ? scale[j] : 0.f);
+            for (int i = i0; i < i1; ++i) tile_mma<Elt, FP8>(acc[i][j], f.b[i], f.a[j], scale);
+        }
     };
     // The MFMAs are values to the compiler: an empty asm that reads them keeps it
     // from moving them past the waits and barriers that follow.
@@ -496,39 +522,74 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
     };
 
-    const bool ragged = (!TA || !TB) && (p.L * Z) % 128 != 0;
-    for (int j = 0; j < NS && first + j < end; ++j) load(j);
-    int s = 0, kt = first;
-    auto step = [&](auto tail) {
-        // k-tile kt has landed; the one or more after it may be on their way
-        const int younger = min(end - 1 - kt, NS - 1);
-        if (NS > 3 && younger == 3)
-            wait_global_loads<3 * L>();
-        else if (NS > 2 && younger == 2)
-            wait_global_loads<2 * L>();
-        else if (NS > 1 && younger == 1)
-            wait_global_loads<L>();
-        else
-            wait_global_loads<0>();
+    // All but the youngest N k-tiles on their way have landed, for every wave.
+    auto landed = [&](auto n) {
+        wait_global_loads<decltype(n)::value * L>();
         barrier();
-        read(s);
-        if constexpr (decltype(tail)::value) clear_tail(p.nkt - 1);
-        mma(0, FN / 2);
+    };
+    typedef std::integral_constant<int, NS - 1> Others;
+    typedef std::integral_constant<int, NS - 2> Later;
+    const bool ragged = (!TA || !TB) && (p.L * Z) % 128 != 0;
+    Frags f[2];
+    int s = 0, kt = first;
+    // One k-tile, not the last: its fragments are in registers (f[P]); the next k-tile's
+    // are read while it is multiplied.  The loads into the stage that it has left go out
+    // between the MFMAs: a CU takes in 64 bytes a clock, and a wave that issues them in
+    // one go waits out the others' too (1024^2, a 64 x 64 tile's k-tile: 640 clocks).
+    auto step = [&](auto which) {
+        constexpr int P = decltype(which)::value;
+        const int sn = (s + 1 == NS) ? 0 : s + 1;
+        landed(Later{});                          // and every wave has read stage s
+        if constexpr (!TA) read_a(sn, f[P ^ 1]);
+        if constexpr (!TB) read_b(sn, f[P ^ 1]);
+        __builtin_amdgcn_sched_barrier(0);
+        load(s);
+        mma(f[P], 0, FN / 2);
+#pragma unroll
+        for (int m = 0; m < L; ++m) {             // masks: 0x008 MFMA, 0x020 global read
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, FM * FN * (FP8 ? 1 : 2) / ((TA || TB ? 2 : 1) * L), 0);
+        }
+        // turned fragments come with their wait: under the MFMAs issued before them
+        if constexpr (TA) read_a(sn, f[P ^ 1]);
+        mma(f[P], FN / 2, FN);
+        if constexpr (TB) read_b(sn, f[P ^ 1]);
         pin();
-        barrier();                                // every wave has read stage s
-        if (kt + NS < end) load(s);
-        mma(FN / 2, FN);
-        pin();
-        s = (s + 1 == NS) ? 0 : s + 1;
+        s = sn;
         ++kt;
     };
-    // A product's last k-tile, if it is partial, has a copy of the step of its own.
-    while (kt < end) {
-        const int stop = min(end, kt < p.nkt ? p.nkt : 2 * p.nkt) - (ragged ? 1 : 0);
-        const bool partial = ragged && (stop + 1 == p.nkt || stop + 1 == 2 * p.nkt);
-        const int whole = ragged && !partial ? stop + 1 : stop;
-        while (kt < whole) step(std::false_type{});
-        if (partial) step(std::true_type{});
+    if (first < end) {
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            load(j);
+            second_product();
+        }
+        landed(Others{});
+        read_a(0, f[0]);
+        read_b(0, f[0]);
+        while (kt < end) {
+            // the next k-tile that is partial, the last, or whose load ends a product
+            const int product = kt < p.nkt ? p.nkt : 2 * p.nkt;
+            int special = (ragged ? min(product, end) : end) - 1;
+            if (p.products == 2 && coming <= p.nkt) special = min(special, p.nkt - 1 - NS);
+            while (kt + 2 <= special) {
+                step(std::integral_constant<int, 0>{});
+                step(std::integral_constant<int, 1>{});
+            }
+            // one k-tile by itself
+            if (ragged && kt == product - 1) clear_tail(f[0]);
+            mma(f[0], 0, FN);
+            pin();
+            if (kt + 1 == end) break;
+            landed(Later{});
+            load(s);
+            second_product();
+            s = (s + 1 == NS) ? 0 : s + 1;
+            ++kt;
+            read_a(s, f[0]);
+            read_b(s, f[0]);
+        }
+        wait_global_loads<0>();                   // none is left when the workgroup ends
     }
 
     if (p.splits > 1) {
@@ -650,15 +711,7 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
     for (int j = 0; j < min(n, NS); ++j) load(wave + j * NW, j);
     int stage = 0;
     for (int j = 0; j < n; ++j) {
-        const int younger = min(n - 1 - j, NS - 1);
-        if (NS > 3 && younger == 3)
-            wait_global_loads<NS == 4 ? 3 * L : 0>();
-        else if (NS > 2 && younger == 2)
-            wait_global_loads<NS >= 3 ? 2 * L : 0>();
-        else if (NS > 1 && younger == 1)
-            wait_global_loads<L>();
-        else
-            wait_global_loads<0>();
+        wait_tiles<NS - 1, L>(min(n - 1 - j, NS - 1));
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("" ::: "memory");
         const int4_t* at = mine + stage * STAGE;
