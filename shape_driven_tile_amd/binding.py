@@ -44,10 +44,11 @@ EXPORTS = (
     "sdt_moe_experts_workspace_size", "moe_experts_mx4_f16", "moe_experts_mx4_bf16",
     "fp8_quantize_f16", "fp8_quantize_bf16",
     "fp8_dequantize_f16", "fp8_dequantize_bf16", "fp8_dequantize_f32",
-    "gemm_fp8_f16", "gemm_fp8_bf16",
+    "gemm_fp8_f16", "gemm_fp8_bf16", "sdt_gemm_fp8_workspace_size",
     "rms_norm_f16", "rms_norm_bf16", "rms_norm_backward_f16", "rms_norm_backward_bf16",
     "sdt_rms_norm_workspace_size",
-    "gated_ff_f16", "gated_ff_bf16", "gated_ff_backward_f16", "gated_ff_backward_bf16",
+    "gated_ff_f16", "gated_ff_bf16", "sdt_gated_ff_split_size",
+    "gated_ff_backward_f16", "gated_ff_backward_bf16",
     "sdt_gated_ff_workspace_size",
     "gemm_f16_nn", "gemm_bf16_nn", "gemm_f16_tn", "gemm_bf16_tn",
     "sdt_gemm_turned_workspace_size",
@@ -137,7 +138,7 @@ class SdtNormGrad(ctypes.Structure):
 
 class SdtGatedFf(ctypes.Structure):
     _fields_ = _fields("M i N i K i x p ldx i gate p ldgate i up p ldup i act n h p ldh i "
-                       "g p ldg i u p ldu i wide n")
+                       "g p ldg i u p ldu i wide n workspace p workspace_bytes i")
 
 
 class SdtGatedFfGrad(ctypes.Structure):
@@ -279,7 +280,7 @@ def _declare_ffn(L):
         getattr(L, f"fp8_quantize_{t}").argtypes = [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int,
                                                     _vp]
         getattr(L, f"gemm_fp8_{t}").argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
-                                                _i64, _vp, _i64, _vp]
+                                                _i64, _vp, _i64, _vp, _i64, _vp]
         for layout in ("nn", "tn"):
             getattr(L, f"gemm_{t}_{layout}").argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp,
                                                          _i64, _vp, _i64, _vp]
@@ -290,7 +291,9 @@ def _declare_ffn(L):
         getattr(L, f"fp8_dequantize_{t}").argtypes = [_i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64,
                                                       _vp]
     L.sdt_rms_norm_workspace_size.argtypes = [_i64, _i64]
-    L.sdt_gated_ff_workspace_size.argtypes = [_i64, _i64, _i64]
+    for name in ("sdt_gated_ff_workspace_size", "sdt_gated_ff_split_size",
+                 "sdt_gemm_fp8_workspace_size"):
+        getattr(L, name).argtypes = [_i64, _i64, _i64]
     L.sdt_gemm_turned_workspace_size.argtypes = [_i64, _i64, _i64]
     for name in EXPORTS[EXPORTS.index("fp8_quantize_f16"):]:
         getattr(L, name).restype = _i64 if name.startswith("sdt_") else _int
@@ -1287,28 +1290,69 @@ def fp8_dequantize_f32(m: Fp8, Y, stream=None) -> None:
     _dequantize8("fp8_dequantize_f32", m, Y, torch.float32, stream)
 
 
-def _gemm_fp8(entry, A, B, C, dtype, stream):
-    if A.K != B.K or C.shape != (A.rows, B.rows):
-        raise ValueError(f"shape mismatch A({A.rows}, {A.K}) B({B.rows}, {B.K}) C{tuple(C.shape)}")
+_split_sizes = {}          # (entry point, sizes): bytes that let the product be split
+
+
+def _split_size(entry, M, N, K):
+    key = (entry, M, N, K)
+    need = _split_sizes.get(key)
+    if need is None:
+        need = int(getattr(lib(), entry)(M, N, K))
+        if len(_split_sizes) >= 4096:
+            _split_sizes.clear()
+        _split_sizes[key] = need
+    return need
+
+
+def _split_buffer(need, workspace, where, stream):
+    """A work buffer's address, its bytes and what keeps it: `workspace`, or `need` bytes made here, of
+    the stream that runs the call (the allocator gives them to no other while they are in use)."""
+    if workspace is not None or need <= 0:
+        return (*_buffer(workspace, where), workspace)
+    import torch
+    if stream is None:
+        t = torch.empty(need, dtype=torch.uint8, device=where)
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty(need, dtype=torch.uint8, device=where)
+    return t.data_ptr(), need, t
+
+
+def gemm_fp8_workspace_size(M: int, N: int, K: int) -> int:
+    """Workspace bytes that let gemm_fp8 split a C [M, N] along K (0: no split)."""
+    v = int(lib().sdt_gemm_fp8_workspace_size(int(M), int(N), int(K)))
+    if v < 0:
+        raise SdtError(SDT_ERR_INVALID_ARG, "sdt_gemm_fp8_workspace_size")
+    return v
+
+
+def _gemm_fp8(entry, A, B, C, dtype, workspace, stream):
+    M, N, K = A.rows, B.rows, A.K
+    if K != B.K or C.shape != (M, N):
+        raise ValueError(f"shape mismatch A({M}, {K}) B({N}, {B.K}) C{tuple(C.shape)}")
     if A.block != 1 or B.block != 128:
         raise ValueError(f"A must have blocks of 1 x 128 and B of 128 x 128, not {A.block} and {B.block}")
     pc, ldc = _rows(C, "C", dtype)
-    if not (A.device == B.device == C.get_device()):
-        raise _apart(entry, A.device, B.device, C.get_device())
-    _check(getattr(lib(), entry)(A.rows, B.rows, A.K, *A._args(), *B._args(), pc, ldc,
+    where = A.device
+    if not (where == B.device == C.get_device()):
+        raise _apart(entry, where, B.device, C.get_device())
+    need = _split_size("sdt_gemm_fp8_workspace_size", M, N, K) if M > 16 else 0
+    wp, wn, _kept = _split_buffer(need, workspace, where, stream)
+    _check(getattr(lib(), entry)(M, N, K, *A._args(), *B._args(), pc, ldc, wp, wn,
                                  _stream_handle(stream)), entry)
 
 
-def gemm_fp8_f16(A: Fp8, B: Fp8, C, stream=None) -> None:
+def gemm_fp8_f16(A: Fp8, B: Fp8, C, workspace=None, stream=None) -> None:
     """C[M, N] = A[M, K] . B[N, K]^T for 8-bit matrices (A of block 1, B of block
-    128), fp32 accumulate, fp16 out."""
+    128), fp32 accumulate, fp16 out.  workspace: a uint8 device tensor of
+    gemm_fp8_workspace_size bytes instead of one that the call makes."""
     import torch
-    _gemm_fp8("gemm_fp8_f16", A, B, C, torch.float16, stream)
+    _gemm_fp8("gemm_fp8_f16", A, B, C, torch.float16, workspace, stream)
 
 
-def gemm_fp8_bf16(A: Fp8, B: Fp8, C, stream=None) -> None:
+def gemm_fp8_bf16(A: Fp8, B: Fp8, C, workspace=None, stream=None) -> None:
     import torch
-    _gemm_fp8("gemm_fp8_bf16", A, B, C, torch.bfloat16, stream)
+    _gemm_fp8("gemm_fp8_bf16", A, B, C, torch.bfloat16, workspace, stream)
 
 
 # ---- the norm and the gated feed-forward block ------------------------------------------
@@ -1436,10 +1480,19 @@ def _factors(g, u, shape, dtype, where):
             1 if kept is torch.float32 else 0)
 
 
-def gated_ff(x, gate, up, h, act: str = "silu", g=None, u=None, stream=None) -> None:
+def gated_ff_split_size(M: int, N: int, K: int) -> int:
+    """Workspace bytes that let gated_ff split its products along K (0: no split)."""
+    v = int(lib().sdt_gated_ff_split_size(int(M), int(N), int(K)))
+    if v < 0:
+        raise SdtError(SDT_ERR_INVALID_ARG, "sdt_gated_ff_split_size")
+    return v
+
+
+def gated_ff(x, gate, up, h, act: str = "silu", g=None, u=None, workspace=None, stream=None) -> None:
     """h [M, N] = a(x . gate^T) * (x . up^T) for x [M, K], gate and up [N, K], float16 or
     bfloat16; a: silu, or gelu in its tanh form.  g and u [M, N], float32 or the type:
-    the two products, kept for gated_ff_backward."""
+    the two products, kept for gated_ff_backward.  workspace: a uint8 device tensor of
+    gated_ff_split_size bytes instead of one that the call makes."""
     kind = _kind16(x, "x")
     px, ldx = _rows(x, "x", x.dtype)
     dtype, where = x.dtype, x.get_device()
@@ -1448,8 +1501,10 @@ def gated_ff(x, gate, up, h, act: str = "silu", g=None, u=None, stream=None) -> 
     pu, ldu = _matrix(up, "up", (N, K), dtype, where)
     ph, ldh = _matrix(h, "h", (M, N), dtype, where)
     entry = "gated_ff_" + kind
+    need = _split_size("sdt_gated_ff_split_size", M, N, K) if M > 16 else 0
+    wp, wn, _kept = _split_buffer(need, workspace, where, stream)
     args = SdtGatedFf(M, N, K, px, ldx, pg, ldg, pu, ldu, _act(act), ph, ldh,
-                      *_factors(g, u, (M, N), dtype, where))
+                      *_factors(g, u, (M, N), dtype, where), wp, wn)
     _check(getattr(lib(), entry)(ctypes.byref(args), _stream_handle(stream)), entry)
 
 

@@ -155,9 +155,13 @@ int launch_tile(TileGemm& p, void* stream) {
     const int rc = launch(
         reinterpret_cast<const void*>(&tile_gemm_kernel<Elt, FP8, BM, BN, WM, WN, NS, TA, TB, GATED>), grid,
         WM * WN * 64, p, stream);
-    if (rc != SDT_OK || p.splits == 1) return rc;
-    return launch(reinterpret_cast<const void*>(&tile_reduce_kernel<Elt, BM, BN, WM, WN>),
-                  (int64_t)p.gm * p.gn * p.batch, WM * WN * 64, p, stream);
+    // only 64-row tiles are split: where 128-row ones are taken they fill the CUs
+    if constexpr (BM == 64) {
+        if (rc == SDT_OK && p.splits > 1)
+            return launch(reinterpret_cast<const void*>(&tile_reduce_kernel<Elt, BM, BN, WM, WN, GATED>),
+                          (int64_t)p.gm * p.gn * p.batch, WM * WN * 64, p, stream);
+    }
+    return rc;
 }
 
 template <typename Elt, bool TA, bool TB, bool GATED>
@@ -168,27 +172,86 @@ int launch_pp(TileGemm& p, void* stream) {
                   (int64_t)p.gm * p.gn * p.batch, 512, p, stream);
 }
 
-// Whether 256 x 256 tiles, a workgroup a CU, beat 128 x 128 ones, two.
-bool large_tiles(int64_t t256, int64_t cu) { return t256 >= cu; }
+// Whether t256 tiles of 256 x 256, a workgroup a CU, beat t128 of 128 x 128, two: by a
+// CU's time in us, `kt` k-tiles of 128 bytes a tile (16 bits, gated and turned, and 8
+// bits; fitted to 18 sizes).  A round of 256 x 256 tiles takes 1.3 a k-tile and 11
+// besides, one of 128 x 128 tiles 0.9 and 4.5 (8 bits 1.05 and 4), with a tile a CU or
+// less 0.72 and 4 (0.85 and 3.5).  4096^3: nn 94 (256) against 119, 8 bits 56 against
+// 73; 2048 x 4096 x 4096: 87 against 63 and 45 against 39; 6000 x 6000 x 500: 71
+// against 54 and 54 against 37.
+bool large_tiles(int64_t t256, int64_t t128, int64_t kt, int64_t cu, bool fp8) {
+    const double k = (double)kt;
+    const double full = fp8 ? 1.05 * k + 4.0 : 0.9 * k + 4.5, half = fp8 ? 0.85 * k + 3.5 : 0.72 * k + 4.0;
+    const int64_t rest = t128 % (2 * cu);
+    const double small = (double)(t128 / (2 * cu)) * full + (rest > cu ? full : rest > 0 ? half : 0.0);
+    return (double)ceil_div(t256, cu) * (1.3 * k + 11.0) < small;
+}
 
-template <typename Elt, bool FP8, bool GATED, int PB, int NMB, int NS>
+// Up to kFewRows rows.
+constexpr int kFewRows = 16;
+template <typename Elt, bool FP8, bool GATED, int PB, int NS>
 int launch_rows(TileGemm& p, void* stream) {
-    p.gm = (int)ceil_div(p.M, NMB * 16);
+    p.gm = 1;
     p.gn = (int)ceil_div(p.N, PB * 16);
-    return launch(reinterpret_cast<const void*>(&rows_gemm_kernel<Elt, FP8, GATED, 4, PB, NMB, NS>),
-                  (int64_t)p.gm * p.gn, 256, p, stream);
+    return launch(reinterpret_cast<const void*>(&rows_gemm_kernel<Elt, FP8, GATED, 4, PB, NS>), p.gn, 256, p,
+                  stream);
+}
+
+// How a product with a workspace is laid out: its tiles' side and the workgroups
+// along each tile's k-tiles.  `from`: 128 x 128 tiles that are worth more than 64 x 64
+// ones (256 x 12288 x 4096, 192 of them: turned 45-51 us against 49, 8 bits 30 against
+// 28).  Where tiles leave CUs idle, each split keeps eight k-tiles at least.
+struct Split {
+    int side, splits;
+    int64_t bytes;
+};
+Split plan_split(int64_t M, int64_t N, int64_t kt, int batch, int64_t from) {
+    Split s;
+    const int64_t t128 = ceil_div(M, 128) * ceil_div(N, 128) * batch;
+    s.side = t128 >= from ? 128 : 64;
+    const int64_t tiles = ceil_div(M, s.side) * ceil_div(N, s.side) * batch;
+    int64_t n = tiles > 0 ? kSplitTarget / tiles : 1;
+    n = std::min(n, kt / 8);
+    s.splits = s.side == 128 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(n, 16));
+    s.bytes = s.splits > 1 ? tiles * s.splits * 64 * 64 * 4 : 0;
+    return s;
+}
+Split plan_turned(int64_t M, int64_t N, int64_t kt, int batch) {
+    return plan_split(M, N, kt, batch, kSplitTarget * 3 / 4);
+}
+Split plan_split8(int64_t M, int64_t N, int64_t K) {
+    return plan_split(M, N, ceil_div(K, 128), 1, kSplitTarget);
+}
+// Gated: 64 columns of both matrices a tile.  128 rows only where there are tiles for
+// more than one a CU (512 x 4096 x 4096, 256 of them: 51 us against 36; 1024 x 4096 x
+// 4096, 512: 60 against 70).
+Split plan_gated(int64_t M, int64_t N, int64_t K) {
+    Split s;
+    s.side = ceil_div(M, 128) * ceil_div(N, 64) >= kSplitTarget * 3 / 2 ? 128 : 64;
+    const int64_t tiles = ceil_div(M, s.side) * ceil_div(N, 64), kt = ceil_div(K, 64);
+    const int64_t n = std::min(tiles > 0 ? kSplitTarget / tiles : 1, kt / 8);
+    s.splits = s.side == 128 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(n, 16));
+    s.bytes = s.splits > 1 ? tiles * s.splits * 64 * 128 * 4 : 0;
+    return s;
+}
+void take_split(TileGemm& p, const Split& s, void* ws, int64_t ws_bytes) {
+    if (s.splits > 1 && ws_bytes >= s.bytes) {
+        p.splits = s.splits;
+        p.ws = static_cast<float*>(ws);
+    }
 }
 
 template <typename Elt>
 int gemm8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* SA, int64_t ldsa,
-          const void* B, int64_t ldb, const float* SB, int64_t ldsb, void* C, int64_t ldc, void* stream) {
-    if (M < 0 || N < 0 || K < 0) return SDT_ERR_INVALID_ARG;
+          const void* B, int64_t ldb, const float* SB, int64_t ldsb, void* C, int64_t ldc, void* ws, int64_t ws_bytes,
+          void* stream) {
+    if (M < 0 || N < 0 || K < 0 || ws_bytes < 0 || (ws_bytes > 0 && !ws)) return SDT_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return SDT_OK;
     int rc = check_out(M, N, C, ldc);
     if (rc == SDT_OK && K > 0) rc = check_fp8(M, K, A, lda, SA, ldsa, 1);
     if (rc == SDT_OK && K > 0) rc = check_fp8(N, K, B, ldb, SB, ldsb, 128);
     if (rc != SDT_OK) return rc;
-    if (M > kMaxRows || N > kMaxRows) return SDT_ERR_UNSUPPORTED;
+    if (M > kMaxRows || N > kMaxRows || misaligned(ws, 16)) return SDT_ERR_UNSUPPORTED;
     DeviceInfo dev;
     rc = device_info(&dev);
     if (rc != SDT_OK) return rc;
@@ -203,47 +266,28 @@ int gemm8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const flo
     p.ldsa = ldsa;
     p.ldsb = ldsb;
     p.ldc[0] = ldc;
-    const int64_t cu = dev.num_cu;
-    if (M <= 16) return launch_rows<Elt, true, false, 2, 1, 3>(p, stream);
-    if (M <= 64) return launch_rows<Elt, true, false, 2, 4, 2>(p, stream);
-    if (large_tiles(ceil_div(M, 256) * ceil_div(N, 256), cu)) {
+    if (M <= kFewRows) return launch_rows<Elt, true, false, 2, 3>(p, stream);
+    if (large_tiles(ceil_div(M, 256) * ceil_div(N, 256), ceil_div(M, 128) * ceil_div(N, 128), p.nkt, dev.num_cu,
+                    true)) {
         p.gm = (int)ceil_div(M, 256);
         p.gn = (int)ceil_div(N, 256);
         return launch(reinterpret_cast<const void*>(&fp8_pp_kernel<Elt>), (int64_t)p.gm * p.gn, 512, p, stream);
     }
-    if (ceil_div(M, 128) * ceil_div(N, 128) >= cu)
-        return launch_tile<Elt, true, 128, 128, 2, 2, 2, false, false, false>(p, stream);
-    return launch_tile<Elt, true, 64, 64, 2, 2, 4, false, false, false>(p, stream);
-}
-
-// How a product with a workspace is laid out: its tiles' side and the workgroups
-// along each tile's k-tiles.
-struct Split {
-    int side, splits;
-    int64_t bytes;
-};
-Split plan_split(int64_t M, int64_t N, int64_t kt, int batch) {
-    Split s;
-    const int64_t t128 = ceil_div(M, 128) * ceil_div(N, 128) * batch;
-    s.side = t128 >= kSplitTarget * 3 / 4 ? 128 : 64;
-    const int64_t tiles = ceil_div(M, s.side) * ceil_div(N, s.side) * batch;
-    int64_t n = tiles > 0 ? kSplitTarget / tiles : 1;
-    n = std::min(n, kt / 8);
-    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(n, 16));
-    s.bytes = s.splits > 1 ? tiles * s.splits * s.side * s.side * 4 : 0;
-    return s;
+    const Split s = plan_split8(M, N, K);
+    take_split(p, s, ws, ws_bytes);
+    return s.side == 128 ? launch_tile<Elt, true, 128, 128, 2, 2, 2, false, false, false>(p, stream)
+                         : launch_tile<Elt, true, 64, 64, 2, 2, 4, false, false, false>(p, stream);
 }
 
 template <typename Elt, bool TA, bool TB>
 int launch_split(TileGemm& p, void* ws, int64_t ws_bytes, int num_cu, void* stream) {
-    const Split s = plan_split(p.M, p.N, (int64_t)p.nkt * p.products, p.batch);
+    const int64_t kt = (int64_t)p.nkt * p.products;
+    const Split s = plan_turned(p.M, p.N, kt, p.batch);
     const bool strides = p.products == 1 || (p.lda[0] == p.lda[1] && p.ldb[0] == p.ldb[1]);
-    if (strides && large_tiles(ceil_div(p.M, 256) * ceil_div(p.N, 256) * p.batch, num_cu))
+    if (strides && large_tiles(ceil_div(p.M, 256) * ceil_div(p.N, 256) * p.batch,
+                               ceil_div(p.M, 128) * ceil_div(p.N, 128) * p.batch, kt, num_cu, false))
         return launch_pp<Elt, TA, TB, false>(p, stream);
-    if (s.splits > 1 && ws_bytes >= s.bytes) {
-        p.splits = s.splits;
-        p.ws = static_cast<float*>(ws);
-    }
+    take_split(p, s, ws, ws_bytes);
     return s.side == 128 ? launch_tile<Elt, false, 128, 128, 2, 2, 2, TA, TB, false>(p, stream)
                          : launch_tile<Elt, false, 64, 64, 2, 2, 4, TA, TB, false>(p, stream);
 }
@@ -412,7 +456,8 @@ int gated(const sdt_gated_ff* a, void* stream) {
     if (rc == SDT_OK && K > 0) rc = check_in(N, K, a->up, a->ldup);
     if (rc == SDT_OK && (a->g || a->u)) rc = check_factors(M, N, a->g, a->ldg, a->u, a->ldu, a->wide);
     if (rc != SDT_OK) return rc;
-    if (M > kMaxRows || N > kMaxRows || K > kMaxK) return SDT_ERR_UNSUPPORTED;
+    if (a->workspace_bytes < 0 || (a->workspace_bytes > 0 && !a->workspace)) return SDT_ERR_INVALID_ARG;
+    if (M > kMaxRows || N > kMaxRows || K > kMaxK || misaligned(a->workspace, 16)) return SDT_ERR_UNSUPPORTED;
     DeviceInfo dev;
     rc = device_info(&dev);
     if (rc != SDT_OK) return rc;
@@ -431,13 +476,14 @@ int gated(const sdt_gated_ff* a, void* stream) {
     p.ldu = a->ldu;
     p.wide = a->wide;
     p.act = a->act;
-    if (M <= 16) return launch_rows<Elt, false, true, 1, 1, 4>(p, stream);
-    if (M <= 64) return launch_rows<Elt, false, true, 1, 4, 2>(p, stream);
-    if (large_tiles(ceil_div(M, 256) * ceil_div(N, 128), dev.num_cu))
+    if (M <= kFewRows) return launch_rows<Elt, false, true, 1, 4>(p, stream);
+    if (large_tiles(ceil_div(M, 256) * ceil_div(N, 128), ceil_div(M, 128) * ceil_div(N, 64), p.nkt, dev.num_cu,
+                    false))
         return launch_pp<Elt, false, false, true>(p, stream);
-    if (ceil_div(M, 128) * ceil_div(N, 64) >= dev.num_cu)
-        return launch_tile<Elt, false, 128, 128, 2, 2, 2, false, false, true>(p, stream);
-    return launch_tile<Elt, false, 64, 128, 2, 2, 3, false, false, true>(p, stream);
+    const Split s = plan_gated(M, N, K);
+    take_split(p, s, a->workspace, a->workspace_bytes);
+    return s.side == 128 ? launch_tile<Elt, false, 128, 128, 2, 2, 2, false, false, true>(p, stream)
+                         : launch_tile<Elt, false, 64, 128, 2, 2, 3, false, false, true>(p, stream);
 }
 
 // The backward's buffer: dg and du side by side (rows of 2 N' elements), then the
@@ -450,8 +496,8 @@ GatedLayout gated_layout(int64_t M, int64_t N, int64_t K) {
     const int64_t np = ceil_div(N, 8) * 8;
     l.ld = 2 * np;
     l.at = ceil_div(M * l.ld * 2, 256) * 256;
-    l.bytes = l.at + std::max(plan_split(M, K, 2 * ceil_div(N, 64), 1).bytes,
-                              plan_split(N, K, ceil_div(M, 64), 2).bytes);
+    l.bytes = l.at + std::max(plan_turned(M, K, 2 * ceil_div(N, 64), 1).bytes,
+                              plan_turned(N, K, ceil_div(M, 64), 2).bytes);
     return l;
 }
 
@@ -570,13 +616,20 @@ int fp8_dequantize_f32(int64_t rows, int64_t K, const void* Q, int64_t ldq, cons
 }
 int gemm_fp8_f16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* SA, int64_t ldsa,
                  const void* B, int64_t ldb, const float* SB, int64_t ldsb, void* C, int64_t ldc,
-                 void* stream) {
-    return sdt::gemm8<F16>(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, stream);
+                 void* workspace, int64_t workspace_bytes, void* stream) {
+    return sdt::gemm8<F16>(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, workspace, workspace_bytes,
+                           stream);
 }
 int gemm_fp8_bf16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* SA, int64_t ldsa,
-                  const void* B, int64_t ldb, const float* SB, int64_t ldsb, void* C, int64_t ldc,
-                  void* stream) {
-    return sdt::gemm8<BF16>(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, stream);
+                 const void* B, int64_t ldb, const float* SB, int64_t ldsb, void* C, int64_t ldc,
+                 void* workspace, int64_t workspace_bytes, void* stream) {
+    return sdt::gemm8<BF16>(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, workspace, workspace_bytes,
+                           stream);
+}
+
+int64_t sdt_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0 || M > sdt::kMaxRows || N > sdt::kMaxRows || K > sdt::kMaxK) return -1;
+    return M <= sdt::kFewRows ? 0 : sdt::plan_split8(M, N, K).bytes;
 }
 
 int rms_norm_f16(const sdt_norm* args, void* stream) { return sdt::norm<F16>(args, stream); }
@@ -594,6 +647,10 @@ int64_t sdt_rms_norm_workspace_size(int64_t rows, int64_t K) {
 
 int gated_ff_f16(const sdt_gated_ff* args, void* stream) { return sdt::gated<F16>(args, stream); }
 int gated_ff_bf16(const sdt_gated_ff* args, void* stream) { return sdt::gated<BF16>(args, stream); }
+int64_t sdt_gated_ff_split_size(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0 || M > sdt::kMaxRows || N > sdt::kMaxRows || K > sdt::kMaxK) return -1;
+    return M <= sdt::kFewRows ? 0 : sdt::plan_gated(M, N, K).bytes;
+}
 int gated_ff_backward_f16(const sdt_gated_ff_grad* args, void* stream) {
     return sdt::gated_backward<F16>(args, stream);
 }
@@ -623,7 +680,7 @@ int gemm_bf16_tn(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, co
 }
 int64_t sdt_gemm_turned_workspace_size(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K < 0 || M > sdt::kMaxRows || N > sdt::kMaxRows || K > sdt::kMaxRows) return -1;
-    return sdt::plan_split(M, N, sdt::ceil_div(K, 64), 1).bytes;
+    return sdt::plan_turned(M, N, sdt::ceil_div(K, 64), 1).bytes;
 }
 
 }  // extern "C"

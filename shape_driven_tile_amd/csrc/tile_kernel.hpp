@@ -601,7 +601,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
 }
 
 // Adds the splits of a tile in their order and stores it.
-template <typename Elt, int BM, int BN, int WM, int WN>
+template <typename Elt, int BM, int BN, int WM, int WN, bool GATED>
 __global__ __launch_bounds__(WM * WN * 64) void tile_reduce_kernel(TileGemm p) {
     constexpr int NW = WM * WN;
     constexpr int WTM = BM / WM, WTN = BN / WN;
@@ -615,33 +615,34 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_reduce_kernel(TileGemm p) {
     gp.gm = p.gm;
     gp.gn = p.gn;
     int64_t m0, n0;
-    grouped_origin(gp, tile, BM, BN, m0, n0);
+    constexpr int BNO = GATED ? BN / 2 : BN;
+    grouped_origin(gp, tile, BM, BNO, m0, n0);
     floatx4_t acc[FN][FM];
     load_partial<0, false>(acc, split_slot<FN, FM>(p, blockIdx.x, 0, wave, NW), lane);
     for (int s = 1; s < p.splits; ++s)
         load_partial<0, true>(acc, split_slot<FN, FM>(p, blockIdx.x, s, wave, NW), lane);
     const int rows = (int)min((int64_t)BM, p.M - m0);
-    tile_store<Elt, false, FN, FM>(p, batch, acc, (uint32_t)m0 + wave_m * WTM, rows - wave_m * WTM,
-                                   (uint32_t)n0 + wave_n * WTN, lane);
+    tile_store<Elt, GATED, FN, FM>(p, batch, acc, (uint32_t)m0 + wave_m * WTM, rows - wave_m * WTM,
+                                   (uint32_t)n0 + wave_n * (WTN * BNO / BN), lane);
 }
 
 // ---- few rows ------------------------------------------------------------------------
-// PB * 16 columns of C (gated: of each matrix) and NMB * 16 rows a workgroup, whose
+// PB * 16 columns of C (gated: of each matrix) and up to 16 rows a workgroup, whose
 // NW waves take every NW-th k-tile and stream B once.  Every wave has LDS of its
 // own, so the loop has no barrier: rows come straight into it in whole 128-byte
 // lines, NS k-tiles in flight, and are read from there as fragments.  The waves'
 // sums are added in wave order.  Bound by B's stream.
-template <typename Elt, bool FP8, bool GATED, int NW, int PB, int NMB, int NS>
+template <typename Elt, bool FP8, bool GATED, int NW, int PB, int NS>
 __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
     constexpr int MATS = GATED ? 2 : 1;
     constexpr int BN = PB * 16;
     constexpr int Z = FP8 ? 1 : 2;
-    constexpr int A_UNITS = NMB * 128, B_UNITS = BN * 8;       // of one matrix
+    constexpr int A_UNITS = 128, B_UNITS = BN * 8;       // of one matrix
     constexpr int S_UNITS = FP8 ? 32 : 0;                      // 64 floats of rows, 64 of columns
     constexpr int STAGE = A_UNITS + MATS * B_UNITS + S_UNITS;
     constexpr int A_DMA = A_UNITS / 64, B_DMA = B_UNITS / 64;
     constexpr int L = A_DMA + MATS * B_DMA + (FP8 ? 2 : 0);
-    constexpr int SUMS = MATS * PB * NMB * 64;                 // 16-byte units
+    constexpr int SUMS = MATS * PB * 64;                       // 16-byte units
     constexpr int MINE = NS * STAGE > SUMS ? NS * STAGE : SUMS;
     static_assert(!FP8 || !GATED, "one matrix of scales");
     static_assert(NW * MINE * 16 <= 160 * 1024, "LDS");
@@ -650,9 +651,8 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fr = lane & 15, fq = lane >> 4;
     const int w = xcd_remap(blockIdx.x, gridDim.x, p.nxcd);
-    const int g = w / p.gn;
-    const int64_t m0 = (int64_t)g * (NMB * 16), n0 = (int64_t)(w - g * p.gn) * BN;
-    const int rows_a = (int)min((int64_t)NMB * 16, p.M - m0);
+    const int64_t n0 = (int64_t)w * BN;
+    const int rows_a = p.M;
     const int rows_b = (int)min((int64_t)BN, p.N - n0);
 
     const int chunk = ((lane & 7) ^ swz_pp(lane >> 3)) * 16;
@@ -666,13 +666,13 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
             voff_b[m][j] = (uint32_t)((j * 8 + (lane >> 3)) * p.ldb[m]) + chunk;
     const float *sa_at = nullptr, *sb_at = nullptr;
     if constexpr (FP8) {
-        sa_at = p.SA + min(m0 + lane, (int64_t)p.M - 1);
+        sa_at = p.SA + min(lane, p.M - 1);
         sb_at = p.SB + (n0 >> 7) * p.ldsb;
     }
     int4_t* const mine = smem + wave * MINE;
-    typedef Operand<false, NMB * 16, 1> OpA;
+    typedef Operand<false, 16, 1> OpA;
     typedef Operand<false, BN, 1> OpB;
-    const uint8_t* const a0 = p.A[0] + m0 * p.lda[0];
+    const uint8_t* const a0 = p.A[0];
     const uint8_t* const b0[2] = {p.B[0] + n0 * p.ldb[0], GATED ? p.B[1] + n0 * p.ldb[1] : nullptr};
     // bytes up to the last row's end, which is rounded up to 4
     const int row_end = (p.L * Z + 3) & ~3;
@@ -698,13 +698,11 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
         }
     };
 
-    floatx4_t acc[MATS][PB][NMB];
+    floatx4_t acc[MATS][PB];
 #pragma unroll
     for (int m = 0; m < MATS; ++m)
 #pragma unroll
-        for (int i = 0; i < PB; ++i)
-#pragma unroll
-            for (int j = 0; j < NMB; ++j) acc[m][i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < PB; ++i) acc[m][i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 
     const int place = OpA::place(0, lane);        // the same in B's rows
     const int n = (p.nkt - wave + NW - 1) / NW;   // this wave's k-tiles (0 or less: none)
@@ -715,23 +713,20 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("" ::: "memory");
         const int4_t* at = mine + stage * STAGE;
-        int4_t fa[NMB][2], fb[MATS][PB][2];
+        int4_t fa[2], fb[MATS][PB][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int i = 0; i < NMB; ++i) fa[i][h] = OpA::fragment(at, place, i, h);
+            fa[h] = OpA::fragment(at, place, 0, h);
 #pragma unroll
             for (int m = 0; m < MATS; ++m)
 #pragma unroll
                 for (int i = 0; i < PB; ++i)
                     fb[m][i][h] = OpB::fragment(at + A_UNITS + m * B_UNITS, place, i, h);
         }
-        float scale[NMB];
+        float scale = 0.0f;
         if constexpr (FP8) {
             const float* sc = reinterpret_cast<const float*>(at + A_UNITS + MATS * B_UNITS);
-            const float sb = sc[64];
-#pragma unroll
-            for (int i = 0; i < NMB; ++i) scale[i] = sc[i * 16 + fr] * sb;
+            scale = sc[fr] * sc[64];
         }
         wait_lds();
         __builtin_amdgcn_sched_barrier(0);
@@ -741,8 +736,7 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int4_t mask = tail_mask(p.L * Z - kt * 128 - (4 * h + fq) * 16);
-#pragma unroll
-                for (int i = 0; i < NMB; ++i) fa[i][h] &= mask;
+                fa[h] &= mask;
 #pragma unroll
                 for (int m = 0; m < MATS; ++m)
 #pragma unroll
@@ -752,10 +746,7 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
 #pragma unroll
         for (int m = 0; m < MATS; ++m)
 #pragma unroll
-            for (int i = 0; i < PB; ++i)
-#pragma unroll
-                for (int b = 0; b < NMB; ++b)
-                    tile_mma<Elt, FP8>(acc[m][i][b], fb[m][i], fa[b], FP8 ? scale[b] : 0.f);
+            for (int i = 0; i < PB; ++i) tile_mma<Elt, FP8>(acc[m][i], fb[m][i], fa, scale);
         stage = stage + 1 == NS ? 0 : stage + 1;
     }
 
@@ -763,27 +754,24 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
 #pragma unroll
     for (int m = 0; m < MATS; ++m)
 #pragma unroll
-        for (int i = 0; i < PB; ++i)
-#pragma unroll
-            for (int j = 0; j < NMB; ++j) red[((m * PB + i) * NMB + j) * 64 + lane] = acc[m][i][j];
+        for (int i = 0; i < PB; ++i) red[(m * PB + i) * 64 + lane] = acc[m][i];
     __syncthreads();
-    auto total = [&](int m, int i, int j) {
-        const floatx4_t* at = reinterpret_cast<const floatx4_t*>(smem) + ((m * PB + i) * NMB + j) * 64 + lane;
+    auto total = [&](int m, int i) {
+        const floatx4_t* at = reinterpret_cast<const floatx4_t*>(smem) + (m * PB + i) * 64 + lane;
         floatx4_t s = at[0];
 #pragma unroll
         for (int v = 1; v < NW; ++v) s += at[v * MINE];
         return s;
     };
-    for (int u = wave; u < PB * NMB; u += NW) {
-        const int i = u / NMB, j = u - i * NMB;
-        const int r = j * 16 + fr;
+    for (int i = wave; i < PB; i += NW) {
+        const int r = fr;
         const int c0 = (int)n0 + i * 16 + fq * 4;
         floatx4_t v[3];
-        v[0] = total(0, i, j);
+        v[0] = total(0, i);
         int outs = 1;
         if constexpr (GATED) {
             v[1] = v[0];
-            v[2] = total(1, i, j);
+            v[2] = total(1, i);
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[0][e] = act_mul(v[1][e], v[2][e], p.act);
             if (p.G) outs = 3;
@@ -795,13 +783,13 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
             const int64_t ld = o == 0 ? p.ldc[0] : o == 1 ? p.ldg : p.ldu;
             void* to = o == 0 ? static_cast<void*>(p.C[0]) : o == 1 ? p.G : p.U;
             if (GATED && o > 0 && p.wide) {
-                float* c = static_cast<float*>(to) + (m0 + r) * ld + c0;
+                float* c = static_cast<float*>(to) + r * ld + c0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (c0 + e < p.N) c[e] = v[o][e];
                 continue;
             }
-            uint16_t* c = static_cast<uint16_t*>(to) + (m0 + r) * ld + c0;
+            uint16_t* c = static_cast<uint16_t*>(to) + r * ld + c0;
             const uint32_t lo = pack2<Elt>(v[o][0], v[o][1]), hi = pack2<Elt>(v[o][2], v[o][3]);
             if (c0 + 3 < p.N) {
                 *reinterpret_cast<uint2_t*>(c) = uint2_t{lo, hi};

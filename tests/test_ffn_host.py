@@ -50,10 +50,12 @@ def test_dequantize_refusals(t, change, want):
     ({"ldc": 300}, UNSUPPORTED), ({"C": P + 8}, UNSUPPORTED), ({"A": None}, INVALID),
     ({"lda": 192}, INVALID), ({"lda": 200}, UNSUPPORTED), ({"ldsa": 9}, INVALID), ({"ldsb": 1}, INVALID),
     ({"B": P + 4}, UNSUPPORTED), ({"SB": P + 1}, UNSUPPORTED), ({"M": 0}, OK), ({"N": 0}, OK),
-    ({"M": 2 ** 31 - 200, "ldsa": 2 ** 31 - 1}, UNSUPPORTED),
+    ({"M": 2 ** 31 - 200, "ldsa": 2 ** 31 - 1}, UNSUPPORTED), ({"ws": None, "bytes": 4}, INVALID),
+    ({"bytes": -1}, INVALID), ({"ws": P + 8}, UNSUPPORTED),
 ])
 def test_gemm_refusals(t, change, want):
-    a = dict(M=10, N=300, K=200, A=P, lda=208, SA=P, ldsa=10, B=P, ldb=208, SB=P, ldsb=2, C=P, ldc=304)
+    a = dict(M=10, N=300, K=200, A=P, lda=208, SA=P, ldsa=10, B=P, ldb=208, SB=P, ldsb=2, C=P, ldc=304,
+             ws=P, bytes=1 << 20)
     a.update(change)
     assert call(f"gemm_fp8_{t}", *a.values(), None) == want
 
@@ -104,7 +106,7 @@ def test_norm_backward_refusals(t, change, want):
 
 
 GATED = dict(M=10, N=300, K=200, x=P, ldx=200, gate=P, ldgate=200, up=P, ldup=208, act=0, h=P, ldh=304,
-             g=P, ldg=300, u=P, ldu=300, wide=1)
+             g=P, ldg=300, u=P, ldu=300, wide=1, workspace=P, workspace_bytes=1 << 20)
 
 
 @pytest.mark.parametrize("t", ["f16", "bf16"])
@@ -114,6 +116,7 @@ GATED = dict(M=10, N=300, K=200, x=P, ldx=200, gate=P, ldgate=200, up=P, ldup=20
     ({"ldh": 300}, UNSUPPORTED), ({"h": P + 2}, UNSUPPORTED), ({"gate": P + 8}, UNSUPPORTED),
     ({"g": None}, INVALID), ({"ldu": 299}, INVALID), ({"wide": 2}, INVALID), ({"ldg": 301}, UNSUPPORTED),
     ({"wide": 0}, UNSUPPORTED), ({"ldgate": 1 << 22}, UNSUPPORTED), ({"M": 0}, OK), ({"N": 0}, OK),
+    ({"workspace": None}, INVALID), ({"workspace_bytes": -1}, INVALID), ({"workspace": P + 8}, UNSUPPORTED),
 ])
 def test_gated_refusals(t, change, want):
     assert call(f"gated_ff_{t}", _struct(sdt.SdtGatedFf, GATED, change), None) == want
@@ -162,6 +165,13 @@ def test_workspace_sizes():
     assert sdt.gated_ff_workspace_size(0, 300, 200) >= 0
     with pytest.raises(sdt.SdtError):
         sdt.gated_ff_workspace_size(1, -1, 1)
+    for size in (sdt.gemm_fp8_workspace_size, sdt.gated_ff_split_size):
+        assert size(16, 64, 8192) == 0                                  # streamed
+        assert size(64, 64, 8192) > 0
+        assert size(64, 64, 256) == 0
+        assert size(4096, 4096, 4096) == 0
+        with pytest.raises(sdt.SdtError):
+            size(-1, 1, 1)
     assert sdt.gemm_turned_workspace_size(8192, 8192, 8192) == 0        # tiles enough
     assert sdt.gemm_turned_workspace_size(64, 64, 8192) > 0             # one tile, long
     assert sdt.gemm_turned_workspace_size(64, 64, 100) == 0             # and short

@@ -248,6 +248,37 @@ def test_gemm_fp8(dtype, M, N, K, plain):
     assert untouched(full, N)
 
 
+@pytest.mark.parametrize("M, N, K", [(64, 100, 4000), (17, 64, 2048), (300, 250, 1100), (300, 250, 2200)])
+def test_split(M, N, K):
+    """Split along K through a buffer of junk: the bits of the call that makes its own;
+    without one, whole numbers' same bits unsplit."""
+    import torch
+    sdt = _sdt()
+    a, av = fp8_matrix(M, K, 1, 1, True)
+    b, bv = fp8_matrix(N, K, 128, 2, True)
+    want = (av @ bv.t()).float().bfloat16()
+    need = sdt.gemm_fp8_workspace_size(M, N, K)
+    assert (need > 0) == (K >= 16 * 128 - 127)               # eight k-tiles of 128 a split
+    for size in (need, 16):
+        c = torch.empty(M, -(-N // 8) * 8, dtype=torch.bfloat16, device=DEV)[:, :N]
+        sdt.gemm_fp8_bf16(a, b, c, workspace=torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV))
+        assert torch.equal(c, want)
+    x, gate, up = (rows_of(whole(s, torch.bfloat16, i), 8)[0] for i, s in enumerate([(M, K), (N, K), (N, K)]))
+    need = sdt.gated_ff_split_size(M, N, K)
+    assert need > 0
+    got = []
+    for size in (None, need, 16):
+        h = torch.empty(M, -(-N // 8) * 8, dtype=torch.bfloat16, device=DEV)[:, :N]
+        ws = None if size is None else torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV)
+        g, u = (out_like(M, N, torch.float32)[0] for _ in range(2))
+        sdt.gated_ff(x, gate, up, h, workspace=ws, g=g, u=u)
+        got.append((h, g, u))
+    assert torch.equal(got[0][1].double(), x.double() @ gate.double().t())
+    assert torch.equal(got[0][2].double(), x.double() @ up.double().t())
+    for other in got[1:]:
+        assert all(torch.equal(p, q) for p, q in zip(got[0], other))
+
+
 def test_gemm_fp8_all_codes():
     """Every pair of finite codes in a product of one term, subnormals among them."""
     import torch
@@ -676,6 +707,7 @@ def block(sdt, s):
     sdt.rms_norm_backward(s["t"], s["w"], s["rstd"], s["dn"], s["dx"], s["dw"], s["ws"], dtotal=s["dy"])
     sdt.fp8_quantize_bf16(s["n"], s["n8"])
     sdt.gemm_fp8_bf16(s["n8"], s["w8"], s["y8"])
+    sdt.gemm_fp8_bf16(s["h8"], s["down8"], s["z8"])           # through a buffer that the call makes
 
 
 def block_state(M=70, N=200, K=136):
@@ -685,7 +717,8 @@ def block_state(M=70, N=200, K=136):
     s = {"x": normal((M, K), t, 1), "r": normal((M, K), t, 2), "w": normal((K,), t, 3),
          "gate": normal((N, K), t, 4, K ** -0.5), "up": normal((N, K), t, 5, K ** -0.5),
          "down": normal((K, N), t, 6, N ** -0.5), "dy": normal((M, K), t, 7)}
-    s.update(n=e(M, K), t=e(M, K), h=e(M, N), y=e(M, K), dh=e(M, N), ddown=e(K, N), dn=e(M, K), dgate=e(N, K),
+    s["h8"], s["down8"] = fp8_matrix(M, 2100, 1, 8)[0], fp8_matrix(K, 2100, 128, 9)[0]
+    s.update(z8=e(M, K), n=e(M, K), t=e(M, K), h=e(M, N), y=e(M, K), dh=e(M, N), ddown=e(K, N), dn=e(M, K), dgate=e(N, K),
              dup=e(N, K), dx=e(M, K), y8=e(M, N), rstd=torch.empty(M, device=DEV),
              g=torch.empty(M, N, device=DEV), u=torch.empty(M, N, device=DEV), dw=torch.empty(K, device=DEV),
              n8=sdt.Fp8.empty(M, K, device=DEV), w8=sdt.Fp8.empty(N, K, block=128, device=DEV))
@@ -696,7 +729,7 @@ def block_state(M=70, N=200, K=136):
     return s
 
 
-OUTPUTS = ["n", "t", "h", "y", "dh", "ddown", "dn", "dgate", "dup", "dx", "dw", "y8", "g", "u", "rstd"]
+OUTPUTS = ["n", "t", "h", "y", "dh", "ddown", "dn", "dgate", "dup", "dx", "dw", "y8", "z8", "g", "u", "rstd"]
 
 
 def test_run_together_in_a_graph():
