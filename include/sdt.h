@@ -510,49 +510,50 @@ int moe_experts_mx4_bf16(const sdt_moe_layer* layer, const int32_t* idx, const f
                          void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ---- 8-bit matrices with a scale for each block of 128 ---------------------------------
- * Q: rows of K codes, OCP e4m3 (1 sign, 4 exponent, 3 fraction bits, largest 448; 0x7f
- * and 0xff NaN), ldq bytes apart.  S: fp32 scales, a value is its code times its block's
- * scale; `block` says what a block is:
- *   1    (activations) 128 consecutive k of one row: S[(k / 128) * lds + row], lds >= rows;
- *   128  (weights) 128 k of 128 rows: S[(row / 128) * lds + k / 128], lds >= ceil(K / 128).
- * Requirements everywhere: Q 16-byte aligned, ldq >= K a multiple of 16 (any for a single
- * row) below 2^23, S 4-byte aligned, K at most 2^23, lds at most 2^31 - 1. */
+ * Rows of K codes, OCP e4m3 (1 sign, 4 exponent, 3 fraction bits, largest 448; 0x7f and 0xff
+ * NaN), and fp32 scales: a value is its code times its block's scale.
+ * Requirements everywhere: q 16-byte aligned, ldq >= K a multiple of 16 (any for a single
+ * row) below 2^23, s 4-byte aligned, K at most 2^23, lds at most 2^31 - 1. */
+typedef struct sdt_fp8 {
+    void* q;        /* codes, rows ldq bytes apart */
+    int64_t ldq;
+    float* s;       /* scales, lds floats from row to row of them */
+    int64_t lds;
+    int block;      /* 1 (activations): a block is 128 consecutive k of one row, its scale
+                       s[(k / 128) * lds + row], lds >= rows;
+                       128 (weights): 128 k of 128 rows, s[(row / 128) * lds + k / 128], lds >=
+                       ceil(K / 128) */
+} sdt_fp8;
 
-/* Q, S = X (rows x K, row stride ldx >= K elements, any alignment of the element type).  A
+/* out = X (rows x K, row stride ldx >= K elements, any alignment of the element type).  A
  * block's scale is its largest magnitude / 448 in fp32, at least 2^-126; a code is the fp32
  * quotient x / scale rounded to nearest even.  A block that holds an infinity or a NaN has a
- * NaN scale and zero codes.  Bytes of Q past a row's K are left as they are.  rows == 0 or K
+ * NaN scale and zero codes.  Bytes of q past a row's K are left as they are.  rows == 0 or K
  * == 0 is a no-op. */
-int fp8_quantize_f16(int64_t rows, int64_t K, const void* X, int64_t ldx,
-                     void* Q, int64_t ldq, float* S, int64_t lds, int block, void* stream);
-int fp8_quantize_bf16(int64_t rows, int64_t K, const void* X, int64_t ldx,
-                      void* Q, int64_t ldq, float* S, int64_t lds, int block, void* stream);
+int fp8_quantize_f16(int64_t rows, int64_t K, const void* X, int64_t ldx, const sdt_fp8* out,
+                     void* stream);
+int fp8_quantize_bf16(int64_t rows, int64_t K, const void* X, int64_t ldx, const sdt_fp8* out,
+                      void* stream);
 
 /* Y (rows x K, row stride ldy >= K elements) = code * scale in fp32, rounded to the type
  * of the name. */
-int fp8_dequantize_f16(int64_t rows, int64_t K, const void* Q, int64_t ldq, const float* S,
-                       int64_t lds, int block, void* Y, int64_t ldy, void* stream);
-int fp8_dequantize_bf16(int64_t rows, int64_t K, const void* Q, int64_t ldq, const float* S,
-                        int64_t lds, int block, void* Y, int64_t ldy, void* stream);
-int fp8_dequantize_f32(int64_t rows, int64_t K, const void* Q, int64_t ldq, const float* S,
-                       int64_t lds, int block, void* Y, int64_t ldy, void* stream);
+int fp8_dequantize_f16(int64_t rows, int64_t K, const sdt_fp8* m, void* Y, int64_t ldy, void* stream);
+int fp8_dequantize_bf16(int64_t rows, int64_t K, const sdt_fp8* m, void* Y, int64_t ldy, void* stream);
+int fp8_dequantize_f32(int64_t rows, int64_t K, const sdt_fp8* m, void* Y, int64_t ldy, void* stream);
 
 /* C = A . B^T for A (M x K, block 1) and B (N x K, block 128): the sum over k of each block
  * on the MFMAs, times both scales (their product, in fp32, has to be finite), added in fp32,
  * rounded once to the type of the name.  A block's sum is in fp32, but the MFMA keeps each of
- * eight consecutive products to 2^-13 of the largest of the eight.  C as gemm_f16's: 16-byte aligned, ldc >= N
- * a multiple of 8 (any for a single row).  M == 0 or N == 0 is a no-op; K == 0 writes zeros.
- * Deterministic.  Up to 16 rows stream B once.  workspace: device memory, 16-byte aligned, no
- * initialisation; with at least sdt_gemm_fp8_workspace_size bytes (0: not needed) a product of few
- * tiles is split along K, the splits added in their order (fewer bytes, or NULL with 0: not
- * split).  Calls that share it are ordered. */
-int gemm_fp8_f16(int64_t M, int64_t N, int64_t K,
-                 const void* A, int64_t lda, const float* SA, int64_t ldsa,
-                 const void* B, int64_t ldb, const float* SB, int64_t ldsb,
+ * eight consecutive products to 2^-13 of the largest of the eight.  C as gemm_f16's: 16-byte
+ * aligned, ldc >= N a multiple of 8 (any for a single row).  M == 0 or N == 0 is a no-op; K ==
+ * 0 writes zeros.  Deterministic.  Up to 16 rows (64 of small weights) stream B once.
+ * workspace: device memory, 16-byte aligned, no initialisation; with at least
+ * sdt_gemm_fp8_workspace_size bytes (0: not needed) a product of few tiles is split along K,
+ * the splits added in their order (fewer bytes, or NULL with 0: not split).  Calls that share
+ * it are ordered. */
+int gemm_fp8_f16(int64_t M, int64_t N, int64_t K, const sdt_fp8* A, const sdt_fp8* B,
                  void* C, int64_t ldc, void* workspace, int64_t workspace_bytes, void* stream);
-int gemm_fp8_bf16(int64_t M, int64_t N, int64_t K,
-                  const void* A, int64_t lda, const float* SA, int64_t ldsa,
-                  const void* B, int64_t ldb, const float* SB, int64_t ldsb,
+int gemm_fp8_bf16(int64_t M, int64_t N, int64_t K, const sdt_fp8* A, const sdt_fp8* B,
                   void* C, int64_t ldc, void* workspace, int64_t workspace_bytes, void* stream);
 int64_t sdt_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K);   /* -1: outside the limits */
 

@@ -627,22 +627,22 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_reduce_kernel(TileGemm p) {
 }
 
 // ---- few rows ------------------------------------------------------------------------
-// PB * 16 columns of C (gated: of each matrix) and up to 16 rows a workgroup, whose
+// PB * 16 columns of C (gated: of each matrix) and up to NMB * 16 rows a workgroup, whose
 // NW waves take every NW-th k-tile and stream B once.  Every wave has LDS of its
 // own, so the loop has no barrier: rows come straight into it in whole 128-byte
 // lines, NS k-tiles in flight, and are read from there as fragments.  The waves'
 // sums are added in wave order.  Bound by B's stream.
-template <typename Elt, bool FP8, bool GATED, int NW, int PB, int NS>
+template <typename Elt, bool FP8, bool GATED, int NW, int PB, int NMB, int NS>
 __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
     constexpr int MATS = GATED ? 2 : 1;
     constexpr int BN = PB * 16;
     constexpr int Z = FP8 ? 1 : 2;
-    constexpr int A_UNITS = 128, B_UNITS = BN * 8;       // of one matrix
+    constexpr int A_UNITS = NMB * 128, B_UNITS = BN * 8;       // of one matrix
     constexpr int S_UNITS = FP8 ? 32 : 0;                      // 64 floats of rows, 64 of columns
     constexpr int STAGE = A_UNITS + MATS * B_UNITS + S_UNITS;
     constexpr int A_DMA = A_UNITS / 64, B_DMA = B_UNITS / 64;
     constexpr int L = A_DMA + MATS * B_DMA + (FP8 ? 2 : 0);
-    constexpr int SUMS = MATS * PB * 64;                       // 16-byte units
+    constexpr int SUMS = MATS * PB * NMB * 64;                 // 16-byte units
     constexpr int MINE = NS * STAGE > SUMS ? NS * STAGE : SUMS;
     static_assert(!FP8 || !GATED, "one matrix of scales");
     static_assert(NW * MINE * 16 <= 160 * 1024, "LDS");
@@ -670,7 +670,7 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
         sb_at = p.SB + (n0 >> 7) * p.ldsb;
     }
     int4_t* const mine = smem + wave * MINE;
-    typedef Operand<false, 16, 1> OpA;
+    typedef Operand<false, NMB * 16, 1> OpA;
     typedef Operand<false, BN, 1> OpB;
     const uint8_t* const a0 = p.A[0];
     const uint8_t* const b0[2] = {p.B[0] + n0 * p.ldb[0], GATED ? p.B[1] + n0 * p.ldb[1] : nullptr};
@@ -698,11 +698,13 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
         }
     };
 
-    floatx4_t acc[MATS][PB];
+    floatx4_t acc[MATS][PB][NMB];
 #pragma unroll
     for (int m = 0; m < MATS; ++m)
 #pragma unroll
-        for (int i = 0; i < PB; ++i) acc[m][i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < PB; ++i)
+#pragma unroll
+            for (int j = 0; j < NMB; ++j) acc[m][i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 
     const int place = OpA::place(0, lane);        // the same in B's rows
     const int n = (p.nkt - wave + NW - 1) / NW;   // this wave's k-tiles (0 or less: none)
@@ -713,20 +715,22 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("" ::: "memory");
         const int4_t* at = mine + stage * STAGE;
-        int4_t fa[2], fb[MATS][PB][2];
+        int4_t fa[NMB][2], fb[MATS][PB][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            fa[h] = OpA::fragment(at, place, 0, h);
+#pragma unroll
+            for (int j = 0; j < NMB; ++j) fa[j][h] = OpA::fragment(at, place, j, h);
 #pragma unroll
             for (int m = 0; m < MATS; ++m)
 #pragma unroll
                 for (int i = 0; i < PB; ++i)
                     fb[m][i][h] = OpB::fragment(at + A_UNITS + m * B_UNITS, place, i, h);
         }
-        float scale = 0.0f;
+        float scale[NMB] = {};
         if constexpr (FP8) {
             const float* sc = reinterpret_cast<const float*>(at + A_UNITS + MATS * B_UNITS);
-            scale = sc[fr] * sc[64];
+#pragma unroll
+            for (int j = 0; j < NMB; ++j) scale[j] = sc[j * 16 + fr] * sc[64];
         }
         wait_lds();
         __builtin_amdgcn_sched_barrier(0);
@@ -736,7 +740,8 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int4_t mask = tail_mask(p.L * Z - kt * 128 - (4 * h + fq) * 16);
-                fa[h] &= mask;
+#pragma unroll
+                for (int j = 0; j < NMB; ++j) fa[j][h] &= mask;
 #pragma unroll
                 for (int m = 0; m < MATS; ++m)
 #pragma unroll
@@ -746,7 +751,9 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
 #pragma unroll
         for (int m = 0; m < MATS; ++m)
 #pragma unroll
-            for (int i = 0; i < PB; ++i) tile_mma<Elt, FP8>(acc[m][i], fb[m][i], fa, scale);
+            for (int i = 0; i < PB; ++i)
+#pragma unroll
+                for (int j = 0; j < NMB; ++j) tile_mma<Elt, FP8>(acc[m][i][j], fb[m][i], fa[j], scale[j]);
         stage = stage + 1 == NS ? 0 : stage + 1;
     }
 
@@ -754,24 +761,27 @@ __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
 #pragma unroll
     for (int m = 0; m < MATS; ++m)
 #pragma unroll
-        for (int i = 0; i < PB; ++i) red[(m * PB + i) * 64 + lane] = acc[m][i];
+        for (int i = 0; i < PB; ++i)
+#pragma unroll
+            for (int j = 0; j < NMB; ++j) red[((m * PB + i) * NMB + j) * 64 + lane] = acc[m][i][j];
     __syncthreads();
-    auto total = [&](int m, int i) {
-        const floatx4_t* at = reinterpret_cast<const floatx4_t*>(smem) + (m * PB + i) * 64 + lane;
+    auto total = [&](int m, int i, int j) {
+        const floatx4_t* at = reinterpret_cast<const floatx4_t*>(smem) + ((m * PB + i) * NMB + j) * 64 + lane;
         floatx4_t s = at[0];
 #pragma unroll
         for (int v = 1; v < NW; ++v) s += at[v * MINE];
         return s;
     };
-    for (int i = wave; i < PB; i += NW) {
-        const int r = fr;
+    for (int u = wave; u < PB * NMB; u += NW) {
+        const int i = u / NMB, j = u - i * NMB;
+        const int r = j * 16 + fr;
         const int c0 = (int)n0 + i * 16 + fq * 4;
         floatx4_t v[3];
-        v[0] = total(0, i);
+        v[0] = total(0, i, j);
         int outs = 1;
         if constexpr (GATED) {
             v[1] = v[0];
-            v[2] = total(1, i);
+            v[2] = total(1, i, j);
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[0][e] = act_mul(v[1][e], v[2][e], p.act);
             if (p.G) outs = 3;

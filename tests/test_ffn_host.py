@@ -11,6 +11,11 @@ OK, INVALID, UNSUPPORTED = sdt.SDT_OK, sdt.SDT_ERR_INVALID_ARG, sdt.SDT_ERR_UNSU
 P = 0x10000          # an address that is never read
 
 
+def fp8(a, names):
+    """An sdt_fp8 of some of a's values, which leave it."""
+    return ctypes.byref(sdt.SdtFp8(*[a.pop(n) for n in names]))
+
+
 def call(name, *args):
     return int(getattr(sdt.lib(), name)(*args))
 
@@ -30,7 +35,8 @@ def test_quantize_refusals(t, change, want):
     a.update(change)
     if want is None:
         return            # the base case would launch: the GPU tests run it
-    assert call(f"fp8_quantize_{t}", *a.values(), None) == want
+    out = fp8(a, ("Q", "ldq", "S", "lds", "block"))
+    assert call(f"fp8_quantize_{t}", *a.values(), out, None) == want
 
 
 @pytest.mark.parametrize("t", ["f16", "bf16", "f32"])
@@ -41,7 +47,8 @@ def test_quantize_refusals(t, change, want):
 def test_dequantize_refusals(t, change, want):
     a = dict(rows=10, K=200, Q=P, ldq=208, S=P, lds=10, block=1, Y=P, ldy=200)
     a.update(change)
-    assert call(f"fp8_dequantize_{t}", *a.values(), None) == want
+    m = fp8(a, ("Q", "ldq", "S", "lds", "block"))
+    assert call(f"fp8_dequantize_{t}", a["rows"], a["K"], m, a["Y"], a["ldy"], None) == want
 
 
 @pytest.mark.parametrize("t", ["f16", "bf16"])
@@ -51,13 +58,16 @@ def test_dequantize_refusals(t, change, want):
     ({"lda": 192}, INVALID), ({"lda": 200}, UNSUPPORTED), ({"ldsa": 9}, INVALID), ({"ldsb": 1}, INVALID),
     ({"B": P + 4}, UNSUPPORTED), ({"SB": P + 1}, UNSUPPORTED), ({"M": 0}, OK), ({"N": 0}, OK),
     ({"M": 2 ** 31 - 200, "ldsa": 2 ** 31 - 1}, UNSUPPORTED), ({"ws": None, "bytes": 4}, INVALID),
-    ({"bytes": -1}, INVALID), ({"ws": P + 8}, UNSUPPORTED),
+    ({"bytes": -1}, INVALID), ({"ws": P + 8}, UNSUPPORTED), ({"block_a": 128}, INVALID),
+    ({"block_b": 1}, INVALID), ({"block_b": 0}, INVALID),
 ])
 def test_gemm_refusals(t, change, want):
     a = dict(M=10, N=300, K=200, A=P, lda=208, SA=P, ldsa=10, B=P, ldb=208, SB=P, ldsb=2, C=P, ldc=304,
-             ws=P, bytes=1 << 20)
+             ws=P, bytes=1 << 20, block_a=1, block_b=128)
     a.update(change)
-    assert call(f"gemm_fp8_{t}", *a.values(), None) == want
+    m = fp8(a, ("A", "lda", "SA", "ldsa", "block_a")), fp8(a, ("B", "ldb", "SB", "ldsb", "block_b"))
+    assert call(f"gemm_fp8_{t}", a["M"], a["N"], a["K"], *m, a["C"], a["ldc"], a["ws"], a["bytes"],
+                None) == want
 
 
 def _struct(kind, base, change):
@@ -85,6 +95,9 @@ def test_norm_refusals(t, change, want):
 
 
 def test_null_structs():
+    assert call("fp8_quantize_f16", 1, 1, P, 1, None, None) == INVALID
+    assert call("fp8_dequantize_f32", 1, 1, None, P, 1, None) == INVALID
+    assert call("gemm_fp8_bf16", 1, 1, 1, None, None, P, 8, None, 0, None) == INVALID
     for name in ("rms_norm_f16", "rms_norm_backward_bf16", "gated_ff_f16", "gated_ff_backward_bf16"):
         assert call(name, None, None) == INVALID
 
@@ -167,8 +180,8 @@ def test_workspace_sizes():
         sdt.gated_ff_workspace_size(1, -1, 1)
     for size in (sdt.gemm_fp8_workspace_size, sdt.gated_ff_split_size):
         assert size(16, 64, 8192) == 0                                  # streamed
-        assert size(64, 64, 8192) > 0
-        assert size(64, 64, 256) == 0
+        assert size(100, 64, 8192) > 0
+        assert size(100, 64, 256) == 0
         assert size(4096, 4096, 4096) == 0
         with pytest.raises(sdt.SdtError):
             size(-1, 1, 1)

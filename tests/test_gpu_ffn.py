@@ -248,7 +248,8 @@ def test_gemm_fp8(dtype, M, N, K, plain):
     assert untouched(full, N)
 
 
-@pytest.mark.parametrize("M, N, K", [(64, 100, 4000), (17, 64, 2048), (300, 250, 1100), (300, 250, 2200)])
+@pytest.mark.parametrize("M, N, K", [(64, 100, 4000), (17, 64, 2048), (300, 250, 1100), (300, 250, 2200),
+                                     (40, 5000, 8000)])
 def test_split(M, N, K):
     """Split along K through a buffer of junk: the bits of the call that makes its own;
     without one, whole numbers' same bits unsplit."""
@@ -258,7 +259,8 @@ def test_split(M, N, K):
     b, bv = fp8_matrix(N, K, 128, 2, True)
     want = (av @ bv.t()).float().bfloat16()
     need = sdt.gemm_fp8_workspace_size(M, N, K)
-    assert (need > 0) == (K >= 16 * 128 - 127)               # eight k-tiles of 128 a split
+    # eight k-tiles of 128 a split, and more rows than stream such weights
+    assert (need > 0) == (K >= 16 * 128 - 127 and (M > 64 or N * K > 2 ** 25))
     for size in (need, 16):
         c = torch.empty(M, -(-N // 8) * 8, dtype=torch.bfloat16, device=DEV)[:, :N]
         sdt.gemm_fp8_bf16(a, b, c, workspace=torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV))
