@@ -1209,9 +1209,10 @@ class Fp8:
     """An 8-bit matrix on the device (the format: include/sdt.h): float8_e4m3fn codes
     `q` [rows, K], rows a multiple of 16 bytes apart, and float32 scales `s`: of each
     row and block of 128 k, [ceil(K / 128), rows] (block 1, activations), or of each
-    block of 128 rows x 128 k, [ceil(rows / 128), ceil(K / 128)] (block 128, weights)."""
+    block of 128 rows x 128 k, [ceil(rows / 128), ceil(K / 128)] (block 128, weights).
+    The tensors stay the matrix's own: it keeps their addresses."""
 
-    __slots__ = ("q", "s", "rows", "K", "block", "device")      # device: its index, -1 the host
+    __slots__ = ("q", "s", "rows", "K", "block", "device", "_bytes")  # device: its index, -1 the host
 
     def __init__(self, q, s, block: int = 1):
         import torch
@@ -1234,6 +1235,7 @@ class Fp8:
         if (K > 1 and q.stride(1) != 1) or (fits[1] > 1 and s.stride(1) != 1):
             raise ValueError("Fp8: unit stride along rows of codes and of scales")
         self.q, self.s, self.rows, self.K, self.block, self.device = q, s, rows, K, block, where
+        self._bytes = None
 
     @classmethod
     def empty(cls, rows: int, K: int, block: int = 1, device="cuda") -> "Fp8":
@@ -1246,7 +1248,7 @@ class Fp8:
         m.q = q if ld == K else q[:, :K]
         m.s = torch.empty((kb, rows) if block == 1 else (-(-rows // 128), kb), dtype=torch.float32,
                           device=device)
-        m.rows, m.K, m.block, m.device = rows, K, block, q.get_device()
+        m.rows, m.K, m.block, m.device, m._bytes = rows, K, block, q.get_device(), None
         return m
 
     def _args(self):
@@ -1259,7 +1261,9 @@ class Fp8:
 
     def _packed(self):
         """An sdt_fp8, as bytes."""
-        return _pack_fp8(*self._args(), self.block)
+        if self._bytes is None:
+            self._bytes = _pack_fp8(*self._args(), self.block)
+        return self._bytes
 
 
 def _quantize8(entry, X, out, dtype, stream):
