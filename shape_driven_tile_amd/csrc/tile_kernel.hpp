@@ -227,6 +227,14 @@ __device__ __forceinline__ int4_t tail_mask(int valid) {
     return m;
 }
 
+// The sums of a block of 128 codes (lane l: row l % 16 of A, four columns of B).
+__device__ __forceinline__ floatx4_t fp8_block(const int4_t (&b)[2], const int4_t (&a)[2]) {
+    const int8v_t b8 = {b[0][0], b[0][1], b[0][2], b[0][3], b[1][0], b[1][1], b[1][2], b[1][3]};
+    const int8v_t a8 = {a[0][0], a[0][1], a[0][2], a[0][3], a[1][0], a[1][1], a[1][2], a[1][3]};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b8, a8, floatx4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0,
+                                                           0, 0);
+}
+
 // acc += B . A^T over a k-tile (lane l: row l % 16 of A, four columns of B); 8 bits:
 // times the blocks' scales.  The MFMA of a block starts from zero and its sums are
 // scaled and added in fp32.  Inside the MFMA the products of eight neighbouring codes
@@ -238,10 +246,7 @@ template <typename Elt, bool FP8>
 __device__ __forceinline__ void tile_mma(floatx4_t& acc, const int4_t (&b)[2], const int4_t (&a)[2],
                                          float scale) {
     if constexpr (FP8) {
-        const int8v_t b8 = {b[0][0], b[0][1], b[0][2], b[0][3], b[1][0], b[1][1], b[1][2], b[1][3]};
-        const int8v_t a8 = {a[0][0], a[0][1], a[0][2], a[0][3], a[1][0], a[1][1], a[1][2], a[1][3]};
-        const floatx4_t v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            b8, a8, floatx4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+        const floatx4_t v = fp8_block(b, a);
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(v[e], scale, acc[e]);
     } else {
@@ -423,29 +428,41 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
     }
 
     int coming = first;                           // the k-tile that the next load takes
-    auto load = [&](int stage) {
-        int4_t* base = smem + stage * STAGE;
+    // The loads of a k-tile, one by one: 0 (8 bits) scales, then A's, then B's.
+    struct Target {
+        int4_t* base;
+        __amdgpu_buffer_rsrc_t ra, rb, r2;
+    };
+    auto begin = [&](int stage) {
         const bool some = coming < end;
-        if constexpr (FP8)
-            dma4(scale_at + min(load_k, p.nkt - 1) * scale_step,
-                 reinterpret_cast<float*>(base + OpA::UNITS + OpB::UNITS + wave * 16));
-        const __amdgpu_buffer_rsrc_t ra = sa.next(some), rb = sb.next(some);
-#pragma unroll
-        for (int j = 0; j < OpA::DMA; ++j) dma16(ra, base + (wave * OpA::DMA + j) * 64, voff_a[j], 0);
-        if constexpr (GATED) {
-            const __amdgpu_buffer_rsrc_t r2 = sb2.next(some);
-#pragma unroll
-            for (int j = 0; j < OpB::DMA; ++j) {
-                const bool second = ((wave * OpB::DMA + j) * 8) % WTN >= WTN / 2;
-                dma16(second ? r2 : rb, base + OpA::UNITS + (wave * OpB::DMA + j) * 64, voff_b[j], 0);
-            }
+        Target x{smem + stage * STAGE, sa.next(some), sb.next(some)};
+        if constexpr (GATED) x.r2 = sb2.next(some);
+        return x;
+    };
+    auto issue = [&](const Target& x, int n) {
+        constexpr int S = FP8 ? 1 : 0;
+        if (FP8 && n == 0) {
+            if constexpr (FP8)
+                dma4(scale_at + min(load_k, p.nkt - 1) * scale_step,
+                     reinterpret_cast<float*>(x.base + OpA::UNITS + OpB::UNITS + wave * 16));
+        } else if (n < S + OpA::DMA) {
+            const int j = n - S;
+            dma16(x.ra, x.base + (wave * OpA::DMA + j) * 64, voff_a[j], 0);
         } else {
-#pragma unroll
-            for (int j = 0; j < OpB::DMA; ++j)
-                dma16(rb, base + OpA::UNITS + (wave * OpB::DMA + j) * 64, voff_b[j], 0);
+            const int j = n - S - OpA::DMA;
+            const bool second = GATED && ((wave * OpB::DMA + j) * 8) % WTN >= WTN / 2;
+            dma16(second ? x.r2 : x.rb, x.base + OpA::UNITS + (wave * OpB::DMA + j) * 64, voff_b[j], 0);
         }
+    };
+    auto done = [&]() {
         ++coming;
         ++load_k;
+    };
+    auto load = [&](int stage) {
+        const Target x = begin(stage);
+#pragma unroll
+        for (int n = 0; n < L; ++n) issue(x, n);
+        done();
     };
     // The loads have come to the end of a product that another is added to.
     auto second_product = [&]() {
@@ -543,6 +560,40 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
         if constexpr (!TA) read_a(sn, f[P ^ 1]);
         if constexpr (!TB) read_b(sn, f[P ^ 1]);
         __builtin_amdgcn_sched_barrier(0);
+        if constexpr (FP8) {
+            // An MFMA's sums are scaled and added four MFMAs later: sooner the wave would
+            // have to wait for them.
+            const Target x = begin(s);
+            floatx4_t v[4];
+            float scale[4];
+            constexpr int ALL = FM * FN;
+            auto add = [&](int n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[n % FN][n / FN][e] = __builtin_fmaf(v[n % 4][e], scale[n % 4], acc[n % FN][n / FN][e]);
+            };
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+#pragma unroll
+                for (int i = 0; i < FN; ++i) {
+                    const int n = j * FN + i;
+                    if (n >= 4) add(n - 4);
+                    __builtin_amdgcn_sched_barrier(0);
+                    scale[n % 4] = f[P].sa[j] * f[P].sb;
+                    v[n % 4] = fp8_block(f[P].b[i], f[P].a[j]);
+                    if (n % (ALL > L ? ALL / L : 1) == 0 && n / (ALL > L ? ALL / L : 1) < L)
+                        issue(x, n / (ALL > L ? ALL / L : 1));
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+            for (int n = ALL > L ? L : ALL; n < L; ++n) issue(x, n);
+#pragma unroll
+            for (int n = ALL - 4; n < ALL; ++n) add(n);
+            done();
+            s = sn;
+            ++kt;
+            return;
+        }
         load(s);
         mma(f[P], 0, FN / 2);
 #pragma unroll
