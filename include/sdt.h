@@ -578,7 +578,8 @@ typedef struct sdt_norm {
 } sdt_norm;
 
 /* total may be x or residual itself (same pointer and stride), y x, residual or neither.
- * rows == 0 or K == 0 is a no-op.  SDT_ERR_UNSUPPORTED: K > 32768. */
+ * rows == 0 or K == 0 is a no-op.  SDT_ERR_UNSUPPORTED: K > 32768, or rows for more threads
+ * than a launch has (2^32; a row takes 64 for K up to 512, up to 1024 past 8192). */
 int rms_norm_f16(const sdt_norm* args, void* stream);
 int rms_norm_bf16(const sdt_norm* args, void* stream);
 

@@ -31,7 +31,7 @@ int launched(hipError_t e) { return e == hipSuccess ? SDT_OK : fail_hip(e); }
 
 template <typename P>
 int launch(const void* kernel, int64_t grid, int threads, P& params, void* stream) {
-    if (grid > INT_MAX) return SDT_ERR_UNSUPPORTED;
+    if (grid * threads > UINT32_MAX) return SDT_ERR_UNSUPPORTED;      // a launch's threads
     if (grid == 0) return SDT_OK;
     void* args[] = {&params};
     return launched(hipLaunchKernel(kernel, dim3((unsigned)grid), dim3((unsigned)threads), args, 0,

@@ -89,6 +89,9 @@ NORM = dict(rows=4, K=100, x=P, ldx=100, residual=P, ldr=100, weight=P, eps=1e-6
     ({"x": P + 1}, UNSUPPORTED), ({"weight": P + 1}, UNSUPPORTED), ({"rstd": P + 2}, UNSUPPORTED),
     ({"q": P + 8}, UNSUPPORTED), ({"ldq": 104}, UNSUPPORTED), ({"rows": 0}, OK), ({"K": 0}, OK),
     ({"K": 32769, **{k: 1 << 20 for k in ("ldx", "ldr", "ldt", "ldy", "ldq")}}, UNSUPPORTED),
+    # 2^22 rows of 1024 threads: one more than a launch has
+    ({"K": 16384, "rows": 1 << 22, "lds": 1 << 22,
+      **{k: 16384 for k in ("ldx", "ldr", "ldt", "ldy", "ldq")}}, UNSUPPORTED),
 ])
 def test_norm_refusals(t, change, want):
     assert call(f"rms_norm_{t}", _struct(sdt.SdtNorm, NORM, change), None) == want
