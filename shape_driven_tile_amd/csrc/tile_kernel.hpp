@@ -483,18 +483,18 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
         int4_t a[FM][2], b[FN][2];
         float sa[FM], sb;                         // scales
     };
-    auto read_a = [&](int stage, Frags& f) {
-        const int4_t* base = smem + stage * STAGE;
-        OpA::template fragments<FM>(base, at_a, f.a);
-        if constexpr (FP8) {
-            const float* sc = reinterpret_cast<const float*>(base + OpA::UNITS + OpB::UNITS);
-            f.sb = sc[32];
+    auto read_scales = [&](int stage, Frags& f) {
+        const float* sc = reinterpret_cast<const float*>(smem + stage * STAGE + OpA::UNITS + OpB::UNITS);
+        f.sb = sc[32];
 #pragma unroll
-            for (int j = 0; j < FM; ++j) {
-                const int r = (wave_m * FM + j) * 16 + (lane & 15);
-                f.sa[j] = sc[(r / RW) * 64 + r % RW];
-            }
+        for (int j = 0; j < FM; ++j) {
+            const int r = (wave_m * FM + j) * 16 + (lane & 15);
+            f.sa[j] = sc[(r / RW) * 64 + r % RW];
         }
+    };
+    auto read_a = [&](int stage, Frags& f) {
+        OpA::template fragments<FM>(smem + stage * STAGE, at_a, f.a);
+        if constexpr (FP8) read_scales(stage, f);
     };
     auto read_b = [&](int stage, Frags& f) {
         OpB::template fragments<FN>(smem + stage * STAGE + OpA::UNITS, at_b, f.b);
@@ -557,54 +557,63 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) 
         constexpr int P = decltype(which)::value;
         const int sn = (s + 1 == NS) ? 0 : s + 1;
         landed(Later{});                          // and every wave has read stage s
-        if constexpr (!TA) read_a(sn, f[P ^ 1]);
-        if constexpr (!TB) read_b(sn, f[P ^ 1]);
-        __builtin_amdgcn_sched_barrier(0);
+        Frags& next = f[P ^ 1];
         if constexpr (FP8) {
             // An MFMA's sums are scaled and added four MFMAs later: sooner the wave would
-            // have to wait for them.
+            // have to wait for them (2048^3 17.5 us, so 16.4).  Two fragments are read after
+            // each MFMA until all are (before the first: 16.4 us, so 15.3).
+            constexpr int ALL = FM * FN, GAP = ALL > L ? ALL / L : 1;
+            static_assert(ALL >= FM + FN, "every fragment has its MFMA");
             const Target x = begin(s);
+            const int4_t* const from = smem + sn * STAGE;
+            auto read = [&](int part) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (part < FN)
+                        next.b[part][h] = OpB::fragment(from + OpA::UNITS, at_b, part, h);
+                    else if (part < FN + FM)
+                        next.a[part - FN][h] = OpA::fragment(from, at_a, part - FN, h);
+                }
+            };
             floatx4_t v[4];
             float scale[4];
-            constexpr int ALL = FM * FN;
             auto add = [&](int n) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     acc[n % FN][n / FN][e] = __builtin_fmaf(v[n % 4][e], scale[n % 4], acc[n % FN][n / FN][e]);
             };
+            read_scales(sn, next);
 #pragma unroll
-            for (int j = 0; j < FM; ++j)
+            for (int n = 0; n < ALL; ++n) {
+                if (n >= 4) add(n - 4);
+                __builtin_amdgcn_sched_barrier(0);
+                scale[n % 4] = f[P].sa[n / FN] * f[P].sb;
+                v[n % 4] = fp8_block(f[P].b[n % FN], f[P].a[n / FN]);
+                read(n);
+                if (n % GAP == 0 && n / GAP < L) issue(x, n / GAP);
+                __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
-                for (int i = 0; i < FN; ++i) {
-                    const int n = j * FN + i;
-                    if (n >= 4) add(n - 4);
-                    __builtin_amdgcn_sched_barrier(0);
-                    scale[n % 4] = f[P].sa[j] * f[P].sb;
-                    v[n % 4] = fp8_block(f[P].b[i], f[P].a[j]);
-                    if (n % (ALL > L ? ALL / L : 1) == 0 && n / (ALL > L ? ALL / L : 1) < L)
-                        issue(x, n / (ALL > L ? ALL / L : 1));
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-#pragma unroll
-            for (int n = ALL > L ? L : ALL; n < L; ++n) issue(x, n);
+            for (int l = ALL / GAP; l < L; ++l) issue(x, l);
 #pragma unroll
             for (int n = ALL - 4; n < ALL; ++n) add(n);
             done();
-            s = sn;
-            ++kt;
-            return;
-        }
-        load(s);
-        mma(f[P], 0, FN / 2);
+        } else {
+            if constexpr (!TA) read_a(sn, next);
+            if constexpr (!TB) read_b(sn, next);
+            __builtin_amdgcn_sched_barrier(0);
+            load(s);
+            mma(f[P], 0, FN / 2);
 #pragma unroll
-        for (int m = 0; m < L; ++m) {             // masks: 0x008 MFMA, 0x020 global read
-            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x008, FM * FN * (FP8 ? 1 : 2) / ((TA || TB ? 2 : 1) * L), 0);
+            for (int m = 0; m < L; ++m) {             // masks: 0x008 MFMA, 0x020 global read
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, FM * FN * 2 / ((TA || TB ? 2 : 1) * L), 0);
+            }
+            // turned fragments come with their wait: under the MFMAs issued before them
+            if constexpr (TA) read_a(sn, next);
+            mma(f[P], FN / 2, FN);
+            if constexpr (TB) read_b(sn, next);
         }
-        // turned fragments come with their wait: under the MFMAs issued before them
-        if constexpr (TA) read_a(sn, f[P ^ 1]);
-        mma(f[P], FN / 2, FN);
-        if constexpr (TB) read_b(sn, f[P ^ 1]);
         pin();
         s = sn;
         ++kt;
