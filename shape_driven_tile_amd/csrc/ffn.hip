@@ -211,15 +211,20 @@ int launch_rows8(TileGemm& p, int num_cu, void* stream) {
 // How a product with a workspace is laid out: its tiles' side and the workgroups
 // along each tile's k-tiles.  `from`: 128 x 128 tiles that are worth more than 64 x 64
 // ones (256 x 12288 x 4096, 192 of them: turned 45-51 us against 49, 8 bits 30 against
-// 28).  Where tiles leave CUs idle, each split keeps eight k-tiles at least.
+// 28).  Fewer are where the 64 x 64 ones are more than the two a CU that run at once and
+// K is at most 1024 (`brief` k-tiles): 1408 x 2048, 176 of them, turned 9.3 us against 10.7
+// at K = 512, 13.7 against 14.8 at 1024 and 24.8 against 24.7 at 2048; 8 bits 7.3 against
+// 9.1, 9.1 against 11.0 and 16.0 against 15.7.  Where tiles leave CUs idle, each split
+// keeps eight k-tiles at least.
 struct Split {
     int side, splits;
     int64_t bytes;
 };
-Split plan_split(int64_t M, int64_t N, int64_t kt, int batch, int64_t from) {
+Split plan_split(int64_t M, int64_t N, int64_t kt, int batch, int64_t from, int64_t brief) {
     Split s;
     const int64_t t128 = ceil_div(M, 128) * ceil_div(N, 128) * batch;
-    s.side = t128 >= from ? 128 : 64;
+    const int64_t t64 = ceil_div(M, 64) * ceil_div(N, 64) * batch;
+    s.side = t128 >= from || (t64 > 2 * kSplitTarget && kt <= brief) ? 128 : 64;
     const int64_t tiles = ceil_div(M, s.side) * ceil_div(N, s.side) * batch;
     int64_t n = tiles > 0 ? kSplitTarget / tiles : 1;
     n = std::min(n, kt / 8);
@@ -228,10 +233,10 @@ Split plan_split(int64_t M, int64_t N, int64_t kt, int batch, int64_t from) {
     return s;
 }
 Split plan_turned(int64_t M, int64_t N, int64_t kt, int batch) {
-    return plan_split(M, N, kt, batch, kSplitTarget * 3 / 4);
+    return plan_split(M, N, kt, batch, kSplitTarget * 3 / 4, 16);
 }
 Split plan_split8(int64_t M, int64_t N, int64_t K) {
-    return plan_split(M, N, ceil_div(K, 128), 1, kSplitTarget);
+    return plan_split(M, N, ceil_div(K, 128), 1, kSplitTarget, 8);
 }
 // Gated: 64 columns of both matrices a tile.  128 rows only where there are tiles for
 // more than one a CU (512 x 4096 x 4096, 256 of them: 51 us against 36; 1024 x 4096 x
