@@ -1210,9 +1210,17 @@ class Fp8:
     `q` [rows, K], rows a multiple of 16 bytes apart, and float32 scales `s`: of each
     row and block of 128 k, [ceil(K / 128), rows] (block 1, activations), or of each
     block of 128 rows x 128 k, [ceil(rows / 128), ceil(K / 128)] (block 128, weights).
-    The tensors stay the matrix's own: it keeps their addresses."""
+    The two tensors are the matrix's for good; what they hold may change."""
 
-    __slots__ = ("q", "s", "rows", "K", "block", "device", "_bytes")  # device: its index, -1 the host
+    __slots__ = ("_q", "_s", "rows", "K", "block", "device", "_at", "_bytes")  # device: its index, -1 the host
+
+    @property
+    def q(self):
+        return self._q
+
+    @property
+    def s(self):
+        return self._s
 
     def __init__(self, q, s, block: int = 1):
         import torch
@@ -1234,8 +1242,8 @@ class Fp8:
                              f"{tuple(s.shape)}")
         if (K > 1 and q.stride(1) != 1) or (fits[1] > 1 and s.stride(1) != 1):
             raise ValueError("Fp8: unit stride along rows of codes and of scales")
-        self.q, self.s, self.rows, self.K, self.block, self.device = q, s, rows, K, block, where
-        self._bytes = None
+        self._q, self._s, self.rows, self.K, self.block, self.device = q, s, rows, K, block, where
+        self._at = self._bytes = None
 
     @classmethod
     def empty(cls, rows: int, K: int, block: int = 1, device="cuda") -> "Fp8":
@@ -1245,24 +1253,25 @@ class Fp8:
         m = cls.__new__(cls)                 # tensors that fit by construction: no checks
         kb, ld = -(-K // 128), -(-K // 16) * 16
         q = torch.empty(rows, ld, dtype=torch.float8_e4m3fn, device=device)
-        m.q = q if ld == K else q[:, :K]
-        m.s = torch.empty((kb, rows) if block == 1 else (-(-rows // 128), kb), dtype=torch.float32,
+        m._q = q if ld == K else q[:, :K]
+        m._s = torch.empty((kb, rows) if block == 1 else (-(-rows // 128), kb), dtype=torch.float32,
                           device=device)
-        m.rows, m.K, m.block, m.device, m._bytes = rows, K, block, q.get_device(), None
+        m.rows, m.K, m.block, m.device, m._at, m._bytes = rows, K, block, q.get_device(), None, None
         return m
 
     def _args(self):
         """Codes, bytes from row to row, scales, floats from row to row of them."""
-        q, s = self.q, self.s
+        q, s = self._q, self._s
         ld = q.stride(0)
         if self.rows <= 1:
             ld = max(ld, self.K)
         return q.data_ptr(), ld, s.data_ptr(), max(s.stride(0), s.shape[1])
 
     def _packed(self):
-        """An sdt_fp8, as bytes."""
-        if self._bytes is None:
-            self._bytes = _pack_fp8(*self._args(), self.block)
+        """An sdt_fp8, as bytes, made again where the tensors have been given other memory."""
+        at = self._q.data_ptr(), self._s.data_ptr()
+        if at != self._at:
+            self._at, self._bytes = at, _pack_fp8(*self._args(), self.block)
         return self._bytes
 
 

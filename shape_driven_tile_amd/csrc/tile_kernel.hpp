@@ -341,9 +341,13 @@ __device__ __forceinline__ void wait_tiles(int n) {
 // ---- the tiled product -----------------------------------------------------------------
 // Output tiles of BM x BN by WM x WN waves, NS stages; two workgroups a CU, one's
 // reads and waits under the other's MFMAs.  The loads of the k-tile NS further on go
-// into a stage once its fragments are in registers, under the second half of the
-// MFMAs.  GATED: B's LDS rows alternate between the two matrices, so that a lane
-// holds both factors of its outputs; BN / 2 columns a tile.
+// into a stage once its fragments are in registers, between the MFMAs.  GATED: B's
+// LDS rows alternate between the two matrices, so that a lane holds both factors of
+// its outputs; BN / 2 columns a tile.  A k-tile of 128 x 128 costs a CU 0.35 us a tile
+// with two of them, 0.7 with one: bound by a workgroup's own chain of waits, which the
+// other fills.  Deeper stages instead of the second workgroup do not (2048 x 3000 x 2048
+// turned, 384 tiles: 53 us against 32).  2048^3: nn 29.1 us, tn 28.3, 8 bits 15.3; gated 500
+// x 1400 x 1000 13.0.
 template <typename Elt, bool FP8, int BM, int BN, int WM, int WN, int NS, bool TA, bool TB, bool GATED>
 __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) {
     constexpr int NW = WM * WN;
@@ -691,7 +695,8 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_reduce_kernel(TileGemm p) {
 // NW waves take every NW-th k-tile and stream B once.  Every wave has LDS of its
 // own, so the loop has no barrier: rows come straight into it in whole 128-byte
 // lines, NS k-tiles in flight, and are read from there as fragments.  The waves'
-// sums are added in wave order.  Bound by B's stream.
+// sums are added in wave order.  Bound by B's stream: one row of 12288 x 4096, 8 bits
+// 10.2 us (50 MB, 4.9 TB/s), gated of 16 bits 38.0 (201 MB, 5.3 TB/s).
 template <typename Elt, bool FP8, bool GATED, int NW, int PB, int NMB, int NS>
 __global__ __launch_bounds__(NW * 64) void rows_gemm_kernel(TileGemm p) {
     constexpr int MATS = GATED ? 2 : 1;
@@ -889,7 +894,8 @@ struct GatedGrad {
 };
 
 // dg = dh u a'(g), du = dh a(g), eight columns of a row a lane.  Both are rounded to
-// the type, which the MFMAs of the three products that read them take.
+// the type, which the MFMAs of the three products that read them take.  Bound by memory:
+// 4096 x 12288 from fp32 factors 145 us (704 MB, 4.9 TB/s).
 template <typename Elt, int RPT>
 __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGrad p) {
     const int64_t r0 = (int64_t)(blockIdx.x / p.nct) * RPT;

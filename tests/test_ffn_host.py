@@ -217,3 +217,18 @@ def test_host_tensors_are_refused():
         sdt.rms_norm(x.float(), v, y=x)
     with pytest.raises(TypeError):
         sdt.rms_norm_backward(x, v, torch.zeros(4), x, x)
+
+
+def test_fp8_follows_its_tensors():
+    """The tensors cannot be exchanged, and memory that they are given later is found."""
+    import torch
+    m = sdt.Fp8.empty(4, 128, device="cpu")
+    for name in ("q", "s"):
+        with pytest.raises(AttributeError):
+            setattr(m, name, getattr(m, name).clone())
+        first = m._packed()
+        assert m._packed() == first
+        kept = getattr(m, name).data                     # not freed: the next one lies elsewhere
+        getattr(m, name).data = torch.empty_like(kept)
+        assert m._packed() != first
+        assert m._packed() == sdt._pack_fp8(*m._args(), 1)

@@ -74,6 +74,20 @@ def test_layer_without_residual():
         ffn.FeedForward(torch.ones(32, device=DEV).half(), w, w, w.t().contiguous(), act="relu")
 
 
+def test_layer_without_tokens():
+    """An empty batch: empty outputs, gradients of the weights of zero."""
+    import torch
+    from shape_driven_tile_amd import ffn
+    w = torch.randn(64, 32, device=DEV).half()
+    layer = ffn.FeedForward(torch.ones(32, device=DEV).half(), w, w, torch.randn(32, 64, device=DEV).half())
+    x = torch.empty(0, 32, device=DEV, dtype=torch.float16)
+    y, total, saved = layer.forward(x, x)
+    dx, grads = layer.backward(saved, y, dtotal=y)
+    assert y.shape == total.shape == dx.shape == (0, 32)
+    for name, shape in (("norm", (32,)), ("gate", (64, 32)), ("up", (64, 32)), ("down", (32, 64))):
+        assert grads[name].shape == shape and not grads[name].any(), name
+
+
 @pytest.mark.parametrize("T", [1, 40, 300])
 def test_fp8_projection(T):
     """The product of the 8-bit rows that the norm makes with the 8-bit weights."""
