@@ -345,7 +345,7 @@ __device__ __forceinline__ float row_sum(float v, float* sm) {
 // A row by T threads, CH chunks of eight elements each (K <= 8 T CH).  T = 64:
 // four rows a workgroup.  The row stays in registers between its two passes, so memory
 // is read once: with residual and total 8192 x 4096 bf16 48 us (5.6 TB/s), in 8 bits 48.3
-// (4.9), 4097 x 8170 52 (4.5: rows at odd addresses).
+// (4.9), 4097 x 8170 52 (4.5).
 template <typename Elt, int T, int CH>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void rms_norm_kernel(Norm p) {
     __shared__ float sm[T / 64];
