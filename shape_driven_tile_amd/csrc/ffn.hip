@@ -172,17 +172,19 @@ int launch_pp(TileGemm& p, void* stream) {
 
 // Whether t256 tiles of 256 x 256, a workgroup a CU, beat t128 of 128 x 128, two: by a
 // CU's time in us, `kt` k-tiles of 128 bytes a tile (16 bits, gated and turned, and 8
-// bits; fitted to 18 sizes).  A round of 256 x 256 tiles takes 1.3 a k-tile and 11
-// besides, one of 128 x 128 tiles 0.9 and 4.5 (8 bits 1.05 and 4), with a tile a CU or
-// less 0.72 and 4 (0.85 and 3.5).  4096^3: nn 94 (256) against 119, 8 bits 56 against
-// 73; 2048 x 4096 x 4096: 87 against 63 and 45 against 39; 6000 x 6000 x 500: 71
-// against 54 and 54 against 37.
+// bits; fitted to 20 sizes).  A round of 256 x 256 tiles takes 1.45 a k-tile (8 bits
+// 1.55) and 9.5 besides, however full.  One of 128 x 128 tiles takes 0.95 and 6 (1.05
+// and 5.5), a partial one its share and a tenth, since CUs go on to it as they come free.
+// 256 against 128: 4096^3 nn 104 and 134, 8 bits 59 and 73; 4096 x 4096 x 512 20 and 27,
+// 17 and 24; 2048 x 4096 x 4096 83 and 67, 49 and 39; 4096 x 5000 x 4096 tn 194 and 168,
+// 113 and 93; 6000 x 6000 x 512 71 and 54, 57 and 38.
 bool large_tiles(int64_t t256, int64_t t128, int64_t kt, int64_t cu, bool fp8) {
     const double k = (double)kt;
-    const double full = fp8 ? 1.05 * k + 4.0 : 0.9 * k + 4.5, half = fp8 ? 0.85 * k + 3.5 : 0.72 * k + 4.0;
-    const int64_t rest = t128 % (2 * cu);
-    const double small = (double)(t128 / (2 * cu)) * full + (rest > cu ? full : rest > 0 ? half : 0.0);
-    return (double)ceil_div(t256, cu) * (1.3 * k + 11.0) < small;
+    const double full = fp8 ? 1.05 * k + 5.5 : 0.95 * k + 6.0;
+    const double large = (double)ceil_div(t256, cu) * ((fp8 ? 1.55 : 1.45) * k + 9.5);
+    const int64_t whole = t128 / (2 * cu), rest = t128 % (2 * cu);
+    const double part = rest > 0 ? 0.1 + 0.9 * (double)rest / (2.0 * (double)cu) : 0.0;
+    return large < full * ((double)whole + part);
 }
 
 // Few rows: the weights are streamed.

@@ -1,7 +1,7 @@
-"""The products whose sizes take the 256 x 256 tiles (some 250 of them and more, five
-k-tiles and more): turned, 8-bit and gated, and the gated block's gradients, on whole
-numbers small enough for every sum to be exact in fp32, compared bit for bit, and the
-8-bit product on random values within the bound of the smaller ones."""
+"""The products whose sizes take the 256 x 256 tiles (some 250 of them and more): turned,
+8-bit and gated, and the gated block's gradients, on whole numbers small enough for every
+sum to be exact in fp32, compared bit for bit, and the 8-bit product on random values
+within the bound of the smaller ones.  K from none over one and two k-tiles on."""
 import pytest
 
 from gpu_helpers import DEV, say
@@ -10,7 +10,8 @@ from test_gpu_ffn import U, check, fp8_matrix, mfma_bound, out_like, rows_of, un
 pytestmark = pytest.mark.gpu
 
 # tiles of 256: 16 x 16 with ragged ends, 15 x 17, 16 x 16 full
-SIZES = [(4000, 3999, 1001), (3800, 4300, 330), (4096, 4096, 320)]
+SIZES = [(4000, 3999, 1001), (3800, 4300, 330), (4096, 4096, 320), (4000, 3999, 128), (4096, 4096, 40),
+         (3800, 4300, 0)]
 
 
 def _sdt():
@@ -38,7 +39,8 @@ def test_turned(dtype, M, N, K, layout):
     assert untouched(full, N)
 
 
-@pytest.mark.parametrize("M, N, K", [(4000, 3999, 1001), (3800, 4300, 400), (4096, 4096, 512)])
+@pytest.mark.parametrize("M, N, K", [(4000, 3999, 1001), (3800, 4300, 400), (4096, 4096, 512), (4000, 3999, 200),
+                                     (4096, 4096, 100), (3800, 4300, 0)])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_fp8(dtype, M, N, K):
     import torch
@@ -57,7 +59,8 @@ def test_fp8(dtype, M, N, K):
         assert untouched(full, N)
 
 
-@pytest.mark.parametrize("M, N, K", [(4000, 1999, 1001), (3800, 2150, 330), (4096, 2048, 320)])
+@pytest.mark.parametrize("M, N, K", [(4000, 1999, 1001), (3800, 2150, 330), (4096, 2048, 320), (4000, 1999, 100),
+                                     (3800, 2150, 0)])
 @pytest.mark.parametrize("wide", [True, False])
 def test_gated(M, N, K, wide):
     """The factors bit for bit; h within the activation's steps of its exact value."""
@@ -79,12 +82,13 @@ def test_gated(M, N, K, wide):
     assert untouched(full, N) and untouched(gf, N) and untouched(uf, N)
 
 
+@pytest.mark.parametrize("N", [1999, 100, 40])
 @pytest.mark.parametrize("pads", [(8, 8), (8, 16)])
-def test_gated_gradients(pads):
+def test_gated_gradients(pads, N):
     """Both weights' strides alike and not (only alike take the large tiles for dx)."""
     import torch
     sdt, t = _sdt(), torch.bfloat16
-    M, N, K = 4000, 1999, 3900
+    M, K = 4000, 3900
     say(f"large gradients {M}x{N}x{K} {pads}")
     x, dh = operand(M, K, t, 1), operand(M, N, t, 2)
     gate, up = operand(N, K, t, 3, pads[0]), operand(N, K, t, 4, pads[1])
@@ -92,9 +96,9 @@ def test_gated_gradients(pads):
     # after it: dg = 0.  There g = 40, where a(g) = 40 in fp32: du = 40 dh, whole and
     # below 128.
     g = torch.zeros(M, N, device=DEV)
-    g[:, 1000:] = 40.0
+    g[:, N // 2:] = 40.0
     u = whole((M, N), torch.float32, 5)
-    u[:, 1000:] = 0.0
+    u[:, N // 2:] = 0.0
     g, u = rows_of(g, 1, align=4)[0], rows_of(u, 1, align=4)[0]
     dx, fx = out_like(M, K, t, pad=8)
     dgate, fg = out_like(N, K, t, pad=8)
