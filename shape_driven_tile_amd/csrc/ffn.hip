@@ -134,6 +134,15 @@ int check_in(int64_t rows, int64_t K, const void* A, int64_t lda) {
     return SDT_OK;
 }
 
+// Bytes from row to row of an operand of `rows` rows, `size` bytes an element, whose caller
+// gave a stride of `ld` elements.  A single row's may be any, but the kernels address the
+// rows after it too and find them past its end: at whole 16 bytes they are.  (A row of five
+// 16-bit values, turned: it ends in the 4 bytes 8 .. 11, and at a stride of 10 bytes the next
+// row would begin in them.)
+int64_t row_bytes(int64_t rows, int64_t ld, int size) {
+    return rows > 1 ? ld * size : ceil_div(ld * size, 16) * 16;
+}
+
 TileGemm product(int64_t M, int64_t N, int64_t L, int z, int nxcd) {
     TileGemm p = {};
     p.M = (int)M;
@@ -279,8 +288,8 @@ int gemm8(int64_t M, int64_t N, int64_t K, const sdt_fp8* A, const sdt_fp8* B, v
     p.SA = A->s;
     p.SB = B->s;
     p.C[0] = static_cast<uint16_t*>(C);
-    p.lda[0] = A->ldq;
-    p.ldb[0] = B->ldq;
+    p.lda[0] = row_bytes(M, A->ldq, 1);
+    p.ldb[0] = row_bytes(N, B->ldq, 1);
     p.ldsa = A->lds;
     p.ldsb = B->lds;
     p.ldc[0] = ldc;
@@ -328,8 +337,8 @@ int gemm_turned(int64_t M, int64_t N, int64_t L, const void* A, int64_t lda, con
     p.A[0] = static_cast<const uint8_t*>(A);
     p.B[0] = static_cast<const uint8_t*>(B);
     p.C[0] = static_cast<uint16_t*>(C);
-    p.lda[0] = lda * 2;
-    p.ldb[0] = ldb * 2;
+    p.lda[0] = row_bytes(TA ? L : M, lda, 2);
+    p.ldb[0] = row_bytes(L, ldb, 2);
     p.ldc[0] = ldc;
     return launch_split<Elt, TA, true>(p, ws, ws_bytes, dev.num_cu, stream);
 }
@@ -484,9 +493,9 @@ int gated(const sdt_gated_ff* a, void* stream) {
     p.B[0] = static_cast<const uint8_t*>(a->gate);
     p.B[1] = static_cast<const uint8_t*>(a->up);
     p.C[0] = static_cast<uint16_t*>(a->h);
-    p.lda[0] = a->ldx * 2;
-    p.ldb[0] = a->ldgate * 2;
-    p.ldb[1] = a->ldup * 2;
+    p.lda[0] = row_bytes(M, a->ldx, 2);
+    p.ldb[0] = row_bytes(N, a->ldgate, 2);
+    p.ldb[1] = row_bytes(N, a->ldup, 2);
     p.ldc[0] = a->ldh;
     p.G = a->g;
     p.U = a->u;
@@ -580,8 +589,8 @@ int gated_backward(const sdt_gated_ff_grad* a, void* stream) {
         p.B[1] = static_cast<const uint8_t*>(a->up);
         p.C[0] = static_cast<uint16_t*>(a->dx);
         p.lda[0] = p.lda[1] = l.ld * 2;
-        p.ldb[0] = a->ldgate * 2;
-        p.ldb[1] = a->ldup * 2;
+        p.ldb[0] = row_bytes(N, a->ldgate, 2);
+        p.ldb[1] = row_bytes(N, a->ldup, 2);
         p.ldc[0] = a->lddx;
         p.products = 2;
         rc = launch_split<Elt, false, true>(p, ws, l.bytes - l.at, dev.num_cu, stream);
@@ -595,7 +604,7 @@ int gated_backward(const sdt_gated_ff_grad* a, void* stream) {
         p.C[0] = static_cast<uint16_t*>(a->dgate);
         p.C[1] = static_cast<uint16_t*>(a->dup);
         p.lda[0] = p.lda[1] = l.ld * 2;
-        p.ldb[0] = p.ldb[1] = a->ldx * 2;
+        p.ldb[0] = p.ldb[1] = row_bytes(M, a->ldx, 2);
         p.ldc[0] = a->lddgate;
         p.ldc[1] = a->lddup;
         p.batch = 2;
