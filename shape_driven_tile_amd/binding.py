@@ -1265,7 +1265,8 @@ class Fp8:
         ld = q.stride(0)
         if self.rows <= 1:
             ld = max(ld, self.K)
-        return q.data_ptr(), ld, s.data_ptr(), max(s.stride(0), s.shape[1])
+        # several rows of scales: their own stride, so that rows that overlap are refused
+        return q.data_ptr(), ld, s.data_ptr(), s.stride(0) if s.shape[0] > 1 else s.shape[1]
 
     def _packed(self):
         """An sdt_fp8, as bytes, made again where the tensors have been given other memory."""

@@ -232,3 +232,30 @@ def test_fp8_follows_its_tensors():
         getattr(m, name).data = torch.empty_like(kept)
         assert m._packed() != first
         assert m._packed() == sdt._pack_fp8(*m._args(), 1)
+
+
+@pytest.mark.parametrize("rows, K, block, stride", [(64, 512, 1, 0), (64, 512, 1, 1), (64, 512, 1, 63), (300, 512, 128, 0),
+                                                    (300, 512, 128, 3), (300, 100, 128, 0)])
+def test_fp8_scales_that_overlap(rows, K, block, stride):
+    """Scales expanded over the blocks, or rows of them that overlap: their stride is passed
+    on as it is and refused, not read as if every row had memory of its own."""
+    import torch
+    m = sdt.Fp8.empty(rows, K, block=block, device="cpu")
+    shape = tuple(m.s.shape)
+    assert shape[0] > 1
+    few = torch.ones(shape[0] * shape[1])
+    m.s.set_(few.as_strided(shape, (stride, 1)))
+    assert m._args()[3] == stride
+    X = torch.zeros(1, dtype=torch.float16)                 # never read
+    assert call("fp8_quantize_f16", rows, K, X.data_ptr(), K, m._packed(), None) == INVALID
+    assert call("fp8_dequantize_f16", rows, K, m._packed(), X.data_ptr(), K, None) == INVALID
+
+
+def test_fp8_one_row_of_scales():
+    """Its stride is of no matter."""
+    import torch
+    for rows, K, block in ((64, 100, 1), (100, 512, 128), (1, 1, 1)):
+        m = sdt.Fp8.empty(rows, K, block=block, device="cpu")
+        wide = tuple(m.s.shape)[1]
+        m.s.set_(torch.ones(wide).as_strided((1, wide), (0, 1)))
+        assert m._args()[3] == wide
