@@ -1212,7 +1212,8 @@ class Fp8:
     block of 128 rows x 128 k, [ceil(rows / 128), ceil(K / 128)] (block 128, weights).
     The two tensors are the matrix's for good; what they hold may change."""
 
-    __slots__ = ("_q", "_s", "rows", "K", "block", "device", "_at", "_bytes")  # device: its index, -1 the host
+    # device: its index, -1 the host; _at: the memory that _given and _bytes are made from
+    __slots__ = ("_q", "_s", "rows", "K", "block", "device", "_at", "_given", "_bytes")
 
     @property
     def q(self):
@@ -1232,18 +1233,11 @@ class Fp8:
         where = q.get_device() if q.is_cuda else -1
         if where < 0 or not s.is_cuda or s.get_device() != where:
             raise TypeError("Fp8: codes and scales must be on one device")
-        if q.dim() != 2 or s.dim() != 2:
-            raise ValueError(f"Fp8: codes {tuple(q.shape)} and scales {tuple(s.shape)} must be 2-D")
-        rows, K = q.shape
-        kb = -(-K // 128)
-        fits = (kb, rows) if block == 1 else (-(-rows // 128), kb)
-        if tuple(s.shape) != fits:
-            raise ValueError(f"Fp8: a {rows} x {K} matrix of block {block} has scales {fits}, not "
-                             f"{tuple(s.shape)}")
-        if (K > 1 and q.stride(1) != 1) or (fits[1] > 1 and s.stride(1) != 1):
-            raise ValueError("Fp8: unit stride along rows of codes and of scales")
-        self._q, self._s, self.rows, self.K, self.block, self.device = q, s, rows, K, block, where
-        self._at = self._bytes = None
+        if q.dim() != 2:
+            raise ValueError(f"Fp8: codes {tuple(q.shape)} must be 2-D")
+        (self.rows, self.K), self.block, self.device = q.shape, block, where
+        self._q, self._s, self._at = q, s, None
+        self._args()
 
     @classmethod
     def empty(cls, rows: int, K: int, block: int = 1, device="cuda") -> "Fp8":
@@ -1256,23 +1250,31 @@ class Fp8:
         m._q = q if ld == K else q[:, :K]
         m._s = torch.empty((kb, rows) if block == 1 else (-(-rows // 128), kb), dtype=torch.float32,
                           device=device)
-        m.rows, m.K, m.block, m.device, m._at, m._bytes = rows, K, block, q.get_device(), None, None
+        m.rows, m.K, m.block, m.device, m._at = rows, K, block, q.get_device(), None
         return m
 
     def _args(self):
-        """Codes, bytes from row to row, scales, floats from row to row of them."""
+        """Codes, bytes from row to row, scales, floats from row to row of them; made again
+        where the tensors have been given other memory or strides."""
         q, s = self._q, self._s
-        ld = q.stride(0)
-        if self.rows <= 1:
-            ld = max(ld, self.K)
-        # several rows of scales: their own stride, so that rows that overlap are refused
-        return q.data_ptr(), ld, s.data_ptr(), s.stride(0) if s.shape[0] > 1 else s.shape[1]
+        qs, ss = q.stride(), s.stride()
+        at = q.data_ptr(), qs, s.data_ptr(), ss
+        if at != self._at:
+            rows, K, kb = self.rows, self.K, -(-self.K // 128)
+            fits = (kb, rows) if self.block == 1 else (-(-rows // 128), kb)
+            if q.shape != (rows, K) or s.shape != fits:
+                raise ValueError(f"Fp8: a {rows} x {K} matrix of block {self.block} has scales {fits}, not "
+                                 f"codes {tuple(q.shape)} and scales {tuple(s.shape)}")
+            if (K > 1 and qs[1] != 1) or (fits[1] > 1 and ss[1] != 1):
+                raise ValueError("Fp8: unit stride along rows of codes and of scales")
+            # several rows of scales: their own stride, so that rows that overlap are refused
+            given = (at[0], qs[0] if rows > 1 else max(qs[0], K), at[2], ss[0] if fits[0] > 1 else fits[1])
+            self._at, self._given, self._bytes = at, given, _pack_fp8(*given, self.block)
+        return self._given
 
     def _packed(self):
-        """An sdt_fp8, as bytes, made again where the tensors have been given other memory."""
-        at = self._q.data_ptr(), self._s.data_ptr()
-        if at != self._at:
-            self._at, self._bytes = at, _pack_fp8(*self._args(), self.block)
+        """An sdt_fp8, as bytes."""
+        self._args()
         return self._bytes
 
 

@@ -259,3 +259,29 @@ def test_fp8_one_row_of_scales():
         wide = tuple(m.s.shape)[1]
         m.s.set_(torch.ones(wide).as_strided((1, wide), (0, 1)))
         assert m._args()[3] == wide
+
+
+def test_fp8_follows_its_tensors_strides():
+    """Other strides at the same address are found; another shape is refused."""
+    import torch
+    m = sdt.Fp8.empty(64, 512, device="cpu")
+    scales, codes = torch.ones(4 * 80), torch.zeros(64 * 640, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    m.s.set_(scales.as_strided((4, 64), (64, 1)))
+    m.q.set_(codes.as_strided((64, 512), (512, 1)))
+    assert m._packed() == sdt._pack_fp8(codes.data_ptr(), 512, scales.data_ptr(), 64, 1)
+    m.s.set_(scales.as_strided((4, 64), (80, 1)))
+    assert m._packed() == sdt._pack_fp8(codes.data_ptr(), 512, scales.data_ptr(), 80, 1)
+    m.q.set_(codes.as_strided((64, 512), (640, 1)))
+    assert m._packed() == sdt._pack_fp8(codes.data_ptr(), 640, scales.data_ptr(), 80, 1)
+    assert m._args() == (codes.data_ptr(), 640, scales.data_ptr(), 80)
+    for name, other in (("s", torch.ones(2, 64)), ("s", torch.ones(4, 128)[:, ::2]),
+                        ("q", codes[:64 * 256].view(64, 256)), ("q", codes[:64 * 512].view(512, 64).t())):
+        t = getattr(m, name)
+        kept = t.data
+        t.set_(other)
+        with pytest.raises(ValueError):
+            m._packed()
+        with pytest.raises(ValueError):
+            m._args()
+        t.set_(kept)
+        assert m._args() == (codes.data_ptr(), 640, scales.data_ptr(), 80)
