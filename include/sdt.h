@@ -513,7 +513,7 @@ int moe_experts_mx4_bf16(const sdt_moe_layer* layer, const int32_t* idx, const f
  * Rows of K codes, OCP e4m3 (1 sign, 4 exponent, 3 fraction bits, largest 448; 0x7f and 0xff
  * NaN), and fp32 scales: a value is its code times its block's scale.
  * Requirements everywhere: q 16-byte aligned, ldq >= K a multiple of 16 (any for a single
- * row) below 2^23, s 4-byte aligned, K at most 2^23, lds at most 2^31 - 1. */
+ * row) below 2^23, s 4-byte aligned, lds at most 2^31 - 1. */
 typedef struct sdt_fp8 {
     void* q;        /* codes, rows ldq bytes apart */
     int64_t ldq;

@@ -516,12 +516,19 @@ int gated(const sdt_gated_ff* a, void* stream) {
 // The backward's buffer: dg and du side by side (rows of 2 N' elements), then the
 // splits' sums of the product that needs most.
 struct GatedLayout {
-    int64_t ld, at, bytes;                        // elements of a row; the sums' offset
+    int64_t ld, at, bytes;                        // elements of a row; the sums' offset; -1: more
+                                                  // than operands may have
 };
 GatedLayout gated_layout(int64_t M, int64_t N, int64_t K) {
     GatedLayout l;
     const int64_t np = ceil_div(N, 8) * 8;
     l.ld = 2 * np;
+    l.at = l.bytes = 0;
+    if (M == 0 || N == 0 || K == 0) return l;     // no buffer is used
+    if (M > kMaxRows || l.ld >= kMaxLd || K >= kMaxLd) {
+        l.bytes = -1;
+        return l;
+    }
     l.at = ceil_div(M * l.ld * 2, 256) * 256;
     l.bytes = l.at + std::max(plan_turned(M, K, 2 * ceil_div(N, 64), 1).bytes,
                               plan_turned(N, K, ceil_div(M, 64), 2).bytes);
@@ -549,8 +556,9 @@ int gated_backward(const sdt_gated_ff_grad* a, void* stream) {
         if (rc == SDT_OK) rc = check_factors(M, N, a->g, a->ldg, a->u, a->ldu, a->wide);
         if (rc == SDT_OK) rc = check_rows(N, a->dh, a->lddh, true);
         if (rc != SDT_OK) return rc;
+        if (l.bytes < 0) return SDT_ERR_UNSUPPORTED;
         if (!a->workspace || a->workspace_bytes < l.bytes) return SDT_ERR_INVALID_ARG;
-        if (misaligned(a->workspace, 16) || l.ld >= kMaxLd) return SDT_ERR_UNSUPPORTED;
+        if (misaligned(a->workspace, 16)) return SDT_ERR_UNSUPPORTED;
     }
     if (M > kMaxRows || N > kMaxRows || K > kMaxRows) return SDT_ERR_UNSUPPORTED;
     DeviceInfo dev;
@@ -646,6 +654,7 @@ int gemm_fp8_bf16(int64_t M, int64_t N, int64_t K, const sdt_fp8* A, const sdt_f
 }
 int64_t sdt_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K < 0 || M > sdt::kMaxRows || N > sdt::kMaxRows || K > sdt::kMaxK) return -1;
+    if (M > 0 && N > 0 && K >= 2 * sdt::kMaxLd) return -1;
     return sdt::few_rows8(M, N, K) ? 0 : sdt::plan_split8(M, N, K).bytes;
 }
 
@@ -658,7 +667,7 @@ int rms_norm_backward_bf16(const sdt_norm_grad* args, void* stream) {
     return sdt::norm_backward<BF16>(args, stream);
 }
 int64_t sdt_rms_norm_workspace_size(int64_t rows, int64_t K) {
-    if (rows < 0 || K < 0 || K > sdt::kMaxNorm) return -1;
+    if (rows < 0 || K < 0 || rows > sdt::kMaxRows || K > sdt::kMaxNorm) return -1;
     return sdt::norm_parts(rows, K) * K * 4;
 }
 
@@ -666,6 +675,7 @@ int gated_ff_f16(const sdt_gated_ff* args, void* stream) { return sdt::gated<F16
 int gated_ff_bf16(const sdt_gated_ff* args, void* stream) { return sdt::gated<BF16>(args, stream); }
 int64_t sdt_gated_ff_split_size(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K < 0 || M > sdt::kMaxRows || N > sdt::kMaxRows || K > sdt::kMaxK) return -1;
+    if (M > 0 && N > 0 && K >= sdt::kMaxLd) return -1;
     return M <= sdt::kFewRows ? 0 : sdt::plan_gated(M, N, K).bytes;
 }
 int gated_ff_backward_f16(const sdt_gated_ff_grad* args, void* stream) {
@@ -697,6 +707,8 @@ int gemm_bf16_tn(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, co
 }
 int64_t sdt_gemm_turned_workspace_size(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K < 0 || M > sdt::kMaxRows || N > sdt::kMaxRows || K > sdt::kMaxRows) return -1;
+    // one layout's operands at least have to be such: B's rows are N long, A's K or M
+    if (M > 0 && K > 0 && (N >= sdt::kMaxLd || (M >= sdt::kMaxLd && K >= sdt::kMaxLd))) return -1;
     return sdt::plan_turned(M, N, sdt::ceil_div(K, 64), 1).bytes;
 }
 

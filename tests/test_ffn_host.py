@@ -285,3 +285,46 @@ def test_fp8_follows_its_tensors_strides():
             m._args()
         t.set_(kept)
         assert m._args() == (codes.data_ptr(), 640, scales.data_ptr(), 80)
+
+
+def test_workspace_sizes_outside_the_limits():
+    """No size for what the calls refuse: -1 from the library, an error from the binding."""
+    top = 2 ** 31 - 256
+    for size, refused in [
+            # rows of dg and du past gemm operands' strides (2 N' < 2^22)
+            (sdt.gated_ff_workspace_size, [(4, 1 << 22, 64), (4, 1 << 21, 64), (top, top, 8), (top, 1 << 21, 8)]),
+            # rows of x past them; of both operands of one layout and of the other
+            (sdt.gated_ff_split_size, [(20, 64, 1 << 22)]),
+            (sdt.gemm_turned_workspace_size, [(4, 1 << 22, 64), (1 << 22, 64, 1 << 22)]),
+            (sdt.gemm_fp8_workspace_size, [(100, 64, 1 << 23)])]:
+        entry = getattr(sdt.lib(), "sdt_" + size.__name__)
+        for sizes in refused:
+            assert entry(*sizes) == -1, (size.__name__, sizes)
+            with pytest.raises(sdt.SdtError):
+                size(*sizes)
+    with pytest.raises(sdt.SdtError):
+        sdt.rms_norm_workspace_size(1 << 31, 64)
+    # the largest that are taken
+    assert sdt.gated_ff_workspace_size(4, (1 << 21) - 8, 64) >= 4 * 2 * ((1 << 21) - 8) * 2
+    assert sdt.gemm_turned_workspace_size(1 << 22, 64, 64) == 0 and sdt.gemm_turned_workspace_size(64, 64, 1 << 22) > 0
+    assert sdt.gated_ff_split_size(20, 64, (1 << 22) - 8) > 0
+    assert sdt.gemm_fp8_workspace_size(100, 64, (1 << 23) - 16) > 0
+    # nothing to compute, nothing refused
+    assert sdt.gated_ff_workspace_size(0, 1 << 22, 64) >= 0 and sdt.gated_ff_workspace_size(4, 1 << 22, 0) >= 0
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+def test_sizes_that_are_refused(t):
+    """The calls themselves, at those sizes and strides that would hold them."""
+    n = 1 << 21
+    a = dict(GATED_GRAD, N=n, **{k: n for k in ("ldg", "ldu", "lddh")}, workspace_bytes=1 << 40)
+    assert call(f"gated_ff_backward_{t}", _struct(sdt.SdtGatedFfGrad, a, {}), None) == UNSUPPORTED
+    a = dict(GATED, K=1 << 22, **{k: 1 << 22 for k in ("ldx", "ldgate", "ldup")})
+    assert call(f"gated_ff_{t}", _struct(sdt.SdtGatedFf, a, {}), None) == UNSUPPORTED
+    for layout, (M, N, K) in (("nn", (4, 1 << 22, 64)), ("tn", (4, 1 << 22, 64)), ("nn", (1 << 22, 64, 1 << 22)),
+                              ("tn", (1 << 22, 64, 1 << 22))):
+        lda = K if layout == "nn" else M
+        assert call(f"gemm_{t}_{layout}", M, N, K, P, lda, P, N, P, N, None, 0, None) == UNSUPPORTED
+    K = 1 << 23
+    A, B = (ctypes.byref(sdt.SdtFp8(P, K, P, 1 << 16, block)) for block in (1, 128))
+    assert call(f"gemm_fp8_{t}", 100, 64, K, A, B, P, 64, None, 0, None) == UNSUPPORTED
