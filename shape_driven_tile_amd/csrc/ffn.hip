@@ -20,7 +20,7 @@ namespace sdt {
 namespace {
 
 constexpr int64_t kMaxK = int64_t(1) << 23;
-constexpr int64_t kMaxLd = int64_t(1) << 22;          // elements, exclusive (gemm_f16's)
+constexpr int64_t kMaxStride = int64_t(1) << 22;          // elements, exclusive (gemm_f16's)
 constexpr int64_t kMaxRows = INT_MAX - 255;           // the last tile's end fits 32 bits
 constexpr int64_t kMaxNorm = 32768;                   // elements of a normed row
 constexpr int kSplitTarget = 256;                     // workgroups that a split aims at
@@ -46,7 +46,7 @@ bool known_block(const sdt_fp8* m) { return m && (m->block == 1 || m->block == 1
 int check_fp8(int64_t rows, int64_t K, const sdt_fp8& m) {
     if (!m.q || !m.s) return SDT_ERR_INVALID_ARG;
     if (m.ldq < K || m.lds < (m.block == 1 ? rows : ceil_div(K, 128))) return SDT_ERR_INVALID_ARG;
-    if (K > kMaxK || rows > kMaxRows || m.ldq >= 2 * kMaxLd || m.lds > INT_MAX) return SDT_ERR_UNSUPPORTED;
+    if (K > kMaxK || rows > kMaxRows || m.ldq >= 2 * kMaxStride || m.lds > INT_MAX) return SDT_ERR_UNSUPPORTED;
     if (misaligned(m.q, 16) || misaligned(m.s, 4) || (rows > 1 && m.ldq % 16 != 0))
         return SDT_ERR_UNSUPPORTED;
     return SDT_OK;
@@ -129,7 +129,7 @@ int check_out(int64_t rows, int64_t N, const void* C, int64_t ldc) {
 // A 16-bit operand of `rows` rows of K (> 0) elements, as gemm_f16's.
 int check_in(int64_t rows, int64_t K, const void* A, int64_t lda) {
     if (!A || lda < K) return SDT_ERR_INVALID_ARG;
-    if (lda >= kMaxLd) return SDT_ERR_UNSUPPORTED;
+    if (lda >= kMaxStride) return SDT_ERR_UNSUPPORTED;
     if (misaligned(A, 16) || (rows > 1 && lda % 8 != 0)) return SDT_ERR_UNSUPPORTED;
     return SDT_OK;
 }
@@ -525,7 +525,7 @@ GatedLayout gated_layout(int64_t M, int64_t N, int64_t K) {
     l.ld = 2 * np;
     l.at = l.bytes = 0;
     if (M == 0 || N == 0 || K == 0) return l;     // no buffer is used
-    if (M > kMaxRows || l.ld >= kMaxLd || K >= kMaxLd) {
+    if (M > kMaxRows || l.ld >= kMaxStride || K >= kMaxStride) {
         l.bytes = -1;
         return l;
     }
@@ -654,7 +654,7 @@ int gemm_fp8_bf16(int64_t M, int64_t N, int64_t K, const sdt_fp8* A, const sdt_f
 }
 int64_t sdt_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K < 0 || M > sdt::kMaxRows || N > sdt::kMaxRows || K > sdt::kMaxK) return -1;
-    if (M > 0 && N > 0 && K >= 2 * sdt::kMaxLd) return -1;
+    if (M > 0 && N > 0 && K >= 2 * sdt::kMaxStride) return -1;
     return sdt::few_rows8(M, N, K) ? 0 : sdt::plan_split8(M, N, K).bytes;
 }
 
@@ -675,7 +675,7 @@ int gated_ff_f16(const sdt_gated_ff* args, void* stream) { return sdt::gated<F16
 int gated_ff_bf16(const sdt_gated_ff* args, void* stream) { return sdt::gated<BF16>(args, stream); }
 int64_t sdt_gated_ff_split_size(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K < 0 || M > sdt::kMaxRows || N > sdt::kMaxRows || K > sdt::kMaxK) return -1;
-    if (M > 0 && N > 0 && K >= sdt::kMaxLd) return -1;
+    if (M > 0 && N > 0 && K >= sdt::kMaxStride) return -1;
     return M <= sdt::kFewRows ? 0 : sdt::plan_gated(M, N, K).bytes;
 }
 int gated_ff_backward_f16(const sdt_gated_ff_grad* args, void* stream) {
@@ -708,7 +708,7 @@ int gemm_bf16_tn(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, co
 int64_t sdt_gemm_turned_workspace_size(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K < 0 || M > sdt::kMaxRows || N > sdt::kMaxRows || K > sdt::kMaxRows) return -1;
     // one layout's operands at least have to be such: B's rows are N long, A's K or M
-    if (M > 0 && K > 0 && (N >= sdt::kMaxLd || (M >= sdt::kMaxLd && K >= sdt::kMaxLd))) return -1;
+    if (M > 0 && K > 0 && (N >= sdt::kMaxStride || (M >= sdt::kMaxStride && K >= sdt::kMaxStride))) return -1;
     return sdt::plan_turned(M, N, sdt::ceil_div(K, 64), 1).bytes;
 }
 
