@@ -111,7 +111,9 @@ __device__ __forceinline__ float fp8_scale(uint32_t top) {
 // Eight codes.  The quotients are correctly rounded by one correction of x * (1 /
 // s) (Markstein's): its residual is exact, and what is left of the reciprocal's
 // error is 2^-47 of the quotient.  Small scales are brought up first, so that the
-// residual does not underflow; both factors are powers of two.
+// residual does not underflow; both factors are powers of two.  The residual is taken as
+// -(t s - v): where v is a zero, v - t s would be +0 whatever its sign, and the code's
+// with it.
 __device__ __forceinline__ uint2_t fp8_codes(const float (&x)[8], float scale) {
     if (scale != scale) return uint2_t{0, 0};
     const float lift = scale < 0x1p-60f ? 0x1p64f : 1.0f;
@@ -120,7 +122,7 @@ __device__ __forceinline__ uint2_t fp8_codes(const float (&x)[8], float scale) {
 #pragma unroll
     for (int d = 0; d < 8; ++d) {
         const float v = x[d] * lift, t = v * inv;
-        q[d] = __builtin_fmaf(__builtin_fmaf(-t, s, v), inv, t);
+        q[d] = __builtin_fmaf(-__builtin_fmaf(t, s, -v), inv, t);
     }
     int lo = 0, hi = 0;
     lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], lo, false);
