@@ -52,9 +52,19 @@ int check_fp8(int64_t rows, int64_t K, const sdt_fp8& m) {
     return SDT_OK;
 }
 
-// Rows a workgroup takes: eight loads in flight a lane where that still gives every
-// CU two workgroups, else one (a token: latency).
-bool many_rows(int64_t rows, int64_t nct, int num_cu) { return rows * nct >= int64_t(16) * num_cu; }
+// Rows a workgroup of 256 lanes, eight elements each, takes.  One, as a rule: codes of
+// 4096 x 4096 13.3 us and 15.7 by eight rows together, 8192 x 8192 39.1 and 42.1, dg and du of
+// 8192 x 4096 110 and 116.  Short rows leave lanes idle: from 128 of them a CU on, codes of up
+// to 1024 elements by eight together (65536 x 512 32.9 us and 29.7, 262144 x 128 112 and 101;
+// 16384 x 512 11.1 and 11.7, 32768 x 1500 30.7 and 29.9), dg and du of up to 256 by four
+// (131072 x 256 118 and 112, 262144 x 128 193 and 166; 65536 x 512 103 and 108).
+bool many_short(int64_t rows, int64_t K, int64_t most, int num_cu) {
+    return K <= most && rows >= int64_t(128) * num_cu;
+}
+// Values back, which are less work a row: eight rows together from 32 row tiles a CU on
+// (8192 x 2048 10.8 us and 8.9, 32768 x 512 17.5 and 13.2, 8192 x 8192 39.0 and 39.7; 4096 x
+// 2048 5.4 and 5.8).
+bool many_tiles(int64_t rows, int64_t nct, int num_cu) { return rows * nct >= int64_t(32) * num_cu; }
 
 template <typename Elt>
 int quantize8(int64_t rows, int64_t K, const void* X, int64_t ldx, const sdt_fp8* out, void* stream) {
@@ -83,7 +93,7 @@ int quantize8(int64_t rows, int64_t K, const void* X, int64_t ldx, const sdt_fp8
                       ceil_div(rows, 128) * p.nct, 256, p, stream);
     }
     p.nct = (int)ceil_div(K, 2048);
-    if (K >= 8 && many_rows(rows, p.nct, dev.num_cu))
+    if (K >= 8 && many_short(rows, K, 1024, dev.num_cu))
         return launch(reinterpret_cast<const void*>(&fp8_quantize_rows_kernel<Elt, 8>),
                       ceil_div(rows, 8) * p.nct, 256, p, stream);
     return launch(reinterpret_cast<const void*>(&fp8_quantize_rows_kernel<Elt, 1>), rows * p.nct, 256, p,
@@ -112,7 +122,7 @@ int dequantize8(int64_t rows, int64_t K, const sdt_fp8* m, void* Y, int64_t ldy,
     p.rows = rows;
     p.K = (int)K;
     p.nct = (int)ceil_div(K, 2048);
-    if (K >= 8 && many_rows(rows, p.nct, dev.num_cu))
+    if (K >= 8 && many_tiles(rows, p.nct, dev.num_cu))
         return launch(reinterpret_cast<const void*>(&fp8_dequantize_kernel<Out, 8>), ceil_div(rows, 8) * p.nct,
                       256, p, stream);
     return launch(reinterpret_cast<const void*>(&fp8_dequantize_kernel<Out, 1>), rows * p.nct, 256, p, stream);
@@ -583,7 +593,7 @@ int gated_backward(const sdt_gated_ff_grad* a, void* stream) {
         p.nct = (int)ceil_div(N, 2048);
         p.wide = a->wide;
         p.act = a->act;
-        rc = many_rows(M, p.nct, dev.num_cu)
+        rc = many_short(M, N, 256, dev.num_cu)
                  ? launch(reinterpret_cast<const void*>(&gated_grad_kernel<Elt, 4>), ceil_div(M, 4) * p.nct, 256,
                           p, stream)
                  : launch(reinterpret_cast<const void*>(&gated_grad_kernel<Elt, 1>), M * p.nct, 256, p, stream);

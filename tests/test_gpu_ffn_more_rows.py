@@ -1,5 +1,5 @@
-"""The row-wise kernels where a workgroup takes several rows at a time (from some 4096 row
-tiles on), where a workgroup of the norm's gradient takes rows in turn, and the signs of
+"""The row-wise kernels at the sizes where a workgroup takes several rows at a time (short
+rows from 32768 on, values back from 8192 row tiles on) and around, where a workgroup of the norm's gradient takes rows in turn, and the signs of
 zeros among the codes."""
 import numpy as np
 import pytest
@@ -42,7 +42,8 @@ def quantized(x, block):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("block", [1, 128])
 @pytest.mark.parametrize("rows, K, pad", [(4096, 8, 0), (5003, 9, 0), (4099, 130, 1), (4101, 7, 0), (2051, 2100, 4),
-                                          (1371, 4097, 0)])
+                                          (1371, 4097, 0), (8200, 300, 0), (4100, 2050, 1), (32768, 8, 0),
+                                          (33001, 9, 2), (32771, 130, 0), (40003, 33, 0), (32769, 7, 0)])
 def test_quantize_many_rows(dtype, block, rows, K, pad):
     import torch
     say(f"quantize many rows {dtype} block {block} {rows}x{K}+{pad}")
@@ -70,7 +71,7 @@ def test_quantize_many_rows(dtype, block, rows, K, pad):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("block", [1, 128])
-@pytest.mark.parametrize("rows", [3, 5000])
+@pytest.mark.parametrize("rows", [3, 5000, 33000])
 def test_signs_of_zeros(dtype, block, rows):
     """The quotient's sign is the code's, of zeros and of quotients that round to zero."""
     import torch
@@ -95,7 +96,8 @@ def test_signs_of_zeros(dtype, block, rows):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M, N, K", [(4099, 70, 40), (2050, 2060, 72), (5000, 1, 8)])
+@pytest.mark.parametrize("M, N, K", [(4099, 70, 40), (2050, 2060, 72), (5000, 1, 8), (32771, 70, 40),
+                                     (33000, 3, 8)])
 @pytest.mark.parametrize("act, kept", [("silu", "wide"), ("gelu", "type")])
 def test_gated_backward_many_rows(dtype, M, N, K, act, kept):
     base.test_gated_backward(dtype, M, N, K, act, kept)
