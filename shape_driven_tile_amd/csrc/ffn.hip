@@ -191,18 +191,27 @@ int launch_pp(TileGemm& p, void* stream) {
 
 // Whether t256 tiles of 256 x 256, a workgroup a CU, beat t128 of 128 x 128, two: by a
 // CU's time in us, `kt` k-tiles of 128 bytes a tile (16 bits, gated and turned, and 8
-// bits; fitted to 20 sizes).  A round of 256 x 256 tiles takes 1.45 a k-tile (8 bits
-// 1.55) and 9.5 besides, however full.  One of 128 x 128 tiles takes 0.95 and 6 (1.05
-// and 5.5), a partial one its share and a tenth, since CUs go on to it as they come free.
-// 256 against 128: 4096^3 nn 104 and 134, 8 bits 59 and 73; 4096 x 4096 x 512 20 and 27,
-// 17 and 24; 2048 x 4096 x 4096 83 and 67, 49 and 39; 4096 x 5000 x 4096 tn 194 and 168,
-// 113 and 93; 6000 x 6000 x 512 71 and 54, 57 and 38.
+// bits; fitted to both sides at 81 sizes of 64 to 1024 large tiles, 8 to 64 k-tiles, half of
+// them with rows off 128 bytes).  A round of 256 x 256 tiles takes 1.4 a k-tile (8 bits 1.55)
+// and 10.5 (9.5) besides, a partial one down to 0.7 of the 1.4 as its tiles get fewer.  One
+// of 128 x 128 tiles takes 0.95 and 6 (1.05 and 5.5), a partial one its share and a tenth,
+// since CUs go on to it as they come free; right after the first round, whose tiles end
+// together, 0.65 at least.  256 against 128, nn and 8 bits: 128 large tiles, 2048 x 4096 x
+// 4096 73 and 62, 46 and 38; 144 (3000^3) 62 and 92, 39 and 50; 160 (2560 x 4096 x 2048) 42
+// and 54, 27 and 33; 256 (4096^3) 95 and 125, 55 and 68; 288 (2304 x 8192 x 8192) 311 and 295,
+// 179 and 165; 512 (8192 x 4096 x 1024) 57 and 77, 36 and 48; 576 (6000 x 6000 x 512) 63 and
+// 52, 49 and 35.  What it takes is 0.4% slower than the better side in the mean, 13% (8 bits
+// 22%: 7064 x 4008 x 472, 40 and 33) at most.
 bool large_tiles(int64_t t256, int64_t t128, int64_t kt, int64_t cu, bool fp8) {
     const double k = (double)kt;
-    const double full = fp8 ? 1.05 * k + 5.5 : 0.95 * k + 6.0;
-    const double large = (double)ceil_div(t256, cu) * ((fp8 ? 1.55 : 1.45) * k + 9.5);
+    const double slope = fp8 ? 1.55 : 1.4, besides = fp8 ? 9.5 : 10.5;
+    const int64_t rest256 = t256 % cu;
+    double large = (double)(t256 / cu) * (slope * k + besides);
+    if (rest256 > 0) large += slope * (0.7 + 0.3 * (double)rest256 / (double)cu) * k + besides;
     const int64_t whole = t128 / (2 * cu), rest = t128 % (2 * cu);
-    const double part = rest > 0 ? 0.1 + 0.9 * (double)rest / (2.0 * (double)cu) : 0.0;
+    double part = rest > 0 ? 0.1 + 0.9 * (double)rest / (2.0 * (double)cu) : 0.0;
+    if (rest > 0 && whole == 1) part = std::max(part, 0.65);
+    const double full = fp8 ? 1.05 * k + 5.5 : 0.95 * k + 6.0;
     return large < full * ((double)whole + part);
 }
 
@@ -216,9 +225,11 @@ int launch_rows(TileGemm& p, void* stream) {
 }
 constexpr int kFewRows = 16;
 
-// 8 bits, up to 16 rows, or up to 64 of weights that are soon read (16 MB: 7.9 us against
-// 11.1 on split tiles; 50 MB: 22.3 against 19.9).  16 columns a workgroup where 32 would
-// leave CUs idle.
+// 8 bits, up to 16 rows, or up to 64 of weights that are soon read: 64 rows, weights from
+// memory, streamed against split tiles: 4096 x 4096 (16 MB) 9.3 us and 12.2, 3000 x 8192 (23
+// MB) 14.3 and 14.6, 4096 x 8192 (32 MB) 14.5 and 15.0, 8192 x 4096 (32 MB) 16.4 and 14.6, 10240
+// x 4096 (40 MB) 22.9 and 18.1, 4096 x 12288 (48 MB) 22.1 and 20.1; 17 rows of the last 16.3 and
+// 18.1.  16 columns a workgroup where 32 would leave CUs idle.
 bool few_rows8(int64_t M, int64_t N, int64_t K) {
     return M <= kFewRows || (M <= 64 && N * K <= int64_t(1) << 25);
 }
