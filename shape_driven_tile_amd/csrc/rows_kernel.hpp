@@ -24,7 +24,7 @@ __device__ __forceinline__ float widen(BF16, uint32_t bits16) {
 // Eight elements of a row of K >= 8 from column k on, zeros past K: a partial chunk is
 // loaded as the row's last eight elements and moved down, and one past the row is that
 // load cleared, so that no load depends on a branch (with one around each, the eight of
-// a lane's rows wait for each other: 78 us for 8192 x 8192 fp16 codes).
+// a lane's rows wait for each other: 78 us for 8192 x 8192 fp16 codes by eight rows).
 __device__ __forceinline__ uint4_t load_wide(const uint16_t* row, int k, int K) {
     return *reinterpret_cast<const uint4_any_t*>(row + min(k, K - 8));
 }
@@ -156,9 +156,9 @@ struct Fp8Quant {
     int K, nct;            // column tiles of 2048 (rows' scales) or 128
 };
 
-// Scales for each row: RPT rows x 2048 columns a workgroup, 16 lanes a block.  All
-// rows of a lane are loaded before the first is used.  Bound by memory: 8192 x 8192 fp16
-// 38-42 us (4.8-5.2 TB/s; a copy 5.1), 4096 x 4096 13 us (3.9).
+// Scales for each row: RPT rows x 2048 columns a workgroup (one, or eight short ones), 16
+// lanes a block.  All rows of a lane are loaded before the first is used.  Bound by memory:
+// 8192 x 8192 fp16 36-41 us (5.0-5.5 TB/s; a copy 5.1), 4096 x 4096 13.3 us (3.8).
 template <typename Elt, int RPT>
 __global__ __launch_bounds__(256) void fp8_quantize_rows_kernel(Fp8Quant p) {
     const int t = threadIdx.x;
@@ -434,7 +434,8 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void rms_norm_kernel(Norm p) {
 // workgroup's sums of dy n over its rows (row, row + grid, ...).  T = 64: the
 // workgroup's four waves take rows in turn and add up in LDS.  Bound by memory where rows
 // fit the registers, 8192 x 4096 bf16 with the columns' sums 51-57 us (4.7-5.3 TB/s), and by
-// them and the second reading where not (1024 x 32768 142 us, 1.9).
+// them and the second reading where not (1024 x 32768 142 us, 1.9; without dtotal 122,
+// 1.65).
 template <typename Elt, int T, int CH>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void rms_norm_backward_kernel(Norm p) {
     constexpr int WG = T == 64 ? 256 : T;

@@ -343,11 +343,11 @@ __device__ __forceinline__ void wait_tiles(int n) {
 // reads and waits under the other's MFMAs.  The loads of the k-tile NS further on go
 // into a stage once its fragments are in registers, between the MFMAs.  GATED: B's
 // LDS rows alternate between the two matrices, so that a lane holds both factors of
-// its outputs; BN / 2 columns a tile.  A k-tile of 128 x 128 costs a CU 0.35 us a tile
-// with two of them, 0.7 with one: bound by a workgroup's own chain of waits, which the
-// other fills.  Deeper stages instead of the second workgroup do not (2048 x 3000 x 2048
-// turned, 384 tiles: 53 us against 32).  2048^3: nn 29.1 us, tn 28.3, 8 bits 15.3; gated 500
-// x 1400 x 1000 13.0.
+// its outputs; BN / 2 columns a tile.  A k-tile of 128 x 128 costs a CU 0.92 us with two
+// tiles at a time (0.46 a tile), 0.72 with one: bound by a workgroup's own chain of waits,
+// which the other fills.  Deeper stages instead of the second workgroup do not (2048 x 3000 x 2048
+// turned, 384 tiles: 53 us against 32).  2048^3: nn 28.9 us, tn 27.8, 8 bits 14.7; gated 500
+// x 1400 x 1000 13.1.
 template <typename Elt, bool FP8, int BM, int BN, int WM, int WN, int NS, bool TA, bool TB, bool GATED>
 __global__ __launch_bounds__(WM * WN * 64, 2) void tile_gemm_kernel(TileGemm p) {
     constexpr int NW = WM * WN;
@@ -895,7 +895,7 @@ struct GatedGrad {
 
 // dg = dh u a'(g), du = dh a(g), eight columns of a row a lane.  Both are rounded to
 // the type, which the MFMAs of the three products that read them take.  Bound by memory:
-// 4096 x 12288 from fp32 factors 145 us (704 MB, 4.9 TB/s).
+// 4096 x 12288 from fp32 factors 138 us (704 MB, 5.1 TB/s).
 template <typename Elt, int RPT>
 __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGrad p) {
     const int64_t r0 = (int64_t)(blockIdx.x / p.nct) * RPT;

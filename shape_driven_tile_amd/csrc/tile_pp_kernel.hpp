@@ -9,7 +9,7 @@
 // ds_read_b64_tr_b16 where a K-major one's take one ds_read_b128: as many bytes and,
 // on distinct banks, as many LDS clocks.  Two products that are added have the same
 // strides here: other offsets for the second would not fit the registers.  Bound by the
-// part's power: 8192 x 4096 x 4096 nn 190 us, tn 192-203 (1350-1450 TFLOP/s; the library's
+// part's power: 8192 x 4096 x 4096 nn 190-203 us, tn 192-222 (1240-1450 TFLOP/s; the library's
 // product of K-major operands 1460); gated 4096 x 12288 x 4096 604-647 (1270-1365).
 #pragma once
 
