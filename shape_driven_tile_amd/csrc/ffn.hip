@@ -57,9 +57,10 @@ int check_fp8(int64_t rows, int64_t K, const sdt_fp8& m) {
 // 8192 x 4096 110 and 116.  Short rows leave lanes idle: from 128 of them a CU on, codes of up
 // to 1024 elements by eight together (65536 x 512 32.9 us and 29.7, 262144 x 128 112 and 101;
 // 16384 x 512 11.1 and 11.7, 32768 x 1500 30.7 and 29.9), dg and du of up to 256 by four
-// (131072 x 256 118 and 112, 262144 x 128 193 and 166; 65536 x 512 103 and 108).
+// (131072 x 256 118 and 112, 262144 x 128 193 and 166; 65536 x 512 103 and 108).  Besides,
+// where one by one would be more threads than a launch has.
 bool many_short(int64_t rows, int64_t K, int64_t most, int num_cu) {
-    return K <= most && rows >= int64_t(128) * num_cu;
+    return (K <= most && rows >= int64_t(128) * num_cu) || rows * ceil_div(K, 2048) * 256 > UINT32_MAX;
 }
 // Values back, which are less work a row: eight rows together from 32 row tiles a CU on
 // (8192 x 2048 10.8 us and 8.9, 32768 x 512 17.5 and 13.2, 8192 x 8192 39.0 and 39.7; 4096 x
