@@ -4,7 +4,7 @@
 // A k-tile is one block of scales: 128 codes a row, 32 v_mfma_f32_16x16x128 a wave
 // and, since their sums are scaled before they are added, 128 v_fma_f32 beside them:
 // half the MFMAs' clocks, issued between them.  8192^3: 408-410 us launch after launch (2.7
-// PFLOP/s), 465-515 launched by itself or under the profiler, the MFMAs busy 67% of the
+// PFLOP/s), 430-515 launched by itself or under the profiler, the MFMAs busy 67% of the
 // clocks at some 1.53 GHz, the part's power limit; 4096^3 56 us.
 //
 // Waves 0-3 (group 0, columns 0-127 of the tile) and 4-7 (group 1) run one barrier
