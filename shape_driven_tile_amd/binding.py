@@ -1269,7 +1269,8 @@ class Fp8:
                 raise ValueError("Fp8: unit stride along rows of codes and of scales")
             # several rows of scales: their own stride, so that rows that overlap are refused
             given = (at[0], qs[0] if rows > 1 else max(qs[0], K), at[2], ss[0] if fits[0] > 1 else fits[1])
-            self._at, self._given, self._bytes = at, given, _pack_fp8(*given, self.block)
+            # _at last: another thread that finds it finds the rest
+            self._given, self._bytes, self._at = given, _pack_fp8(*given, self.block), at
         return self._given
 
     def _packed(self):

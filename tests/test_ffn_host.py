@@ -328,3 +328,24 @@ def test_sizes_that_are_refused(t):
     K = 1 << 23
     A, B = (ctypes.byref(sdt.SdtFp8(P, K, P, 1 << 16, block)) for block in (1, 128))
     assert call(f"gemm_fp8_{t}", 100, 64, K, A, B, P, 64, None, 0, None) == UNSUPPORTED
+
+
+def test_fp8_packed_by_two_threads():
+    """What a matrix keeps of its memory is there before it counts as kept: another thread that
+    finds the same memory in between would use the rest."""
+    import torch
+
+    class Watched(sdt.Fp8):
+        __slots__ = ("order",)
+
+        def __setattr__(self, name, value):
+            object.__setattr__(self, name, value)
+            if hasattr(self, "order") and name != "order":
+                self.order.append(name)
+    m = Watched.empty(4, 128, device="cpu")
+    m.order = []
+    m._packed()
+    m.s.set_(torch.ones(1, 4))
+    m._packed()
+    m._args()
+    assert len(m.order) == 6 and m.order[2] == m.order[5] == "_at"
